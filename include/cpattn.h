@@ -47,8 +47,10 @@ typedef enum {
   CPATTN_E_CUDA = 3,         /* a CUDA runtime/driver call or launch failed */
   CPATTN_E_NOMEM = 4,        /* host or device allocation failed (create only) */
   CPATTN_E_TIMEOUT = 5,      /* a device-side bounded wait expired; context still usable */
-  CPATTN_E_RANGE = 6         /* a V value converted to fp16 (fp16 V cache or V staging)
+  CPATTN_E_RANGE = 6,        /* a V value converted to fp16 (fp16 V cache or V staging)
                                 lies outside fp16's range */
+  CPATTN_E_PAGE = 7          /* a paged call met a page id outside the pool, or a length
+                                beyond the block table or the striped cache */
 } cpattn_status;
 
 typedef struct {
@@ -424,6 +426,150 @@ cpattn_status cpattn_prefill_noalloc(const cpattn_config* cfg, int32_t num_seqs,
 
 /* Free the context (NULL-safe).  Does not synchronise. */
 void cpattn_destroy(cpattn_ctx* ctx);
+
+/*
+ * Causal attention over whole prompts, packed one behind the other: for every
+ * sequence b of seq_lens[b] tokens (rows r_b = sum of the earlier lengths),
+ * q head h and token i,
+ *   O[r_b+i, h, :] = softmax_{j<=i}( scale * <q_i, k_j> ) . v_j
+ * over the sequence's own keys of kv head h/(NQ/NKV) -- cpattn_prefill without
+ * a cache and without padding rows.  The sequences may have any lengths, 0
+ * and 1 among them; chunk_size, num_shards and shard_capacity of the
+ * configuration play no part.  A sequence's result does not depend on its
+ * neighbours' rows, whatever they hold (NaN and infinities included).  A
+ * non-finite V row reaches the earlier rows of its own sequence that share
+ * its 128-token tile (0 * NaN), as in cpattn_prefill.
+ *   seq_lens[B]    host int32, >= 0; read during the call only
+ *   q, out         device bf16 [sum of seq_lens, NQ, HD]
+ *   k, v           device bf16 [sum of seq_lens, NKV, HD]
+ *   lse            device fp32 [sum of seq_lens, NQ], or NULL
+ *   workspace      device memory, 256-byte aligned, at least
+ *                  cpattn_prefill_packed_workspace() bytes, used by the
+ *                  call's kernels only: V is staged there with every sequence
+ *                  on a tile boundary.  Calls that overlap on the GPU must not
+ *                  share one.
+ * With cpattn_config.v_cache_f16 the staged V is fp16 and P.V one product of
+ * fp16 P (a value beyond 65504 is reported by cpattn_sync_status as E_RANGE);
+ * otherwise V stays bf16 and P is a bf16 hi + lo pair (fast_p: bf16).  Short
+ * prompts run GQA-packed and units are dealt as in cpattn_prefill.  Two
+ * launches (the staging, then the prefill kernel); a walk is never split.
+ * Errors: E_INVALID, E_UNSUPPORTED (more than CPATTN_MAX_SEQS sequences or
+ * CPATTN_MAX_ROW_BLOCKS row blocks of 128 tokens), E_CUDA, E_NOMEM (host).
+ */
+cpattn_status cpattn_prefill_packed_workspace(const cpattn_ctx* ctx, int32_t num_seqs,
+                                              const int32_t* seq_lens, uint64_t* bytes);
+cpattn_status cpattn_prefill_packed(cpattn_ctx* ctx, int32_t num_seqs, const int32_t* seq_lens,
+                                    const void* q, const void* k, const void* v, void* out,
+                                    float* lse, void* workspace, uint64_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * The paged KV cache
+ * ------------------
+ * A pool of pages of page_size consecutive tokens, shared by all sequences:
+ *   k_pages, v_pages   [num_pages, NKV, page_size, HD]
+ * Token t of sequence b lives in page block_table[b][t / page_size] at slot
+ * t mod page_size.  Formats:
+ *   CPATTN_PAGES_BF16  bf16 values
+ *   CPATTN_PAGES_E4M3  8-bit e4m3 values (4 exponent and 3 mantissa bits, no
+ *                      infinities) with one fp32 scale per token and kv head,
+ *                      k_scales and v_scales [num_pages, NKV, page_size]:
+ *                        s = max(amax, 2^-110) / 448
+ *                        x8 = e4m3(x * (448 / max(amax, 2^-110)))   (fp32, nearest even)
+ *                      and the value read back is s * x8.  A row that holds
+ *                      an infinity or a NaN is stored with a NaN scale.
+ * Lengths, row_starts and block_table are DEVICE arrays, read when the kernels
+ * run: a captured graph of these calls can be replayed after they changed.
+ * So they are checked on the device: a page id outside [0, num_pages), or a
+ * length beyond the table's row, makes the next cpattn_sync_status return
+ * CPATTN_E_PAGE; such tokens are skipped, and nothing outside the pool is
+ * touched.  Table columns behind a sequence's last page are never read.
+ * Slots behind a sequence's last token may hold anything, NaN included.
+ * head_dim, the head counts and softmax_scale come from the context, as does
+ * the V format of the striped cache; v_cache_f16 says nothing about pages.
+ */
+#define CPATTN_PAGES_BF16 0
+#define CPATTN_PAGES_E4M3 1
+#define CPATTN_MAX_PAGED_SEQS 4096
+
+typedef struct {
+  int32_t format;              /* CPATTN_PAGES_BF16 or CPATTN_PAGES_E4M3 */
+  int32_t page_size;           /* 16, 32, 64, 128 or 256 tokens */
+  int32_t num_pages;           /* pages in the pool */
+  int32_t max_pages;           /* columns of block_table in use, >= 1 */
+  int64_t table_stride;        /* elements between its rows, >= max_pages */
+  void* k_pages;               /* device, 16-byte aligned */
+  void* v_pages;
+  float* k_scales;             /* device, 16-byte aligned; e4m3 only, else NULL */
+  float* v_scales;
+  const int32_t* block_table;  /* device int32 [num_seqs][table_stride] */
+} cpattn_pages;
+
+/*
+ * Write new tokens into their pages (quantising them for e4m3 pages): rows
+ * row_starts[b] .. row_starts[b+1]-1 of k_new and v_new are tokens
+ * cache_lens[b], cache_lens[b]+1, ... of sequence b.
+ *   num_seqs     B, 1..CPATTN_MAX_PAGED_SEQS
+ *   num_rows     rows of k_new and v_new; rows before row_starts[0] or from
+ *                row_starts[B] on belong to no sequence and are ignored
+ *   cache_lens   device int32 [B] tokens already cached; negative: the
+ *                sequence is skipped (a padded slot of a captured batch)
+ *   row_starts   device int32 [B+1], non-decreasing; or NULL: one token per
+ *                sequence (a decode step), row b for sequence b, num_rows == B
+ *   k_new, v_new device bf16 [num_rows, NKV, HD]
+ * Nothing else of the pool is written.  Two tokens of one call must not share
+ * a slot (two sequences whose tables name the same page there): which of them
+ * is stored would be undefined, and their values and scales might mix.
+ * One launch.  Errors: E_INVALID, E_UNSUPPORTED, E_CUDA; E_PAGE by
+ * cpattn_sync_status.
+ */
+cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                                    int32_t num_rows, const int32_t* cache_lens,
+                                    const int32_t* row_starts, const void* k_new,
+                                    const void* v_new, void* stream);
+
+/*
+ * Read tokens first[b] .. lens[b]-1 of every sequence back from its pages
+ * into the striped caches that cpattn_prefill takes:
+ *   k_cache[b, g, t mod P, t div P, :] = value of token t, kv head g   (same for V)
+ * rounded to bf16 (V to fp16 with v_cache_f16; a value beyond 65504 is
+ * reported as E_RANGE).  No other cache row is written, so a prefix of which
+ * the cache holds first[b] tokens already is only extended.
+ *   first     device int32 [B], or NULL: 0 for every sequence
+ *   lens      device int32 [B]; lens[b] <= first[b]: nothing is read
+ *   k_cache   device bf16 [B, NKV, P, S, HD]
+ *   v_cache   the same, bf16 or (v_cache_f16) fp16
+ * A length beyond P*S or the table's row is cut there and reported as E_PAGE.
+ * One launch.  Errors: as cpattn_paged_write_kv.
+ */
+cpattn_status cpattn_paged_read_kv(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                                   const int32_t* first, const int32_t* lens, void* k_cache,
+                                   void* v_cache, void* stream);
+
+/*
+ * Decode attention: one new token per sequence over its pages.  For every
+ * sequence b and q head h
+ *   O[b, h, :] = softmax_t( scale * <q_b, k_t> ) . v_t,  t in [0, lens[b])
+ * over the cached tokens of kv head h/(NQ/NKV), the new one among them if it
+ * was written before (cpattn_paged_write_kv).  Sums and softmax statistics in
+ * fp32.  A sequence without tokens (lens[b] <= 0) gets O = 0 and an LSE of
+ * -infinity.
+ *   lens        device int32 [B], B in 1..CPATTN_MAX_PAGED_SEQS
+ *   q, out      device bf16 [B, NQ, HD]
+ *   lse         device fp32 [B, NQ] natural-log sum-exp, or NULL
+ *   workspace   device memory, 256-byte aligned, at least
+ *               cpattn_paged_decode_workspace() bytes, used by the call's
+ *               kernels only; its contents need no preparation.  Calls that
+ *               overlap on the GPU must not share one.
+ * Errors: as cpattn_paged_write_kv; E_INVALID also for a small or misaligned
+ * workspace.  After E_PAGE the outputs of the sequences concerned lack the
+ * skipped tokens.
+ */
+cpattn_status cpattn_paged_decode_workspace(const cpattn_ctx* ctx, int32_t num_seqs,
+                                            uint64_t* bytes);
+cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                                  const int32_t* lens, const void* q, void* out, float* lse,
+                                  void* workspace, uint64_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* cpattn_status_string(cpattn_status s);

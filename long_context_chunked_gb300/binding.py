@@ -16,9 +16,11 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 # CPATTN_LIBRARY overrides the library path (e.g. an instrumented build).
 LIB_PATH = os.environ.get("CPATTN_LIBRARY") or os.path.join(_PKG, "libcpattn.so")
 
-OK, E_INVALID, E_UNSUPPORTED, E_CUDA, E_NOMEM, E_TIMEOUT, E_RANGE = range(7)
+OK, E_INVALID, E_UNSUPPORTED, E_CUDA, E_NOMEM, E_TIMEOUT, E_RANGE, E_PAGE = range(8)
 MAX_SEQS = 128
 MAX_ROW_BLOCKS = 2048
+MAX_PAGED_SEQS = 4096
+PAGE_SIZES = (16, 32, 64, 128, 256)
 
 # Every symbol include/cpattn.h declares.
 EXPORTS = ("cpattn_create", "cpattn_write_kv", "cpattn_prefill", "cpattn_sync_status",
@@ -26,7 +28,9 @@ EXPORTS = ("cpattn_create", "cpattn_write_kv", "cpattn_prefill", "cpattn_sync_st
            "cpattn_status_string", "cpattn_last_error", "cpattn_prefill_noalloc",
            "cpattn_two_launch_workspace", "cpattn_prefill_two_launch", "cpattn_set_splitkv",
            "cpattn_splitkv_workspace", "cpattn_cache_walk_from", "cpattn_prefill_write_kv",
-           "cpattn_set_barrier_counts", "cpattn_set_v_staging", "cpattn_v_staging_bytes")
+           "cpattn_set_barrier_counts", "cpattn_set_v_staging", "cpattn_v_staging_bytes",
+           "cpattn_prefill_packed", "cpattn_prefill_packed_workspace", "cpattn_paged_write_kv",
+           "cpattn_paged_read_kv", "cpattn_paged_decode", "cpattn_paged_decode_workspace")
 
 # cpattn_config.pairing values, by name.
 PAIRING = {"mma2": 0, "none": 1, "pingpong": 2}
@@ -47,6 +51,54 @@ class Config(ctypes.Structure):
                 ("softmax_scale", ctypes.c_float), ("fast_p", ctypes.c_int32),
                 ("v_cache_f16", ctypes.c_int32), ("pairing", ctypes.c_int32),
                 ("gqa_packing", ctypes.c_int32)]
+
+
+class Pages(ctypes.Structure):
+    """cpattn_pages."""
+    _fields_ = [("format", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("table_stride", ctypes.c_int64), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
+
+
+class PagedKV:
+    """A paged KV cache: pools [num_pages, NKV, page_size, HD] of bf16, or of
+    torch.float8_e4m3fn with fp32 scales [num_pages, NKV, page_size], and the
+    int32 block table [num_seqs, max_pages] (its rows may be a slice of a wider
+    table).  Holds references to the tensors and checks them once; their
+    contents are read by the kernels of each call."""
+
+    def __init__(self, k_pages, v_pages, block_table, k_scales=None, v_scales=None):
+        import torch
+        if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError(f"pages must be bfloat16 or float8_e4m3fn, got {k_pages.dtype}")
+        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+            raise ValueError("k_pages and v_pages must be alike, [num_pages, NKV, page_size, HD]")
+        e4m3 = k_pages.dtype == torch.float8_e4m3fn
+        if (k_scales is None) != (not e4m3) or (v_scales is None) != (not e4m3):
+            raise ValueError("e4m3 pages need k_scales and v_scales, bf16 pages take none")
+        dense = [k_pages, v_pages] + ([k_scales, v_scales] if e4m3 else [])
+        for t in dense[2:]:
+            if t.dtype != torch.float32 or t.shape != k_pages.shape[:3]:
+                raise ValueError("scales must be float32 [num_pages, NKV, page_size]")
+        if block_table.dim() != 2 or block_table.dtype != torch.int32 or (
+                block_table.shape[1] > 1 and block_table.stride(1) != 1) or (
+                block_table.shape[0] > 1 and block_table.stride(0) < block_table.shape[1]):
+            raise ValueError("block_table must be int32 [num_seqs, max_pages] with dense rows")
+        if any(not t.is_contiguous() for t in dense):
+            raise ValueError("pages and scales must be contiguous")
+        if any(not t.is_cuda or t.device != k_pages.device for t in dense + [block_table]):
+            raise ValueError("pages, scales and block_table must be on one CUDA device")
+        self.k_pages, self.v_pages, self.block_table = k_pages, v_pages, block_table
+        self.k_scales, self.v_scales = k_scales, v_scales
+        self.device = k_pages.device
+        self.num_seqs, cols = block_table.shape
+        self.num_kv_heads, self.head_dim = k_pages.shape[1], k_pages.shape[3]
+        self.c = Pages(int(e4m3), k_pages.shape[2], k_pages.shape[0], cols,
+                       max(block_table.stride(0), cols), _ptr(k_pages), _ptr(v_pages),
+                       _ptr(k_scales), _ptr(v_scales), _ptr(block_table))
+        self.ref = ctypes.byref(self.c)
 
 
 _libs = {}
@@ -103,6 +155,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.cpattn_set_v_staging.restype = I32
         lib.cpattn_v_staging_bytes.argtypes = [P, I32, ctypes.POINTER(ctypes.c_uint64)]
         lib.cpattn_v_staging_bytes.restype = I32
+    if hasattr(lib, "cpattn_paged_decode"):  # absent from older builds (A/B timing only)
+        U64, PAGES = ctypes.c_uint64, ctypes.POINTER(Pages)
+        for name, args in (
+                ("cpattn_prefill_packed_workspace", [P, I32, I32P, ctypes.POINTER(U64)]),
+                ("cpattn_prefill_packed", [P, I32, I32P, P, P, P, P, P, P, U64, P]),
+                ("cpattn_paged_write_kv", [P, PAGES, I32, I32, P, P, P, P, P]),
+                ("cpattn_paged_read_kv", [P, PAGES, I32, P, P, P, P, P]),
+                ("cpattn_paged_decode_workspace", [P, I32, ctypes.POINTER(U64)]),
+                ("cpattn_paged_decode", [P, PAGES, I32, P, P, P, P, P, U64, P])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = I32
     _libs[path] = lib
     return lib
 
@@ -119,6 +182,20 @@ def _ptr(t) -> int:
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _want(name, t, dtype, shape, like=None):
+    """A contiguous CUDA tensor of this dtype and shape, on `like`'s device."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous() or (
+            like is not None and t.device != like.device):
+        raise ValueError(f"{name}: expected a contiguous {dtype} CUDA tensor {list(shape)}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _workspace_bytes(workspace, like) -> int:
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != like.device:
+        raise ValueError("workspace: expected a contiguous CUDA tensor on the inputs' device")
+    return workspace.numel() * workspace.element_size()
 
 
 def _stream(stream) -> int:
@@ -255,6 +332,94 @@ class Context:
         n = ctypes.c_uint64()
         self._check(self.lib.cpattn_v_staging_bytes(self._h, num_seqs, ctypes.byref(n)))
         return n.value
+
+    # -- packed prompts and the paged cache ------------------------------
+    def prefill_packed_workspace(self, seq_lens) -> int:
+        """Workspace bytes of prefill_packed for these prompt lengths."""
+        sl, slp = _i32(seq_lens)
+        n = ctypes.c_uint64()
+        self._check(self.lib.cpattn_prefill_packed_workspace(self._h, len(sl), slp,
+                                                             ctypes.byref(n)))
+        return n.value
+
+    def prefill_packed(self, seq_lens, q, k, v, out, workspace, lse=None, stream=None):
+        """Causal attention over whole prompts packed one behind the other:
+        q, out [sum(seq_lens), NQ, HD], k, v [sum(seq_lens), NKV, HD], bf16."""
+        sl, slp = _i32(seq_lens)
+        rows = int(sl.sum(dtype=np.int64))
+        nq, nkv, hd = self.cfg.num_q_heads, self.cfg.num_kv_heads, self.cfg.head_dim
+        import torch
+        _want("q", q, torch.bfloat16, (rows, nq, hd))
+        _want("k", k, torch.bfloat16, (rows, nkv, hd), q)
+        _want("v", v, torch.bfloat16, (rows, nkv, hd), q)
+        _want("out", out, torch.bfloat16, (rows, nq, hd), q)
+        if lse is not None:
+            _want("lse", lse, torch.float32, (rows, nq), q)
+        self._check(self.lib.cpattn_prefill_packed(
+            self._h, len(sl), slp, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+            _ptr(workspace), _workspace_bytes(workspace, q), _stream(stream)))
+
+    def paged_write_kv(self, pages: PagedKV, cache_lens, k_new, v_new, row_starts=None,
+                       stream=None):
+        """Write (for e4m3 pages: quantise) new tokens into their pages: rows
+        row_starts[b] .. row_starts[b + 1] - 1 of k_new and v_new [rows, NKV, HD]
+        are the tokens of sequence b from cache_lens[b] on; row_starts None: one
+        token per sequence.  cache_lens and row_starts: int32 CUDA tensors."""
+        import torch
+        self._check_pages(pages)
+        b = pages.num_seqs
+        rows = k_new.shape[0]
+        shape = (rows, pages.num_kv_heads, pages.head_dim)
+        _want("k_new", k_new, torch.bfloat16, shape, pages)
+        _want("v_new", v_new, torch.bfloat16, shape, pages)
+        _want("cache_lens", cache_lens, torch.int32, (b,), pages)
+        if row_starts is not None:
+            _want("row_starts", row_starts, torch.int32, (b + 1,), pages)
+        self._check(self.lib.cpattn_paged_write_kv(
+            self._h, pages.ref, b, rows, _ptr(cache_lens), _ptr(row_starts), _ptr(k_new),
+            _ptr(v_new), _stream(stream)))
+
+    def paged_read_kv(self, pages: PagedKV, lens, k_cache, v_cache, first=None, stream=None):
+        """Read tokens first[b] (None: 0) .. lens[b] - 1 back into the striped
+        caches [num_seqs, NKV, P, S, HD] of the chunked prefill."""
+        import torch
+        self._check_pages(pages)
+        c, b = self.cfg, pages.num_seqs
+        shape = (b, c.num_kv_heads, c.num_shards, c.shard_capacity, c.head_dim)
+        _want("k_cache", k_cache, torch.bfloat16, shape, pages)
+        _want("v_cache", v_cache, torch.float16 if self.v_cache_f16 else torch.bfloat16, shape,
+              pages)
+        _want("lens", lens, torch.int32, (b,), pages)
+        if first is not None:
+            _want("first", first, torch.int32, (b,), pages)
+        self._check(self.lib.cpattn_paged_read_kv(self._h, pages.ref, b, _ptr(first), _ptr(lens),
+                                                  _ptr(k_cache), _ptr(v_cache), _stream(stream)))
+
+    def paged_decode_workspace(self, num_seqs: int) -> int:
+        """Workspace bytes of paged_decode for a batch of num_seqs sequences."""
+        n = ctypes.c_uint64()
+        self._check(self.lib.cpattn_paged_decode_workspace(self._h, num_seqs, ctypes.byref(n)))
+        return n.value
+
+    def paged_decode(self, pages: PagedKV, lens, q, out, workspace, lse=None, stream=None):
+        """Attention of one new token per sequence, q [num_seqs, NQ, HD], over
+        the first lens[b] (int32 CUDA tensor) tokens of its pages."""
+        import torch
+        self._check_pages(pages)
+        b, nq = pages.num_seqs, self.cfg.num_q_heads
+        _want("q", q, torch.bfloat16, (b, nq, pages.head_dim), pages)
+        _want("out", out, torch.bfloat16, (b, nq, pages.head_dim), pages)
+        _want("lens", lens, torch.int32, (b,), pages)
+        if lse is not None:
+            _want("lse", lse, torch.float32, (b, nq), pages)
+        self._check(self.lib.cpattn_paged_decode(
+            self._h, pages.ref, b, _ptr(lens), _ptr(q), _ptr(out), _ptr(lse), _ptr(workspace),
+            _workspace_bytes(workspace, pages), _stream(stream)))
+
+    def _check_pages(self, pages: PagedKV):
+        if (pages.num_kv_heads, pages.head_dim) != (self.cfg.num_kv_heads, self.cfg.head_dim):
+            raise ValueError(f"pages hold {pages.num_kv_heads} kv heads of {pages.head_dim}, the "
+                             f"context {self.cfg.num_kv_heads} of {self.cfg.head_dim}")
 
     def sync_status(self, stream=None) -> int:
         """Synchronise and return the status code (E_TIMEOUT if a device wait expired)."""

@@ -20,6 +20,7 @@
 #include "prefill_pingpong.cuh"
 #include "walk.cuh"
 #include "write_kv.cuh"
+#include "paged.cuh"
 #include "merge.cuh"
 #include "plan.h"
 
@@ -82,6 +83,7 @@ cpattn_status cuda_fail(cpattn_ctx* ctx, cudaError_t e, const char* what) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -139,6 +141,16 @@ cpattn_status check_seqs(cpattn_ctx* ctx, int32_t num_seqs, const int32_t* cache
   const long long tokens = static_cast<long long>(num_seqs) * c.chunk_size;
   if (cache_rows + kBKV >= (1LL << 31) || tokens + kBQ >= (1LL << 31))
     return fail(ctx, CPATTN_E_UNSUPPORTED, "cache or token row count exceeds 2^31");
+  return CPATTN_OK;
+}
+
+// A context's launches go to the device that was current when it was created.
+cpattn_status check_device(cpattn_ctx* ctx) {
+  int dev = -1;
+  if (ctx->d_status == nullptr) return CPATTN_OK;  // no device: refused at the launch
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail(ctx, CPATTN_E_CUDA, "cudaGetDevice");
+  if (dev != ctx->device)
+    return fail(ctx, CPATTN_E_INVALID, "the context belongs to another device than the current one");
   return CPATTN_OK;
 }
 
@@ -373,6 +385,37 @@ cpattn_status launch_splitkv_merge(cpattn_ctx* ctx, const cpattn::WorkPlan& plan
   return after_launch(ctx, st, "split-KV merge launch");
 }
 
+// The plan's work blocks in dealing order, and the number of units.
+void deal_blocks(cpattn_ctx* ctx, const cpattn::WorkPlan& plan, bool packed, int executors,
+                 int units_per_block, cpattn::PrefillParams* out) {
+  cpattn::PrefillParams& prm = *out;
+  const int NQ = ctx->cfg.num_q_heads, NKV = ctx->cfg.num_kv_heads;
+  // Unit order (PrefillParams::per): kv-head-major takes one block entry per
+  // (row block, kv head), so it needs NKV times the entries.
+  const size_t nblk = plan.blocks.size();
+  bool kv_major = false;
+  if (!packed && NKV > 1 && NQ <= 16384 && nblk * NKV <= CPATTN_MAX_ROW_BLOCKS &&
+      ctx->unit_order != 1) {
+    std::vector<int>& lens = ctx->block_lens;
+    lens.clear();
+    for (const cpattn::WorkBlock& b : plan.blocks) lens.push_back(b.v1 - b.v0);
+    // Executors take units_per_block units of a block (q heads, or head pairs).
+    kv_major = ctx->unit_order == 2 ||
+               cpattn::prefer_kv_major(lens, units_per_block / NKV, NKV, executors);
+  }
+  const int G = NQ / NKV;
+  const int reps = kv_major ? NKV : 1;
+  prm.per = kv_major ? G : (packed ? NKV : NQ);
+  for (int g = 0, i = 0; g < reps; ++g)
+    for (size_t j = 0; j < nblk; ++j, ++i) {
+      const cpattn::WorkBlock& w = plan.blocks[j];
+      prm.blocks[i] = cpattn::pack_block(w.b, w.qb, g * G);
+      prm.range[i] = (static_cast<uint32_t>(w.v0) << 16) | static_cast<uint32_t>(w.v1);
+      prm.part[i] = w.part;
+    }
+  prm.num_units = static_cast<int>(nblk * reps) * prm.per;
+}
+
 // Plan and launch one prefill: all regions (optionally split-KV, then the
 // merge), or one region of the two-launch variant.  Arguments already
 // validated.
@@ -450,31 +493,9 @@ cpattn_status prefill_launch(cpattn_ctx* ctx, int32_t num_seqs, const int32_t* c
   prm.debug_flags = ctx->debug_flags;
   prm.scale_log2 = c.softmax_scale * 1.4426950408889634f;
   for (int b = 0; b < num_seqs; ++b)
-    prm.seqs[b] = cpattn::SeqInfo{cache_lens[b], chunk_lens[b], plan.ncache[b], 0};
-  // Unit order (PrefillParams::per): kv-head-major takes one block entry per
-  // (row block, kv head), so it needs NKV times the entries.
-  const size_t nblk = plan.blocks.size();
-  bool kv_major = false;
-  if (!packed && NKV > 1 && NQ <= 16384 && nblk * NKV <= CPATTN_MAX_ROW_BLOCKS &&
-      ctx->unit_order != 1) {
-    std::vector<int>& lens = ctx->block_lens;
-    lens.clear();
-    for (const cpattn::WorkBlock& b : plan.blocks) lens.push_back(b.v1 - b.v0);
-    // Executors take units_per_block units of a block (q heads, or head pairs).
-    kv_major = ctx->unit_order == 2 ||
-               cpattn::prefer_kv_major(lens, units_per_block / NKV, NKV, executors);
-  }
-  const int G = NQ / NKV;
-  const int reps = kv_major ? NKV : 1;
-  prm.per = kv_major ? G : (packed ? NKV : NQ);
-  for (int g = 0, i = 0; g < reps; ++g)
-    for (size_t j = 0; j < nblk; ++j, ++i) {
-      const cpattn::WorkBlock& w = plan.blocks[j];
-      prm.blocks[i] = cpattn::pack_block(w.b, w.qb, g * G);
-      prm.range[i] = (static_cast<uint32_t>(w.v0) << 16) | static_cast<uint32_t>(w.v1);
-      prm.part[i] = w.part;
-    }
-  prm.num_units = static_cast<int>(nblk * reps) * prm.per;
+    prm.seqs[b] = cpattn::SeqInfo{cache_lens[b], chunk_lens[b], plan.ncache[b], b * c.chunk_size,
+                                  b * c.chunk_size};
+  deal_blocks(ctx, plan, packed, executors, units_per_block, &prm);
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cpattn_status s = dispatch_prefill(ctx, &prm, st, packed, cur_f16 != 0);
@@ -541,6 +562,7 @@ const char* cpattn_status_string(cpattn_status s) {
     case CPATTN_E_NOMEM: return "out of memory";
     case CPATTN_E_TIMEOUT: return "device-side wait timed out";
     case CPATTN_E_RANGE: return "value outside the fp16 V cache's range";
+    case CPATTN_E_PAGE: return "page id or length outside the paged cache";
   }
   return "unknown status";
 }
@@ -705,6 +727,10 @@ cpattn_status cpattn_sync_status(cpattn_ctx* ctx, void* stream) {
       return fail(ctx, CPATTN_E_RANGE,
                   "a V value converted to fp16 (for the fp16 V cache, or staged) lies outside "
                   "fp16's finite range");
+    if ((word & 0xFF) == cpattn::kStatusPage)
+      return fail(ctx, CPATTN_E_PAGE,
+                  "a paged call met a page id outside the pool, or a length beyond the block "
+                  "table's row or the striped cache; those tokens were skipped");
     return fail(ctx, CPATTN_E_TIMEOUT,
                 "a bounded device wait expired (site " + std::to_string(word >> 8) + ")");
   }
@@ -1079,7 +1105,8 @@ extern "C" cpattn_status cpattn_prefill_noalloc(const cpattn_config* cfg, int32_
   int n = 0;
   for (int b = 0; b < num_seqs; ++b) {
     const int ncache = cpattn::cache_tile_count(cache_lens[b], c.num_shards, c.shard_capacity);
-    prm.seqs[b] = cpattn::SeqInfo{cache_lens[b], chunk_lens[b], ncache, 0};
+    prm.seqs[b] = cpattn::SeqInfo{cache_lens[b], chunk_lens[b], ncache, b * c.chunk_size,
+                                  b * c.chunk_size};
     const int nqb = (chunk_lens[b] + kBQ - 1) / kBQ;
     for (int qb = 0; qb < nqb; ++qb) {
       const uint64_t work = static_cast<uint64_t>(ncache + qb + 1);
@@ -1140,3 +1167,153 @@ extern "C" cpattn_status cpattn_prefill_noalloc(const cpattn_config* cfg, int32_
   }
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_E_CUDA;
 }
+
+// ---------------------------------------------------------------------------
+// Packed prompts: whole prompts of different lengths, one behind the other.
+
+namespace {
+
+// First row of every sequence's V in the staging: each starts on a tile
+// boundary, so no tile of one sequence holds a row of another.
+uint64_t packed_stage_rows(int32_t num_seqs, const int32_t* seq_lens) {
+  uint64_t rows = 0;
+  for (int b = 0; b < num_seqs; ++b)
+    rows += (static_cast<uint64_t>(seq_lens[b]) + kBKV - 1) / kBKV * kBKV;
+  return rows;
+}
+
+cpattn_status check_packed(cpattn_ctx* ctx, int32_t num_seqs, const int32_t* seq_lens) {
+  if (num_seqs < 1) return fail(ctx, CPATTN_E_INVALID, "num_seqs must be >= 1");
+  if (num_seqs > CPATTN_MAX_SEQS)
+    return fail(ctx, CPATTN_E_UNSUPPORTED, "num_seqs exceeds CPATTN_MAX_SEQS");
+  if (seq_lens == nullptr) return fail(ctx, CPATTN_E_INVALID, "seq_lens must not be NULL");
+  for (int b = 0; b < num_seqs; ++b)
+    if (seq_lens[b] < 0)
+      return fail(ctx, CPATTN_E_INVALID, "seq_lens[" + std::to_string(b) + "] < 0");
+  // Staged rows are at least the packed ones; the kernel's row indices are 32-bit.
+  if (packed_stage_rows(num_seqs, seq_lens) + kBQ >= (1ull << 31))
+    return fail(ctx, CPATTN_E_UNSUPPORTED, "packed row count exceeds 2^31");
+  return CPATTN_OK;
+}
+
+cpattn_status packed_launch(cpattn_ctx* ctx, int32_t num_seqs, const int32_t* seq_lens,
+                            const void* q, const void* k, const void* v, void* out, float* lse,
+                            void* workspace, uint64_t workspace_bytes, void* stream) {
+  const cpattn_config& c = ctx->cfg;
+  const int HD = c.head_dim, NQ = c.num_q_heads, NKV = c.num_kv_heads;
+  static thread_local cpattn::WorkPlan plan;
+  static thread_local std::vector<int32_t> no_cache;
+  no_cache.assign(static_cast<size_t>(num_seqs), 0);
+  std::string why;
+  const int block_tokens = pack_block_tokens(ctx, num_seqs, seq_lens, cpattn::kRegionAll);
+  const bool packed = block_tokens != kBQ;
+  int executors = 0, units_per_block = 0;
+  plan_shape(ctx, packed, &executors, &units_per_block);
+  if (!cpattn::make_plan(c, num_seqs, no_cache.data(), seq_lens, cpattn::kRegionAll,
+                         cpattn::kSplitOff, executors, units_per_block, block_tokens, &plan, &why))
+    return fail(ctx, CPATTN_E_UNSUPPORTED, why);
+  if (plan.blocks.empty()) return CPATTN_OK;
+  const uint64_t stage_rows = packed_stage_rows(num_seqs, seq_lens);
+  const uint64_t rb = static_cast<uint64_t>(HD) * 2;
+  if (workspace_bytes < stage_rows * NKV * rb)
+    return fail(ctx, CPATTN_E_INVALID, "workspace too small (cpattn_prefill_packed_workspace)");
+  if (ctx->d_status == nullptr) return fail(ctx, CPATTN_E_CUDA, "no CUDA device");
+
+  static thread_local cpattn::PrefillParams prm;
+  static thread_local cpattn::StagePackedParams sp;
+  std::memset(&prm, 0, sizeof(prm));
+  uint64_t T = 0, staged = 0;
+  for (int b = 0; b < num_seqs; ++b) {
+    prm.seqs[b] = cpattn::SeqInfo{0, seq_lens[b], 0, static_cast<int>(T), static_cast<int>(staged)};
+    sp.row0[b] = static_cast<int>(T);
+    sp.staged0[b] = static_cast<int>(staged);
+    sp.len[b] = seq_lens[b];
+    T += static_cast<uint64_t>(seq_lens[b]);
+    staged += (static_cast<uint64_t>(seq_lens[b]) + kBKV - 1) / kBKV * kBKV;
+  }
+  const uint32_t vrows = 8192u / static_cast<uint32_t>(HD);
+  const bool ok =
+      encode3d(&prm.tm_q, q, HD, NQ, T, rb, rb * NQ, 64, 1, kBQ) &&
+      encode3d(&prm.tm_k_new, k, HD, NKV, T, rb, rb * NKV, 64, 1, kBKV) &&
+      encode3d(&prm.tm_k_new_h, k, HD, NKV, T, rb, rb * NKV, 64, 1, kBKV / 2) &&
+      encode3d(&prm.tm_v_new, workspace, HD, NKV, stage_rows, rb, rb * NKV, 64, 1, vrows) &&
+      encode3d(&prm.tm_v_new_h, workspace, HD, NKV, stage_rows, rb, rb * NKV, 64, 1, 64) &&
+      (!packed || encode3d(&prm.tm_q_packed, q, HD, NQ, T, rb, rb * NQ, 64,
+                           static_cast<uint32_t>(NQ / NKV), static_cast<uint32_t>(block_tokens)));
+  if (!ok) return fail(ctx, CPATTN_E_CUDA, "cuTensorMapEncodeTiled failed");
+  // No cache tiles: the kernel prefetches these maps and never loads from them.
+  prm.tm_k_cache = prm.tm_k_new;
+  prm.tm_k_cache_h = prm.tm_k_new_h;
+  prm.tm_v_cache = prm.tm_v_new;
+  prm.tm_v_cache_h = prm.tm_v_new_h;
+  prm.packed = packed ? 1 : 0;
+  prm.tb = block_tokens;
+  prm.out = static_cast<__nv_bfloat16*>(out);
+  prm.lse = lse;
+  prm.status = ctx->d_status;
+  prm.timeout_ns = ctx->timeout_ns;
+  prm.nq = NQ;
+  prm.nkv = NKV;
+  prm.group = NQ / NKV;
+  prm.P = 1;
+  prm.S = 1;
+  prm.C = c.chunk_size;
+  prm.debug_flags = ctx->debug_flags;
+  prm.scale_log2 = c.softmax_scale * 1.4426950408889634f;
+  deal_blocks(ctx, plan, packed, executors, units_per_block, &prm);
+
+  sp.v = static_cast<const uint4*>(v);
+  sp.staged = static_cast<uint4*>(workspace);
+  sp.status = ctx->d_status;
+  sp.num_seqs = num_seqs;
+  sp.f16 = c.v_cache_f16;
+  sp.vec_per_token = NKV * HD * 2 / 16;
+  sp.total_vecs = static_cast<long long>(stage_rows) * sp.vec_per_token;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int grid = static_cast<int>(std::min<long long>(
+      (sp.total_vecs + 255) / 256, static_cast<long long>(ctx->num_sms) * 4));
+  cpattn::stage_v_packed_kernel<<<grid, 256, 0, st>>>(sp);
+  cpattn_status s = after_launch(ctx, st, "packed V staging launch");
+  if (s != CPATTN_OK) return s;
+  return dispatch_prefill(ctx, &prm, st, packed, c.v_cache_f16 != 0);
+}
+
+}  // namespace
+
+extern "C" {
+
+cpattn_status cpattn_prefill_packed_workspace(const cpattn_ctx* ctx, int32_t num_seqs,
+                                              const int32_t* seq_lens, uint64_t* bytes) try {
+  if (ctx == nullptr || bytes == nullptr) return CPATTN_E_INVALID;
+  cpattn_status s = check_packed(const_cast<cpattn_ctx*>(ctx), num_seqs, seq_lens);
+  if (s != CPATTN_OK) return s;
+  *bytes = packed_stage_rows(num_seqs, seq_lens) * ctx->cfg.num_kv_heads * ctx->cfg.head_dim * 2;
+  return CPATTN_OK;
+} catch (...) {
+  return CPATTN_E_NOMEM;
+}
+
+cpattn_status cpattn_prefill_packed(cpattn_ctx* ctx, int32_t num_seqs, const int32_t* seq_lens,
+                                    const void* q, const void* k, const void* v, void* out,
+                                    float* lse, void* workspace, uint64_t workspace_bytes,
+                                    void* stream) try {
+  if (ctx == nullptr) return CPATTN_E_INVALID;
+  cpattn_status s = check_packed(ctx, num_seqs, seq_lens);
+  if (s != CPATTN_OK) return s;
+  if (packed_stage_rows(num_seqs, seq_lens) == 0) return CPATTN_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || out == nullptr || workspace == nullptr)
+    return fail(ctx, CPATTN_E_INVALID, "device pointers must not be NULL");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
+      (lse != nullptr && !aligned16(lse)) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(ctx, CPATTN_E_INVALID, "pointer alignment (16 B; workspace 256 B)");
+  s = check_device(ctx);
+  if (s != CPATTN_OK) return s;
+  return packed_launch(ctx, num_seqs, seq_lens, q, k, v, out, lse, workspace, workspace_bytes,
+                       stream);
+} catch (...) {
+  return CPATTN_E_NOMEM;
+}
+
+}  // extern "C"
+
+#include "paged_host.cuh"

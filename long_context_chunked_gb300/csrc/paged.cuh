@@ -1,0 +1,366 @@
+// The paged KV cache: writing new tokens into pages (as bf16, or quantised to
+// e4m3), reading pages back into the striped cache of the chunked prefill,
+// and the attention of one new token per sequence over the pages.
+//
+// A page holds page_size consecutive tokens of one sequence for every kv
+// head: pages[page][kv head][slot][HD], so the rows of one (page, kv head)
+// are contiguous.  Token t of sequence b sits in page table[b][t / page_size]
+// at slot t mod page_size.  Lengths and the table are read on the device, so
+// a captured step can be replayed after they changed; the kernels therefore
+// check every page id and length themselves: what lies outside is skipped and
+// reported through the status word (kStatusPage).
+//
+// e4m3 pages carry one fp32 scale per (token, kv head) and for K and V each:
+//   s = max(amax, 2^-110) / 448,  x8 = e4m3(x * (448 / amax)),  x ~ s * x8,
+// so that a token can be appended without touching the page's earlier ones.
+// The scale is one factor of a whole row: the attention multiplies it into a
+// logit (K) or a probability (V), never into the row's HD values.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "walk.cuh"
+
+namespace cpattn {
+
+struct PagedPool {
+  void* k;           // bf16 or e4m3 [num_pages][NKV][page_size][HD]
+  void* v;
+  float* k_scales;   // e4m3: [num_pages][NKV][page_size]
+  float* v_scales;
+  const int* table;  // [num_seqs][table_stride], the first max_pages columns used
+  long long table_stride;
+  int num_pages, max_pages, page_shift, nkv;
+};
+
+// Page holding tokens [idx * page_size, ...) of sequence b, or -1 (reported).
+__device__ __forceinline__ int page_id(const PagedPool& c, int b, int idx, int* status) {
+  int id = -1;
+  if (idx < c.max_pages) {
+    id = __ldg(c.table + b * c.table_stride + idx);
+    if (id >= c.num_pages) id = -1;
+  }
+  if (id < 0) {
+    id = -1;
+    if (status != nullptr) atomicCAS(status, kStatusOk, kStatusPage);
+  }
+  return id;
+}
+
+// Row of (page, kv head, slot) in the pool's [num_pages * NKV * page_size, HD].
+__device__ __forceinline__ long long pool_row(const PagedPool& c, int page, int g, int slot) {
+  return ((static_cast<long long>(page) * c.nkv + g) << c.page_shift) + slot;
+}
+
+// ----------------------------------------------------------- conversions
+constexpr float kE4m3Max = 448.f;
+constexpr float kTinyAmax = 7.703719777548943e-34f;  // 2^-110: keeps 448 / amax finite
+
+// Two fp32 values as e4m3 (round to nearest even, saturating), lo in the low byte.
+__device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e4m3 values as fp16 (exact), the low byte in the lower half.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+  return r;
+}
+
+// Largest magnitude of eight bf16 values, as bf16 bits: for sign-less bf16
+// the order of the bit patterns is the order of the values, with infinities
+// and NaNs on top.
+__device__ __forceinline__ uint32_t amax_bits(uint4 x) {
+  const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                              __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// ------------------------------------------------------------------ write
+struct PagedWriteParams {
+  PagedPool pool;
+  const uint4* k_new;     // bf16 [rows][NKV][HD]
+  const uint4* v_new;
+  const int* cache_lens;  // [num_seqs]; < 0: the sequence is skipped
+  const int* row_starts;  // [num_seqs + 1], or null: row b belongs to sequence b
+  int* status;
+  int num_seqs, rows;
+  int heads_per_item;     // kv heads one warp takes of a row
+};
+
+// One warp per (row, group of kv heads).  A row's 16-byte vectors: at HD = 128
+// the lower half-warp holds K and the upper one V, at HD = 256 the whole warp
+// holds K, then V.  HBM-bound copy: 2 bytes read and 1 (e4m3) or 2 written per
+// value.
+template <int HD, bool Q8>
+__global__ void __launch_bounds__(256)
+    paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
+  constexpr int VECS = HD / 8;        // 16-byte vectors per row
+  constexpr int LOADS = HD / 128;     // rows (K, V) a warp takes one after the other
+  const int lane = threadIdx.x & 31;
+  const int nkv = p.pool.nkv;
+  const int groups = (nkv + p.heads_per_item - 1) / p.heads_per_item;
+  const long long items = static_cast<long long>(p.rows) * groups;
+  const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+  for (long long it = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+       it < items; it += warps) {
+    const int row = static_cast<int>(it / groups);
+    const int g0 = static_cast<int>(it - static_cast<long long>(row) * groups) * p.heads_per_item;
+    int b = row, i = 0;
+    if (p.row_starts != nullptr) {
+      // The last sequence that starts at or before this row; rows before the
+      // first sequence or behind the last one belong to nobody.
+      if (row < p.row_starts[0] || row >= p.row_starts[p.num_seqs]) continue;
+      int lo = 0, hi = p.num_seqs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.row_starts[mid] <= row) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
+      i = row - p.row_starts[b];
+    }
+    const int have = p.cache_lens[b];
+    if (have < 0) continue;
+    const long long t = static_cast<long long>(have) + i;
+    const int page = page_id(p.pool, b, static_cast<int>(min(t >> p.pool.page_shift, 0x7FFFFFFFLL)), p.status);
+    if (page < 0) continue;
+    const int slot = static_cast<int>(t) & ((1 << p.pool.page_shift) - 1);
+    const int g1 = min(nkv, g0 + p.heads_per_item);
+    for (int g = g0; g < g1; ++g) {
+      const long long src = (static_cast<long long>(row) * nkv + g) * VECS;
+      const long long dst = pool_row(p.pool, page, g, slot);
+#pragma unroll
+      for (int l = 0; l < LOADS; ++l) {
+        const bool is_k = LOADS == 1 ? lane < 16 : l == 0;
+        const int vec = LOADS == 1 ? lane & 15 : lane;
+        const uint4 x = __ldg((is_k ? p.k_new : p.v_new) + src + vec);
+        void* pool = is_k ? p.pool.k : p.pool.v;
+        if constexpr (Q8) {
+          uint32_t m = amax_bits(x);
+#pragma unroll
+          for (int o = VECS / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          // A row with an infinity or a NaN has no scale: all of it reads back as NaN.
+          float amax = __uint_as_float(m << 16);
+          amax = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : fmaxf(amax, kTinyAmax);
+          const float inv = kE4m3Max / amax;
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            h[j] = pack_e4m3x2(__uint_as_float(w[j] << 16) * inv,
+                               __uint_as_float(w[j] & 0xFFFF0000u) * inv);
+          reinterpret_cast<uint2*>(pool)[dst * VECS + vec] =
+              make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+          if (vec == 0) (is_k ? p.pool.k_scales : p.pool.v_scales)[dst] = amax / kE4m3Max;
+        } else {
+          reinterpret_cast<uint4*>(pool)[dst * VECS + vec] = x;
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- read
+struct PagedReadParams {
+  PagedPool pool;
+  const int* first;  // [num_seqs] first token read, or null: 0
+  const int* lens;   // [num_seqs] tokens [first, lens) are read; lens <= first: none
+  uint4* k_cache;    // bf16 [num_seqs][NKV][P][S][HD]
+  uint4* v_cache;    // bf16 or fp16
+  int* status;
+  int num_seqs, P, S, v_f16;
+  int heads_per_item;
+};
+
+// Exclusive prefix sums of count(b), b < n, into prefix[0..n] (shared memory),
+// by the whole block of 256 threads.
+template <class Count>
+__device__ __forceinline__ void block_prefix(int n, int* prefix, Count count) {
+  __shared__ int warp_sum[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (n + 255) / 256;
+  const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += count(b);
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < warp; ++w) base += warp_sum[w];
+  int at = base + inc - sum;
+  for (int b = b0; b < b1; ++b) {
+    prefix[b] = at;
+    at += count(b);
+  }
+  if (b1 == n && (b0 < n || tid == 0)) prefix[n] = at;
+  __syncthreads();
+}
+
+// One 16-byte vector of a cache row (8 values) from the pool.  F16: as fp16.
+template <bool Q8>
+__device__ __forceinline__ uint4 widen_vec(const void* pool, const float* scales, long long row,
+                                           int vecs, int vec, bool f16, bool* overflow) {
+  if constexpr (Q8) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(pool) + row * vecs + vec);
+    const float s = __ldg(scales + row);
+    const uint32_t w[2] = {x.x, x.y};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      if (f16) {
+        o[j] = pack_f16x2(f.x * s, f.y * s);
+        if ((o[j] & 0x7C00u) == 0x7C00u || (o[j] & 0x7C000000u) == 0x7C000000u) *overflow = true;
+      } else {
+        o[j] = pack_bf16x2(f.x * s, f.y * s);
+      }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(pool) + row * vecs + vec);
+    return f16 ? bf16x8_to_f16x8(x, overflow) : x;
+  }
+}
+
+// One warp per (token, group of kv heads), lanes as in the write.  HBM-bound.
+template <int HD, bool Q8>
+__global__ void __launch_bounds__(256)
+    paged_read_kernel(const __grid_constant__ PagedReadParams p) {
+  constexpr int VECS = HD / 8;
+  constexpr int LOADS = HD / 128;
+  extern __shared__ int prefix[];
+  const int lane = threadIdx.x & 31;
+  const int nkv = p.pool.nkv;
+  // Tokens that both the striped cache and the table's row can hold.
+  const long long room = min(static_cast<long long>(p.P) * p.S,
+                             static_cast<long long>(p.pool.max_pages) << p.pool.page_shift);
+  auto start = [&](int b) { return p.first != nullptr ? max(p.first[b], 0) : 0; };
+  block_prefix(p.num_seqs, prefix, [&](int b) {
+    const int n = p.lens[b];
+    if (n > room && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusPage);
+    return static_cast<int>(max(0LL, min(static_cast<long long>(n), room) - start(b)));
+  });
+  const int total = prefix[p.num_seqs];
+  const int groups = (nkv + p.heads_per_item - 1) / p.heads_per_item;
+  const long long items = static_cast<long long>(total) * groups;
+  const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+  for (long long it = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+       it < items; it += warps) {
+    const int row = static_cast<int>(it / groups);
+    const int g0 = static_cast<int>(it - static_cast<long long>(row) * groups) * p.heads_per_item;
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= row) lo = mid; else hi = mid - 1;
+    }
+    const int t = start(lo) + row - prefix[lo];
+    const int page = page_id(p.pool, lo, t >> p.pool.page_shift, p.status);
+    if (page < 0) continue;
+    const int slot = t & ((1 << p.pool.page_shift) - 1);
+    const int g1 = min(nkv, g0 + p.heads_per_item);
+    for (int g = g0; g < g1; ++g) {
+      const long long src = pool_row(p.pool, page, g, slot);
+      const long long dst =
+          (static_cast<long long>(lo) * nkv + g) * p.P * p.S + static_cast<long long>(t % p.P) * p.S + t / p.P;
+#pragma unroll
+      for (int l = 0; l < LOADS; ++l) {
+        const bool is_k = LOADS == 1 ? lane < 16 : l == 0;
+        const int vec = LOADS == 1 ? lane & 15 : lane;
+        bool overflow = false;
+        const uint4 x = widen_vec<Q8>(is_k ? p.pool.k : p.pool.v,
+                                      is_k ? p.pool.k_scales : p.pool.v_scales, src, VECS, vec,
+                                      !is_k && p.v_f16 != 0, &overflow);
+        if (overflow && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusRange);
+        (is_k ? p.k_cache : p.v_cache)[dst * VECS + vec] = x;
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- decode
+struct PagedDecodeParams {
+  PagedPool pool;
+  const int* lens;            // [num_seqs]; <= 0: no tokens
+  const __nv_bfloat16* q;     // [num_seqs][NQ][HD]
+  __nv_bfloat16* out;         // [num_seqs][NQ][HD]
+  float* lse;                 // [num_seqs][NQ] or null
+  int* status;
+  int num_seqs, nq, group;
+  float scale_log2;
+};
+
+// One warp per (sequence, q head), one token at a time:
+//   x_t = scale <q, k_t>,  m = max x_t,  l = sum 2^(x_t - m),
+//   O = sum 2^(x_t - m) v_t / l,  LSE = (m + log2 l) ln 2   (log2 units),
+// with m, l and O carried along and rescaled when m grows.
+template <int HD, bool Q8>
+__global__ void __launch_bounds__(128)
+    paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
+  constexpr int E = HD / 32;  // dims 32 j + lane of this lane
+  const int lane = threadIdx.x & 31;
+  const long long w = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (w >= static_cast<long long>(p.num_seqs) * p.nq) return;
+  const int b = static_cast<int>(w / p.nq), h = static_cast<int>(w % p.nq), g = h / p.group;
+  const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
+  int n = p.lens[b];
+  if (n > room) {
+    n = static_cast<int>(room);
+    if (p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusPage);
+  }
+  float q[E], o[E];
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    q[j] = __bfloat162float(p.q[w * HD + 32 * j + lane]) * p.scale_log2;
+    o[j] = 0.f;
+  }
+  float m = -INFINITY, l = 0.f;
+  auto value = [&](const void* pool, long long row, int j) {
+    const long long e = row * HD + 32 * j + lane;
+    if constexpr (Q8) {
+      const uint32_t h2 = e4m3x2_to_f16x2(reinterpret_cast<const uint8_t*>(pool)[e]);
+      return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xFFFFu)));
+    } else {
+      return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pool)[e]);
+    }
+  };
+  const int ps = 1 << p.pool.page_shift;
+  for (int t0 = 0; t0 < n; t0 += ps) {
+    const int page = page_id(p.pool, b, t0 >> p.pool.page_shift, p.status);
+    if (page < 0) continue;
+    const int m1 = min(ps, n - t0);
+    for (int slot = 0; slot < m1; ++slot) {
+      const long long row = pool_row(p.pool, page, g, slot);
+      float x = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) x = fmaf(q[j], value(p.pool.k, row, j), x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+      if (Q8) x *= p.pool.k_scales[row];
+      const float mn = fmaxf(m, x);
+      const float a = ex2_approx(m - mn), e = ex2_approx(x - mn);
+      const float ev = Q8 ? e * p.pool.v_scales[row] : e;
+      l = l * a + e;
+#pragma unroll
+      for (int j = 0; j < E; ++j) o[j] = fmaf(ev, value(p.pool.v, row, j), o[j] * a);
+      m = mn;
+    }
+  }
+  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+  for (int j = 0; j < E; ++j) p.out[w * HD + 32 * j + lane] = __float2bfloat16(o[j] * inv);
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[w] = l > 0.f || l != l ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+}  // namespace cpattn

@@ -1,0 +1,200 @@
+// Entry points of the paged KV cache (part of cpattn.cu's translation unit):
+// argument checks and launches.  Contracts: include/cpattn.h.
+#pragma once
+
+namespace {
+
+// Checks shared by the paged entry points; *out receives the device view.
+cpattn_status check_pages(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                          cpattn::PagedPool* out) {
+  if (num_seqs < 1) return fail(ctx, CPATTN_E_INVALID, "num_seqs must be >= 1");
+  if (num_seqs > CPATTN_MAX_PAGED_SEQS)
+    return fail(ctx, CPATTN_E_UNSUPPORTED, "num_seqs exceeds CPATTN_MAX_PAGED_SEQS");
+  if (pages == nullptr) return fail(ctx, CPATTN_E_INVALID, "pages must not be NULL");
+  if (pages->format != CPATTN_PAGES_BF16 && pages->format != CPATTN_PAGES_E4M3)
+    return fail(ctx, CPATTN_E_INVALID, "pages: unknown format");
+  int shift = 4;
+  while (shift < 8 && (1 << shift) != pages->page_size) ++shift;
+  if ((1 << shift) != pages->page_size)
+    return fail(ctx, CPATTN_E_UNSUPPORTED, "pages: page_size must be 16, 32, 64, 128 or 256");
+  if (pages->num_pages < 1 || pages->max_pages < 1 || pages->table_stride < pages->max_pages)
+    return fail(ctx, CPATTN_E_INVALID, "pages: num_pages, max_pages >= 1, table_stride >= max_pages");
+  const long long nkv = ctx->cfg.num_kv_heads;
+  if (static_cast<long long>(pages->num_pages) * pages->page_size * nkv >= (1LL << 31) ||
+      static_cast<long long>(pages->max_pages) * pages->page_size >= (1LL << 31))
+    return fail(ctx, CPATTN_E_UNSUPPORTED, "pages: pool rows or a sequence's capacity exceed 2^31");
+  if (pages->k_pages == nullptr || pages->v_pages == nullptr || pages->block_table == nullptr)
+    return fail(ctx, CPATTN_E_INVALID, "pages: pointers must not be NULL");
+  if (!aligned16(pages->k_pages) || !aligned16(pages->v_pages) || !aligned4(pages->block_table))
+    return fail(ctx, CPATTN_E_INVALID, "pages: pools 16-byte, table 4-byte aligned");
+  if (pages->format == CPATTN_PAGES_E4M3 &&
+      (pages->k_scales == nullptr || pages->v_scales == nullptr || !aligned16(pages->k_scales) ||
+       !aligned16(pages->v_scales)))
+    return fail(ctx, CPATTN_E_INVALID, "pages: e4m3 needs 16-byte aligned scales");
+  out->k = pages->k_pages;
+  out->v = pages->v_pages;
+  out->k_scales = pages->k_scales;
+  out->v_scales = pages->v_scales;
+  out->table = pages->block_table;
+  out->table_stride = pages->table_stride;
+  out->num_pages = pages->num_pages;
+  out->max_pages = pages->max_pages;
+  out->page_shift = shift;
+  out->nkv = ctx->cfg.num_kv_heads;
+  return check_device(ctx);
+}
+
+// kv heads a warp of the paged copies takes of one token: one while there are
+// fewer than 32 warps per SM for them, else up to four, which share the
+// token's table lookups.
+int heads_per_item(const cpattn_ctx* ctx, long long tokens) {
+  const long long rows = tokens * ctx->cfg.num_kv_heads;
+  const long long h = rows / (static_cast<long long>(std::max(ctx->num_sms, 1)) * 32);
+  return static_cast<int>(std::max(1LL, std::min<long long>({h, 4, ctx->cfg.num_kv_heads})));
+}
+
+int copy_grid(const cpattn_ctx* ctx, long long tokens, int hpi) {
+  const long long items = tokens * ((ctx->cfg.num_kv_heads + hpi - 1) / hpi);
+  return static_cast<int>(std::max(1LL, std::min<long long>((items + 7) / 8,
+                                                            static_cast<long long>(ctx->num_sms) * 8)));
+}
+
+}  // namespace
+
+extern "C" {
+
+cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                                    int32_t num_rows, const int32_t* cache_lens,
+                                    const int32_t* row_starts, const void* k_new,
+                                    const void* v_new, void* stream) try {
+  if (ctx == nullptr) return CPATTN_E_INVALID;
+  cpattn::PagedWriteParams p;
+  cpattn_status s = check_pages(ctx, pages, num_seqs, &p.pool);
+  if (s != CPATTN_OK) return s;
+  if (num_rows < 0) return fail(ctx, CPATTN_E_INVALID, "num_rows must be >= 0");
+  if (row_starts == nullptr && num_rows != num_seqs)
+    return fail(ctx, CPATTN_E_INVALID, "without row_starts, num_rows must equal num_seqs");
+  if (num_rows == 0) return CPATTN_OK;
+  if (cache_lens == nullptr || k_new == nullptr || v_new == nullptr)
+    return fail(ctx, CPATTN_E_INVALID, "device pointers must not be NULL");
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned4(cache_lens) || !aligned4(row_starts))
+    return fail(ctx, CPATTN_E_INVALID, "k_new, v_new 16-byte, integer arrays 4-byte aligned");
+  if (ctx->d_status == nullptr) return fail(ctx, CPATTN_E_CUDA, "no CUDA device");
+  p.k_new = static_cast<const uint4*>(k_new);
+  p.v_new = static_cast<const uint4*>(v_new);
+  p.cache_lens = cache_lens;
+  p.row_starts = row_starts;
+  p.status = ctx->d_status;
+  p.num_seqs = num_seqs;
+  p.rows = num_rows;
+  p.heads_per_item = heads_per_item(ctx, num_rows);
+  const int grid = copy_grid(ctx, num_rows, p.heads_per_item);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool q8 = pages->format == CPATTN_PAGES_E4M3;
+  if (ctx->cfg.head_dim == 128)
+    q8 ? cpattn::paged_write_kernel<128, true><<<grid, 256, 0, st>>>(p)
+       : cpattn::paged_write_kernel<128, false><<<grid, 256, 0, st>>>(p);
+  else
+    q8 ? cpattn::paged_write_kernel<256, true><<<grid, 256, 0, st>>>(p)
+       : cpattn::paged_write_kernel<256, false><<<grid, 256, 0, st>>>(p);
+  return after_launch(ctx, st, "paged write launch");
+} catch (...) {
+  return CPATTN_E_NOMEM;
+}
+
+cpattn_status cpattn_paged_read_kv(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                                   const int32_t* first, const int32_t* lens, void* k_cache,
+                                   void* v_cache, void* stream) try {
+  if (ctx == nullptr) return CPATTN_E_INVALID;
+  cpattn::PagedReadParams p;
+  cpattn_status s = check_pages(ctx, pages, num_seqs, &p.pool);
+  if (s != CPATTN_OK) return s;
+  if (lens == nullptr || k_cache == nullptr || v_cache == nullptr)
+    return fail(ctx, CPATTN_E_INVALID, "device pointers must not be NULL");
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(lens) || !aligned4(first))
+    return fail(ctx, CPATTN_E_INVALID, "caches 16-byte, integer arrays 4-byte aligned");
+  const cpattn_config& c = ctx->cfg;
+  const long long tokens = static_cast<long long>(num_seqs) * c.num_shards * c.shard_capacity;
+  if (tokens * c.num_kv_heads >= (1LL << 31))
+    return fail(ctx, CPATTN_E_UNSUPPORTED, "cache row count exceeds 2^31");
+  if (ctx->d_status == nullptr) return fail(ctx, CPATTN_E_CUDA, "no CUDA device");
+  p.first = first;
+  p.lens = lens;
+  p.k_cache = static_cast<uint4*>(k_cache);
+  p.v_cache = static_cast<uint4*>(v_cache);
+  p.status = ctx->d_status;
+  p.num_seqs = num_seqs;
+  p.P = c.num_shards;
+  p.S = c.shard_capacity;
+  p.v_f16 = c.v_cache_f16;
+  // The most tokens the lengths can ask for (they are known on the device only).
+  const long long most = std::min<long long>(
+      tokens, static_cast<long long>(num_seqs) * pages->max_pages * pages->page_size);
+  p.heads_per_item = heads_per_item(ctx, most);
+  const int grid = copy_grid(ctx, most, p.heads_per_item);
+  const size_t smem = (static_cast<size_t>(num_seqs) + 1) * sizeof(int);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool q8 = pages->format == CPATTN_PAGES_E4M3;
+  if (c.head_dim == 128)
+    q8 ? cpattn::paged_read_kernel<128, true><<<grid, 256, smem, st>>>(p)
+       : cpattn::paged_read_kernel<128, false><<<grid, 256, smem, st>>>(p);
+  else
+    q8 ? cpattn::paged_read_kernel<256, true><<<grid, 256, smem, st>>>(p)
+       : cpattn::paged_read_kernel<256, false><<<grid, 256, smem, st>>>(p);
+  return after_launch(ctx, st, "paged read launch");
+} catch (...) {
+  return CPATTN_E_NOMEM;
+}
+
+cpattn_status cpattn_paged_decode_workspace(const cpattn_ctx* ctx, int32_t num_seqs,
+                                            uint64_t* bytes) {
+  if (ctx == nullptr || bytes == nullptr || num_seqs < 1) return CPATTN_E_INVALID;
+  if (num_seqs > CPATTN_MAX_PAGED_SEQS) return CPATTN_E_UNSUPPORTED;
+  *bytes = 256;
+  return CPATTN_OK;
+}
+
+cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                                  const int32_t* lens, const void* q, void* out, float* lse,
+                                  void* workspace, uint64_t workspace_bytes, void* stream) try {
+  if (ctx == nullptr) return CPATTN_E_INVALID;
+  cpattn::PagedDecodeParams p;
+  cpattn_status s = check_pages(ctx, pages, num_seqs, &p.pool);
+  if (s != CPATTN_OK) return s;
+  if (lens == nullptr || q == nullptr || out == nullptr || workspace == nullptr)
+    return fail(ctx, CPATTN_E_INVALID, "device pointers must not be NULL");
+  if (!aligned16(q) || !aligned16(out) || !aligned4(lens) || !aligned4(lse) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(ctx, CPATTN_E_INVALID,
+                "q, out 16-byte, lens, lse 4-byte, workspace 256-byte aligned");
+  uint64_t need = 0;
+  s = cpattn_paged_decode_workspace(ctx, num_seqs, &need);
+  if (s != CPATTN_OK) return s;
+  if (workspace_bytes < need)
+    return fail(ctx, CPATTN_E_INVALID, "workspace too small (cpattn_paged_decode_workspace)");
+  if (ctx->d_status == nullptr) return fail(ctx, CPATTN_E_CUDA, "no CUDA device");
+  const cpattn_config& c = ctx->cfg;
+  p.lens = lens;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.status = ctx->d_status;
+  p.num_seqs = num_seqs;
+  p.nq = c.num_q_heads;
+  p.group = c.num_q_heads / c.num_kv_heads;
+  p.scale_log2 = c.softmax_scale * 1.4426950408889634f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int grid = static_cast<int>((static_cast<long long>(num_seqs) * p.nq + 3) / 4);
+  const bool q8 = pages->format == CPATTN_PAGES_E4M3;
+  if (c.head_dim == 128)
+    q8 ? cpattn::paged_decode_kernel<128, true><<<grid, 128, 0, st>>>(p)
+       : cpattn::paged_decode_kernel<128, false><<<grid, 128, 0, st>>>(p);
+  else
+    q8 ? cpattn::paged_decode_kernel<256, true><<<grid, 128, 0, st>>>(p)
+       : cpattn::paged_decode_kernel<256, false><<<grid, 128, 0, st>>>(p);
+  return after_launch(ctx, st, "paged decode launch");
+} catch (...) {
+  return CPATTN_E_NOMEM;
+}
+
+}  // extern "C"

@@ -44,8 +44,12 @@
 
 namespace cpattn {
 
+// row0: the sequence's first row in Q, K_new and the output (b * C in the
+// padded token order, the sum of the earlier lengths in the packed one);
+// vrow0: its first row in the V that the current tiles read (the same, or its
+// 128-row aligned place in a packed staging).
 struct SeqInfo {
-  int cache_len, chunk_len, n_cache_tiles, pad;
+  int cache_len, chunk_len, n_cache_tiles, row0, vrow0;
 };
 
 struct PrefillParams {
@@ -197,7 +201,7 @@ static_assert(sizeof(PrefillParams) <= 32764, "kernel parameter budget");
 struct Unit {
   // h: the q head (packed: the group's first q head); qb: the row block (packed:
   // the token block); q0: its first token.
-  int b, h, g, qb, q0, L, c, n_cache;
+  int b, h, g, qb, q0, L, c, n_cache, row0, vrow0;
   int v0, n_tiles;  // this work block's tiles: virtual indices [v0, v0 + n_tiles)
   int part;         // -1, or the first partial row of a split-KV piece
 };
@@ -216,6 +220,8 @@ __device__ __forceinline__ Unit decode_unit(const PrefillParams& p, int u) {
   U.L = p.seqs[U.b].cache_len;
   U.c = p.seqs[U.b].chunk_len;
   U.n_cache = p.seqs[U.b].n_cache_tiles;
+  U.row0 = p.seqs[U.b].row0;
+  U.vrow0 = p.seqs[U.b].vrow0;
   const uint32_t rg = p.range[blk];
   U.v0 = static_cast<int>(rg >> 16);
   U.n_tiles = static_cast<int>(rg & 0xFFFFu) - U.v0;
@@ -314,7 +320,7 @@ __device__ __forceinline__ void producer_role(const PrefillParams& p, uint32_t s
     mbar_arrive_expect_tx(bar(Ly::B_QFULL), Ly::Q_BYTES);
     for (int c = 0; c < Ly::KCH; ++c)
       tma_load_3d(sbase + Ly::OFF_Q + c * (kBQ * 128), p.packed ? &p.tm_q_packed : &p.tm_q,
-                  bar(Ly::B_QFULL), 64 * c, U.h, U.b * p.C + U.q0);
+                  bar(Ly::B_QFULL), 64 * c, U.h, U.row0 + U.q0);
     ++q_issued;
 
     const int head_row = ((U.b * p.nkv + U.g) * p.P) * p.S;
@@ -328,7 +334,7 @@ __device__ __forceinline__ void producer_role(const PrefillParams& p, uint32_t s
       const int tile = in_cache ? wk.next() : 0;
       const CUtensorMap* m = in_cache ? &p.tm_k_cache : &p.tm_k_new;
       const int y = in_cache ? 0 : U.g;
-      const int z = in_cache ? head_row + tile * kBKV : U.b * p.C + (v - U.n_cache) * kBKV;
+      const int z = in_cache ? head_row + tile * kBKV : U.row0 + (v - U.n_cache) * kBKV;
       for (int c = 0; c < Ly::KCH; ++c)
         if (!load_sub(true, m, y, z, 64 * c)) return false;
       return true;
@@ -338,7 +344,7 @@ __device__ __forceinline__ void producer_role(const PrefillParams& p, uint32_t s
       const int tile = in_cache ? wv.next() : 0;
       const CUtensorMap* m = in_cache ? &p.tm_v_cache : &p.tm_v_new;
       const int y = in_cache ? 0 : U.g;
-      const int z = in_cache ? head_row + tile * kBKV : U.b * p.C + (v - U.n_cache) * kBKV;
+      const int z = in_cache ? head_row + tile * kBKV : U.vrow0 + (v - U.n_cache) * kBKV;
       for (int j = 0; j < Ly::VSUB; ++j)
         if (!load_sub(false, m, y, z + j * Ly::VROWS, 0)) return false;
       return true;
@@ -385,7 +391,7 @@ __device__ __forceinline__ void kv_write_units(const PrefillParams& p, int lane,
     for (int i = lane; i < rows * VECS; i += 32) {
       const int r = i / VECS, x = i - r * VECS;
       const int t = U.L + U.q0 + r;
-      const long long src = ((static_cast<long long>(U.b) * p.C + U.q0 + r) * p.nkv + U.g) * HD;
+      const long long src = ((static_cast<long long>(U.row0) + U.q0 + r) * p.nkv + U.g) * HD;
       const long long dst = (head_row + static_cast<long long>(t % p.P) * p.S + t / p.P) * HD;
       const uint4 kv = reinterpret_cast<const uint4*>(p.k_new + src)[x];
       uint4 vv = reinterpret_cast<const uint4*>(p.v_new + src)[x];
@@ -590,7 +596,7 @@ __device__ __forceinline__ void store_row(const PrefillParams& p, const Unit& U,
   const bool valid = row < U.c;
   const float inv_l = 1.f / l_row;
   const bool partial = U.part >= 0;
-  const long long tok_g = static_cast<long long>(U.b) * p.C + row;  // token-order row
+  const long long tok_g = static_cast<long long>(U.row0) + row;  // token-order row
   const long long orow_i =
       (partial ? static_cast<long long>(U.part + (row - U.q0)) : tok_g) * p.nq + head;
   const bool f32 = partial || p.out_f32 != 0;
@@ -637,7 +643,7 @@ __device__ __forceinline__ void store_row_merged(const PrefillParams& p, const U
   const float inv_l = 1.f / l_row;
   const float a0 = w0 * inv_l, a1 = w1 * inv_l;
   const bool partial = U.part >= 0;
-  const long long tok_g = static_cast<long long>(U.b) * p.C + row;
+  const long long tok_g = static_cast<long long>(U.row0) + row;
   const long long orow_i =
       (partial ? static_cast<long long>(U.part + (row - U.q0)) : tok_g) * p.nq + head;
   const bool f32 = partial || p.out_f32 != 0;

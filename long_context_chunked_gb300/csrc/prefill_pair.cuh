@@ -94,7 +94,7 @@ __device__ __forceinline__ void producer_role_pair2(const PrefillParams& p, uint
     mbar_arrive_expect_tx_remote(qfull, Ly::Q_BYTES);
     for (int c = 0; c < Ly::KCH; ++c)
       tma_load_3d_pair(sbase + Ly::OFF_Q + c * (kBQ * 128), &p.tm_q, qfull, 64 * c, U.h,
-                       U.b * p.C + U.q0);
+                       U.row0 + U.q0);
     ++q_issued;
 
     const int head_row = ((U.b * p.nkv + U.g) * p.P) * p.S;
@@ -107,7 +107,7 @@ __device__ __forceinline__ void producer_role_pair2(const PrefillParams& p, uint
       const int tile = in_cache ? wk.next() : 0;
       const CUtensorMap* m = in_cache ? &p.tm_k_cache_h : &p.tm_k_new_h;
       const int y = in_cache ? 0 : U.g;
-      const int z = (in_cache ? head_row + tile * kBKV : U.b * p.C + (v - U.n_cache) * kBKV) +
+      const int z = (in_cache ? head_row + tile * kBKV : U.row0 + (v - U.n_cache) * kBKV) +
                     static_cast<int>(rank) * (kBKV / 2);
       for (int j = 0; j < Pl::KSLOTS; ++j) {
         const bool r = load_slot([&](uint32_t dst, uint32_t full) {
@@ -123,7 +123,7 @@ __device__ __forceinline__ void producer_role_pair2(const PrefillParams& p, uint
       const int tile = in_cache ? wv.next() : 0;
       const CUtensorMap* m = in_cache ? &p.tm_v_cache_h : &p.tm_v_new_h;
       const int y = in_cache ? 0 : U.g;
-      const int z = in_cache ? head_row + tile * kBKV : U.b * p.C + (v - U.n_cache) * kBKV;
+      const int z = in_cache ? head_row + tile * kBKV : U.vrow0 + (v - U.n_cache) * kBKV;
       const int x0 = static_cast<int>(rank) * Pl::NH;
       for (int j = 0; j < Pl::VSLOTS; ++j) {
         const bool r = load_slot([&](uint32_t dst, uint32_t full) {

@@ -117,7 +117,7 @@ __device__ __forceinline__ void producer_role_pingpong(const PrefillParams& p, u
     for (int t = 0; t < 2; ++t)
       for (int c = 0; c < Ly::KCH; ++c)
         tma_load_3d(sbase + Ly::OFF_Q + t * Ly::Q_BYTES + c * (kBQ * 128), &p.tm_q,
-                    bar(Ly::B_QFULL), 64 * c, U.h + t, U.b * p.C + U.q0);
+                    bar(Ly::B_QFULL), 64 * c, U.h + t, U.row0 + U.q0);
     ++q_issued;
 
     const int head_row = ((U.b * p.nkv + U.g) * p.P) * p.S;
@@ -132,8 +132,8 @@ __device__ __forceinline__ void producer_role_pingpong(const PrefillParams& p, u
     for (int v = U.v0; ok && v < U.v0 + U.n_tiles; ++v) {
       const bool in_cache = v < U.n_cache;
       const int y = in_cache ? 0 : U.g;
-      const int zk = in_cache ? head_row + wk.next() * kBKV : U.b * p.C + (v - U.n_cache) * kBKV;
-      const int zv = in_cache ? head_row + wv.next() * kBKV : U.b * p.C + (v - U.n_cache) * kBKV;
+      const int zk = in_cache ? head_row + wk.next() * kBKV : U.row0 + (v - U.n_cache) * kBKV;
+      const int zv = in_cache ? head_row + wv.next() * kBKV : U.vrow0 + (v - U.n_cache) * kBKV;
       // K: one 64-column box of 128 rows per slot; V: VROWS rows of all
       // columns per slot, one box per 64 columns.
       for (int c = 0; ok && c < Ly::KCH; ++c)

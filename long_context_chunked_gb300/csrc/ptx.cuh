@@ -79,7 +79,8 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_remote(uint32_t bar_cluste
 }
 
 // Device status word codes (written by the first role that gives up).
-enum : int { kStatusOk = 0, kStatusTimeout = 1, kStatusLayout = 2, kStatusRange = 3 };
+enum : int { kStatusOk = 0, kStatusTimeout = 1, kStatusLayout = 2, kStatusRange = 3,
+           kStatusPage = 4 };
 
 // ------------------------------------------------------ barrier-count build
 // Built with -DCPATTN_COUNT_BARRIERS, the prefill kernels count every

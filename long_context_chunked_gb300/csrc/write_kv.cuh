@@ -107,4 +107,50 @@ __global__ void __launch_bounds__(256) stage_v_f16_kernel(const __grid_constant_
   }
 }
 
+// The V of packed prompts, staged for the prefill kernel: sequence b's rows
+// [row0, row0 + len) of `v` go to rows staged0.. of the staging, where every
+// sequence starts on a 128-row tile boundary, and the rest of its last tile
+// is zeros.  Packed, that tile's last columns would be the next sequence's
+// rows, and a NaN or infinity there would reach this sequence as 0 * NaN in
+// the masked columns of P.V; a staged tile holds one sequence only.  f16:
+// converted to fp16 as stage_v_f16_kernel converts (one P.V product of fp16
+// P per tile), else copied.  HBM-bound: one 16-byte vector per thread.
+struct StagePackedParams {
+  const uint4* v;
+  uint4* staged;
+  int* status;
+  int num_seqs, f16, vec_per_token;
+  long long total_vecs;  // staged rows * vec_per_token
+  int row0[CPATTN_MAX_SEQS], staged0[CPATTN_MAX_SEQS], len[CPATTN_MAX_SEQS];
+};
+
+__global__ void __launch_bounds__(256)
+    stage_v_packed_kernel(const __grid_constant__ StagePackedParams p) {
+  griddep_launch_dependents();  // as stage_v_f16_kernel
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+       idx < p.total_vecs; idx += stride) {
+    const int row = static_cast<int>(idx / p.vec_per_token);
+    const int vec = static_cast<int>(idx - static_cast<long long>(row) * p.vec_per_token);
+    // The last sequence that starts at or before this row (empty ones share
+    // their start with the one behind them).
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.staged0[mid] <= row) lo = mid; else hi = mid - 1;
+    }
+    const int i = row - p.staged0[lo];
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (i < p.len[lo]) {
+      x = __ldg(p.v + (static_cast<long long>(p.row0[lo]) + i) * p.vec_per_token + vec);
+      if (p.f16) {
+        bool overflow = false;
+        x = bf16x8_to_f16x8(x, &overflow);
+        if (overflow && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusRange);
+      }
+    }
+    p.staged[idx] = x;
+  }
+}
+
 }  // namespace cpattn

@@ -19,7 +19,11 @@ from .striped import (bf16_bits, bf16_to_f16_bits, bits_to_f64, build_striped_ca
                       f16_bits_to_f64, read_logical, shard_fill, shard_of_token, write_kv_ref)
 from .attention import (attend_ref, attend_region_ref, attend_rows_ref, attention_probs_ref,
                         brute_force_ref, kv_head_of, lse_merge)
+from .paged import (e4m3_values, paged_decode_ref, paged_rows, paged_write_ref, quantise_rows,
+                    to_e4m3)
 
 __all__ = ["bf16_bits", "bf16_to_f16_bits", "f16_bits_to_f64", "bits_to_f64", "build_striped_cache", "read_logical", "shard_fill",
            "shard_of_token", "write_kv_ref", "attend_ref", "attend_rows_ref",
-           "attend_region_ref", "attention_probs_ref", "brute_force_ref", "kv_head_of", "lse_merge"]
+           "attend_region_ref", "attention_probs_ref", "brute_force_ref", "kv_head_of", "lse_merge",
+           "e4m3_values", "to_e4m3", "quantise_rows", "paged_write_ref", "paged_rows",
+           "paged_decode_ref"]
