@@ -21,6 +21,7 @@
 #include "walk.cuh"
 #include "write_kv.cuh"
 #include "paged.cuh"
+#include "paged_decode.cuh"
 #include "merge.cuh"
 #include "plan.h"
 
@@ -55,6 +56,7 @@ struct cpattn_ctx {
   // GQA packing for short-chunk launches (cpattn_config.gqa_packing, or the
   // CPATTN_GQA_PACKING override).
   bool gqa_packing = true;
+  int decode_ctas[2][2] = {};   // [HD == 256][e4m3]: CTAs of a decode launch; 0 until set up
   std::vector<int> block_lens;  // scratch of the unit-order choice
   // Unit order (test override CPATTN_UNIT_ORDER): 0 chosen by the cost
   // model, 1 longest first, 2 kv-head-major.
@@ -100,17 +102,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 3-D bf16 tensor map with 128-byte swizzle: dims (d0 innermost), byte
-// strides of dims 1 and 2, box (b0, b1, b2).
+// 3-D tensor map with 128-byte swizzle: dims (d0 innermost), byte strides of
+// dims 1 and 2, box (b0, b1, b2); bf16 elements unless said otherwise.
 bool encode3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-              uint64_t st1, uint64_t st2, uint32_t b0, uint32_t b1, uint32_t b2) {
+              uint64_t st1, uint64_t st2, uint32_t b0, uint32_t b1, uint32_t b2,
+              CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {d0, d1, d2};
   const cuuint64_t strides[2] = {st1, st2};
   const cuuint32_t box[3] = {b0, b1, b2};
   const cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+  return fn(m, type, 3, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

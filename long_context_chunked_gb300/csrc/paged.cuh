@@ -1,6 +1,6 @@
 // The paged KV cache: writing new tokens into pages (as bf16, or quantised to
-// e4m3), reading pages back into the striped cache of the chunked prefill,
-// and the attention of one new token per sequence over the pages.
+// e4m3) and reading pages back into the striped cache of the chunked prefill.
+// The attention over the pages is in paged_decode.cuh.
 //
 // A page holds page_size consecutive tokens of one sequence for every kv
 // head: pages[page][kv head][slot][HD], so the rows of one (page, kv head)
@@ -286,81 +286,6 @@ __global__ void __launch_bounds__(256)
       }
     }
   }
-}
-
-// ----------------------------------------------------------------- decode
-struct PagedDecodeParams {
-  PagedPool pool;
-  const int* lens;            // [num_seqs]; <= 0: no tokens
-  const __nv_bfloat16* q;     // [num_seqs][NQ][HD]
-  __nv_bfloat16* out;         // [num_seqs][NQ][HD]
-  float* lse;                 // [num_seqs][NQ] or null
-  int* status;
-  int num_seqs, nq, group;
-  float scale_log2;
-};
-
-// One warp per (sequence, q head), one token at a time:
-//   x_t = scale <q, k_t>,  m = max x_t,  l = sum 2^(x_t - m),
-//   O = sum 2^(x_t - m) v_t / l,  LSE = (m + log2 l) ln 2   (log2 units),
-// with m, l and O carried along and rescaled when m grows.
-template <int HD, bool Q8>
-__global__ void __launch_bounds__(128)
-    paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
-  constexpr int E = HD / 32;  // dims 32 j + lane of this lane
-  const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (w >= static_cast<long long>(p.num_seqs) * p.nq) return;
-  const int b = static_cast<int>(w / p.nq), h = static_cast<int>(w % p.nq), g = h / p.group;
-  const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
-  int n = p.lens[b];
-  if (n > room) {
-    n = static_cast<int>(room);
-    if (p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusPage);
-  }
-  float q[E], o[E];
-#pragma unroll
-  for (int j = 0; j < E; ++j) {
-    q[j] = __bfloat162float(p.q[w * HD + 32 * j + lane]) * p.scale_log2;
-    o[j] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  auto value = [&](const void* pool, long long row, int j) {
-    const long long e = row * HD + 32 * j + lane;
-    if constexpr (Q8) {
-      const uint32_t h2 = e4m3x2_to_f16x2(reinterpret_cast<const uint8_t*>(pool)[e]);
-      return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xFFFFu)));
-    } else {
-      return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(pool)[e]);
-    }
-  };
-  const int ps = 1 << p.pool.page_shift;
-  for (int t0 = 0; t0 < n; t0 += ps) {
-    const int page = page_id(p.pool, b, t0 >> p.pool.page_shift, p.status);
-    if (page < 0) continue;
-    const int m1 = min(ps, n - t0);
-    for (int slot = 0; slot < m1; ++slot) {
-      const long long row = pool_row(p.pool, page, g, slot);
-      float x = 0.f;
-#pragma unroll
-      for (int j = 0; j < E; ++j) x = fmaf(q[j], value(p.pool.k, row, j), x);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-      if (Q8) x *= p.pool.k_scales[row];
-      const float mn = fmaxf(m, x);
-      const float a = ex2_approx(m - mn), e = ex2_approx(x - mn);
-      const float ev = Q8 ? e * p.pool.v_scales[row] : e;
-      l = l * a + e;
-#pragma unroll
-      for (int j = 0; j < E; ++j) o[j] = fmaf(ev, value(p.pool.v, row, j), o[j] * a);
-      m = mn;
-    }
-  }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-  for (int j = 0; j < E; ++j) p.out[w * HD + 32 * j + lane] = __float2bfloat16(o[j] * inv);
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[w] = l > 0.f || l != l ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace cpattn

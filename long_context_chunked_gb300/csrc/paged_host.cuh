@@ -59,6 +59,77 @@ int copy_grid(const cpattn_ctx* ctx, long long tokens, int hpi) {
                                                             static_cast<long long>(ctx->num_sms) * 8)));
 }
 
+// Most CTAs of a decode launch: two per SM.
+int decode_max_ctas(const cpattn_ctx* ctx) { return 2 * (ctx->num_sms > 0 ? ctx->num_sms : 152); }
+
+// Workspace of a decode: O, then (m, l) of every CTA's first and last row,
+// then the CTAs' descriptions of the rows they began.  It depends on neither
+// the lengths nor the number of sequences.
+struct DecodeWorkspace {
+  uint64_t ml, desc, total;  // byte offsets
+};
+DecodeWorkspace decode_workspace(const cpattn_ctx* ctx) {
+  const uint64_t ctas = static_cast<uint64_t>(decode_max_ctas(ctx));
+  const uint64_t rows = 2 * ctas * cpattn::kDecRows;
+  DecodeWorkspace w;
+  w.ml = cpattn::align256(rows * ctx->cfg.head_dim * sizeof(float));
+  w.desc = w.ml + cpattn::align256(rows * sizeof(float2));
+  w.total = w.desc + cpattn::align256(ctas * sizeof(int4));
+  return w;
+}
+
+template <int HD, bool Q8>
+cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
+                            cpattn::PagedDecodeParams* p, cudaStream_t st) {
+  using Ly = cpattn::DecodeLayout<HD, Q8>;
+  int& ctas = ctx->decode_ctas[HD == 256][Q8];
+  if (ctas == 0) {
+    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Ly::SMEM_BYTES);
+    int per_sm = 0;
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+          &per_sm, cpattn::paged_decode_kernel<HD, Q8>, cpattn::kDecThreads, Ly::SMEM_BYTES);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "paged decode set-up");
+    if (per_sm < 1) return fail(ctx, CPATTN_E_CUDA, "the paged decode kernel does not fit an SM");
+    ctas = std::min({per_sm * ctx->num_sms, decode_max_ctas(ctx), cpattn::kJoinMaxPieces});
+  }
+  const uint64_t rb = static_cast<uint64_t>(HD) * Ly::ESZ;
+  const uint32_t box_rows = static_cast<uint32_t>(std::min(pages->page_size, Ly::TT));
+  const CUtensorMapDataType type =
+      Q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t rows = static_cast<uint64_t>(p->pool_rows);
+  if (!encode3d(&p->tm_k, pages->k_pages, HD, 1, rows, rb, rb, Ly::BOXW, 1, box_rows, type) ||
+      !encode3d(&p->tm_v, pages->v_pages, HD, 1, rows, rb, rb, Ly::BOXW, 1, box_rows, type))
+    return fail(ctx, CPATTN_E_CUDA, "cuTensorMapEncodeTiled failed");
+  // The lengths are known on the device only: the grid is sized for the most
+  // tiles they can ask for, and a CTA without a tile leaves at once.
+  const long long rows_all = static_cast<long long>(p->num_seqs) * p->pool.nkv * p->hblocks;
+  const long long tiles =
+      (static_cast<long long>(pages->max_pages) * pages->page_size + Ly::TT - 1) / Ly::TT;
+  p->num_ctas = static_cast<int>(std::min<long long>(ctas, rows_all * std::min(tiles, 1024LL)));
+  cpattn::paged_decode_kernel<HD, Q8><<<p->num_ctas, cpattn::kDecThreads, Ly::SMEM_BYTES, st>>>(*p);
+  cpattn_status s = after_launch(ctx, st, "paged decode launch");
+  if (s != CPATTN_OK || tiles == 1) return s;  // rows of one tile are never cut
+  // Blocks: one per row that may have been cut, times heads where those are few.
+  const int cut = static_cast<int>(std::min<long long>(rows_all, p->num_ctas));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cut),
+                     static_cast<unsigned>(std::min({std::max(1, 2 * ctx->num_sms / cut), p->group,
+                                                     cpattn::kDecRows})));
+  cfg.blockDim = dim3(cpattn::kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, cpattn::paged_join_kernel<HD>, *p);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "paged join launch");
+  return after_launch(ctx, st, "paged join launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -150,7 +221,7 @@ cpattn_status cpattn_paged_decode_workspace(const cpattn_ctx* ctx, int32_t num_s
                                             uint64_t* bytes) {
   if (ctx == nullptr || bytes == nullptr || num_seqs < 1) return CPATTN_E_INVALID;
   if (num_seqs > CPATTN_MAX_PAGED_SEQS) return CPATTN_E_UNSUPPORTED;
-  *bytes = 256;
+  *bytes = decode_workspace(ctx).total;
   return CPATTN_OK;
 }
 
@@ -167,32 +238,35 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(ctx, CPATTN_E_INVALID,
                 "q, out 16-byte, lens, lse 4-byte, workspace 256-byte aligned");
-  uint64_t need = 0;
-  s = cpattn_paged_decode_workspace(ctx, num_seqs, &need);
-  if (s != CPATTN_OK) return s;
-  if (workspace_bytes < need)
+  const DecodeWorkspace w = decode_workspace(ctx);
+  if (workspace_bytes < w.total)
     return fail(ctx, CPATTN_E_INVALID, "workspace too small (cpattn_paged_decode_workspace)");
   if (ctx->d_status == nullptr) return fail(ctx, CPATTN_E_CUDA, "no CUDA device");
   const cpattn_config& c = ctx->cfg;
+  char* ws = static_cast<char*>(workspace);
   p.lens = lens;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
+  p.ws_o = reinterpret_cast<float*>(ws);
+  p.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.ws_desc = reinterpret_cast<int4*>(ws + w.desc);
   p.status = ctx->d_status;
+  p.timeout_ns = ctx->timeout_ns;
+  p.debug_flags = ctx->debug_flags;
+  p.pool_rows = pages->num_pages * pages->page_size * c.num_kv_heads;
   p.num_seqs = num_seqs;
   p.nq = c.num_q_heads;
   p.group = c.num_q_heads / c.num_kv_heads;
+  p.hblocks = (p.group + cpattn::kDecRows - 1) / cpattn::kDecRows;
   p.scale_log2 = c.softmax_scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = static_cast<int>((static_cast<long long>(num_seqs) * p.nq + 3) / 4);
   const bool q8 = pages->format == CPATTN_PAGES_E4M3;
   if (c.head_dim == 128)
-    q8 ? cpattn::paged_decode_kernel<128, true><<<grid, 128, 0, st>>>(p)
-       : cpattn::paged_decode_kernel<128, false><<<grid, 128, 0, st>>>(p);
-  else
-    q8 ? cpattn::paged_decode_kernel<256, true><<<grid, 128, 0, st>>>(p)
-       : cpattn::paged_decode_kernel<256, false><<<grid, 128, 0, st>>>(p);
-  return after_launch(ctx, st, "paged decode launch");
+    return q8 ? launch_decode<128, true>(ctx, pages, &p, st)
+              : launch_decode<128, false>(ctx, pages, &p, st);
+  return q8 ? launch_decode<256, true>(ctx, pages, &p, st)
+            : launch_decode<256, false>(ctx, pages, &p, st);
 } catch (...) {
   return CPATTN_E_NOMEM;
 }

@@ -455,3 +455,25 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(ValueError):
         ctx.paged_read_kv(c.kv, lens, k, k)
     _ok(ctx)
+
+
+@FORMATS
+@pytest.mark.parametrize("hd", [128, 256])
+def test_decode_wait_that_expires_is_reported(hd, e4m3):
+    """A slot release skipped in the first CTA: its producer's wait runs into
+    its limit, the kernel ends, the status says so, and the next call is right.
+    (The first CTA must reuse its slots: two kv heads of 150000 tokens are
+    2344 tiles of 128 or more, over 304 CTAs at least 7 each of two slots; the
+    largest ring has 6.)"""
+    lens = [150000, 5]
+    c = Paged(2, hd, 64, lens, e4m3, seed=15)
+    c.fill(np.random.default_rng(15), lens)
+    c.upload()
+    ctx = cp.Context(8, 2, hd, 1, 1, 1)
+    q = torch.zeros(2, 8, hd, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(ctx.paged_decode_workspace(2), dtype=torch.uint8, device="cuda")
+    ctx.set_fault_injection(1, 50)
+    ctx.paged_decode(c.kv, i32(lens), q, torch.zeros_like(q), ws)
+    assert ctx.sync_status() == cp.E_TIMEOUT
+    ctx.set_fault_injection(0)
+    _decode(c, 8, lens, ctx=ctx)
