@@ -56,7 +56,7 @@ struct cpattn_ctx {
   // GQA packing for short-chunk launches (cpattn_config.gqa_packing, or the
   // CPATTN_GQA_PACKING override).
   bool gqa_packing = true;
-  int decode_ctas[2][2] = {};   // [HD == 256][e4m3]: CTAs of a decode launch; 0 until set up
+  bool decode_ready[2][2] = {};  // [HD == 256][e4m3]: the decode kernel has been set up
   std::vector<int> block_lens;  // scratch of the unit-order choice
   // Unit order (test override CPATTN_UNIT_ORDER): 0 chosen by the cost
   // model, 1 longest first, 2 kv-head-major.

@@ -1,6 +1,6 @@
 // Decode attention over the paged KV cache: one new token per sequence,
 //   O[b, h] = sum_t p_t v_t / l,  p_t = 2^(x_t - m),  x_t = scale log2(e) <q, k_t>,
-//   m = max_t x_t,  l = sum_t p_t,  LSE = (m + log2 l) ln 2
+//   m >= max_t x_t - 8,  l = sum_t p_t,  LSE = (m + log2 l) ln 2
 // over the cached tokens of kv head g = h / G.
 //
 // HBM-bound: every cached row is read once and used for the G q heads of its
@@ -11,7 +11,7 @@
 // its rows empty and would need e4m3 converted to fp16 through shared memory
 // first, while here the conversion sits in registers between ldmatrix and mma.
 //
-// Work split.  The cache is cut into tiles of TT tokens of one row = (sequence,
+// Work split.  The cache is cut into tiles of WT tokens of one row = (sequence,
 // kv head, block of up to 16 q heads).  All tiles of all rows form one list
 // (sequence-major, then kv head), and each CTA takes an equal, contiguous
 // slice of it, whatever the lengths are: one long sequence and many ragged
@@ -21,20 +21,28 @@
 // pieces in order, so results do not depend on timing:
 //   m = max m_i,  O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
 //
-// Roles (288 threads, two CTAs per SM): warps 0-7 compute, warp 8 issues TMA
-// copies into a ring of slots (K and V tiles alternate).  Per tile, warp w
-// computes S for TT/8 of the tokens and all heads, the warps agree on the row
-// maxima (one named barrier), write P to shared memory (a second one), and
-// warp w multiplies P with HD/8 of V's columns.
+// Within a CTA (one per SM, 8 warps) warp w takes the tiles w, w + 8, ... of a
+// row, alone: it issues its own TMA copies into its own ring of slots (K and V
+// tiles alternate, the next copy goes out as soon as a slot is read), holds
+// its own m, l and O (all HD columns), and turns the accumulators of Q K^T
+// into the operand of P V in registers.  No barrier, no shared P; the warps
+// meet once per row, where their O are summed in warp order.  (Splitting a
+// tile over the warps instead, tokens for Q K^T and columns for P V, took two
+// barriers and a shared P per tile and twice the instructions: e4m3 87 us
+// where this takes the time below.)
 //
 // e4m3 (Q8): K and V are converted to fp16 (exact) in registers.  Q is fp16,
 // scaled by a power of two per head so that its largest element is in
 // [1, 2): elements below 2^-14 of it lose bits, at most 2^-25 of the largest.
 // A K row's scale multiplies its logit.  A V row's scale multiplies its
-// probability; to stay in fp16's range, P is stored as
-// p_t (s_t / s_ref) 2^14, s_ref the largest scale so far and at least 2^-100
-// (O is rescaled when it grows, as for m), rounded once to fp16's 11 bits.
+// probability; to stay in fp16's range, P is stored as p_t (s_t / s_ref) 2^7,
+// rounded once to fp16's 11 bits, with s_ref at least every scale so far and
+// at least 2^-100.
 // bf16: P is carried as a bf16 hi + lo pair (16 bits) against bf16 V.
+//
+// m and s_ref are references, not exact maxima: they are raised (and O and l
+// rescaled) only when a logit exceeds m by 8 or a scale exceeds s_ref, which
+// after a row's first tile hardly happens; p then stays below 2^8.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -46,45 +54,48 @@
 
 namespace cpattn {
 
-constexpr int kDecWarps = 8;                     // compute warps
-constexpr int kDecThreads = 32 * (kDecWarps + 1);
+constexpr int kDecWarps = 8;
+constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecRows = 16;                     // q heads of a row (mma M)
-constexpr uint32_t kDecBarrier = 1;              // named barrier of the compute warps
-constexpr float kPScale = 16384.f;               // Q8: P is stored times 2^14
+constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7
 constexpr float kMinSref = 7.888609052210118e-31f;  // 2^-100: kPScale / s_ref stays finite
+constexpr float kRaise = 8.f;                    // m is raised when a logit exceeds it by this
+constexpr int kDecStages = 8;                    // tiles whose pages a warp remembers (power of two)
+constexpr int kMaxBoxes = 4;                     // page pieces of a tile
 
 template <int HD, bool Q8>
 struct DecodeLayout {
   static constexpr int ESZ = Q8 ? 1 : 2;
-  static constexpr int TT = Q8 ? 128 : 64;       // tokens per tile
+  static constexpr int SLOT = 8192;
+  static constexpr int NSLOT = 3;                // per warp; 192 KB per CTA
+  static constexpr int WT = SLOT / (HD * ESZ);   // tokens per tile: 16 .. 64
+  static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : 6);
   static constexpr int BOXW = 128 / ESZ;         // values per 128-byte box row
   static constexpr int NBOX = HD / BOXW;         // column blocks of a tile
-  static constexpr int SLOT = TT * HD * ESZ;
-  static constexpr int NSLOT = 96 * 1024 / SLOT; // 96 KB of copies in flight per CTA
-  static constexpr int WTOK = TT / kDecWarps;    // tokens per warp in Q K^T
-  static constexpr int NT = WTOK / 8;            // their n-tiles
-  static constexpr int DW = HD / kDecWarps;      // V columns per warp
-  static constexpr int P_STRIDE = TT + 8;        // 16-bit values; rows 16 bytes apart mod 128
-  static constexpr int Q_STRIDE = HD + 8;
-  static constexpr int P_BYTES = kDecRows * P_STRIDE * 2;
-  static constexpr int OFF_SCALE = NSLOT * SLOT;
-  static constexpr int OFF_P = OFF_SCALE + (Q8 ? NSLOT * TT * 4 : 0);
-  static constexpr int OFF_Q = OFF_P + P_BYTES * (Q8 ? 1 : 2);
-  static constexpr int OFF_MAX = OFF_Q + kDecRows * Q_STRIDE * 2;  // [16][8] row maxima by warp
-  static constexpr int OFF_SUM = OFF_MAX + kDecRows * kDecWarps * 4;
-  static constexpr int OFF_SMAX = OFF_SUM + kDecRows * kDecWarps * 4;  // [8] largest V scale by warp
-  static constexpr int OFF_QEXP = OFF_SMAX + kDecWarps * 4;            // [16] 2^e of each Q row
+  static constexpr int NT = WT / 8;              // n-tiles of Q K^T
+  static constexpr int NO = HD / 8;              // n-tiles of P V
+  static constexpr int Q_STRIDE = HD + 8;        // 16-bit values; rows 16 bytes apart mod 128
+  static constexpr int CD = 32;                  // columns summed over the warps at a time
+  static constexpr int C_STRIDE = CD + 8;
+  static constexpr int OFF_SCALE = kDecWarps * NSLOT * SLOT;
+  static constexpr int OFF_Q = OFF_SCALE + (Q8 ? kDecWarps * NSLOT * WT * 4 : 0);
+  static constexpr int OFF_SUM = OFF_Q + kDecRows * Q_STRIDE * 2;  // [8][16][C_STRIDE]
+  static constexpr int OFF_ML = OFF_SUM + kDecWarps * kDecRows * C_STRIDE * 4;  // [8][16] (m, l)
+  static constexpr int OFF_QEXP = OFF_ML + kDecWarps * kDecRows * 8;  // [16] 2^e of each Q row
   static constexpr int OFF_BAR = OFF_QEXP + kDecRows * 4;
-  static constexpr int OFF_BAD = OFF_BAR + 2 * NSLOT * 8;  // [NSLOT] pages of the tile that are absent
-  static constexpr int OFF_MISC = OFF_BAD + NSLOT * 4;     // start of the slice, abort flag
-  static constexpr int SMEM_BYTES = OFF_MISC + 64;
-  static_assert(OFF_BAR % 8 == 0 && OFF_SCALE % 128 == 0 && OFF_P % 16 == 0 && OFF_Q % 16 == 0,
+  // [8][kDecStages] pool rows of the tile's boxes, and the mask of absent pages
+  static constexpr int OFF_ROWS = OFF_BAR + kDecWarps * NSLOT * 8;
+  static constexpr int OFF_BAD = OFF_ROWS + kDecWarps * kDecStages * kMaxBoxes * 4;
+  static constexpr int OFF_MISC = OFF_BAD + kDecWarps * kDecStages * 4;
+  static constexpr int SMEM_BYTES = OFF_MISC + 192;
+  static_assert(OFF_BAR % 8 == 0 && OFF_SCALE % 128 == 0 && OFF_Q % 16 == 0 && OFF_SUM % 16 == 0,
                 "shared memory alignment");
-  static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(WT / 16 <= kMaxBoxes && NSLOT / 2 + 2 <= kDecStages, "page table of a warp");
 };
 
 struct PagedDecodeParams {
-  CUtensorMap tm_k;  // [pool rows][HD], box BOXW x 1 x min(page_size, TT)
+  CUtensorMap tm_k;  // [pool rows][HD], box BOXW x 1 x min(page_size, WT)
   CUtensorMap tm_v;
   PagedPool pool;
   const int* lens;            // [num_seqs]; <= 0: no tokens
@@ -103,7 +114,7 @@ struct PagedDecodeParams {
   float scale_log2;
 };
 
-enum : int { kSiteDecFull = 9, kSiteDecEmpty = 10 };  // after the prefill's sites
+enum : int { kSiteDecFull = 9 };  // after the prefill's sites
 
 // ------------------------------------------------------------------ mma.sync
 template <bool F16>
@@ -143,6 +154,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Four e4m3 values as two fp16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t* lo, uint32_t* hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(*lo), "=r"(*hi)
+      : "r"(x));
+}
+
 // Shared address of 16-byte chunk `chunk` of row `row` in the column block at
 // `base` (rows of 128 bytes, as a 128-byte-swizzled TMA box stores them).
 __device__ __forceinline__ uint32_t sw128(uint32_t base, int row, int chunk) {
@@ -150,32 +171,58 @@ __device__ __forceinline__ uint32_t sw128(uint32_t base, int row, int chunk) {
 }
 
 // ------------------------------------------------------------- the slices
-// Tile list position: sequence b, row rr = kv head * hblocks + head block, tile.
-struct DecodeSpot {
-  int b, rr, tile;
-};
-
 // Tokens of sequence b, cut to what its table row can name.
 __device__ __forceinline__ int decode_len(const PagedDecodeParams& p, int b) {
   const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
   return static_cast<int>(max(0LL, min(static_cast<long long>(__ldg(p.lens + b)), room)));
 }
 
-// Whole block (kDecThreads threads): tiles over all rows, and this CTA's slice
-// [s0, s1) of them; *spot receives the position of s0 (valid if s0 < s1).
-// `active` CTAs share the list, one tile each at least.
-template <int TT>
+// A CTA's way through its slice [s, s1) of the tile list, one row segment at a
+// time: tiles tile0 .. tile0 + tiles - 1 of row rr = kv head * hblocks + head
+// block of sequence b.  tiles == 0: the slice is done.
+struct DecodeWalk {
+  long long s, s1;
+  int b, rr, tile0, tiles, nt, n;
+
+  template <int WT>
+  __device__ __forceinline__ void enter(const PagedDecodeParams& p) {
+    n = decode_len(p, b);
+    nt = (n + WT - 1) / WT;
+    tiles = static_cast<int>(min(static_cast<long long>(nt - tile0), s1 - s));
+  }
+  template <int WT>
+  __device__ __forceinline__ void next(const PagedDecodeParams& p, int rows_per_seq) {
+    s += tiles;
+    if (s >= s1) {
+      tiles = 0;
+      return;
+    }
+    tile0 = 0;
+    if (++rr == rows_per_seq) {
+      rr = 0;
+      do {
+        n = decode_len(p, ++b);
+      } while (n == 0);
+      nt = (n + WT - 1) / WT;
+    }
+    tiles = static_cast<int>(min(static_cast<long long>(nt), s1 - s));
+  }
+};
+
+// Whole block: tiles over all rows, and this CTA's slice of them, in *spot
+// (shared memory; spot->s >= spot->s1: none).  `active` CTAs share the list,
+// at least one tile per warp each where there are that many.
+template <int WT>
 __device__ __forceinline__ long long decode_slice(const PagedDecodeParams& p, int rows_per_seq,
-                                                  long long* s0, long long* s1, int* active,
-                                                  DecodeSpot* spot) {
-  __shared__ long long warp_sum[kDecWarps + 1];
+                                                  long long* warp_sum, int* active,
+                                                  DecodeWalk* spot) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.num_seqs + kDecThreads - 1) / kDecThreads;
   const int b0 = min(p.num_seqs, tid * per), b1 = min(p.num_seqs, b0 + per);
   const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
   long long sum = 0;
   for (int b = b0; b < b1; ++b) {
-    sum += (decode_len(p, b) + TT - 1) / TT;
+    sum += (decode_len(p, b) + WT - 1) / WT;
     if (p.lens[b] > room && blockIdx.x == 0 && p.status != nullptr)
       atomicCAS(p.status, kStatusOk, kStatusPage);
   }
@@ -188,25 +235,30 @@ __device__ __forceinline__ long long decode_slice(const PagedDecodeParams& p, in
   if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
   long long base = 0, total = 0;
-  for (int w = 0; w <= kDecWarps; ++w) {
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
     if (w < warp) base += warp_sum[w];
     total += warp_sum[w];
   }
   total *= rows_per_seq;
-  *active = static_cast<int>(min(total, static_cast<long long>(gridDim.x)));
+  *active = static_cast<int>(
+      min((total + kDecWarps - 1) / kDecWarps, static_cast<long long>(gridDim.x)));
   const int c = blockIdx.x;
-  *s0 = c < *active ? total * c / *active : 0;
-  *s1 = c < *active ? total * (c + 1) / *active : 0;
+  const long long s0 = c < *active ? total * c / *active : 0;
+  const long long s1 = c < *active ? total * (c + 1) / *active : 0;
+  if (tid == 0) {
+    spot->s = s0;
+    spot->s1 = s1;
+  }
   long long at = (base + inc - sum) * rows_per_seq;  // list index of sequence b0's first tile
-  if (*s0 < *s1 && at <= *s0 && *s0 < at + sum * rows_per_seq) {
+  if (s0 < s1 && at <= s0 && s0 < at + sum * rows_per_seq) {
     for (int b = b0; b < b1; ++b) {
-      const int nt = (decode_len(p, b) + TT - 1) / TT;
+      const int nt = (decode_len(p, b) + WT - 1) / WT;
       const long long n = static_cast<long long>(nt) * rows_per_seq;
-      if (*s0 < at + n) {
-        const long long off = *s0 - at;
+      if (s0 < at + n) {
         spot->b = b;
-        spot->rr = static_cast<int>(off / nt);
-        spot->tile = static_cast<int>(off % nt);
+        spot->rr = static_cast<int>((s0 - at) / nt);
+        spot->tile0 = static_cast<int>((s0 - at) % nt);
         break;
       }
       at += n;
@@ -217,11 +269,14 @@ __device__ __forceinline__ long long decode_slice(const PagedDecodeParams& p, in
 }
 
 // ------------------------------------------------------------------ kernel
-template <int HD, bool Q8>
-__global__ void __launch_bounds__(kDecThreads, 2)
+// HALF: at most 8 q heads per kv head, so accumulator rows 8 .. 15 are unused
+// and their softmax is left out.
+template <int HD, bool Q8, bool HALF>
+__global__ void __launch_bounds__(kDecThreads, 1)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   using Ly = DecodeLayout<HD, Q8>;
-  constexpr int TT = Ly::TT, NT = Ly::NT, DW = Ly::DW, NSLOT = Ly::NSLOT;
+  constexpr int WT = Ly::WT, NT = Ly::NT, NO = Ly::NO, NSLOT = Ly::NSLOT;
+  constexpr int RI = HALF ? 1 : 2;  // accumulator row halves in use
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -232,24 +287,119 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     if (tid == 0) p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  auto full = [&](int s) { return sbase + Ly::OFF_BAR + 8u * static_cast<uint32_t>(s); };
-  auto empty = [&](int s) { return sbase + Ly::OFF_BAR + 8u * static_cast<uint32_t>(NSLOT + s); };
-  volatile uint32_t* bad_pages = reinterpret_cast<volatile uint32_t*>(smem + Ly::OFF_BAD);
-  DecodeSpot* spot = reinterpret_cast<DecodeSpot*>(smem + Ly::OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::OFF_MISC + 32);
-  if (tid == 0) {
-    for (int s = 0; s < NSLOT; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), kDecWarps);
-    }
-    *abort_flag = 0;
+  const uint32_t ring = sbase + warp * (NSLOT * Ly::SLOT);
+  auto full = [&](int s) {
+    return sbase + Ly::OFF_BAR + 8u * static_cast<uint32_t>(warp * NSLOT + s);
+  };
+  DecodeWalk* spot = reinterpret_cast<DecodeWalk*>(smem + Ly::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::OFF_MISC + 64);
+  if (lane == 0) {
+    for (int s = 0; s < NSLOT; ++s) mbar_init(full(s), 1);
+    if (warp == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   const int rows_per_seq = p.pool.nkv * p.hblocks;
-  long long s0, s1;
   int active;
-  const long long total = decode_slice<TT>(p, rows_per_seq, &s0, &s1, &active, spot);
+  const long long total =
+      decode_slice<WT>(p, rows_per_seq, reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 128),
+                       &active, spot);
   const BoundedWait wait{abort_flag, p.status, p.timeout_ns, nullptr, 0u, 0};
+
+  DecodeWalk at = *spot;
+  if (at.s < at.s1) at.template enter<WT>(p);
+
+  // ------------------------------------------- this warp's stream of copies
+  // Copy u of the warp is K (u even) or V (u odd) of its tile u / 2, in slot
+  // u % NSLOT.  Where K of a tile goes out, its pages are known (looked up
+  // one tile ahead) and kept for V.
+  const int ps = 1 << p.pool.page_shift;
+  const int box = min(ps, WT), box_shift = min(p.pool.page_shift, Ly::WT_SHIFT);
+  const int boxes = WT >> box_shift;
+  volatile int* my_rows =
+      reinterpret_cast<volatile int*>(smem + Ly::OFF_ROWS) + warp * (kDecStages * kMaxBoxes);
+  volatile uint32_t* my_bad =
+      reinterpret_cast<volatile uint32_t*>(smem + Ly::OFF_BAD) + warp * kDecStages;
+  DecodeWalk ahead = at;  // the tile whose K goes out next
+  int aj = warp;          // its index in ahead's segment
+  int issued = 0, slot_out = 0;
+  int next_row = 0;       // lane i < boxes: pool row of its box i
+  bool next_bad = false, more = at.s < at.s1;
+  auto settle = [&]() {   // to the segment that holds tile aj, or to the end
+    while (more && aj >= ahead.tiles) {
+      ahead.template next<WT>(p, rows_per_seq);
+      aj = warp;
+      more = ahead.tiles > 0;
+    }
+  };
+  auto look_up = [&]() {
+    // Where box i starts, or p.pool_rows (out of range: TMA fills zeros) when
+    // it lies behind the last token or its page is absent.
+    next_bad = false;
+    next_row = p.pool_rows;
+    const long long t = static_cast<long long>(ahead.tile0 + aj) * WT + (lane << box_shift);
+    if (more && lane < boxes && t < ahead.n) {
+      const int id = page_id(p.pool, ahead.b, static_cast<int>(t >> p.pool.page_shift), p.status);
+      next_bad = id < 0;
+      if (id >= 0)
+        next_row = static_cast<int>(
+            pool_row(p.pool, id, ahead.rr / p.hblocks, static_cast<int>(t) & (ps - 1)));
+    }
+  };
+  auto send = [&](const CUtensorMap* m, const float* scales, int row) {
+    const uint32_t bar = full(slot_out), dst = ring + slot_out * Ly::SLOT;
+    const uint32_t here = __ballot_sync(0xFFFFFFFFu, lane < boxes && row < p.pool_rows);
+    if (lane == 0)
+      mbar_arrive_expect_tx(bar, Ly::SLOT + (Q8 ? __popc(here) * (box * 4) : 0));
+    __syncwarp();
+    if (lane < boxes) {
+#pragma unroll
+      for (int c = 0; c < Ly::NBOX; ++c)
+        tma_load_3d(dst + c * (WT * 128) + (lane << box_shift) * 128, m, bar, c * Ly::BOXW, 0, row);
+      if (Q8 && row < p.pool_rows)
+        bulk_load(sbase + Ly::OFF_SCALE + (warp * NSLOT + slot_out) * (WT * 4) +
+                      (lane << box_shift) * 4,
+                  scales + row, box * 4, bar);
+    }
+    if (++slot_out == NSLOT) slot_out = 0;
+    ++issued;
+  };
+  // The next copy, if there is one: called NSLOT times at first, then once for
+  // every slot read.
+  auto issue = [&]() {
+    const int stage = (issued >> 1) & (kDecStages - 1);
+    if (issued & 1) {
+      const int row = lane < boxes ? my_rows[stage * kMaxBoxes + lane] : p.pool_rows;
+      send(&p.tm_v, p.pool.v_scales, row);
+    } else if (more) {
+      const int row = next_row;
+      const uint32_t bad = __ballot_sync(0xFFFFFFFFu, next_bad);
+      if (lane < boxes) my_rows[stage * kMaxBoxes + lane] = row;
+      if (lane == 0) my_bad[stage] = bad;
+      __syncwarp();
+      send(&p.tm_k, p.pool.k_scales, row);
+      aj += kDecWarps;
+      settle();
+      look_up();
+    }
+  };
+  settle();
+  look_up();
+  const bool drop = (p.debug_flags & kDebugDropArrive) && blockIdx.x == 0 && warp == 0;
+  if (drop && more) {  // fault injection: the first copy is never sent
+    slot_out = 1;
+    issued = 1;
+    if (lane < boxes) my_rows[lane] = next_row;
+    if (lane == 0) my_bad[0] = 0u;
+    __syncwarp();
+    aj += kDecWarps;
+    settle();
+    look_up();
+  }
+  while (issued < NSLOT) {
+    const int before = issued;
+    issue();
+    if (issued == before) break;
+  }
 
   // Sequences without tokens: zeros, and an LSE of -infinity.
   for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
@@ -260,139 +410,45 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       for (int h = tid; h < p.nq; h += kDecThreads)
         p.lse[static_cast<long long>(b) * p.nq + h] = -INFINITY;
   }
-  if (s0 >= s1) {
+  if (at.s >= at.s1) {
     if (tid == 0) p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  DecodeSpot at = *spot;
-  int n = decode_len(p, at.b);
-  int nt = (n + TT - 1) / TT;
 
-  if (warp == kDecWarps) {
-    // ---------------------------------------------------------- TMA producer
-    const int ps = 1 << p.pool.page_shift;
-    const int chunk = min(ps, TT);            // tokens per box
-    const int chunk_shift = min(p.pool.page_shift, TT == 64 ? 6 : 7);
-    const int chunks = TT >> chunk_shift;     // boxes (of each column block) per tile
-    if (lane == 0) {
-      prefetch_tmap(&p.tm_k);
-      prefetch_tmap(&p.tm_v);
-    }
-    int slot = 0, round = 0;
-    uint32_t phase = 0;
-    long long issued = 0;
-    // Lane i holds the pool row of the tile's i-th box: where it starts, or
-    // p.pool_rows (out of range: TMA fills zeros) when it lies behind the last
-    // token or its page is absent (bad).
-    auto rows_of = [&](const DecodeSpot& s, int len, bool* bad) {
-      *bad = false;
-      const long long t = static_cast<long long>(s.tile) * TT + (lane << chunk_shift);
-      if (lane >= chunks || t >= len) return p.pool_rows;
-      const int id = page_id(p.pool, s.b, static_cast<int>(t >> p.pool.page_shift), p.status);
-      if (id < 0) {
-        *bad = true;
-        return p.pool_rows;
-      }
-      return static_cast<int>(pool_row(p.pool, id, s.rr / p.hblocks, static_cast<int>(t) & (ps - 1)));
-    };
-    auto load = [&](const CUtensorMap* m, const float* scales, int row, uint32_t bad) {
-      bool ok = true;
-      if (round > 0) ok = wait(empty(slot), phase ^ 1u, kSiteDecEmpty);
-      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-      const uint32_t here = __ballot_sync(0xFFFFFFFFu, lane < chunks && row < p.pool_rows);
-      const uint32_t dst = sbase + slot * Ly::SLOT;
-      if (lane == 0) {
-        bad_pages[slot] = bad;
-        mbar_arrive_expect_tx(full(slot),
-                              Ly::SLOT + (Q8 ? __popc(here) * (chunk * 4) : 0));
-      }
-      __syncwarp();
-      if (lane < chunks) {
-#pragma unroll
-        for (int c = 0; c < Ly::NBOX; ++c)
-          tma_load_3d(dst + c * (TT * 128) + (lane << chunk_shift) * 128, m, full(slot),
-                      c * Ly::BOXW, 0, row);
-        if (Q8 && row < p.pool_rows)
-          bulk_load(sbase + Ly::OFF_SCALE + slot * (TT * 4) + (lane << chunk_shift) * 4,
-                    scales + row, chunk * 4, full(slot));
-      }
-      if (++slot == NSLOT) {
-        slot = 0;
-        phase ^= 1u;
-        round = 1;
-      }
-      ++issued;
-      return true;
-    };
-    bool ok = true;
-    bool bad;
-    int row = rows_of(at, n, &bad);
-    for (long long s = s0; ok && s < s1; ++s) {
-      // The next tile's pages are looked up before this tile's slots are waited for.
-      const int cur = row;
-      const uint32_t badm = __ballot_sync(0xFFFFFFFFu, bad);
-      if (s + 1 < s1) {
-        if (++at.tile == nt) {
-          at.tile = 0;
-          if (++at.rr == rows_per_seq) {
-            at.rr = 0;
-            do {
-              n = decode_len(p, ++at.b);
-            } while (n == 0);
-            nt = (n + TT - 1) / TT;
-          }
-        }
-        row = rows_of(at, n, &bad);
-      }
-      ok = load(&p.tm_k, p.pool.k_scales, cur, badm) && load(&p.tm_v, p.pool.v_scales, cur, badm);
-    }
-    if (!ok && lane == 0) {
-      // Let copies already issued land before this CTA can exit.
-      const long long first = issued > NSLOT ? issued - NSLOT : 0;
-      for (long long z = first; z < issued; ++z)
-        mbar_wait_drain(full(static_cast<int>(z % NSLOT)), static_cast<uint32_t>((z / NSLOT) & 1),
-                        200ull * 1000 * 1000);
-    }
-    return;
-  }
-
-  // ------------------------------------------------------------ compute warps
-  // A warp whose wait expired (ok = false) waits for no more copies: its loops
-  // run to their end on stale data, every warp still meets every barrier, and
-  // the status word tells the host.
-  bool ok = true;
-  bool drop_one = (p.debug_flags & kDebugDropArrive) && blockIdx.x == 0 && tid == 0;
   const int quad = lane & 3, r0 = lane >> 2;      // accumulator rows r0 and r0 + 8
-  float* maxs = reinterpret_cast<float*>(smem + Ly::OFF_MAX);
-  float* sums = reinterpret_cast<float*>(smem + Ly::OFF_SUM);
-  float* smaxs = reinterpret_cast<float*>(smem + Ly::OFF_SMAX);
+  float2* mls = reinterpret_cast<float2*>(smem + Ly::OFF_ML);
   float* qexp = reinterpret_cast<float*>(smem + Ly::OFF_QEXP);
   uint16_t* qs = reinterpret_cast<uint16_t*>(smem + Ly::OFF_Q);
-  uint32_t* ps32 = reinterpret_cast<uint32_t*>(smem + Ly::OFF_P);
-  const uint32_t p_sm = sbase + Ly::OFF_P, q_sm = sbase + Ly::OFF_Q;
-  const int chunk_shift = min(p.pool.page_shift, TT == 64 ? 6 : 7);
-  const int dim0 = warp * DW;                     // this warp's V columns
-  constexpr int NO = DW / 8;                      // their n-tiles
-  int slot = 0;
+  float* summed = reinterpret_cast<float*>(smem + Ly::OFF_SUM);
+  const uint32_t q_sm = sbase + Ly::OFF_Q;
+  int slot = 0, used = 0;  // the next slot to read, and copies read so far
   uint32_t phase = 0;
-  auto next_slot = [&]() {
+  // A warp whose wait expired (ok = false) waits for no more copies: it runs
+  // to its end on stale data, still meets every barrier, and the status word
+  // tells the host.
+  bool ok = true;
+  auto await = [&]() {
+    if (ok) ok = __all_sync(0xFFFFFFFFu, wait(full(slot), phase, kSiteDecFull));
+    __syncwarp();
+  };
+  auto release = [&]() {  // the slot has been read by every lane
+    __syncwarp();
     if (++slot == NSLOT) {
       slot = 0;
       phase ^= 1u;
     }
+    ++used;
+    if (ok) issue();
   };
 
-  long long s = s0;
-  while (s < s1) {
+  for (; at.tiles > 0; at.template next<WT>(p, rows_per_seq)) {
     const int g = at.rr / p.hblocks, h0 = g * p.group + (at.rr % p.hblocks) * kDecRows;
     const int heads = min(kDecRows, (g + 1) * p.group - h0);
-    const int tile0 = at.tile;
-    const int tiles = static_cast<int>(min(static_cast<long long>(nt - tile0), s1 - s));
 
     // Q of the row into shared memory: warp w stages rows 2w and 2w + 1; bf16
     // as it is, or (Q8) fp16 scaled by a power of two, with the dims of each
     // 16-block in the order in which the e4m3 K fragments come out of ldmatrix.
-    bar_sync(kDecBarrier, 32 * kDecWarps);  // the last row's Q and sums are no longer read
+    __syncthreads();  // the last row's Q and sums are no longer read
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = 2 * warp + j;
@@ -406,11 +462,14 @@ __global__ void __launch_bounds__(kDecThreads, 2)
       }
       if constexpr (Q8) {
         big = __reduce_max_sync(0xFFFFFFFFu, big);
-        // 2^-e as a float, e the exponent of the row's largest value (a row of
-        // zeros or subnormals: 2^126, where the product stays finite).
+        // e: the exponent of the row's largest value (zeros and subnormals:
+        // -126), down = 2^-e, and qexp = 2^e gives it back to the logits.
+        // 2^-127, 2^-128 and 2^128 are made in two steps.
         const int e = max(static_cast<int>(big >> 7), 1) - 127;
-        const float down = e > 126 ? exp2f(-127.f) * (e == 128 ? 0.5f : 1.f) : exp2f(static_cast<float>(-e));
-        if (lane == 0) qexp[r] = e > 126 ? exp2f(127.f) * (e == 128 ? 2.f : 1.f) : exp2f(static_cast<float>(e));
+        const int e1 = min(e, 126), e2 = e - e1;
+        const float down = __int_as_float((127 - e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 0.5f : 0.25f));
+        if (lane == 0)
+          qexp[r] = __int_as_float((127 + e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 2.f : 4.f));
 #pragma unroll
         for (int i = 0; i < HD / 64; ++i) {
           const int d = 2 * (32 * i + lane);     // dims d, d + 1 (d even)
@@ -426,331 +485,340 @@ __global__ void __launch_bounds__(kDecThreads, 2)
           *reinterpret_cast<uint32_t*>(qs + r * Ly::Q_STRIDE + 2 * (32 * i + lane)) = w[i];
       }
     }
-    bar_sync(kDecBarrier, 32 * kDecWarps);
-    float sl[2] = {p.scale_log2, p.scale_log2};
-    if (Q8) {
-      sl[0] *= qexp[r0];
-      sl[1] *= qexp[r0 + 8];
-    }
+    __syncthreads();
+    float sl[RI];
+#pragma unroll
+    for (int i = 0; i < RI; ++i) sl[i] = Q8 ? p.scale_log2 * qexp[r0 + 8 * i] : p.scale_log2;
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float sref = kMinSref;  // Q8: the largest V scale so far
+    float m[RI], l[RI];
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+    float sref = kMinSref, pscale = kPScale / kMinSref;
     float o[NO][4];
 #pragma unroll
     for (int i = 0; i < NO; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 
-    for (int v = 0; v < tiles; ++v) {
-      const int valid = min(TT, n - (tile0 + v) * TT);  // tokens of the tile
+    for (int v = warp; v < at.tiles; v += kDecWarps) {
+      const int valid = min(WT, at.n - (at.tile0 + v) * WT);  // tokens of the tile
+      const uint32_t bad = my_bad[(used >> 1) & (kDecStages - 1)];
+      const bool partial = valid < WT || bad != 0u;
 
-      // ---- S = Q K^T for this warp's tokens
-      const int kslot = slot;
-      if (ok) ok = wait(full(kslot), phase, kSiteDecFull);
-      __syncwarp();
-      const uint32_t kb = sbase + kslot * Ly::SLOT;
-      const uint32_t bad = bad_pages[kslot];
-      float c[NT][4], c2[NT][4];
+      // ---- S = Q K^T
+      await();
+      const uint32_t kb = ring + slot * Ly::SLOT;
+      const float* ksc = reinterpret_cast<const float*>(
+          smem + Ly::OFF_SCALE + (warp * NSLOT + slot) * (WT * 4));
+      float c[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[t][j] = c2[t][j] = 0.f;
+        for (int j = 0; j < 4; ++j) c[t][j] = 0.f;
       if constexpr (Q8) {
 #pragma unroll
         for (int blk = 0; blk < HD / 64; ++blk) {  // 64 dims: four k16 steps
-          uint32_t kr[NT][4];
+          uint32_t a[4][4];
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            ldsm4(kr[t], sw128(kb + (blk >> 1) * (TT * 128), warp * Ly::WTOK + t * 8 + (lane & 7),
-                               (blk & 1) * 4 + (lane >> 3)));
+          for (int j = 0; j < 4; ++j)
+            ldsm4(a[j], q_sm + ((lane & 15) * Ly::Q_STRIDE + (4 * blk + j) * 16 + (lane >> 4) * 8) * 2);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t a[4];
-            ldsm4(a, q_sm + ((lane & 15) * Ly::Q_STRIDE + (4 * blk + j) * 16 + (lane >> 4) * 8) * 2);
+          for (int t = 0; t < NT; ++t) {
+            uint32_t kr[4];
+            ldsm4(kr, sw128(kb + (blk >> 1) * (WT * 128), t * 8 + (lane & 7),
+                            (blk & 1) * 4 + (lane >> 3)));
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-              mma16816<true>((j & 1) ? c2[t] : c[t], a,
-                             e4m3x2_to_f16x2(static_cast<uint16_t>(kr[t][j])),
-                             e4m3x2_to_f16x2(static_cast<uint16_t>(kr[t][j] >> 16)));
-          }
-        }
-      } else {
-#pragma unroll
-        for (int blk = 0; blk < HD / 32; ++blk) {  // 32 dims: two k16 steps
-          uint32_t kr[4];
-          ldsm4(kr, sw128(kb + (blk >> 1) * (TT * 128), warp * Ly::WTOK + (lane & 7),
-                          (blk & 1) * 4 + (lane >> 3)));
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t a[4];
-            ldsm4(a, q_sm + ((lane & 15) * Ly::Q_STRIDE + (2 * blk + j) * 16 + (lane >> 4) * 8) * 2);
-            mma16816<false>(j ? c2[0] : c[0], a, kr[2 * j], kr[2 * j + 1]);
-          }
-        }
-      }
-      // Logits in log2 units, by value: what is no token is -infinity.
-      float x[NT][4];
-      float mx[2] = {-INFINITY, -INFINITY};
-      bool seen[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int tok = warp * Ly::WTOK + t * 8 + quad * 2;
-        float ks[2] = {1.f, 1.f};
-        if (Q8) {
-          const float2 f = *reinterpret_cast<const float2*>(smem + Ly::OFF_SCALE +
-                                                            kslot * (TT * 4) + tok * 4);
-          ks[0] = f.x;
-          ks[1] = f.y;
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          seen[t][j] = tok + j < valid && !((bad >> (tok >> chunk_shift)) & 1u);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float y = (c[t][2 * i + j] + c2[t][2 * i + j]) * (sl[i] * ks[j]);
-            x[t][2 * i + j] = seen[t][j] ? y : -INFINITY;
-            mx[i] = fmaxf(mx[i], x[t][2 * i + j]);
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0 && !drop_one) mbar_arrive(empty(kslot));
-      drop_one = false;
-      next_slot();
-
-      // ---- V's scales of this warp's tokens (with the V tile)
-      const int vslot = slot;
-      float vs[NT][2];
-      float smx = 0.f;
-      if (Q8) {
-        if (ok) ok = wait(full(vslot), phase, kSiteDecFull);
-        __syncwarp();
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int tok = warp * Ly::WTOK + t * 8 + quad * 2;
-          const float2 f = *reinterpret_cast<const float2*>(smem + Ly::OFF_SCALE +
-                                                            vslot * (TT * 4) + tok * 4);
-          vs[t][0] = f.x;
-          vs[t][1] = f.y;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (seen[t][j]) smx = fmaxf(smx, fabsf(vs[t][j]));
-        }
-      }
-
-      // ---- row maxima over the tile
-#pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
-        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], d));
-        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xFFFFFFFFu, mx[1], d));
-        if (Q8) smx = fmaxf(smx, __shfl_xor_sync(0xFFFFFFFFu, smx, d));
-      }
-      if (quad == 0) {
-        maxs[r0 * kDecWarps + warp] = mx[0];
-        maxs[(r0 + 8) * kDecWarps + warp] = mx[1];
-        if (Q8 && lane == 0) smaxs[warp] = smx;
-      }
-      bar_sync(kDecBarrier, 32 * kDecWarps);
-      float alpha[2];
-      float mref[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 f0 = *reinterpret_cast<const float4*>(maxs + (r0 + 8 * i) * kDecWarps);
-        const float4 f1 = *reinterpret_cast<const float4*>(maxs + (r0 + 8 * i) * kDecWarps + 4);
-        const float mn = fmaxf(m[i], fmaxf(fmaxf(fmaxf(f0.x, f0.y), fmaxf(f0.z, f0.w)),
-                                           fmaxf(fmaxf(f1.x, f1.y), fmaxf(f1.z, f1.w))));
-        mref[i] = mn == -INFINITY ? 0.f : mn;
-        alpha[i] = ex2_approx(m[i] - mref[i]);
-        m[i] = mn;
-        l[i] *= alpha[i];
-      }
-      float pscale = 1.f;
-      if (Q8) {
-        const float4 f0 = *reinterpret_cast<const float4*>(smaxs);
-        const float4 f1 = *reinterpret_cast<const float4*>(smaxs + 4);
-        const float sn = fmaxf(sref, fmaxf(fmaxf(fmaxf(f0.x, f0.y), fmaxf(f0.z, f0.w)),
-                                           fmaxf(fmaxf(f1.x, f1.y), fmaxf(f1.z, f1.w))));
-        alpha[0] *= sref / sn;
-        alpha[1] *= sref / sn;
-        sref = sn;
-        pscale = kPScale / sn;
-      }
-
-      // ---- P: probabilities of this warp's tokens, to shared memory
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int tok = warp * Ly::WTOK + t * 8 + quad * 2;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float e0 = ex2_approx(x[t][2 * i] - mref[i]);
-          const float e1 = ex2_approx(x[t][2 * i + 1] - mref[i]);
-          l[i] += e0 + e1;
-          uint32_t* dst = ps32 + ((r0 + 8 * i) * Ly::P_STRIDE + tok) / 2;
-          if constexpr (Q8) {
-            // s_t / s_ref first: a scale may be far below s_ref, never above it.
-            *dst = pack_f16x2(seen[t][0] ? e0 * (vs[t][0] * pscale) : 0.f,
-                              seen[t][1] ? e1 * (vs[t][1] * pscale) : 0.f);
-          } else {
-            const uint32_t hi = pack_bf16x2(e0, e1);
-            *dst = hi;
-            dst[Ly::P_BYTES / 4] = pack_bf16x2(e0 - __uint_as_float(hi << 16),
-                                               e1 - __uint_as_float(hi & 0xFFFF0000u));
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NO; ++i) {
-        o[i][0] *= alpha[0];
-        o[i][1] *= alpha[0];
-        o[i][2] *= alpha[1];
-        o[i][3] *= alpha[1];
-      }
-      bar_sync(kDecBarrier, 32 * kDecWarps);
-
-      // ---- O += P V for this warp's columns
-      if (!Q8) {
-        if (ok) ok = wait(full(vslot), phase, kSiteDecFull);
-        __syncwarp();
-      }
-      const uint32_t vb = sbase + vslot * Ly::SLOT + (dim0 / Ly::BOXW) * (TT * 128);
-      const int ch0 = (dim0 % Ly::BOXW) * Ly::ESZ / 16;
-      if (valid < TT) {
-        // Slots behind the last token may hold anything; 0 * NaN must not
-        // reach O.  Each warp clears its own columns.
-        constexpr int CH = DW * Ly::ESZ / 16;
-        for (int i = lane; i < (TT - valid) * CH; i += 32)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                           sw128(vb, valid + i / CH, ch0 + i % CH)),
-                       "r"(0)
-                       : "memory");
-        __syncwarp();
-      }
-      if constexpr (Q8) {
-#pragma unroll
-        for (int kt = 0; kt < TT / 32; ++kt) {  // 32 tokens: two k16 steps
-          uint32_t a0[4], a1[4];
-          const uint32_t pa = p_sm + ((lane & 15) * Ly::P_STRIDE + kt * 32 + (lane >> 4) * 8) * 2;
-          ldsm4(a0, pa);
-          ldsm4(a1, pa + 32);
-#pragma unroll
-          for (int ch = 0; ch < DW / 16; ++ch) {
-            uint32_t vr[4];
-            ldsm4_t(vr, sw128(vb, kt * 32 + lane, ch0 + ch));
-            // Each register holds two tokens x two dims; regrouped by dim.
-#pragma unroll
-            for (int j = 0; j < 4; ++j) vr[j] = __byte_perm(vr[j], 0u, 0x3120);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {  // even dims, odd dims
-              const int sh = 16 * half;
-              mma16816<true>(o[2 * ch + half], a0, e4m3x2_to_f16x2(static_cast<uint16_t>(vr[0] >> sh)),
-                             e4m3x2_to_f16x2(static_cast<uint16_t>(vr[1] >> sh)));
-              mma16816<true>(o[2 * ch + half], a1, e4m3x2_to_f16x2(static_cast<uint16_t>(vr[2] >> sh)),
-                             e4m3x2_to_f16x2(static_cast<uint16_t>(vr[3] >> sh)));
+            for (int j = 0; j < 4; ++j) {
+              uint32_t b0, b1;
+              e4m3x4_to_f16x4(kr[j], &b0, &b1);
+              mma16816<true>(c[t], a[j], b0, b1);
             }
           }
         }
       } else {
 #pragma unroll
-        for (int kt = 0; kt < TT / 16; ++kt) {
-          uint32_t hi[4], lo[4];
-          const uint32_t pa = p_sm + ((lane & 15) * Ly::P_STRIDE + kt * 16 + (lane >> 4) * 8) * 2;
-          ldsm4(hi, pa);
-          ldsm4(lo, pa + Ly::P_BYTES);
+        for (int blk = 0; blk < HD / 32; ++blk) {  // 32 dims: two k16 steps
+          uint32_t a[2][4];
 #pragma unroll
-          for (int ch = 0; ch < NO; ch += 2) {
+          for (int j = 0; j < 2; ++j)
+            ldsm4(a[j], q_sm + ((lane & 15) * Ly::Q_STRIDE + (2 * blk + j) * 16 + (lane >> 4) * 8) * 2);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            uint32_t kr[4];
+            ldsm4(kr, sw128(kb + (blk >> 1) * (WT * 128), t * 8 + (lane & 7),
+                            (blk & 1) * 4 + (lane >> 3)));
+            mma16816<false>(c[t], a[0], kr[0], kr[1]);
+            mma16816<false>(c[t], a[1], kr[2], kr[3]);
+          }
+        }
+      }
+      // Logits in log2 units, in place; what is no token is -infinity, by value.
+      float mx[RI];
+#pragma unroll
+      for (int i = 0; i < RI; ++i) mx[i] = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float2 ks = make_float2(1.f, 1.f);
+        if (Q8) ks = *reinterpret_cast<const float2*>(ksc + t * 8 + quad * 2);
+#pragma unroll
+        for (int i = 0; i < RI; ++i) {
+          c[t][2 * i] *= sl[i] * ks.x;
+          c[t][2 * i + 1] *= sl[i] * ks.y;
+        }
+      }
+      if (partial) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int tok = t * 8 + quad * 2 + j;
+            if (tok >= valid || ((bad >> (tok >> box_shift)) & 1u)) {
+#pragma unroll
+              for (int i = 0; i < RI; ++i) c[t][2 * i + j] = -INFINITY;
+            }
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < RI; ++i) mx[i] = fmaxf(mx[i], fmaxf(c[t][2 * i], c[t][2 * i + 1]));
+      release();
+
+      // ---- references: m, and (Q8) s_ref
+      await();
+      const uint32_t vb = ring + slot * Ly::SLOT;
+      float2 vs[NT];
+      float smx = 0.f;
+      if constexpr (Q8) {
+        const float* vsc = reinterpret_cast<const float*>(
+            smem + Ly::OFF_SCALE + (warp * NSLOT + slot) * (WT * 4));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) vs[t] = *reinterpret_cast<const float2*>(vsc + t * 8 + quad * 2);
+        if (partial) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const int tok = t * 8 + quad * 2;
+            if (tok >= valid || ((bad >> (tok >> box_shift)) & 1u)) vs[t].x = 0.f;
+            if (tok + 1 >= valid || ((bad >> (tok >> box_shift)) & 1u)) vs[t].y = 0.f;
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) smx = fmaxf(smx, fmaxf(fabsf(vs[t].x), fabsf(vs[t].y)));
+      }
+      bool raise = false;
+#pragma unroll
+      for (int i = 0; i < RI; ++i) raise |= mx[i] > m[i] + kRaise;
+      if (Q8) raise |= smx > sref;
+      if (__any_sync(0xFFFFFFFFu, raise)) {
+        float alpha[2] = {1.f, 1.f};
+        if constexpr (Q8) {
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) smx = fmaxf(smx, __shfl_xor_sync(0xFFFFFFFFu, smx, d));
+          if (smx > sref) {  // (the same in every lane: the quads hold the same columns)
+            const float up = 2.f * smx;  // twice: the next scales are likely to fit
+            alpha[0] = alpha[1] = sref / up;
+            sref = up;
+            pscale = kPScale / up;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < RI; ++i) {
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], d));
+          const float mn = fmaxf(m[i], mx[i]);
+          const float a = m[i] == mn ? 1.f : ex2_approx(m[i] - mn);
+          m[i] = mn;
+          l[i] *= a;
+          alpha[i] *= a;
+        }
+        if (HALF) alpha[1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[0];
+          o[i][2] *= alpha[1];
+          o[i][3] *= alpha[1];
+        }
+      }
+
+      // ---- P, as the A operand of P V (16 tokens: n-tiles 2k and 2k + 1)
+      float mref[RI];
+#pragma unroll
+      for (int i = 0; i < RI; ++i) mref[i] = m[i] == -INFINITY ? 0.f : m[i];
+      uint32_t ph[WT / 16][4], pl[Q8 ? 1 : WT / 16][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float sx = Q8 ? vs[t].x * pscale : 1.f, sy = Q8 ? vs[t].y * pscale : 1.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int k = t >> 1, j = 2 * (t & 1) + i;
+          if (i >= RI) {
+            ph[k][j] = 0u;
+            if (!Q8) pl[Q8 ? 0 : k][j] = 0u;
+            continue;
+          }
+          const int ii = i < RI ? i : 0;
+          const float e0 = ex2_approx(c[t][2 * ii] - mref[ii]);
+          const float e1 = ex2_approx(c[t][2 * ii + 1] - mref[ii]);
+          l[ii] += e0 + e1;
+          if constexpr (Q8) {
+            ph[k][j] = pack_f16x2(e0 * sx, e1 * sy);
+          } else {
+            const uint32_t hi = pack_bf16x2(e0, e1);
+            ph[k][j] = hi;
+            pl[k][j] = pack_bf16x2(e0 - __uint_as_float(hi << 16),
+                                   e1 - __uint_as_float(hi & 0xFFFF0000u));
+          }
+        }
+      }
+
+      // ---- O += P V
+      if (valid < WT) {
+        // Slots behind the last token may hold anything; 0 * NaN must not
+        // reach O.
+        constexpr int CH = HD * Ly::ESZ / 16;
+        for (int i = lane; i < (WT - valid) * CH; i += 32) {
+          const int ch = i % CH;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                           sw128(vb + (ch >> 3) * (WT * 128), valid + i / CH, ch & 7)),
+                       "r"(0)
+                       : "memory");
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int k = 0; k < WT / 16; ++k) {
+        // ldmatrix: token half, then 16-byte chunk, by lane octet
+        const int row = k * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+        if constexpr (Q8) {
+#pragma unroll
+          for (int ch = 0; ch < HD / 16; ch += 2) {  // 32 columns
             uint32_t vr[4];
-            ldsm4_t(vr, sw128(vb, kt * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), ch0 + ch + (lane >> 4)));
-            mma16816<false>(o[ch], hi, vr[0], vr[1]);
-            mma16816<false>(o[ch + 1], hi, vr[2], vr[3]);
-            mma16816<false>(o[ch], lo, vr[0], vr[1]);
-            mma16816<false>(o[ch + 1], lo, vr[2], vr[3]);
+            ldsm4_t(vr, sw128(vb + (ch >> 3) * (WT * 128), row, (ch & 7) + (lane >> 4)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              // Each register holds two tokens x two columns; regrouped, the
+              // lower half is the even column's, the upper the odd one's.
+              uint32_t b0e, b0o, b1e, b1o;
+              e4m3x4_to_f16x4(__byte_perm(vr[2 * j], 0u, 0x3120), &b0e, &b0o);
+              e4m3x4_to_f16x4(__byte_perm(vr[2 * j + 1], 0u, 0x3120), &b1e, &b1o);
+              mma16816<true>(o[2 * (ch + j)], ph[k], b0e, b1e);
+              mma16816<true>(o[2 * (ch + j) + 1], ph[k], b0o, b1o);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ch = 0; ch < HD / 8; ch += 2) {   // 16 columns
+            uint32_t vr[4];
+            ldsm4_t(vr, sw128(vb + (ch >> 3) * (WT * 128), row, (ch & 7) + (lane >> 4)));
+            mma16816<false>(o[ch], ph[k], vr[0], vr[1]);
+            mma16816<false>(o[ch + 1], ph[k], vr[2], vr[3]);
+            mma16816<false>(o[ch], pl[k], vr[0], vr[1]);
+            mma16816<false>(o[ch + 1], pl[k], vr[2], vr[3]);
           }
         }
       }
       // Cleared slots: these writes come before the copy that reuses the slot.
-      if (valid < TT) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(vslot));
-      next_slot();
+      if (valid < WT) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      release();
     }
 
-    // ---- the row's (or piece's) end: l over all tokens, then O
+    // ---- the end of the row (or of this CTA's piece of it): the warps' m and
+    // l, then their O, 32 columns at a time, summed in warp order.
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < RI; ++i) {
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], d);
-      if (quad == 0) sums[(r0 + 8 * i) * kDecWarps + warp] = l[i];
+      if (quad == 0) mls[warp * kDecRows + r0 + 8 * i] = make_float2(m[i], l[i]);
     }
-    bar_sync(kDecBarrier, 32 * kDecWarps);
-    const bool whole = tile0 == 0 && tiles == nt;
-    const int piece = 2 * blockIdx.x + (tile0 == 0 ? 1 : 0);
-    const float oscale = Q8 ? sref * (1.f / kPScale) : 1.f;
+    __syncthreads();
+    const bool whole = at.tile0 == 0 && at.tiles == at.nt;
+    const int piece = 2 * blockIdx.x + (at.tile0 == 0 ? 1 : 0);
+    float f[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < RI; ++i) {
       const int r = r0 + 8 * i;
-      float sum = 0.f;
+      float mm = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) sum += sums[r * kDecWarps + w];
-      if (r >= heads) continue;
-      const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
-      // l = 0: every page of the row was absent.
-      const float f = whole ? (sum == 0.f ? 0.f : oscale / sum) : oscale;
-      float y[DW / 4];  // this thread's columns: Q8 runs of four, else of two
+      for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, mls[w * kDecRows + r].x);
+      const float mref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-      for (int k = 0; k < NO; ++k) {
-        y[2 * k] = o[k][2 * i] * f;
-        y[2 * k + 1] = o[k][2 * i + 1] * f;
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float2 ml = mls[w * kDecRows + r];
+        sum = fmaf(ex2_approx(ml.x - mref), ml.y, sum);
       }
+      f[i] = ex2_approx(m[i] - mref) * (Q8 ? sref * (1.f / kPScale) : 1.f);
+      // sum = 0: every page of the row was absent.
+      if (whole) f[i] = sum == 0.f ? 0.f : f[i] / sum;
+      if (warp == 0 && quad == 0 && r < heads) {
+        const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
+        if (!whole)
+          p.ws_ml[piece * kDecRows + r] = make_float2(mm, sum);
+        else if (p.lse != nullptr)
+          p.lse[orow] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.69314718055994531f;
+      }
+    }
+    constexpr int TILES = Ly::CD / 8;  // n-tiles per round
 #pragma unroll
-      for (int k = 0; k < NO; k += 2) {
-        if constexpr (Q8) {
-          // n-tiles k, k + 1: even and odd dims of a 16-column chunk
-          const int d = dim0 + 8 * k + 4 * quad;
-          const float e[4] = {y[2 * k], y[2 * k + 2], y[2 * k + 1], y[2 * k + 3]};
-          if (whole)
-            *reinterpret_cast<uint2*>(p.out + orow * HD + d) =
-                make_uint2(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]));
-          else
-            *reinterpret_cast<float4*>(p.ws_o + (static_cast<long long>(piece) * kDecRows + r) * HD + d) =
-                make_float4(e[0], e[1], e[2], e[3]);
-        } else {
+    for (int cc = 0; cc < HD / Ly::CD; ++cc) {
+      if (cc > 0) __syncthreads();
+      float* mine = summed + warp * (kDecRows * Ly::C_STRIDE);
 #pragma unroll
-          for (int kk = k; kk < k + 2; ++kk) {
-            const int d = dim0 + 8 * kk + 2 * quad;
-            if (whole)
-              *reinterpret_cast<uint32_t*>(p.out + orow * HD + d) = pack_bf16x2(y[2 * kk], y[2 * kk + 1]);
-            else
-              *reinterpret_cast<float2*>(p.ws_o + (static_cast<long long>(piece) * kDecRows + r) * HD + d) =
-                  make_float2(y[2 * kk], y[2 * kk + 1]);
+      for (int i = 0; i < RI; ++i)
+#pragma unroll
+        for (int k = 0; k < TILES; k += 2) {
+          const float* a = o[cc * TILES + k];
+          const float* b = o[cc * TILES + k + 1];
+          float* dst = mine + (r0 + 8 * i) * Ly::C_STRIDE + 8 * k;
+          if constexpr (Q8) {  // n-tiles k, k + 1: even and odd columns of 16
+            *reinterpret_cast<float4*>(dst + 4 * quad) =
+                make_float4(a[2 * i] * f[i], b[2 * i] * f[i], a[2 * i + 1] * f[i], b[2 * i + 1] * f[i]);
+          } else {
+            *reinterpret_cast<float2*>(dst + 2 * quad) = make_float2(a[2 * i] * f[i], a[2 * i + 1] * f[i]);
+            *reinterpret_cast<float2*>(dst + 8 + 2 * quad) = make_float2(b[2 * i] * f[i], b[2 * i + 1] * f[i]);
           }
         }
-      }
-      if (warp == 0 && quad == 0) {
-        if (!whole)
-          p.ws_ml[piece * kDecRows + r] = make_float2(m[i], sum);
-        else if (p.lse != nullptr)
-          p.lse[orow] = sum == 0.f ? -INFINITY : (m[i] + __log2f(sum)) * 0.69314718055994531f;
+      __syncthreads();
+      const int r = tid >> 4, d = 2 * (tid & 15);  // 16 rows x 16 column pairs
+      if (r < heads) {
+        float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+          const float2 z = *reinterpret_cast<const float2*>(
+              summed + (w * kDecRows + r) * Ly::C_STRIDE + d);
+          y.x += z.x;
+          y.y += z.y;
+        }
+        if (whole)
+          *reinterpret_cast<uint32_t*>(
+              p.out + (static_cast<long long>(at.b) * p.nq + h0 + r) * HD + cc * Ly::CD + d) =
+              pack_bf16x2(y.x, y.y);
+        else
+          *reinterpret_cast<float2*>(
+              p.ws_o + (static_cast<long long>(piece) * kDecRows + r) * HD + cc * Ly::CD + d) = y;
       }
     }
-    s += tiles;
-    if (s >= s1 && tid == 0) {
+    if (at.s + at.tiles >= at.s1 && tid == 0) {
       // The CTA whose slice begins a row that others continue describes it.
       int4 d = make_int4(0, 0, 0, 0);
-      if (tile0 == 0 && tiles < nt) {
-        const long long last = s - tiles + nt - 1;  // list index of the row's last tile
+      if (at.tile0 == 0 && at.tiles < at.nt) {
+        const long long last = at.s + at.nt - 1;  // list index of the row's last tile
         const long long cta = ((last + 1) * active - 1) / total;
         d = make_int4(at.b, at.rr, static_cast<int>(cta) - static_cast<int>(blockIdx.x) + 1, 0);
       }
       p.ws_desc[blockIdx.x] = d;
     }
-    if (s < s1) {
-      at.tile = 0;
-      if (++at.rr == rows_per_seq) {
-        at.rr = 0;
-        do {
-          n = decode_len(p, ++at.b);
-        } while (n == 0);
-        nt = (n + TT - 1) / TT;
+  }
+  if (!ok) {
+    // Let copies already sent land before this CTA can exit.
+    for (; used < issued; ++used) {
+      mbar_wait_drain(full(slot), phase, 200ull * 1000 * 1000);
+      if (++slot == NSLOT) {
+        slot = 0;
+        phase ^= 1u;
       }
     }
   }

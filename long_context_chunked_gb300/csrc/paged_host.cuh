@@ -59,8 +59,10 @@ int copy_grid(const cpattn_ctx* ctx, long long tokens, int hpi) {
                                                             static_cast<long long>(ctx->num_sms) * 8)));
 }
 
-// Most CTAs of a decode launch: two per SM.
-int decode_max_ctas(const cpattn_ctx* ctx) { return 2 * (ctx->num_sms > 0 ? ctx->num_sms : 152); }
+// CTAs of a decode launch: at most one per SM.
+int decode_max_ctas(const cpattn_ctx* ctx) {
+  return std::min(ctx->num_sms > 0 ? ctx->num_sms : 152, cpattn::kJoinMaxPieces);
+}
 
 // Workspace of a decode: O, then (m, l) of every CTA's first and last row,
 // then the CTAs' descriptions of the rows they began.  It depends on neither
@@ -78,25 +80,20 @@ DecodeWorkspace decode_workspace(const cpattn_ctx* ctx) {
   return w;
 }
 
-template <int HD, bool Q8>
+template <int HD, bool Q8, bool HALF>
 cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
                             cpattn::PagedDecodeParams* p, cudaStream_t st) {
   using Ly = cpattn::DecodeLayout<HD, Q8>;
-  int& ctas = ctx->decode_ctas[HD == 256][Q8];
-  if (ctas == 0) {
-    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8>,
+  bool& ready = ctx->decode_ready[HD == 256][Q8];
+  if (!ready) {
+    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8, HALF>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Ly::SMEM_BYTES);
-    int per_sm = 0;
-    if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-          &per_sm, cpattn::paged_decode_kernel<HD, Q8>, cpattn::kDecThreads, Ly::SMEM_BYTES);
-    if (e != cudaSuccess) return cuda_fail(ctx, e, "paged decode set-up");
-    if (per_sm < 1) return fail(ctx, CPATTN_E_CUDA, "the paged decode kernel does not fit an SM");
-    ctas = std::min({per_sm * ctx->num_sms, decode_max_ctas(ctx), cpattn::kJoinMaxPieces});
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaFuncSetAttribute(paged decode)");
+    ready = true;
   }
   const uint64_t rb = static_cast<uint64_t>(HD) * Ly::ESZ;
-  const uint32_t box_rows = static_cast<uint32_t>(std::min(pages->page_size, Ly::TT));
+  const uint32_t box_rows = static_cast<uint32_t>(std::min(pages->page_size, Ly::WT));
   const CUtensorMapDataType type =
       Q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t rows = static_cast<uint64_t>(p->pool_rows);
@@ -107,11 +104,13 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
   // tiles they can ask for, and a CTA without a tile leaves at once.
   const long long rows_all = static_cast<long long>(p->num_seqs) * p->pool.nkv * p->hblocks;
   const long long tiles =
-      (static_cast<long long>(pages->max_pages) * pages->page_size + Ly::TT - 1) / Ly::TT;
-  p->num_ctas = static_cast<int>(std::min<long long>(ctas, rows_all * std::min(tiles, 1024LL)));
-  cpattn::paged_decode_kernel<HD, Q8><<<p->num_ctas, cpattn::kDecThreads, Ly::SMEM_BYTES, st>>>(*p);
+      (static_cast<long long>(pages->max_pages) * pages->page_size + Ly::WT - 1) / Ly::WT;
+  p->num_ctas = static_cast<int>(std::min<long long>(
+      decode_max_ctas(ctx),
+      (rows_all * std::min(tiles, 1LL << 20) + cpattn::kDecWarps - 1) / cpattn::kDecWarps));
+  cpattn::paged_decode_kernel<HD, Q8, HALF><<<p->num_ctas, cpattn::kDecThreads, Ly::SMEM_BYTES, st>>>(*p);
   cpattn_status s = after_launch(ctx, st, "paged decode launch");
-  if (s != CPATTN_OK || tiles == 1) return s;  // rows of one tile are never cut
+  if (s != CPATTN_OK || tiles == 1 || p->num_ctas == 1) return s;  // no row can be cut
   // Blocks: one per row that may have been cut, times heads where those are few.
   const int cut = static_cast<int>(std::min<long long>(rows_all, p->num_ctas));
   cudaLaunchConfig_t cfg = {};
@@ -262,11 +261,19 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
   p.scale_log2 = c.softmax_scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool q8 = pages->format == CPATTN_PAGES_E4M3;
-  if (c.head_dim == 128)
-    return q8 ? launch_decode<128, true>(ctx, pages, &p, st)
-              : launch_decode<128, false>(ctx, pages, &p, st);
-  return q8 ? launch_decode<256, true>(ctx, pages, &p, st)
-            : launch_decode<256, false>(ctx, pages, &p, st);
+  const bool half = p.group <= 8;
+  if (c.head_dim == 128) {
+    if (half)
+      return q8 ? launch_decode<128, true, true>(ctx, pages, &p, st)
+                : launch_decode<128, false, true>(ctx, pages, &p, st);
+    return q8 ? launch_decode<128, true, false>(ctx, pages, &p, st)
+              : launch_decode<128, false, false>(ctx, pages, &p, st);
+  }
+  if (half)
+    return q8 ? launch_decode<256, true, true>(ctx, pages, &p, st)
+              : launch_decode<256, false, true>(ctx, pages, &p, st);
+  return q8 ? launch_decode<256, true, false>(ctx, pages, &p, st)
+            : launch_decode<256, false, false>(ctx, pages, &p, st);
 } catch (...) {
   return CPATTN_E_NOMEM;
 }
