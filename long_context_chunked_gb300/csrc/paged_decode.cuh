@@ -6,10 +6,12 @@
 // HBM-bound: every cached row is read once and used for the G q heads of its
 // kv head, 4 HD G flops per 4 HD bytes (bf16), far below what even the
 // legacy tensor path delivers per byte.  So the kernel is built around an
-// unbroken stream of TMA copies, and computes with mma.sync (M = 16 rows:
-// the q heads of one kv head, padded): tcgen05's M = 128 would leave 7/8 of
-// its rows empty and would need e4m3 converted to fp16 through shared memory
-// first, while here the conversion sits in registers between ldmatrix and mma.
+// unbroken stream of TMA copies, and computes with mma.sync, transposed:
+// S^T = K Q^T and O^T += V^T P^T put the cached rows on M = 16 and the q heads
+// on N = 8, so a group of up to 8 heads pays for 8.  tcgen05's M = 128 would
+// leave most of its rows empty, or need e4m3 V converted to fp16 through
+// shared memory, while here that conversion sits in registers between
+// ldmatrix and mma.
 //
 // Work split.  The cache is cut into tiles of WT tokens of one row = (sequence,
 // kv head, block of up to 16 q heads).  All tiles of all rows form one list
@@ -21,23 +23,24 @@
 // pieces in order, so results do not depend on timing:
 //   m = max m_i,  O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
 //
-// Within a CTA (one per SM, 8 warps) warp w takes the tiles w, w + 8, ... of a
-// row, alone: it issues its own TMA copies into its own ring of slots (K and V
+// Within a CTA (one per SM) warp w takes the tiles w, w + NW, ... of a row,
+// alone: it issues its own TMA copies into its own ring of slots (K and V
 // tiles alternate, the next copy goes out as soon as a slot is read), holds
-// its own m, l and O (all HD columns), and turns the accumulators of Q K^T
-// into the operand of P V in registers.  No barrier, no shared P; the warps
-// meet once per row, where their O are summed in warp order.  (Splitting a
-// tile over the warps instead, tokens for Q K^T and columns for P V, took two
-// barriers and a shared P per tile and twice the instructions: e4m3 87 us
-// where this takes the time below.)
+// its own m, l and O (all HD columns), and turns the accumulators of K Q^T
+// into the operand of V^T P^T in registers (movmatrix).  No barrier, no shared
+// P; the warps meet once per row, where their O are summed in warp order.
 //
-// e4m3 (Q8): K and V are converted to fp16 (exact) in registers.  Q is fp16,
-// scaled by a power of two per head so that its largest element is in
-// [1, 2): elements below 2^-14 of it lose bits, at most 2^-25 of the largest.
-// A K row's scale multiplies its logit.  A V row's scale multiplies its
-// probability; to stay in fp16's range, P is stored as p_t (s_t / s_ref) 2^7,
+// e4m3 (Q8).  K Q^T multiplies K's bytes as they are by Q in two e4m3 parts:
+// q 2^(7-e) = hi + lo / 16, e the exponent of the head's largest element.  The
+// two products have their own accumulators.  bf16's 8 significant bits fit
+// the two parts exactly; elements below 2^-13 of the largest lose bits, at
+// most 2^-21 of the largest.  (As fp16, K took one more conversion per value
+// than it takes now, and the products 3.5 times as long.)  A K row's scale
+// multiplies its logit.  V is converted to fp16 (exact) in registers, and its
+// scale multiplies the probability: P is stored as p_t (s_t / s_ref) 2^7,
 // rounded once to fp16's 11 bits, with s_ref at least every scale so far and
-// at least 2^-100.
+// at least 2^-100.  (P in e4m3 parts would need four of them to keep both the
+// bits and the range of small probabilities.)
 // bf16: P is carried as a bf16 hi + lo pair (16 bits) against bf16 V.
 //
 // m and s_ref are references, not exact maxima: they are raised (and O and l
@@ -54,41 +57,45 @@
 
 namespace cpattn {
 
-constexpr int kDecWarps = 8;
-constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDecRows = 16;                     // q heads of a row (mma M)
+constexpr int kDecRows = 16;                     // most q heads of a row
 constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7
 constexpr float kMinSref = 7.888609052210118e-31f;  // 2^-100: kPScale / s_ref stays finite
 constexpr float kRaise = 8.f;                    // m is raised when a logit exceeds it by this
 constexpr int kDecStages = 8;                    // tiles whose pages a warp remembers (power of two)
 constexpr int kMaxBoxes = 4;                     // page pieces of a tile
 
-template <int HD, bool Q8>
+// NB: blocks of 8 q heads of a row (1: groups of up to 8 heads; 2: the rest).
+template <int HD, bool Q8, int NB>
 struct DecodeLayout {
   static constexpr int ESZ = Q8 ? 1 : 2;
+  static constexpr int NW = 8;                   // warps
+  static constexpr int THREADS = 32 * NW;
   static constexpr int SLOT = 8192;
   static constexpr int NSLOT = 3;                // per warp; 192 KB per CTA
   static constexpr int WT = SLOT / (HD * ESZ);   // tokens per tile: 16 .. 64
   static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : 6);
   static constexpr int BOXW = 128 / ESZ;         // values per 128-byte box row
   static constexpr int NBOX = HD / BOXW;         // column blocks of a tile
-  static constexpr int NT = WT / 8;              // n-tiles of Q K^T
-  static constexpr int NO = HD / 8;              // n-tiles of P V
-  static constexpr int Q_STRIDE = HD + 8;        // 16-bit values; rows 16 bytes apart mod 128
+  static constexpr int MT = WT / 16;             // m-tiles of K Q^T
+  static constexpr int MO = HD / 16;             // m-tiles of V^T P^T
+  static constexpr int HEADS = 8 * NB;
+  static constexpr int Q_STRIDE = HD * ESZ + 16; // bytes; rows 16 bytes apart mod 128
+  static constexpr int Q_PART = HEADS * Q_STRIDE;
   static constexpr int CD = 32;                  // columns summed over the warps at a time
   static constexpr int C_STRIDE = CD + 8;
-  static constexpr int OFF_SCALE = kDecWarps * NSLOT * SLOT;
-  static constexpr int OFF_Q = OFF_SCALE + (Q8 ? kDecWarps * NSLOT * WT * 4 : 0);
-  static constexpr int OFF_SUM = OFF_Q + kDecRows * Q_STRIDE * 2;  // [8][16][C_STRIDE]
-  static constexpr int OFF_ML = OFF_SUM + kDecWarps * kDecRows * C_STRIDE * 4;  // [8][16] (m, l)
-  static constexpr int OFF_QEXP = OFF_ML + kDecWarps * kDecRows * 8;  // [16] 2^e of each Q row
-  static constexpr int OFF_BAR = OFF_QEXP + kDecRows * 4;
-  // [8][kDecStages] pool rows of the tile's boxes, and the mask of absent pages
-  static constexpr int OFF_ROWS = OFF_BAR + kDecWarps * NSLOT * 8;
-  static constexpr int OFF_BAD = OFF_ROWS + kDecWarps * kDecStages * kMaxBoxes * 4;
-  static constexpr int OFF_MISC = OFF_BAD + kDecWarps * kDecStages * 4;
-  static constexpr int SMEM_BYTES = OFF_MISC + 192;
-  static_assert(OFF_BAR % 8 == 0 && OFF_SCALE % 128 == 0 && OFF_Q % 16 == 0 && OFF_SUM % 16 == 0,
+  static constexpr int OFF_SCALE = NW * NSLOT * SLOT;
+  static constexpr int OFF_Q = OFF_SCALE + (Q8 ? NW * NSLOT * WT * 4 : 0);
+  static constexpr int OFF_SUM = OFF_Q + (Q8 ? 2 : 1) * Q_PART;    // [NW][HEADS][C_STRIDE]
+  static constexpr int OFF_ML = OFF_SUM + NW * HEADS * C_STRIDE * 4;  // [NW][HEADS] (m, l)
+  static constexpr int OFF_QEXP = OFF_ML + NW * HEADS * 8;  // [HEADS] 2^(e-7) of each Q row
+  static constexpr int OFF_BAR = OFF_QEXP + HEADS * 4;
+  // [NW][kDecStages] pool rows of the tile's boxes, and the mask of absent pages
+  static constexpr int OFF_ROWS = OFF_BAR + NW * NSLOT * 8;
+  static constexpr int OFF_BAD = OFF_ROWS + NW * kDecStages * kMaxBoxes * 4;
+  static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;
+  static constexpr int SMEM_BYTES = OFF_MISC + 96 + NW * 8;
+  static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 8 == 0 && OFF_SCALE % 128 == 0 && OFF_Q % 16 == 0 &&
+                    OFF_SUM % 16 == 0,
                 "shared memory alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(WT / 16 <= kMaxBoxes && NSLOT / 2 + 2 <= kDecStages, "page table of a warp");
@@ -132,6 +139,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// D (16 x 8, fp32) += A (16 x 32) B (32 x 8), both e4m3.
+__device__ __forceinline__ void mma16832_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit values, two neighbouring columns per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -212,12 +234,12 @@ struct DecodeWalk {
 // Whole block: tiles over all rows, and this CTA's slice of them, in *spot
 // (shared memory; spot->s >= spot->s1: none).  `active` CTAs share the list,
 // at least one tile per warp each where there are that many.
-template <int WT>
+template <int WT, int NW>
 __device__ __forceinline__ long long decode_slice(const PagedDecodeParams& p, int rows_per_seq,
                                                   long long* warp_sum, int* active,
                                                   DecodeWalk* spot) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.num_seqs + kDecThreads - 1) / kDecThreads;
+  const int per = (p.num_seqs + 32 * NW - 1) / (32 * NW);
   const int b0 = min(p.num_seqs, tid * per), b1 = min(p.num_seqs, b0 + per);
   const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
   long long sum = 0;
@@ -236,13 +258,13 @@ __device__ __forceinline__ long long decode_slice(const PagedDecodeParams& p, in
   __syncthreads();
   long long base = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
+  for (int w = 0; w < NW; ++w) {
     if (w < warp) base += warp_sum[w];
     total += warp_sum[w];
   }
   total *= rows_per_seq;
   *active = static_cast<int>(
-      min((total + kDecWarps - 1) / kDecWarps, static_cast<long long>(gridDim.x)));
+      min((total + NW - 1) / NW, static_cast<long long>(gridDim.x)));
   const int c = blockIdx.x;
   const long long s0 = c < *active ? total * c / *active : 0;
   const long long s1 = c < *active ? total * (c + 1) / *active : 0;
@@ -269,14 +291,12 @@ __device__ __forceinline__ long long decode_slice(const PagedDecodeParams& p, in
 }
 
 // ------------------------------------------------------------------ kernel
-// HALF: at most 8 q heads per kv head, so accumulator rows 8 .. 15 are unused
-// and their softmax is left out.
-template <int HD, bool Q8, bool HALF>
-__global__ void __launch_bounds__(kDecThreads, 1)
+template <int HD, bool Q8, int NB>
+__global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
-  using Ly = DecodeLayout<HD, Q8>;
-  constexpr int WT = Ly::WT, NT = Ly::NT, NO = Ly::NO, NSLOT = Ly::NSLOT;
-  constexpr int RI = HALF ? 1 : 2;  // accumulator row halves in use
+  using Ly = DecodeLayout<HD, Q8, NB>;
+  constexpr int WT = Ly::WT, MT = Ly::MT, MO = Ly::MO, NSLOT = Ly::NSLOT, NW = Ly::NW;
+  constexpr int HEADS = Ly::HEADS;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -300,9 +320,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   const int rows_per_seq = p.pool.nkv * p.hblocks;
   int active;
-  const long long total =
-      decode_slice<WT>(p, rows_per_seq, reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 128),
-                       &active, spot);
+  const long long total = decode_slice<WT, NW>(
+      p, rows_per_seq, reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 96), &active, spot);
   const BoundedWait wait{abort_flag, p.status, p.timeout_ns, nullptr, 0u, 0};
 
   DecodeWalk at = *spot;
@@ -310,8 +329,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
   // ------------------------------------------- this warp's stream of copies
   // Copy u of the warp is K (u even) or V (u odd) of its tile u / 2, in slot
-  // u % NSLOT.  Where K of a tile goes out, its pages are known (looked up
-  // one tile ahead) and kept for V.
+  // u % NSLOT.  Where K of a tile goes out, its page ids were loaded one tile
+  // before (and are looked at only now, so that nothing waits for them); the
+  // rows they give are kept for V.
   const int ps = 1 << p.pool.page_shift;
   const int box = min(ps, WT), box_shift = min(p.pool.page_shift, Ly::WT_SHIFT);
   const int boxes = WT >> box_shift;
@@ -322,34 +342,29 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   DecodeWalk ahead = at;  // the tile whose K goes out next
   int aj = warp;          // its index in ahead's segment
   int issued = 0, slot_out = 0;
-  int next_row = 0;       // lane i < boxes: pool row of its box i
-  bool next_bad = false, more = at.s < at.s1;
-  auto settle = [&]() {   // to the segment that holds tile aj, or to the end
+  int next_t = -1, next_id = 0;  // lane i: first token of its box i (-1: none), and its page
+  int next_g = 0;
+  bool more = at.s < at.s1;
+  auto look_up = [&]() {
+    // To the segment that holds tile aj, or to the end of the slice.
     while (more && aj >= ahead.tiles) {
       ahead.template next<WT>(p, rows_per_seq);
       aj = warp;
       more = ahead.tiles > 0;
     }
-  };
-  auto look_up = [&]() {
-    // Where box i starts, or p.pool_rows (out of range: TMA fills zeros) when
-    // it lies behind the last token or its page is absent.
-    next_bad = false;
-    next_row = p.pool_rows;
-    const long long t = static_cast<long long>(ahead.tile0 + aj) * WT + (lane << box_shift);
+    next_t = -1;
+    const int t = (ahead.tile0 + aj) * WT + (lane << box_shift);
     if (more && lane < boxes && t < ahead.n) {
-      const int id = page_id(p.pool, ahead.b, static_cast<int>(t >> p.pool.page_shift), p.status);
-      next_bad = id < 0;
-      if (id >= 0)
-        next_row = static_cast<int>(
-            pool_row(p.pool, id, ahead.rr / p.hblocks, static_cast<int>(t) & (ps - 1)));
+      next_t = t;
+      next_id = __ldg(p.pool.table + ahead.b * p.pool.table_stride + (t >> p.pool.page_shift));
     }
+    next_g = ahead.rr / p.hblocks;
   };
   auto send = [&](const CUtensorMap* m, const float* scales, int row) {
     const uint32_t bar = full(slot_out), dst = ring + slot_out * Ly::SLOT;
-    const uint32_t here = __ballot_sync(0xFFFFFFFFu, lane < boxes && row < p.pool_rows);
-    if (lane == 0)
-      mbar_arrive_expect_tx(bar, Ly::SLOT + (Q8 ? __popc(here) * (box * 4) : 0));
+    uint32_t bytes = Ly::SLOT;
+    if (Q8) bytes += __popc(__ballot_sync(0xFFFFFFFFu, row < p.pool_rows)) * (box * 4);
+    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
     __syncwarp();
     if (lane < boxes) {
 #pragma unroll
@@ -363,51 +378,55 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (++slot_out == NSLOT) slot_out = 0;
     ++issued;
   };
+  // The row of a lane's box: where it starts, or p.pool_rows (out of range:
+  // TMA fills zeros) when it lies behind the last token or its page is absent.
+  auto take_rows = [&](int stage) {
+    int row = p.pool_rows;
+    bool bad = false;
+    if (next_t >= 0) {
+      bad = static_cast<unsigned>(next_id) >= static_cast<unsigned>(p.pool.num_pages);
+      if (!bad) row = static_cast<int>(pool_row(p.pool, next_id, next_g, next_t & (ps - 1)));
+    }
+    const uint32_t badm = __ballot_sync(0xFFFFFFFFu, bad);
+    if (badm != 0u && bad && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusPage);
+    if (lane < boxes) my_rows[stage * kMaxBoxes + lane] = row;
+    if (lane == 0) my_bad[stage] = badm;
+    __syncwarp();
+    return row;
+  };
   // The next copy, if there is one: called NSLOT times at first, then once for
   // every slot read.
   auto issue = [&]() {
     const int stage = (issued >> 1) & (kDecStages - 1);
     if (issued & 1) {
-      const int row = lane < boxes ? my_rows[stage * kMaxBoxes + lane] : p.pool_rows;
-      send(&p.tm_v, p.pool.v_scales, row);
+      send(&p.tm_v, p.pool.v_scales,
+           lane < boxes ? my_rows[stage * kMaxBoxes + lane] : p.pool_rows);
     } else if (more) {
-      const int row = next_row;
-      const uint32_t bad = __ballot_sync(0xFFFFFFFFu, next_bad);
-      if (lane < boxes) my_rows[stage * kMaxBoxes + lane] = row;
-      if (lane == 0) my_bad[stage] = bad;
-      __syncwarp();
-      send(&p.tm_k, p.pool.k_scales, row);
-      aj += kDecWarps;
-      settle();
+      send(&p.tm_k, p.pool.k_scales, take_rows(stage));
+      aj += NW;
       look_up();
     }
   };
-  settle();
   look_up();
-  const bool drop = (p.debug_flags & kDebugDropArrive) && blockIdx.x == 0 && warp == 0;
-  if (drop && more) {  // fault injection: the first copy is never sent
+  if ((p.debug_flags & kDebugDropArrive) && blockIdx.x == 0 && warp == 0 && more) {
+    // Fault injection: the warp's first copy is never sent.
+    take_rows(0);
     slot_out = 1;
     issued = 1;
-    if (lane < boxes) my_rows[lane] = next_row;
-    if (lane == 0) my_bad[0] = 0u;
-    __syncwarp();
-    aj += kDecWarps;
-    settle();
+    aj += NW;
     look_up();
   }
-  while (issued < NSLOT) {
-    const int before = issued;
-    issue();
-    if (issued == before) break;
-  }
+#pragma unroll 1
+  for (int i = 0; i < NSLOT; ++i)
+    if (issued == i) issue();
 
   // Sequences without tokens: zeros, and an LSE of -infinity.
   for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
     if (decode_len(p, b) > 0) continue;
     uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<long long>(b) * p.nq * HD);
-    for (int i = tid; i < p.nq * (HD / 8); i += kDecThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < p.nq * (HD / 8); i += Ly::THREADS) o[i] = make_uint4(0u, 0u, 0u, 0u);
     if (p.lse != nullptr)
-      for (int h = tid; h < p.nq; h += kDecThreads)
+      for (int h = tid; h < p.nq; h += Ly::THREADS)
         p.lse[static_cast<long long>(b) * p.nq + h] = -INFINITY;
   }
   if (at.s >= at.s1) {
@@ -415,10 +434,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     return;
   }
 
-  const int quad = lane & 3, r0 = lane >> 2;      // accumulator rows r0 and r0 + 8
+  // Accumulator fragments (16 x 8): rows r0 and r0 + 8 (tokens or columns of
+  // V), columns 2 quad and 2 quad + 1 (q heads of the block).
+  const int quad = lane & 3, r0 = lane >> 2, r8 = lane & 7, oct = lane >> 3;
   float2* mls = reinterpret_cast<float2*>(smem + Ly::OFF_ML);
   float* qexp = reinterpret_cast<float*>(smem + Ly::OFF_QEXP);
-  uint16_t* qs = reinterpret_cast<uint16_t*>(smem + Ly::OFF_Q);
   float* summed = reinterpret_cast<float*>(smem + Ly::OFF_SUM);
   const uint32_t q_sm = sbase + Ly::OFF_Q;
   int slot = 0, used = 0;  // the next slot to read, and copies read so far
@@ -443,15 +463,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
   for (; at.tiles > 0; at.template next<WT>(p, rows_per_seq)) {
     const int g = at.rr / p.hblocks, h0 = g * p.group + (at.rr % p.hblocks) * kDecRows;
-    const int heads = min(kDecRows, (g + 1) * p.group - h0);
+    const int heads = min(HEADS, (g + 1) * p.group - h0);
 
-    // Q of the row into shared memory: warp w stages rows 2w and 2w + 1; bf16
-    // as it is, or (Q8) fp16 scaled by a power of two, with the dims of each
-    // 16-block in the order in which the e4m3 K fragments come out of ldmatrix.
+    // Q of the row into shared memory, a head per warp and turn: bf16 as it
+    // is, or (Q8) as its two e4m3 parts.
     __syncthreads();  // the last row's Q and sums are no longer read
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = 2 * warp + j;
+    for (int r = warp; r < HEADS; r += NW) {
       const __nv_bfloat16* src = p.q + (static_cast<long long>(at.b) * p.nq + h0 + r) * HD;
       uint32_t w[HD / 64];
       uint32_t big = 0;
@@ -460,222 +478,238 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         w[i] = r < heads ? __ldg(reinterpret_cast<const uint32_t*>(src) + 32 * i + lane) : 0u;
         big = max(big, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
       }
+      uint8_t* dst = smem + Ly::OFF_Q + r * Ly::Q_STRIDE;
       if constexpr (Q8) {
         big = __reduce_max_sync(0xFFFFFFFFu, big);
-        // e: the exponent of the row's largest value (zeros and subnormals:
-        // -126), down = 2^-e, and qexp = 2^e gives it back to the logits.
-        // 2^-127, 2^-128 and 2^128 are made in two steps.
-        const int e = max(static_cast<int>(big >> 7), 1) - 127;
-        const int e1 = min(e, 126), e2 = e - e1;
-        const float down = __int_as_float((127 - e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 0.5f : 0.25f));
+        // up = 2^(7-e) brings the largest value into [128, 256) (in two steps
+        // where a float does not hold it); zeros and subnormals: e = -126.  A
+        // row with an infinity or a NaN: NaN logits.
+        const int s = 134 - max(static_cast<int>(big >> 7), 1);  // 7 - e
+        const int s1 = max(min(s, 127), -126), s2 = s - s1;      // s2 in {0 .. 6}, or -1 .. 0
+        const float f1 = __int_as_float((127 + s1) << 23), f2 = __int_as_float((127 + s2) << 23);
         if (lane == 0)
-          qexp[r] = __int_as_float((127 + e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 2.f : 4.f));
+          qexp[r] = big >= 0x7F80u ? __int_as_float(0x7FC00000)
+                                   : __int_as_float((127 - s2) << 23) * exp2f(static_cast<float>(-s1));
 #pragma unroll
         for (int i = 0; i < HD / 64; ++i) {
-          const int d = 2 * (32 * i + lane);     // dims d, d + 1 (d even)
-          const int k = d & 15;                  // dim 4a + 2c -> position 2a + 8c
-          const int pos = (d & ~15) + (k >> 2) * 2 + ((k >> 1) & 1) * 8;
-          *reinterpret_cast<uint32_t*>(qs + r * Ly::Q_STRIDE + pos) =
-              pack_f16x2(__uint_as_float(w[i] << 16) * down,
-                         __uint_as_float(w[i] & 0xFFFF0000u) * down);
+          const float a = __uint_as_float(w[i] << 16) * f1 * f2;
+          const float b = __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2;
+          const uint16_t hi = pack_e4m3x2(a, b);
+          const uint32_t back = e4m3x2_to_f16x2(hi);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+          const uint16_t lo = pack_e4m3x2((a - f.x) * 16.f, (b - f.y) * 16.f);
+          *reinterpret_cast<uint16_t*>(dst + 2 * (32 * i + lane)) = hi;
+          *reinterpret_cast<uint16_t*>(dst + Ly::Q_PART + 2 * (32 * i + lane)) = lo;
         }
       } else {
 #pragma unroll
         for (int i = 0; i < HD / 64; ++i)
-          *reinterpret_cast<uint32_t*>(qs + r * Ly::Q_STRIDE + 2 * (32 * i + lane)) = w[i];
+          *reinterpret_cast<uint32_t*>(dst + 4 * (32 * i + lane)) = w[i];
       }
     }
     __syncthreads();
-    float sl[RI];
+    float sl[NB][2], m[NB][2], l[NB][2];
 #pragma unroll
-    for (int i = 0; i < RI; ++i) sl[i] = Q8 ? p.scale_log2 * qexp[r0 + 8 * i] : p.scale_log2;
-
-    float m[RI], l[RI];
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int i = 0; i < RI; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-    }
+      for (int j = 0; j < 2; ++j) {
+        sl[nb][j] = Q8 ? p.scale_log2 * qexp[8 * nb + 2 * quad + j] : p.scale_log2;
+        m[nb][j] = -INFINITY;
+        l[nb][j] = 0.f;
+      }
     float sref = kMinSref, pscale = kPScale / kMinSref;
-    float o[NO][4];
+    float o[MO][NB][4];
 #pragma unroll
-    for (int i = 0; i < NO; ++i)
+    for (int i = 0; i < MO; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][nb][j] = 0.f;
 
-    for (int v = warp; v < at.tiles; v += kDecWarps) {
+    for (int v = warp; v < at.tiles; v += NW) {
       const int valid = min(WT, at.n - (at.tile0 + v) * WT);  // tokens of the tile
       const uint32_t bad = my_bad[(used >> 1) & (kDecStages - 1)];
       const bool partial = valid < WT || bad != 0u;
 
-      // ---- S = Q K^T
+      // ---- S^T = K Q^T
       await();
       const uint32_t kb = ring + slot * Ly::SLOT;
-      const float* ksc = reinterpret_cast<const float*>(
-          smem + Ly::OFF_SCALE + (warp * NSLOT + slot) * (WT * 4));
-      float c[NT][4];
+      float c[MT][NB][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[t][j] = 0.f;
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[t][nb][j] = 0.f;
       if constexpr (Q8) {
+        float cl[MT][NB][4];
 #pragma unroll
-        for (int blk = 0; blk < HD / 64; ++blk) {  // 64 dims: four k16 steps
-          uint32_t a[4][4];
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            ldsm4(a[j], q_sm + ((lane & 15) * Ly::Q_STRIDE + (4 * blk + j) * 16 + (lane >> 4) * 8) * 2);
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            uint32_t kr[4];
-            ldsm4(kr, sw128(kb + (blk >> 1) * (WT * 128), t * 8 + (lane & 7),
-                            (blk & 1) * 4 + (lane >> 3)));
+            for (int j = 0; j < 4; ++j) cl[t][nb][j] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t b0, b1;
-              e4m3x4_to_f16x4(kr[j], &b0, &b1);
-              mma16816<true>(c[t], a[j], b0, b1);
+        for (int ks = 0; ks < HD / 32; ++ks) {  // 32 dims: chunks 2 ks and 2 ks + 1
+          uint32_t qh[4], ql[4];  // [nb][b0, b1]; NB = 1: the upper two repeat the lower
+          const uint32_t qa = q_sm + ((NB == 2 ? (oct >> 1) * 8 : 0) + r8) * Ly::Q_STRIDE +
+                              (2 * ks + (oct & 1)) * 16;
+          ldsm4(qh, qa);
+          ldsm4(ql, qa + Ly::Q_PART);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            uint32_t a[4];
+            const int ch = 2 * ks + (oct >> 1);
+            ldsm4(a, sw128(kb + (ks >> 2) * (WT * 128), t * 16 + (oct & 1) * 8 + r8, ch & 7));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16832_e4m3(c[t][nb], a, qh[2 * nb], qh[2 * nb + 1]);
+              mma16832_e4m3(cl[t][nb], a, ql[2 * nb], ql[2 * nb + 1]);
             }
           }
         }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[t][nb][j] = fmaf(cl[t][nb][j], 0.0625f, c[t][nb][j]);
       } else {
 #pragma unroll
-        for (int blk = 0; blk < HD / 32; ++blk) {  // 32 dims: two k16 steps
-          uint32_t a[2][4];
+        for (int ks = 0; ks < HD / 16; ++ks) {  // 16 dims: chunks 2 ks and 2 ks + 1
+          uint32_t qf[4];
+          ldsm4(qf, q_sm + ((NB == 2 ? (oct >> 1) * 8 : 0) + r8) * Ly::Q_STRIDE +
+                        (2 * ks + (oct & 1)) * 16);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            ldsm4(a[j], q_sm + ((lane & 15) * Ly::Q_STRIDE + (2 * blk + j) * 16 + (lane >> 4) * 8) * 2);
+          for (int t = 0; t < MT; ++t) {
+            uint32_t a[4];
+            const int ch = 2 * ks + (oct >> 1);
+            ldsm4(a, sw128(kb + (ks >> 2) * (WT * 128), t * 16 + (oct & 1) * 8 + r8, ch & 7));
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            uint32_t kr[4];
-            ldsm4(kr, sw128(kb + (blk >> 1) * (WT * 128), t * 8 + (lane & 7),
-                            (blk & 1) * 4 + (lane >> 3)));
-            mma16816<false>(c[t], a[0], kr[0], kr[1]);
-            mma16816<false>(c[t], a[1], kr[2], kr[3]);
+            for (int nb = 0; nb < NB; ++nb) mma16816<false>(c[t][nb], a, qf[2 * nb], qf[2 * nb + 1]);
           }
         }
       }
       // Logits in log2 units, in place; what is no token is -infinity, by value.
-      float mx[RI];
+      const float* ksc = reinterpret_cast<const float*>(
+          smem + Ly::OFF_SCALE + (warp * NSLOT + slot) * (WT * 4));
 #pragma unroll
-      for (int i = 0; i < RI; ++i) mx[i] = -INFINITY;
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float2 ks = make_float2(1.f, 1.f);
-        if (Q8) ks = *reinterpret_cast<const float2*>(ksc + t * 8 + quad * 2);
+        for (int i = 0; i < 2; ++i) {
+          const float ks = Q8 ? ksc[16 * t + 8 * i + r0] : 1.f;
 #pragma unroll
-        for (int i = 0; i < RI; ++i) {
-          c[t][2 * i] *= sl[i] * ks.x;
-          c[t][2 * i + 1] *= sl[i] * ks.y;
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) c[t][nb][2 * i + j] *= Q8 ? sl[nb][j] * ks : sl[nb][j];
         }
-      }
+      bool seen[MT][2];
       if (partial) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int tok = t * 8 + quad * 2 + j;
-            if (tok >= valid || ((bad >> (tok >> box_shift)) & 1u)) {
+          for (int i = 0; i < 2; ++i) {
+            const int tok = 16 * t + 8 * i + r0;
+            seen[t][i] = tok < valid && !((bad >> (tok >> box_shift)) & 1u);
+            if (!seen[t][i]) {
 #pragma unroll
-              for (int i = 0; i < RI; ++i) c[t][2 * i + j] = -INFINITY;
+              for (int nb = 0; nb < NB; ++nb) c[t][nb][2 * i] = c[t][nb][2 * i + 1] = -INFINITY;
             }
           }
       }
+      float mx[NB][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < RI; ++i) mx[i] = fmaxf(mx[i], fmaxf(c[t][2 * i], c[t][2 * i + 1]));
+        for (int j = 0; j < 2; ++j) {
+          mx[nb][j] = fmaxf(c[0][nb][j], c[0][nb][2 + j]);
+#pragma unroll
+          for (int t = 1; t < MT; ++t)
+            mx[nb][j] = fmaxf(mx[nb][j], fmaxf(c[t][nb][j], c[t][nb][2 + j]));
+        }
       release();
 
       // ---- references: m, and (Q8) s_ref
       await();
       const uint32_t vb = ring + slot * Ly::SLOT;
-      float2 vs[NT];
+      float vs[MT][2];
       float smx = 0.f;
       if constexpr (Q8) {
         const float* vsc = reinterpret_cast<const float*>(
             smem + Ly::OFF_SCALE + (warp * NSLOT + slot) * (WT * 4));
 #pragma unroll
-        for (int t = 0; t < NT; ++t) vs[t] = *reinterpret_cast<const float2*>(vsc + t * 8 + quad * 2);
-        if (partial) {
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const int tok = t * 8 + quad * 2;
-            if (tok >= valid || ((bad >> (tok >> box_shift)) & 1u)) vs[t].x = 0.f;
-            if (tok + 1 >= valid || ((bad >> (tok >> box_shift)) & 1u)) vs[t].y = 0.f;
+          for (int i = 0; i < 2; ++i) {
+            vs[t][i] = vsc[16 * t + 8 * i + r0];
+            if (partial && !seen[t][i]) vs[t][i] = 0.f;
+            smx = fmaxf(smx, fabsf(vs[t][i]));
           }
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) smx = fmaxf(smx, fmaxf(fabsf(vs[t].x), fabsf(vs[t].y)));
       }
-      bool raise = false;
+      bool raise = Q8 && smx > sref;
 #pragma unroll
-      for (int i = 0; i < RI; ++i) raise |= mx[i] > m[i] + kRaise;
-      if (Q8) raise |= smx > sref;
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) raise |= mx[nb][j] > m[nb][j] + kRaise;
       if (__any_sync(0xFFFFFFFFu, raise)) {
-        float alpha[2] = {1.f, 1.f};
+        float shrink = 1.f;
         if constexpr (Q8) {
 #pragma unroll
-          for (int d = 1; d < 4; d <<= 1) smx = fmaxf(smx, __shfl_xor_sync(0xFFFFFFFFu, smx, d));
-          if (smx > sref) {  // (the same in every lane: the quads hold the same columns)
+          for (int d = 4; d < 32; d <<= 1) smx = fmaxf(smx, __shfl_xor_sync(0xFFFFFFFFu, smx, d));
+          if (smx > sref) {  // (every quad of lanes holds the same tokens: alike in the warp)
             const float up = 2.f * smx;  // twice: the next scales are likely to fit
-            alpha[0] = alpha[1] = sref / up;
+            shrink = sref / up;
             sref = up;
             pscale = kPScale / up;
           }
         }
 #pragma unroll
-        for (int i = 0; i < RI; ++i) {
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int d = 1; d < 4; d <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], d));
-          const float mn = fmaxf(m[i], mx[i]);
-          const float a = m[i] == mn ? 1.f : ex2_approx(m[i] - mn);
-          m[i] = mn;
-          l[i] *= a;
-          alpha[i] *= a;
-        }
-        if (HALF) alpha[1] = 0.f;
+          for (int j = 0; j < 2; ++j) {
+            float x = mx[nb][j];
 #pragma unroll
-        for (int i = 0; i < NO; ++i) {
-          o[i][0] *= alpha[0];
-          o[i][1] *= alpha[0];
-          o[i][2] *= alpha[1];
-          o[i][3] *= alpha[1];
-        }
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+            const float mn = fmaxf(m[nb][j], x);
+            const float a = m[nb][j] == mn ? 1.f : ex2_approx(m[nb][j] - mn);
+            m[nb][j] = mn;
+            l[nb][j] *= a;
+            const float as = a * shrink;
+#pragma unroll
+            for (int i = 0; i < MO; ++i) {
+              o[i][nb][j] *= as;
+              o[i][nb][2 + j] *= as;
+            }
+          }
       }
 
-      // ---- P, as the A operand of P V (16 tokens: n-tiles 2k and 2k + 1)
-      float mref[RI];
+      // ---- P, transposed into the B operand of V^T P^T (16 tokens per step)
+      uint32_t ph[MT][NB][2], pl[Q8 ? 1 : MT][NB][2];
 #pragma unroll
-      for (int i = 0; i < RI; ++i) mref[i] = m[i] == -INFINITY ? 0.f : m[i];
-      uint32_t ph[WT / 16][4], pl[Q8 ? 1 : WT / 16][4];
+      for (int nb = 0; nb < NB; ++nb) {
+        const float m0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0];
+        const float m1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float sx = Q8 ? vs[t].x * pscale : 1.f, sy = Q8 ? vs[t].y * pscale : 1.f;
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int k = t >> 1, j = 2 * (t & 1) + i;
-          if (i >= RI) {
-            ph[k][j] = 0u;
-            if (!Q8) pl[Q8 ? 0 : k][j] = 0u;
-            continue;
+          for (int i = 0; i < 2; ++i) {
+            const float e0 = ex2_approx(c[t][nb][2 * i] - m0);
+            const float e1 = ex2_approx(c[t][nb][2 * i + 1] - m1);
+            l[nb][0] += e0;
+            l[nb][1] += e1;
+            if constexpr (Q8) {
+              const float f = vs[t][i] * pscale;
+              ph[t][nb][i] = transpose8(pack_f16x2(e0 * f, e1 * f));
+            } else {
+              const uint32_t hi = pack_bf16x2(e0, e1);
+              ph[t][nb][i] = transpose8(hi);
+              pl[t][nb][i] = transpose8(pack_bf16x2(e0 - __uint_as_float(hi << 16),
+                                                    e1 - __uint_as_float(hi & 0xFFFF0000u)));
+            }
           }
-          const int ii = i < RI ? i : 0;
-          const float e0 = ex2_approx(c[t][2 * ii] - mref[ii]);
-          const float e1 = ex2_approx(c[t][2 * ii + 1] - mref[ii]);
-          l[ii] += e0 + e1;
-          if constexpr (Q8) {
-            ph[k][j] = pack_f16x2(e0 * sx, e1 * sy);
-          } else {
-            const uint32_t hi = pack_bf16x2(e0, e1);
-            ph[k][j] = hi;
-            pl[k][j] = pack_bf16x2(e0 - __uint_as_float(hi << 16),
-                                   e1 - __uint_as_float(hi & 0xFFFF0000u));
-          }
-        }
       }
 
-      // ---- O += P V
+      // ---- O^T += V^T P^T
       if (valid < WT) {
         // Slots behind the last token may hold anything; 0 * NaN must not
         // reach O.
@@ -690,34 +724,37 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         __syncwarp();
       }
 #pragma unroll
-      for (int k = 0; k < WT / 16; ++k) {
-        // ldmatrix: token half, then 16-byte chunk, by lane octet
-        const int row = k * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+      for (int k = 0; k < MT; ++k) {
         if constexpr (Q8) {
 #pragma unroll
-          for (int ch = 0; ch < HD / 16; ch += 2) {  // 32 columns
-            uint32_t vr[4];
-            ldsm4_t(vr, sw128(vb + (ch >> 3) * (WT * 128), row, (ch & 7) + (lane >> 4)));
+          for (int ch = 0; ch < MO; ch += 2) {  // two 16-byte chunks: 32 columns
+            uint32_t vr[4];  // token half, then chunk, by lane octet
+            ldsm4_t(vr, sw128(vb + (ch >> 3) * (WT * 128), k * 16 + (oct & 1) * 8 + r8,
+                              (ch & 7) + (oct >> 1)));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               // Each register holds two tokens x two columns; regrouped, the
-              // lower half is the even column's, the upper the odd one's.
-              uint32_t b0e, b0o, b1e, b1o;
-              e4m3x4_to_f16x4(__byte_perm(vr[2 * j], 0u, 0x3120), &b0e, &b0o);
-              e4m3x4_to_f16x4(__byte_perm(vr[2 * j + 1], 0u, 0x3120), &b1e, &b1o);
-              mma16816<true>(o[2 * (ch + j)], ph[k], b0e, b1e);
-              mma16816<true>(o[2 * (ch + j) + 1], ph[k], b0o, b1o);
+              // lower half is the even column's (rows 0-7 of the m-tile), the
+              // upper the odd one's (rows 8-15).
+              uint32_t a[4];
+              e4m3x4_to_f16x4(__byte_perm(vr[2 * j], 0u, 0x3120), &a[0], &a[1]);
+              e4m3x4_to_f16x4(__byte_perm(vr[2 * j + 1], 0u, 0x3120), &a[2], &a[3]);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816<true>(o[ch + j][nb], a, ph[k][nb][0], ph[k][nb][1]);
             }
           }
         } else {
 #pragma unroll
-          for (int ch = 0; ch < HD / 8; ch += 2) {   // 16 columns
-            uint32_t vr[4];
-            ldsm4_t(vr, sw128(vb + (ch >> 3) * (WT * 128), row, (ch & 7) + (lane >> 4)));
-            mma16816<false>(o[ch], ph[k], vr[0], vr[1]);
-            mma16816<false>(o[ch + 1], ph[k], vr[2], vr[3]);
-            mma16816<false>(o[ch], pl[k], vr[0], vr[1]);
-            mma16816<false>(o[ch + 1], pl[k], vr[2], vr[3]);
+          for (int i = 0; i < MO; ++i) {  // 16 columns: chunks 2 i and 2 i + 1
+            uint32_t a[4];  // chunk, then token half, by lane octet
+            ldsm4_t(a, sw128(vb + (i >> 2) * (WT * 128), k * 16 + (oct >> 1) * 8 + r8,
+                             (2 * i & 7) + (oct & 1)));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816<false>(o[i][nb], a, ph[k][nb][0], ph[k][nb][1]);
+              mma16816<false>(o[i][nb], a, pl[k][nb][0], pl[k][nb][1]);
+            }
           }
         }
       }
@@ -729,66 +766,70 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     // ---- the end of the row (or of this CTA's piece of it): the warps' m and
     // l, then their O, 32 columns at a time, summed in warp order.
 #pragma unroll
-    for (int i = 0; i < RI; ++i) {
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int d = 1; d < 4; d <<= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], d);
-      if (quad == 0) mls[warp * kDecRows + r0 + 8 * i] = make_float2(m[i], l[i]);
-    }
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][j], d);
+        if (r0 == 0) mls[warp * HEADS + 8 * nb + 2 * quad + j] = make_float2(m[nb][j], l[nb][j]);
+      }
     __syncthreads();
     const bool whole = at.tile0 == 0 && at.tiles == at.nt;
     const int piece = 2 * blockIdx.x + (at.tile0 == 0 ? 1 : 0);
-    float f[2] = {0.f, 0.f};
+    float f[NB][2];
 #pragma unroll
-    for (int i = 0; i < RI; ++i) {
-      const int r = r0 + 8 * i;
-      float mm = -INFINITY, sum = 0.f;
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, mls[w * kDecRows + r].x);
-      const float mref = mm == -INFINITY ? 0.f : mm;
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * nb + 2 * quad + j;
+        float mm = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float2 ml = mls[w * kDecRows + r];
-        sum = fmaf(ex2_approx(ml.x - mref), ml.y, sum);
+        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mls[w * HEADS + r].x);
+        const float mref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float2 ml = mls[w * HEADS + r];
+          sum = fmaf(ex2_approx(ml.x - mref), ml.y, sum);
+        }
+        f[nb][j] = ex2_approx(m[nb][j] - mref) * (Q8 ? sref * (1.f / kPScale) : 1.f);
+        // sum = 0: every page of the row was absent.
+        if (whole) f[nb][j] = sum == 0.f ? 0.f : f[nb][j] / sum;
+        if (warp == 0 && r0 == 0 && r < heads) {
+          const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
+          if (!whole)
+            p.ws_ml[piece * kDecRows + r] = make_float2(mm, sum);
+          else if (p.lse != nullptr)
+            p.lse[orow] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.69314718055994531f;
+        }
       }
-      f[i] = ex2_approx(m[i] - mref) * (Q8 ? sref * (1.f / kPScale) : 1.f);
-      // sum = 0: every page of the row was absent.
-      if (whole) f[i] = sum == 0.f ? 0.f : f[i] / sum;
-      if (warp == 0 && quad == 0 && r < heads) {
-        const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
-        if (!whole)
-          p.ws_ml[piece * kDecRows + r] = make_float2(mm, sum);
-        else if (p.lse != nullptr)
-          p.lse[orow] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.69314718055994531f;
-      }
-    }
-    constexpr int TILES = Ly::CD / 8;  // n-tiles per round
 #pragma unroll
     for (int cc = 0; cc < HD / Ly::CD; ++cc) {
       if (cc > 0) __syncthreads();
-      float* mine = summed + warp * (kDecRows * Ly::C_STRIDE);
 #pragma unroll
-      for (int i = 0; i < RI; ++i)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int k = 0; k < TILES; k += 2) {
-          const float* a = o[cc * TILES + k];
-          const float* b = o[cc * TILES + k + 1];
-          float* dst = mine + (r0 + 8 * i) * Ly::C_STRIDE + 8 * k;
-          if constexpr (Q8) {  // n-tiles k, k + 1: even and odd columns of 16
-            *reinterpret_cast<float4*>(dst + 4 * quad) =
-                make_float4(a[2 * i] * f[i], b[2 * i] * f[i], a[2 * i + 1] * f[i], b[2 * i + 1] * f[i]);
-          } else {
-            *reinterpret_cast<float2*>(dst + 2 * quad) = make_float2(a[2 * i] * f[i], a[2 * i + 1] * f[i]);
-            *reinterpret_cast<float2*>(dst + 8 + 2 * quad) = make_float2(b[2 * i] * f[i], b[2 * i + 1] * f[i]);
+        for (int j = 0; j < 2; ++j) {
+          float* dst = summed + (warp * HEADS + 8 * nb + 2 * quad + j) * Ly::C_STRIDE;
+#pragma unroll
+          for (int k = 0; k < Ly::CD / 16; ++k) {
+            const float* a = o[cc * (Ly::CD / 16) + k][nb];
+            if constexpr (Q8) {  // rows r0, r0 + 8 of the m-tile: columns 2 r0 and 2 r0 + 1
+              *reinterpret_cast<float2*>(dst + 16 * k + 2 * r0) =
+                  make_float2(a[j] * f[nb][j], a[2 + j] * f[nb][j]);
+            } else {
+              dst[16 * k + r0] = a[j] * f[nb][j];
+              dst[16 * k + 8 + r0] = a[2 + j] * f[nb][j];
+            }
           }
         }
       __syncthreads();
-      const int r = tid >> 4, d = 2 * (tid & 15);  // 16 rows x 16 column pairs
+      const int r = tid / (Ly::CD / 2), d = 2 * (tid % (Ly::CD / 2));  // column pairs
       if (r < heads) {
         float2 y = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
-          const float2 z = *reinterpret_cast<const float2*>(
-              summed + (w * kDecRows + r) * Ly::C_STRIDE + d);
+        for (int w = 0; w < NW; ++w) {
+          const float2 z =
+              *reinterpret_cast<const float2*>(summed + (w * HEADS + r) * Ly::C_STRIDE + d);
           y.x += z.x;
           y.y += z.y;
         }

@@ -80,13 +80,13 @@ DecodeWorkspace decode_workspace(const cpattn_ctx* ctx) {
   return w;
 }
 
-template <int HD, bool Q8, bool HALF>
+template <int HD, bool Q8, int NB>
 cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
                             cpattn::PagedDecodeParams* p, cudaStream_t st) {
-  using Ly = cpattn::DecodeLayout<HD, Q8>;
+  using Ly = cpattn::DecodeLayout<HD, Q8, NB>;
   bool& ready = ctx->decode_ready[HD == 256][Q8];
   if (!ready) {
-    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8, HALF>,
+    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8, NB>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Ly::SMEM_BYTES);
     if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaFuncSetAttribute(paged decode)");
@@ -107,8 +107,8 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
       (static_cast<long long>(pages->max_pages) * pages->page_size + Ly::WT - 1) / Ly::WT;
   p->num_ctas = static_cast<int>(std::min<long long>(
       decode_max_ctas(ctx),
-      (rows_all * std::min(tiles, 1LL << 20) + cpattn::kDecWarps - 1) / cpattn::kDecWarps));
-  cpattn::paged_decode_kernel<HD, Q8, HALF><<<p->num_ctas, cpattn::kDecThreads, Ly::SMEM_BYTES, st>>>(*p);
+      (rows_all * std::min(tiles, 1LL << 20) + Ly::NW - 1) / Ly::NW));
+  cpattn::paged_decode_kernel<HD, Q8, NB><<<p->num_ctas, Ly::THREADS, Ly::SMEM_BYTES, st>>>(*p);
   cpattn_status s = after_launch(ctx, st, "paged decode launch");
   if (s != CPATTN_OK || tiles == 1 || p->num_ctas == 1) return s;  // no row can be cut
   // Blocks: one per row that may have been cut, times heads where those are few.
@@ -261,19 +261,19 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
   p.scale_log2 = c.softmax_scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool q8 = pages->format == CPATTN_PAGES_E4M3;
-  const bool half = p.group <= 8;
+  const bool one = p.group <= 8;
   if (c.head_dim == 128) {
-    if (half)
-      return q8 ? launch_decode<128, true, true>(ctx, pages, &p, st)
-                : launch_decode<128, false, true>(ctx, pages, &p, st);
-    return q8 ? launch_decode<128, true, false>(ctx, pages, &p, st)
-              : launch_decode<128, false, false>(ctx, pages, &p, st);
+    if (one)
+      return q8 ? launch_decode<128, true, 1>(ctx, pages, &p, st)
+                : launch_decode<128, false, 1>(ctx, pages, &p, st);
+    return q8 ? launch_decode<128, true, 2>(ctx, pages, &p, st)
+              : launch_decode<128, false, 2>(ctx, pages, &p, st);
   }
-  if (half)
-    return q8 ? launch_decode<256, true, true>(ctx, pages, &p, st)
-              : launch_decode<256, false, true>(ctx, pages, &p, st);
-  return q8 ? launch_decode<256, true, false>(ctx, pages, &p, st)
-            : launch_decode<256, false, false>(ctx, pages, &p, st);
+  if (one)
+    return q8 ? launch_decode<256, true, 1>(ctx, pages, &p, st)
+              : launch_decode<256, false, 1>(ctx, pages, &p, st);
+  return q8 ? launch_decode<256, true, 2>(ctx, pages, &p, st)
+            : launch_decode<256, false, 2>(ctx, pages, &p, st);
 } catch (...) {
   return CPATTN_E_NOMEM;
 }
