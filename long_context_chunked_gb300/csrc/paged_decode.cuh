@@ -30,17 +30,14 @@
 // into the operand of V^T P^T in registers (movmatrix).  No barrier, no shared
 // P; the warps meet once per row, where their O are summed in warp order.
 //
-// e4m3 (Q8).  K Q^T multiplies K's bytes as they are by Q in two e4m3 parts:
-// q 2^(7-e) = hi + lo / 16, e the exponent of the head's largest element.  The
-// two products have their own accumulators.  bf16's 8 significant bits fit
-// the two parts exactly; elements below 2^-13 of the largest lose bits, at
-// most 2^-21 of the largest.  (As fp16, K took one more conversion per value
-// than it takes now, and the products 3.5 times as long.)  A K row's scale
-// multiplies its logit.  V is converted to fp16 (exact) in registers, and its
-// scale multiplies the probability: P is stored as p_t (s_t / s_ref) 2^7,
+// e4m3 (Q8): K and V are converted to fp16 (exact) in registers; mma.sync on
+// e4m3 operands takes the same conversions and adds fp32 additions (measured
+// by instruction counters).  Q is fp16, scaled by a power of two per head so
+// that its largest element is in [1, 2): elements below 2^-14 of it lose bits,
+// at most 2^-25 of the largest.  A K row's scale multiplies its logit.  A V
+// row's scale multiplies its probability: P is stored as p_t (s_t / s_ref) 2^7,
 // rounded once to fp16's 11 bits, with s_ref at least every scale so far and
-// at least 2^-100.  (P in e4m3 parts would need four of them to keep both the
-// bits and the range of small probabilities.)
+// at least 2^-100.
 // bf16: P is carried as a bf16 hi + lo pair (16 bits) against bf16 V.
 //
 // m and s_ref are references, not exact maxima: they are raised (and O and l
@@ -79,15 +76,16 @@ struct DecodeLayout {
   static constexpr int MT = WT / 16;             // m-tiles of K Q^T
   static constexpr int MO = HD / 16;             // m-tiles of V^T P^T
   static constexpr int HEADS = 8 * NB;
-  static constexpr int Q_STRIDE = HD * ESZ + 16; // bytes; rows 16 bytes apart mod 128
-  static constexpr int Q_PART = HEADS * Q_STRIDE;
+  static constexpr int Q_STRIDE = 2 * HD + 16;   // bytes; rows 16 bytes apart mod 128
+  // Q's fragments stay in registers for a row where they fit beside O.
+  static constexpr bool Q_REGS = HD * NB <= 256;
   static constexpr int CD = 32;                  // columns summed over the warps at a time
   static constexpr int C_STRIDE = CD + 8;
   static constexpr int OFF_SCALE = NW * NSLOT * SLOT;
   static constexpr int OFF_Q = OFF_SCALE + (Q8 ? NW * NSLOT * WT * 4 : 0);
-  static constexpr int OFF_SUM = OFF_Q + (Q8 ? 2 : 1) * Q_PART;    // [NW][HEADS][C_STRIDE]
+  static constexpr int OFF_SUM = OFF_Q + HEADS * Q_STRIDE;  // [NW][HEADS][C_STRIDE]
   static constexpr int OFF_ML = OFF_SUM + NW * HEADS * C_STRIDE * 4;  // [NW][HEADS] (m, l)
-  static constexpr int OFF_QEXP = OFF_ML + NW * HEADS * 8;  // [HEADS] 2^(e-7) of each Q row
+  static constexpr int OFF_QEXP = OFF_ML + NW * HEADS * 8;  // [HEADS] 2^e of each Q row
   static constexpr int OFF_BAR = OFF_QEXP + HEADS * 4;
   // [NW][kDecStages] pool rows of the tile's boxes, and the mask of absent pages
   static constexpr int OFF_ROWS = OFF_BAR + NW * NSLOT * 8;
@@ -124,35 +122,39 @@ struct PagedDecodeParams {
 enum : int { kSiteDecFull = 9 };  // after the prefill's sites
 
 // ------------------------------------------------------------------ mma.sync
-template <bool F16>
+// c (16 x 8) = (ZERO ? 0 : c) + A (16 x 16) B (16 x 8).
+template <bool F16, bool ZERO = false>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  if constexpr (F16)
-    asm volatile(
+  if constexpr (F16 && ZERO)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else if constexpr (ZERO)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else if constexpr (F16)
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// D (16 x 8, fp32) += A (16 x 32) B (32 x 8), both e4m3.
-__device__ __forceinline__ void mma16832_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                              uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // Transpose of an 8 x 8 matrix of 16-bit values, two neighbouring columns per lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -167,13 +169,15 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-      : "memory");
+// Asynchronous copy of 4 bytes, and an arrival on `bar` once this thread's
+// copies so far have landed.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Four e4m3 values as two fp16 pairs (exact).
@@ -314,7 +318,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   DecodeWalk* spot = reinterpret_cast<DecodeWalk*>(smem + Ly::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::OFF_MISC + 64);
   if (lane == 0) {
-    for (int s = 0; s < NSLOT; ++s) mbar_init(full(s), 1);
+    // (Q8: every lane's copies of the scales arrive too.)
+    for (int s = 0; s < NSLOT; ++s) mbar_init(full(s), Q8 ? 33 : 1);
     if (warp == 0) *abort_flag = 0;
     fence_mbar_init();
   }
@@ -360,21 +365,29 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     }
     next_g = ahead.rr / p.hblocks;
   };
-  auto send = [&](const CUtensorMap* m, const float* scales, int row) {
+  auto send = [&](const CUtensorMap* m, const float* scales, int stage) {
     const uint32_t bar = full(slot_out), dst = ring + slot_out * Ly::SLOT;
-    uint32_t bytes = Ly::SLOT;
-    if (Q8) bytes += __popc(__ballot_sync(0xFFFFFFFFu, row < p.pool_rows)) * (box * 4);
-    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-    __syncwarp();
+    if (lane == 0) mbar_arrive_expect_tx(bar, Ly::SLOT);
     if (lane < boxes) {
+      const int row = my_rows[stage * kMaxBoxes + lane];
 #pragma unroll
       for (int c = 0; c < Ly::NBOX; ++c)
         tma_load_3d(dst + c * (WT * 128) + (lane << box_shift) * 128, m, bar, c * Ly::BOXW, 0, row);
-      if (Q8 && row < p.pool_rows)
-        bulk_load(sbase + Ly::OFF_SCALE + (warp * NSLOT + slot_out) * (WT * 4) +
-                      (lane << box_shift) * 4,
-                  scales + row, box * 4, bar);
     }
+    if constexpr (Q8) {
+#pragma unroll
+      for (int j = 0; j < WT; j += 32) {
+        const int tok = j + lane;
+        if (WT >= 32 || tok < WT) {
+          const int row = my_rows[stage * kMaxBoxes + (tok >> box_shift)];
+          if (row < p.pool_rows)
+            copy4_async(sbase + Ly::OFF_SCALE + (warp * NSLOT + slot_out) * (WT * 4) + tok * 4,
+                        scales + row + (tok & (box - 1)));
+        }
+      }
+      copies_arrive(bar);
+    }
+    __syncwarp();
     if (++slot_out == NSLOT) slot_out = 0;
     ++issued;
   };
@@ -392,17 +405,16 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     if (lane < boxes) my_rows[stage * kMaxBoxes + lane] = row;
     if (lane == 0) my_bad[stage] = badm;
     __syncwarp();
-    return row;
   };
   // The next copy, if there is one: called NSLOT times at first, then once for
   // every slot read.
   auto issue = [&]() {
     const int stage = (issued >> 1) & (kDecStages - 1);
     if (issued & 1) {
-      send(&p.tm_v, p.pool.v_scales,
-           lane < boxes ? my_rows[stage * kMaxBoxes + lane] : p.pool_rows);
+      send(&p.tm_v, p.pool.v_scales, stage);
     } else if (more) {
-      send(&p.tm_k, p.pool.k_scales, take_rows(stage));
+      take_rows(stage);
+      send(&p.tm_k, p.pool.k_scales, stage);
       aj += NW;
       look_up();
     }
@@ -466,7 +478,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     const int heads = min(HEADS, (g + 1) * p.group - h0);
 
     // Q of the row into shared memory, a head per warp and turn: bf16 as it
-    // is, or (Q8) as its two e4m3 parts.
+    // is, or (Q8) fp16 scaled by a power of two, with the dims of each 16-block
+    // in the order in which the e4m3 K fragments come out of ldmatrix.
     __syncthreads();  // the last row's Q and sums are no longer read
 #pragma unroll
     for (int r = warp; r < HEADS; r += NW) {
@@ -481,25 +494,23 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       uint8_t* dst = smem + Ly::OFF_Q + r * Ly::Q_STRIDE;
       if constexpr (Q8) {
         big = __reduce_max_sync(0xFFFFFFFFu, big);
-        // up = 2^(7-e) brings the largest value into [128, 256) (in two steps
-        // where a float does not hold it); zeros and subnormals: e = -126.  A
-        // row with an infinity or a NaN: NaN logits.
-        const int s = 134 - max(static_cast<int>(big >> 7), 1);  // 7 - e
-        const int s1 = max(min(s, 127), -126), s2 = s - s1;      // s2 in {0 .. 6}, or -1 .. 0
-        const float f1 = __int_as_float((127 + s1) << 23), f2 = __int_as_float((127 + s2) << 23);
+        // e: the exponent of the row's largest value (zeros and subnormals:
+        // -126), down = 2^-e, and qexp = 2^e gives it back to the logits.
+        // 2^-127, 2^-128 and 2^128 are made in two steps.
+        const int e = max(static_cast<int>(big >> 7), 1) - 127;
+        const int e1 = min(e, 126), e2 = e - e1;
+        const float down =
+            __int_as_float((127 - e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 0.5f : 0.25f));
         if (lane == 0)
-          qexp[r] = big >= 0x7F80u ? __int_as_float(0x7FC00000)
-                                   : __int_as_float((127 - s2) << 23) * exp2f(static_cast<float>(-s1));
+          qexp[r] = __int_as_float((127 + e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 2.f : 4.f));
 #pragma unroll
         for (int i = 0; i < HD / 64; ++i) {
-          const float a = __uint_as_float(w[i] << 16) * f1 * f2;
-          const float b = __uint_as_float(w[i] & 0xFFFF0000u) * f1 * f2;
-          const uint16_t hi = pack_e4m3x2(a, b);
-          const uint32_t back = e4m3x2_to_f16x2(hi);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-          const uint16_t lo = pack_e4m3x2((a - f.x) * 16.f, (b - f.y) * 16.f);
-          *reinterpret_cast<uint16_t*>(dst + 2 * (32 * i + lane)) = hi;
-          *reinterpret_cast<uint16_t*>(dst + Ly::Q_PART + 2 * (32 * i + lane)) = lo;
+          const int d = 2 * (32 * i + lane);     // dims d, d + 1 (d even)
+          const int k = d & 15;                  // dim 4a + 2c -> position 2a + 8c
+          const int pos = (d & ~15) + (k >> 2) * 2 + ((k >> 1) & 1) * 8;
+          *reinterpret_cast<uint32_t*>(dst + 2 * pos) =
+              pack_f16x2(__uint_as_float(w[i] << 16) * down,
+                         __uint_as_float(w[i] & 0xFFFF0000u) * down);
         }
       } else {
 #pragma unroll
@@ -508,12 +519,34 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       }
     }
     __syncthreads();
+    // B fragments of Q^T for the 16 dims of step ks: [nb][b0, b1].
+    const uint32_t q_lane = q_sm + ((NB == 2 ? (oct >> 1) * 8 : 0) + r8) * Ly::Q_STRIDE + (oct & 1) * 16;
+    uint32_t qreg[Ly::Q_REGS ? HD / 16 : 1][2 * NB];
+    if constexpr (Ly::Q_REGS) {
+#pragma unroll
+      for (int ks = 0; ks < HD / 16; ++ks) {
+        uint32_t f[4];  // NB = 1: the upper two repeat the lower
+        ldsm4(f, q_lane + ks * 32);
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j) qreg[ks][j] = f[j];
+      }
+    }
+    auto q_frag = [&](int ks, uint32_t (&f)[4]) {
+      if constexpr (Ly::Q_REGS) {
+#pragma unroll
+        for (int j = 0; j < 2 * NB; ++j) f[j] = qreg[ks][j];
+      } else {
+        ldsm4(f, q_lane + ks * 32);
+      }
+    };
     float sl[NB][2], m[NB][2], l[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        sl[nb][j] = Q8 ? p.scale_log2 * qexp[8 * nb + 2 * quad + j] : p.scale_log2;
+        // (never 0: -infinity times it has to stay -infinity)
+        sl[nb][j] = fmaxf(Q8 ? p.scale_log2 * qexp[8 * nb + 2 * quad + j] : p.scale_log2,
+                          1.17549435e-38f);
         m[nb][j] = -INFINITY;
         l[nb][j] = 0.f;
       }
@@ -535,62 +568,54 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       await();
       const uint32_t kb = ring + slot * Ly::SLOT;
       float c[MT][NB][4];
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) c[t][nb][j] = 0.f;
       if constexpr (Q8) {
-        float cl[MT][NB][4];
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) cl[t][nb][j] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < HD / 32; ++ks) {  // 32 dims: chunks 2 ks and 2 ks + 1
-          uint32_t qh[4], ql[4];  // [nb][b0, b1]; NB = 1: the upper two repeat the lower
-          const uint32_t qa = q_sm + ((NB == 2 ? (oct >> 1) * 8 : 0) + r8) * Ly::Q_STRIDE +
-                              (2 * ks + (oct & 1)) * 16;
-          ldsm4(qh, qa);
-          ldsm4(ql, qa + Ly::Q_PART);
+        for (int ks = 0; ks < HD / 16; ks += 2) {  // 32 dims: chunks ks and ks + 1
+          uint32_t qa[4], qb[4];
+          q_frag(ks, qa);
+          q_frag(ks + 1, qb);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
-            uint32_t a[4];
-            const int ch = 2 * ks + (oct >> 1);
-            ldsm4(a, sw128(kb + (ks >> 2) * (WT * 128), t * 16 + (oct & 1) * 8 + r8, ch & 7));
+            uint32_t kr[4], a[4];  // token half, then chunk, by lane octet
+            ldsm4(kr, sw128(kb + (ks >> 3) * (WT * 128), t * 16 + (oct & 1) * 8 + r8,
+                            (ks & 7) + (oct >> 1)));
+            e4m3x4_to_f16x4(kr[0], &a[0], &a[2]);
+            e4m3x4_to_f16x4(kr[1], &a[1], &a[3]);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              mma16832_e4m3(c[t][nb], a, qh[2 * nb], qh[2 * nb + 1]);
-              mma16832_e4m3(cl[t][nb], a, ql[2 * nb], ql[2 * nb + 1]);
+              if (ks == 0)
+                mma16816<true, true>(c[t][nb], a, qa[2 * nb], qa[2 * nb + 1]);
+              else
+                mma16816<true>(c[t][nb], a, qa[2 * nb], qa[2 * nb + 1]);
             }
+            e4m3x4_to_f16x4(kr[2], &a[0], &a[2]);
+            e4m3x4_to_f16x4(kr[3], &a[1], &a[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma16816<true>(c[t][nb], a, qb[2 * nb], qb[2 * nb + 1]);
           }
         }
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[t][nb][j] = fmaf(cl[t][nb][j], 0.0625f, c[t][nb][j]);
       } else {
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {  // 16 dims: chunks 2 ks and 2 ks + 1
           uint32_t qf[4];
-          ldsm4(qf, q_sm + ((NB == 2 ? (oct >> 1) * 8 : 0) + r8) * Ly::Q_STRIDE +
-                        (2 * ks + (oct & 1)) * 16);
+          q_frag(ks, qf);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             uint32_t a[4];
-            const int ch = 2 * ks + (oct >> 1);
-            ldsm4(a, sw128(kb + (ks >> 2) * (WT * 128), t * 16 + (oct & 1) * 8 + r8, ch & 7));
+            ldsm4(a, sw128(kb + (ks >> 2) * (WT * 128), t * 16 + (oct & 1) * 8 + r8,
+                           (2 * ks & 7) + (oct >> 1)));
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816<false>(c[t][nb], a, qf[2 * nb], qf[2 * nb + 1]);
+            for (int nb = 0; nb < NB; ++nb) {
+              if (ks == 0)
+                mma16816<false, true>(c[t][nb], a, qf[2 * nb], qf[2 * nb + 1]);
+              else
+                mma16816<false>(c[t][nb], a, qf[2 * nb], qf[2 * nb + 1]);
+            }
           }
         }
       }
-      // Logits in log2 units, in place; what is no token is -infinity, by value.
+      // c becomes <q, k> times the token's scale; what is no token is -infinity,
+      // by value.  The logits (log2 units) are c sl, taken with m below.
       const float* ksc = reinterpret_cast<const float*>(
           smem + Ly::OFF_SCALE + (warp * NSLOT + slot) * (WT * 4));
 #pragma unroll
@@ -601,7 +626,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) c[t][nb][2 * i + j] *= Q8 ? sl[nb][j] * ks : sl[nb][j];
+            for (int j = 0; j < 2; ++j)
+              if (Q8) c[t][nb][2 * i + j] *= ks;
         }
       bool seen[MT][2];
       if (partial) {
@@ -626,6 +652,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
           for (int t = 1; t < MT; ++t)
             mx[nb][j] = fmaxf(mx[nb][j], fmaxf(c[t][nb][j], c[t][nb][2 + j]));
+          mx[nb][j] *= sl[nb][j];  // sl > 0
         }
       release();
 
@@ -693,8 +720,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float e0 = ex2_approx(c[t][nb][2 * i] - m0);
-            const float e1 = ex2_approx(c[t][nb][2 * i + 1] - m1);
+            const float e0 = ex2_approx(fmaf(c[t][nb][2 * i], sl[nb][0], -m0));
+            const float e1 = ex2_approx(fmaf(c[t][nb][2 * i + 1], sl[nb][1], -m1));
             l[nb][0] += e0;
             l[nb][1] += e1;
             if constexpr (Q8) {
