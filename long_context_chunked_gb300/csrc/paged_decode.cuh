@@ -15,20 +15,23 @@
 //
 // Work split.  The cache is cut into tiles of WT tokens of one row = (sequence,
 // kv head, block of up to 16 q heads).  All tiles of all rows form one list
-// (sequence-major, then kv head), and each CTA takes an equal, contiguous
-// slice of it, whatever the lengths are: one long sequence and many ragged
-// ones are balanced alike, and nothing depends on lengths the host does not
-// know.  A CTA holds at most two rows only in part (its first and its last);
-// it writes their O, m, l to the workspace and a second kernel joins the
-// pieces in order, so results do not depend on timing:
+// (sequence-major, then kv head), and each WARP of the grid takes an equal,
+// contiguous slice of it, whatever the lengths are: one long sequence and many
+// ragged ones are balanced alike, and nothing depends on lengths the host does
+// not know.  A warp works alone: it issues its own TMA copies into its own
+// ring of slots (K and V tiles alternate, the next copy goes out as soon as a
+// slot is read), holds Q, m, l and O (all HD columns) in registers, and turns
+// the accumulators of K Q^T into the operand of V^T P^T there (movmatrix).  A
+// row inside its slice it finishes by itself.  At most its first and its last
+// row are shared with other warps; their (m, l, O) go to the workspace as
+// pieces, which a second kernel joins in list order, so that results do not
+// depend on timing:
 //   m = max m_i,  O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
-//
-// Within a CTA (one per SM) warp w takes the tiles w, w + NW, ... of a row,
-// alone: it issues its own TMA copies into its own ring of slots (K and V
-// tiles alternate, the next copy goes out as soon as a slot is read), holds
-// its own m, l and O (all HD columns), and turns the accumulators of K Q^T
-// into the operand of V^T P^T in registers (movmatrix).  No barrier, no shared
-// P; the warps meet once per row, where their O are summed in warp order.
+// A CTA whose whole slice lies in one row (long contexts) sums its warps' O in
+// shared memory first, in warp order, and leaves one piece.  (With the tiles
+// of a row dealt to the warps of a CTA in turn, the warps met at every row's
+// end: 4 us per row, 85 us for 64 ragged sequences where this takes the time
+// in the table of the documentation.)
 //
 // e4m3 (Q8): K and V are converted to fp16 (exact) in registers; mma.sync on
 // e4m3 operands takes the same conversions and adds fp32 additions (measured
@@ -54,6 +57,7 @@
 
 namespace cpattn {
 
+constexpr int kDecWarps = 8;                     // per CTA, one CTA per SM
 constexpr int kDecRows = 16;                     // most q heads of a row
 constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7
 constexpr float kMinSref = 7.888609052210118e-31f;  // 2^-100: kPScale / s_ref stays finite
@@ -65,38 +69,43 @@ constexpr int kMaxBoxes = 4;                     // page pieces of a tile
 template <int HD, bool Q8, int NB>
 struct DecodeLayout {
   static constexpr int ESZ = Q8 ? 1 : 2;
-  static constexpr int NW = 8;                   // warps
+  static constexpr int NW = kDecWarps;
   static constexpr int THREADS = 32 * NW;
-  static constexpr int SLOT = 8192;
-  static constexpr int NSLOT = 3;                // per warp; 192 KB per CTA
-  static constexpr int WT = SLOT / (HD * ESZ);   // tokens per tile: 16 .. 64
+  // 16 .. 64 tokens per tile, 24 KB of slots per warp and 192 KB per CTA.  At
+  // HD = 256 and NB = 2, O and Q take 192 registers, which leaves room for
+  // tiles of 16 tokens.
+  static constexpr int SLOT = Q8 && HD * NB == 512 ? 4096 : 8192;
+  static constexpr int NSLOT = 24576 / SLOT;
+  static constexpr int WT = SLOT / (HD * ESZ);
   static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : 6);
   static constexpr int BOXW = 128 / ESZ;         // values per 128-byte box row
   static constexpr int NBOX = HD / BOXW;         // column blocks of a tile
   static constexpr int MT = WT / 16;             // m-tiles of K Q^T
   static constexpr int MO = HD / 16;             // m-tiles of V^T P^T
   static constexpr int HEADS = 8 * NB;
-  static constexpr int Q_STRIDE = 2 * HD + 16;   // bytes; rows 16 bytes apart mod 128
-  // Q's fragments stay in registers for a row where they fit beside O.
-  static constexpr bool Q_REGS = HD * NB <= 256;
   static constexpr int CD = 32;                  // columns summed over the warps at a time
   static constexpr int C_STRIDE = CD + 8;
   static constexpr int OFF_SCALE = NW * NSLOT * SLOT;
-  static constexpr int OFF_Q = OFF_SCALE + (Q8 ? NW * NSLOT * WT * 4 : 0);
-  static constexpr int OFF_SUM = OFF_Q + HEADS * Q_STRIDE;  // [NW][HEADS][C_STRIDE]
+  static constexpr int OFF_SUM = OFF_SCALE + (Q8 ? NW * NSLOT * WT * 4 : 0);  // [NW][HEADS][C_STRIDE]
   static constexpr int OFF_ML = OFF_SUM + NW * HEADS * C_STRIDE * 4;  // [NW][HEADS] (m, l)
-  static constexpr int OFF_QEXP = OFF_ML + NW * HEADS * 8;  // [HEADS] 2^e of each Q row
-  static constexpr int OFF_BAR = OFF_QEXP + HEADS * 4;
+  static constexpr int OFF_BAR = OFF_ML + NW * HEADS * 8;
   // [NW][kDecStages] pool rows of the tile's boxes, and the mask of absent pages
   static constexpr int OFF_ROWS = OFF_BAR + NW * NSLOT * 8;
   static constexpr int OFF_BAD = OFF_ROWS + NW * kDecStages * kMaxBoxes * 4;
-  static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;
-  static constexpr int SMEM_BYTES = OFF_MISC + 96 + NW * 8;
-  static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 8 == 0 && OFF_SCALE % 128 == 0 && OFF_Q % 16 == 0 &&
-                    OFF_SUM % 16 == 0,
+  static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;  // scan, spots, abort flag
+  static constexpr int SMEM_BYTES = OFF_MISC + NW * 8 + NW * 16 + 16;
+  static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0 && OFF_SUM % 16 == 0,
                 "shared memory alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(HEADS * (CD / 2) <= THREADS, "a thread per column pair");
   static_assert(WT / 16 <= kMaxBoxes && NSLOT / 2 + 2 <= kDecStages, "page table of a warp");
+};
+
+// A row that several warps share: list indices [first, end) of its tiles, the
+// list's length and the warps that share it.  end == 0: there is none.
+struct DecodeCut {
+  long long first, end, total;
+  int b, rr, active, pad;
 };
 
 struct PagedDecodeParams {
@@ -107,13 +116,16 @@ struct PagedDecodeParams {
   const __nv_bfloat16* q;     // [num_seqs][NQ][HD]
   __nv_bfloat16* out;
   float* lse;                 // or null
-  float* ws_o;                // [2 * CTAs][16][HD] O of a CTA's first / last row
-  float2* ws_ml;              // [2 * CTAs][16] its m and l
-  int4* ws_desc;              // [CTAs] (b, kv head * hblocks + block, pieces, 0)
+  float* ws_o;                // [2 * warps][16][HD] O of a warp's first / last row
+  float2* ws_ml;              // [2 * warps][16] its m and l
+  // The cut row that begins in a warp's slice; by row, where there are no more
+  // rows than CTAs, else by warp.
+  DecodeCut* ws_cut;          // [warps]
   int* status;
   unsigned long long timeout_ns;
   int pool_rows;              // num_pages * NKV * page_size
   int debug_flags;
+  int by_row;                 // ws_cut is indexed by row
   int num_ctas;               // CTAs of the decode kernel
   int num_seqs, nq, group, hblocks;  // hblocks: blocks of 16 q heads per kv head
   float scale_log2;
@@ -203,7 +215,16 @@ __device__ __forceinline__ int decode_len(const PagedDecodeParams& p, int b) {
   return static_cast<int>(max(0LL, min(static_cast<long long>(__ldg(p.lens + b)), room)));
 }
 
-// A CTA's way through its slice [s, s1) of the tile list, one row segment at a
+// Slices: warp w of the `active` ones that share the list takes the tiles
+// [start(w), start(w + 1)); tile i belongs to warp owner(i).
+__device__ __forceinline__ long long slice_start(long long total, int active, int w) {
+  return total * w / active;
+}
+__device__ __forceinline__ int slice_owner(long long total, int active, long long i) {
+  return static_cast<int>(((i + 1) * active - 1) / total);
+}
+
+// A warp's way through its slice [s, s1) of the tile list, one row segment at a
 // time: tiles tile0 .. tile0 + tiles - 1 of row rr = kv head * hblocks + head
 // block of sequence b.  tiles == 0: the slice is done.
 struct DecodeWalk {
@@ -235,13 +256,11 @@ struct DecodeWalk {
   }
 };
 
-// Whole block: tiles over all rows, and this CTA's slice of them, in *spot
-// (shared memory; spot->s >= spot->s1: none).  `active` CTAs share the list,
-// at least one tile per warp each where there are that many.
+// Whole block: the list's length, the warps that share it (one tile each at
+// least), and where each warp's slice begins: spot[w] = (b, rr, tile0).
 template <int WT, int NW>
-__device__ __forceinline__ long long decode_slice(const PagedDecodeParams& p, int rows_per_seq,
-                                                  long long* warp_sum, int* active,
-                                                  DecodeWalk* spot) {
+__device__ __forceinline__ long long decode_slices(const PagedDecodeParams& p, int rows_per_seq,
+                                                   long long* warp_sum, int4* spot, int* active) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.num_seqs + 32 * NW - 1) / (32 * NW);
   const int b0 = min(p.num_seqs, tid * per), b1 = min(p.num_seqs, b0 + per);
@@ -267,27 +286,26 @@ __device__ __forceinline__ long long decode_slice(const PagedDecodeParams& p, in
     total += warp_sum[w];
   }
   total *= rows_per_seq;
-  *active = static_cast<int>(
-      min((total + NW - 1) / NW, static_cast<long long>(gridDim.x)));
-  const int c = blockIdx.x;
-  const long long s0 = c < *active ? total * c / *active : 0;
-  const long long s1 = c < *active ? total * (c + 1) / *active : 0;
-  if (tid == 0) {
-    spot->s = s0;
-    spot->s1 = s1;
-  }
+  *active = static_cast<int>(min(total, static_cast<long long>(gridDim.x) * NW));
   long long at = (base + inc - sum) * rows_per_seq;  // list index of sequence b0's first tile
-  if (s0 < s1 && at <= s0 && s0 < at + sum * rows_per_seq) {
-    for (int b = b0; b < b1; ++b) {
-      const int nt = (decode_len(p, b) + WT - 1) / WT;
-      const long long n = static_cast<long long>(nt) * rows_per_seq;
-      if (s0 < at + n) {
-        spot->b = b;
-        spot->rr = static_cast<int>((s0 - at) / nt);
-        spot->tile0 = static_cast<int>((s0 - at) % nt);
-        break;
+  const long long end = at + sum * rows_per_seq;
+  if (sum > 0) {
+#pragma unroll 1
+    for (int w = 0; w < NW; ++w) {
+      const int worker = blockIdx.x * NW + w;
+      if (worker >= *active) break;
+      const long long s0 = slice_start(total, *active, worker);
+      if (s0 < at || s0 >= end) continue;
+      long long a = at;
+      for (int b = b0; b < b1; ++b) {
+        const int nt = (decode_len(p, b) + WT - 1) / WT;
+        const long long n = static_cast<long long>(nt) * rows_per_seq;
+        if (s0 < a + n) {
+          spot[w] = make_int4(b, static_cast<int>((s0 - a) / nt), static_cast<int>((s0 - a) % nt), 0);
+          break;
+        }
+        a += n;
       }
-      at += n;
     }
   }
   __syncthreads();
@@ -308,15 +326,16 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   // Swizzled copies need a 1024-byte aligned base (which the launch gives).
   if ((sbase & 1023u) != 0) {
     if (tid == 0 && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusLayout);
-    if (tid == 0) p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    // Nothing to join (by row: no more rows than CTAs).
+    if (p.by_row ? tid == 0 : lane == 0) p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * NW + warp].end = 0;
     return;
   }
   const uint32_t ring = sbase + warp * (NSLOT * Ly::SLOT);
   auto full = [&](int s) {
     return sbase + Ly::OFF_BAR + 8u * static_cast<uint32_t>(warp * NSLOT + s);
   };
-  DecodeWalk* spot = reinterpret_cast<DecodeWalk*>(smem + Ly::OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::OFF_MISC + 64);
+  int4* spots = reinterpret_cast<int4*>(smem + Ly::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::OFF_MISC + NW * 24);
   if (lane == 0) {
     // (Q8: every lane's copies of the scales arrive too.)
     for (int s = 0; s < NSLOT; ++s) mbar_init(full(s), Q8 ? 33 : 1);
@@ -324,13 +343,30 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     fence_mbar_init();
   }
   const int rows_per_seq = p.pool.nkv * p.hblocks;
+  const int worker = blockIdx.x * NW + warp;
   int active;
-  const long long total = decode_slice<WT, NW>(
-      p, rows_per_seq, reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 96), &active, spot);
+  const long long total = decode_slices<WT, NW>(
+      p, rows_per_seq, reinterpret_cast<long long*>(smem + Ly::OFF_MISC + NW * 16), spots, &active);
   const BoundedWait wait{abort_flag, p.status, p.timeout_ns, nullptr, 0u, 0};
 
-  DecodeWalk at = *spot;
-  if (at.s < at.s1) at.template enter<WT>(p);
+  DecodeWalk at;
+  at.s = at.s1 = 0;
+  at.b = at.rr = at.tile0 = at.tiles = at.nt = at.n = 0;
+  if (worker < active) {
+    at.s = slice_start(total, active, worker);
+    at.s1 = slice_start(total, active, worker + 1);
+    at.b = spots[warp].x;
+    at.rr = spots[warp].y;
+    at.tile0 = spots[warp].z;
+    at.template enter<WT>(p);
+  }
+  // Whether the CTA's whole slice lies in one row (and all its warps have one).
+  bool uniform = false;
+  if (blockIdx.x * NW + NW <= active) {
+    const int nt0 = (decode_len(p, spots[0].x) + WT - 1) / WT;
+    uniform = spots[0].z + slice_start(total, active, blockIdx.x * NW + NW) -
+                  slice_start(total, active, blockIdx.x * NW) <= nt0;
+  }
 
   // ------------------------------------------- this warp's stream of copies
   // Copy u of the warp is K (u even) or V (u odd) of its tile u / 2, in slot
@@ -345,16 +381,16 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   volatile uint32_t* my_bad =
       reinterpret_cast<volatile uint32_t*>(smem + Ly::OFF_BAD) + warp * kDecStages;
   DecodeWalk ahead = at;  // the tile whose K goes out next
-  int aj = warp;          // its index in ahead's segment
+  int aj = 0;             // its index in ahead's segment
   int issued = 0, slot_out = 0;
   int next_t = -1, next_id = 0;  // lane i: first token of its box i (-1: none), and its page
   int next_g = 0;
   bool more = at.s < at.s1;
   auto look_up = [&]() {
-    // To the segment that holds tile aj, or to the end of the slice.
-    while (more && aj >= ahead.tiles) {
+    // To the next segment, or to the end of the slice.
+    if (more && aj >= ahead.tiles) {
       ahead.template next<WT>(p, rows_per_seq);
-      aj = warp;
+      aj = 0;
       more = ahead.tiles > 0;
     }
     next_t = -1;
@@ -415,7 +451,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     } else if (more) {
       take_rows(stage);
       send(&p.tm_k, p.pool.k_scales, stage);
-      aj += NW;
+      ++aj;
       look_up();
     }
   };
@@ -425,7 +461,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     take_rows(0);
     slot_out = 1;
     issued = 1;
-    aj += NW;
+    ++aj;
     look_up();
   }
 #pragma unroll 1
@@ -440,19 +476,14 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     if (p.lse != nullptr)
       for (int h = tid; h < p.nq; h += Ly::THREADS)
         p.lse[static_cast<long long>(b) * p.nq + h] = -INFINITY;
+    if (p.by_row)
+      for (int r = tid; r < rows_per_seq; r += Ly::THREADS) p.ws_cut[b * rows_per_seq + r].end = 0;
   }
-  if (at.s >= at.s1) {
-    if (tid == 0) p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-    return;
-  }
+  if (!p.by_row && lane == 0) p.ws_cut[worker].end = 0;
 
   // Accumulator fragments (16 x 8): rows r0 and r0 + 8 (tokens or columns of
   // V), columns 2 quad and 2 quad + 1 (q heads of the block).
   const int quad = lane & 3, r0 = lane >> 2, r8 = lane & 7, oct = lane >> 3;
-  float2* mls = reinterpret_cast<float2*>(smem + Ly::OFF_ML);
-  float* qexp = reinterpret_cast<float*>(smem + Ly::OFF_QEXP);
-  float* summed = reinterpret_cast<float*>(smem + Ly::OFF_SUM);
-  const uint32_t q_sm = sbase + Ly::OFF_Q;
   int slot = 0, used = 0;  // the next slot to read, and copies read so far
   uint32_t phase = 0;
   // A warp whose wait expired (ok = false) waits for no more copies: it runs
@@ -477,76 +508,63 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     const int g = at.rr / p.hblocks, h0 = g * p.group + (at.rr % p.hblocks) * kDecRows;
     const int heads = min(HEADS, (g + 1) * p.group - h0);
 
-    // Q of the row into shared memory, a head per warp and turn: bf16 as it
-    // is, or (Q8) fp16 scaled by a power of two, with the dims of each 16-block
-    // in the order in which the e4m3 K fragments come out of ldmatrix.
-    __syncthreads();  // the last row's Q and sums are no longer read
+    // B fragments of Q^T, this lane's head (r0 of each block of 8): bf16 as it
+    // is, dims 16 ks + 2 quad + {0, 1} and + 8; or (Q8) fp16 scaled by a power
+    // of two, dims 16 ks + 4 quad + {0 .. 3}, the order in which the e4m3 K
+    // fragments come out of ldmatrix.
+    uint32_t q[HD / 16][2 * NB];
+    float qexp[NB];
 #pragma unroll
-    for (int r = warp; r < HEADS; r += NW) {
-      const __nv_bfloat16* src = p.q + (static_cast<long long>(at.b) * p.nq + h0 + r) * HD;
-      uint32_t w[HD / 64];
+    for (int nb = 0; nb < NB; ++nb) {
+      const bool here = 8 * nb + r0 < heads;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          p.q + (static_cast<long long>(at.b) * p.nq + h0 + (here ? 8 * nb + r0 : 0)) * HD);
       uint32_t big = 0;
 #pragma unroll
-      for (int i = 0; i < HD / 64; ++i) {
-        w[i] = r < heads ? __ldg(reinterpret_cast<const uint32_t*>(src) + 32 * i + lane) : 0u;
-        big = max(big, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+      for (int ks = 0; ks < HD / 16; ++ks) {
+        uint2 w;
+        if constexpr (Q8) {
+          w = __ldg(reinterpret_cast<const uint2*>(src) + 4 * ks + quad);
+        } else {
+          w.x = __ldg(src + 8 * ks + quad);
+          w.y = __ldg(src + 8 * ks + 4 + quad);
+        }
+        if (!here) w = make_uint2(0u, 0u);
+        q[ks][2 * nb] = w.x;
+        q[ks][2 * nb + 1] = w.y;
+        if (Q8) big = __vmaxu2(big, __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu));
       }
-      uint8_t* dst = smem + Ly::OFF_Q + r * Ly::Q_STRIDE;
+      qexp[nb] = 1.f;
       if constexpr (Q8) {
-        big = __reduce_max_sync(0xFFFFFFFFu, big);
-        // e: the exponent of the row's largest value (zeros and subnormals:
+        big = max(big & 0xFFFFu, big >> 16);
+        big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+        big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+        // e: the exponent of the head's largest value (zeros and subnormals:
         // -126), down = 2^-e, and qexp = 2^e gives it back to the logits.
         // 2^-127, 2^-128 and 2^128 are made in two steps.
         const int e = max(static_cast<int>(big >> 7), 1) - 127;
         const int e1 = min(e, 126), e2 = e - e1;
         const float down =
             __int_as_float((127 - e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 0.5f : 0.25f));
-        if (lane == 0)
-          qexp[r] = __int_as_float((127 + e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 2.f : 4.f));
+        qexp[nb] = __int_as_float((127 + e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 2.f : 4.f));
 #pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {
-          const int d = 2 * (32 * i + lane);     // dims d, d + 1 (d even)
-          const int k = d & 15;                  // dim 4a + 2c -> position 2a + 8c
-          const int pos = (d & ~15) + (k >> 2) * 2 + ((k >> 1) & 1) * 8;
-          *reinterpret_cast<uint32_t*>(dst + 2 * pos) =
-              pack_f16x2(__uint_as_float(w[i] << 16) * down,
-                         __uint_as_float(w[i] & 0xFFFF0000u) * down);
-        }
-      } else {
+        for (int ks = 0; ks < HD / 16; ++ks)
 #pragma unroll
-        for (int i = 0; i < HD / 64; ++i)
-          *reinterpret_cast<uint32_t*>(dst + 4 * (32 * i + lane)) = w[i];
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w = q[ks][2 * nb + j];
+            q[ks][2 * nb + j] = pack_f16x2(__uint_as_float(w << 16) * down,
+                                           __uint_as_float(w & 0xFFFF0000u) * down);
+          }
       }
     }
-    __syncthreads();
-    // B fragments of Q^T for the 16 dims of step ks: [nb][b0, b1].
-    const uint32_t q_lane = q_sm + ((NB == 2 ? (oct >> 1) * 8 : 0) + r8) * Ly::Q_STRIDE + (oct & 1) * 16;
-    uint32_t qreg[Ly::Q_REGS ? HD / 16 : 1][2 * NB];
-    if constexpr (Ly::Q_REGS) {
-#pragma unroll
-      for (int ks = 0; ks < HD / 16; ++ks) {
-        uint32_t f[4];  // NB = 1: the upper two repeat the lower
-        ldsm4(f, q_lane + ks * 32);
-#pragma unroll
-        for (int j = 0; j < 2 * NB; ++j) qreg[ks][j] = f[j];
-      }
-    }
-    auto q_frag = [&](int ks, uint32_t (&f)[4]) {
-      if constexpr (Ly::Q_REGS) {
-#pragma unroll
-        for (int j = 0; j < 2 * NB; ++j) f[j] = qreg[ks][j];
-      } else {
-        ldsm4(f, q_lane + ks * 32);
-      }
-    };
     float sl[NB][2], m[NB][2], l[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        // (never 0: -infinity times it has to stay -infinity)
-        sl[nb][j] = fmaxf(Q8 ? p.scale_log2 * qexp[8 * nb + 2 * quad + j] : p.scale_log2,
-                          1.17549435e-38f);
+        // of head 2 quad + j (never 0: -infinity times it has to stay -infinity)
+        const float qe = __shfl_sync(0xFFFFFFFFu, qexp[nb], 4 * (2 * quad + j));
+        sl[nb][j] = fmaxf(p.scale_log2 * qe, 1.17549435e-38f);
         m[nb][j] = -INFINITY;
         l[nb][j] = 0.f;
       }
@@ -559,7 +577,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][nb][j] = 0.f;
 
-    for (int v = warp; v < at.tiles; v += NW) {
+    for (int v = 0; v < at.tiles; ++v) {
       const int valid = min(WT, at.n - (at.tile0 + v) * WT);  // tokens of the tile
       const uint32_t bad = my_bad[(used >> 1) & (kDecStages - 1)];
       const bool partial = valid < WT || bad != 0u;
@@ -571,9 +589,6 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       if constexpr (Q8) {
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ks += 2) {  // 32 dims: chunks ks and ks + 1
-          uint32_t qa[4], qb[4];
-          q_frag(ks, qa);
-          q_frag(ks + 1, qb);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             uint32_t kr[4], a[4];  // token half, then chunk, by lane octet
@@ -584,21 +599,19 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               if (ks == 0)
-                mma16816<true, true>(c[t][nb], a, qa[2 * nb], qa[2 * nb + 1]);
+                mma16816<true, true>(c[t][nb], a, q[ks][2 * nb], q[ks][2 * nb + 1]);
               else
-                mma16816<true>(c[t][nb], a, qa[2 * nb], qa[2 * nb + 1]);
+                mma16816<true>(c[t][nb], a, q[ks][2 * nb], q[ks][2 * nb + 1]);
             }
             e4m3x4_to_f16x4(kr[2], &a[0], &a[2]);
             e4m3x4_to_f16x4(kr[3], &a[1], &a[3]);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816<true>(c[t][nb], a, qb[2 * nb], qb[2 * nb + 1]);
+            for (int nb = 0; nb < NB; ++nb) mma16816<true>(c[t][nb], a, q[ks + 1][2 * nb], q[ks + 1][2 * nb + 1]);
           }
         }
       } else {
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {  // 16 dims: chunks 2 ks and 2 ks + 1
-          uint32_t qf[4];
-          q_frag(ks, qf);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             uint32_t a[4];
@@ -607,9 +620,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               if (ks == 0)
-                mma16816<false, true>(c[t][nb], a, qf[2 * nb], qf[2 * nb + 1]);
+                mma16816<false, true>(c[t][nb], a, q[ks][2 * nb], q[ks][2 * nb + 1]);
               else
-                mma16816<false>(c[t][nb], a, qf[2 * nb], qf[2 * nb + 1]);
+                mma16816<false>(c[t][nb], a, q[ks][2 * nb], q[ks][2 * nb + 1]);
             }
           }
         }
@@ -790,94 +803,153 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       release();
     }
 
-    // ---- the end of the row (or of this CTA's piece of it): the warps' m and
-    // l, then their O, 32 columns at a time, summed in warp order.
+    // ---- the end of the row, or of this warp's part of it
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][j], d);
-        if (r0 == 0) mls[warp * HEADS + 8 * nb + 2 * quad + j] = make_float2(m[nb][j], l[nb][j]);
+    const long long row0 = at.s - at.tile0;  // list index of the row's first tile
+    const bool begins = at.tile0 == 0, ends = at.tile0 + at.tiles == at.nt;
+    if (begins && lane == 0) {
+      // The warp in whose slice a row begins says who shares it.
+      const bool cut = !(ends || (uniform && row0 + at.nt <= slice_start(total, active,
+                                                                         (blockIdx.x + 1) * NW)));
+      DecodeCut d;
+      d.first = row0;
+      d.end = cut ? row0 + at.nt : 0;
+      d.total = total;
+      d.b = at.b;
+      d.rr = at.rr;
+      d.active = active;
+      d.pad = 0;
+      if (p.by_row)
+        p.ws_cut[at.b * rows_per_seq + at.rr] = d;
+      else if (cut)
+        p.ws_cut[worker] = d;
+    }
+    const float oscale = Q8 ? sref * (1.f / kPScale) : 1.f;
+    if (uniform) {
+      // One piece for the CTA: the warps' m and l, then their O, 32 columns at
+      // a time, summed in warp order.  (The only row of every warp here.)
+      float2* mls = reinterpret_cast<float2*>(smem + Ly::OFF_ML);
+      float* summed = reinterpret_cast<float*>(smem + Ly::OFF_SUM);
+      if (r0 == 0) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            mls[warp * HEADS + 8 * nb + 2 * quad + j] = make_float2(m[nb][j], l[nb][j]);
       }
-    __syncthreads();
-    const bool whole = at.tile0 == 0 && at.tiles == at.nt;
-    const int piece = 2 * blockIdx.x + (at.tile0 == 0 ? 1 : 0);
-    float f[NB][2];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = 8 * nb + 2 * quad + j;
-        float mm = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mls[w * HEADS + r].x);
-        const float mref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float2 ml = mls[w * HEADS + r];
-          sum = fmaf(ex2_approx(ml.x - mref), ml.y, sum);
-        }
-        f[nb][j] = ex2_approx(m[nb][j] - mref) * (Q8 ? sref * (1.f / kPScale) : 1.f);
-        // sum = 0: every page of the row was absent.
-        if (whole) f[nb][j] = sum == 0.f ? 0.f : f[nb][j] / sum;
-        if (warp == 0 && r0 == 0 && r < heads) {
-          const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
-          if (!whole)
-            p.ws_ml[piece * kDecRows + r] = make_float2(mm, sum);
-          else if (p.lse != nullptr)
-            p.lse[orow] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.69314718055994531f;
-        }
-      }
-#pragma unroll
-    for (int cc = 0; cc < HD / Ly::CD; ++cc) {
-      if (cc > 0) __syncthreads();
+      __syncthreads();
+      const long long c0 = slice_start(total, active, blockIdx.x * NW);
+      const bool whole = spots[0].z == 0 &&
+                         c0 + at.nt == slice_start(total, active, (blockIdx.x + 1) * NW);
+      const long long piece = 2LL * blockIdx.x * NW;
+      float f[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float* dst = summed + (warp * HEADS + 8 * nb + 2 * quad + j) * Ly::C_STRIDE;
+          const int r = 8 * nb + 2 * quad + j;
+          float mm = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int k = 0; k < Ly::CD / 16; ++k) {
-            const float* a = o[cc * (Ly::CD / 16) + k][nb];
-            if constexpr (Q8) {  // rows r0, r0 + 8 of the m-tile: columns 2 r0 and 2 r0 + 1
-              *reinterpret_cast<float2*>(dst + 16 * k + 2 * r0) =
-                  make_float2(a[j] * f[nb][j], a[2 + j] * f[nb][j]);
-            } else {
-              dst[16 * k + r0] = a[j] * f[nb][j];
-              dst[16 * k + 8 + r0] = a[2 + j] * f[nb][j];
-            }
+          for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mls[w * HEADS + r].x);
+          const float mref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const float2 ml = mls[w * HEADS + r];
+            sum = fmaf(ex2_approx(ml.x - mref), ml.y, sum);
+          }
+          f[nb][j] = ex2_approx(m[nb][j] - mref) * oscale;
+          // sum = 0: every page of the row was absent.
+          if (whole) f[nb][j] = sum == 0.f ? 0.f : f[nb][j] / sum;
+          if (warp == 0 && r0 == 0 && r < heads) {
+            const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
+            if (!whole)
+              p.ws_ml[piece * kDecRows + r] = make_float2(mm, sum);
+            else if (p.lse != nullptr)
+              p.lse[orow] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.69314718055994531f;
           }
         }
-      __syncthreads();
-      const int r = tid / (Ly::CD / 2), d = 2 * (tid % (Ly::CD / 2));  // column pairs
-      if (r < heads) {
-        float2 y = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float2 z =
-              *reinterpret_cast<const float2*>(summed + (w * HEADS + r) * Ly::C_STRIDE + d);
-          y.x += z.x;
-          y.y += z.y;
+      for (int cc = 0; cc < HD / Ly::CD; ++cc) {
+        if (cc > 0) __syncthreads();
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float* dst = summed + (warp * HEADS + 8 * nb + 2 * quad + j) * Ly::C_STRIDE;
+#pragma unroll
+            for (int k = 0; k < Ly::CD / 16; ++k) {
+              const float* a = o[cc * (Ly::CD / 16) + k][nb];
+              if constexpr (Q8) {  // rows r0, r0 + 8 of the m-tile: columns 2 r0 and 2 r0 + 1
+                *reinterpret_cast<float2*>(dst + 16 * k + 2 * r0) =
+                    make_float2(a[j] * f[nb][j], a[2 + j] * f[nb][j]);
+              } else {
+                dst[16 * k + r0] = a[j] * f[nb][j];
+                dst[16 * k + 8 + r0] = a[2 + j] * f[nb][j];
+              }
+            }
+          }
+        __syncthreads();
+        const int r = tid / (Ly::CD / 2), d = 2 * (tid % (Ly::CD / 2));  // column pairs
+        if (r < heads) {
+          float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const float2 z =
+                *reinterpret_cast<const float2*>(summed + (w * HEADS + r) * Ly::C_STRIDE + d);
+            y.x += z.x;
+            y.y += z.y;
+          }
+          if (whole)
+            *reinterpret_cast<uint32_t*>(
+                p.out + (static_cast<long long>(at.b) * p.nq + h0 + r) * HD + cc * Ly::CD + d) =
+                pack_bf16x2(y.x, y.y);
+          else
+            *reinterpret_cast<float2*>(p.ws_o + (piece * kDecRows + r) * HD + cc * Ly::CD + d) = y;
         }
-        if (whole)
-          *reinterpret_cast<uint32_t*>(
-              p.out + (static_cast<long long>(at.b) * p.nq + h0 + r) * HD + cc * Ly::CD + d) =
-              pack_bf16x2(y.x, y.y);
-        else
-          *reinterpret_cast<float2*>(
-              p.ws_o + (static_cast<long long>(piece) * kDecRows + r) * HD + cc * Ly::CD + d) = y;
       }
-    }
-    if (at.s + at.tiles >= at.s1 && tid == 0) {
-      // The CTA whose slice begins a row that others continue describes it.
-      int4 d = make_int4(0, 0, 0, 0);
-      if (at.tile0 == 0 && at.tiles < at.nt) {
-        const long long last = at.s + at.nt - 1;  // list index of the row's last tile
-        const long long cta = ((last + 1) * active - 1) / total;
-        d = make_int4(at.b, at.rr, static_cast<int>(cta) - static_cast<int>(blockIdx.x) + 1, 0);
-      }
-      p.ws_desc[blockIdx.x] = d;
+    } else {
+      // This warp's own row, or its piece of one: straight from the registers.
+      const bool whole = begins && ends;
+      const long long piece = 2LL * worker + (begins ? 1 : 0);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * nb + 2 * quad + j;
+          const float sum = l[nb][j];
+          const float f = whole ? (sum == 0.f ? 0.f : oscale / sum) : oscale;
+          const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
+          if (r0 == 0 && r < heads) {
+            if (!whole)
+              p.ws_ml[piece * kDecRows + r] = make_float2(m[nb][j], sum);
+            else if (p.lse != nullptr)
+              p.lse[orow] = sum == 0.f ? -INFINITY
+                                       : (m[nb][j] + __log2f(sum)) * 0.69314718055994531f;
+          }
+#pragma unroll
+          for (int i = 0; i < MO; ++i) {
+            float2 y = make_float2(o[i][nb][j] * f, o[i][nb][2 + j] * f);
+            int d = 16 * i + 2 * r0;
+            if constexpr (!Q8) {
+              // Rows r0 and r0 + 8 are columns r0 and r0 + 8: a neighbour's
+              // value makes a pair.
+              const bool odd = (r0 & 1) != 0;
+              const float z = __shfl_xor_sync(0xFFFFFFFFu, odd ? y.x : y.y, 4);
+              y = odd ? make_float2(z, y.y) : make_float2(y.x, z);
+              d = 16 * i + (odd ? r0 + 7 : r0);
+            }
+            if (r >= heads) continue;
+            if (whole)
+              *reinterpret_cast<uint32_t*>(p.out + orow * HD + d) = pack_bf16x2(y.x, y.y);
+            else
+              *reinterpret_cast<float2*>(p.ws_o + (piece * kDecRows + r) * HD + d) = y;
+          }
+        }
     }
   }
   if (!ok) {
@@ -893,76 +965,83 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 }
 
 // Joins the pieces of the rows that were cut.  Block (x, y): row x of the
-// batch when there are at most as many rows as CTAs, found by a search of
-// their descriptions, else the row that CTA x began; q heads y, y + gridDim.y,
-// ... of it.  Most blocks of a large batch find nothing to do.  A programmatic
-// dependent of the decode kernel.  Thread (j, y): output elements 4j .. 4j+3
-// over the pieces y, y + GROUPS, ..., summed over y in shared memory: a long
-// row has a piece from every CTA, and their loads should all be in flight.
+// batch, or (where there are more rows than CTAs) the row that begins in warp
+// x's slice; q heads y, y + gridDim.y, ... of it.  Most blocks of a large batch
+// find nothing to do.  A programmatic dependent of the decode kernel.  Thread
+// (j, y): output elements 4j .. 4j+3 over the pieces y, y + GROUPS, ..., summed
+// over y in shared memory.  Each warp reads all pieces' (m, l) itself, while
+// its first loads of O are in flight: two round trips to L2 in all.
 constexpr int kJoinThreads = 512;
-constexpr int kJoinMaxPieces = 1024;  // checked by the host against the CTAs of a launch
+constexpr int kJoinBatch = 4;  // loads of O in flight per thread
 
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads)
     paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
   constexpr int GROUPS = kJoinThreads / (HD / 4);
   __shared__ float4 part[GROUPS][HD / 4];
-  __shared__ float weight[kJoinMaxPieces];
-  __shared__ float stats[2];
-  __shared__ int owner;
-  const int tid = threadIdx.x, j = tid % (HD / 4), y = tid / (HD / 4);
-  const int rows_per_seq = p.pool.nkv * p.hblocks;
-  const bool by_row = static_cast<long long>(p.num_seqs) * rows_per_seq <= p.num_ctas;
-  if (tid == 0) owner = by_row ? -1 : static_cast<int>(blockIdx.x);
-  __syncthreads();
+  const int tid = threadIdx.x, lane = tid & 31, j = tid % (HD / 4), y = tid / (HD / 4);
   griddep_wait();
-  if (by_row) {
-    for (int c = tid; c < p.num_ctas; c += kJoinThreads) {
-      const int4 d = p.ws_desc[c];
-      if (d.z > 0 && d.x * rows_per_seq + d.y == static_cast<int>(blockIdx.x)) owner = c;
-    }
-    __syncthreads();
-    if (owner < 0) return;
-  }
-  const int cta = owner;
-  const int4 d = p.ws_desc[cta];
-  const int pieces = d.z;
-  if (pieces == 0) return;
-  const int g = d.y / p.hblocks, h0 = g * p.group + (d.y % p.hblocks) * kDecRows;
+  const DecodeCut c = p.ws_cut[blockIdx.x];
+  if (c.end == 0) return;
+  const int g = c.rr / p.hblocks, h0 = g * p.group + (c.rr % p.hblocks) * kDecRows;
   const int heads = min(kDecRows, (g + 1) * p.group - h0);
-  // Piece 0 is CTA cta's last row, the others the first rows of those behind it.
-  auto slot = [&](int i) { return 2 * (cta + i) + (i == 0 ? 1 : 0); };
+  // The pieces, in list order: of the row's first CTA, one per warp from the
+  // row's first warp on (one in all if the CTA lies in the row altogether);
+  // one of each CTA between; and of its last CTA again one per warp, or one.
+  const int w0 = slice_owner(c.total, c.active, c.first), w1 = slice_owner(c.total, c.active, c.end - 1);
+  const int cta0 = w0 / kDecWarps, cta1 = w1 / kDecWarps;
+  const bool one0 = w0 % kDecWarps == 0 && slice_start(c.total, c.active, w0) == c.first;
+  const bool one1 = w1 % kDecWarps == kDecWarps - 1 && slice_start(c.total, c.active, w1 + 1) == c.end;
+  int head_n, tail_n;  // pieces of the first and the last CTA (apart from the first)
+  if (cta0 == cta1) {
+    head_n = w1 - w0 + 1;
+    tail_n = 0;
+  } else {
+    head_n = one0 ? 1 : kDecWarps - w0 % kDecWarps;
+    tail_n = one1 ? 1 : w1 % kDecWarps + 1;
+  }
+  const int mid_n = max(cta1 - cta0 - 1, 0), pieces = head_n + mid_n + tail_n;
+  const bool first_own = !(cta0 != cta1 && one0);  // the first piece is a warp's last row
+  auto slot = [&](int i) -> long long {
+    if (i < head_n) return 2LL * (w0 + i) + (i == 0 && first_own ? 1 : 0);
+    i -= head_n;
+    if (i < mid_n) return 2LL * (cta0 + 1 + i) * kDecWarps;
+    return 2LL * (cta1 * kDecWarps + i - mid_n);
+  };
   for (int r = blockIdx.y; r < heads; r += gridDim.y) {
-    if (tid < 32) {
-      float m = -INFINITY, l = 0.f;
-      for (int i = tid; i < pieces; i += 32) m = fmaxf(m, p.ws_ml[slot(i) * kDecRows + r].x);
+    const float* o_at = p.ws_o + static_cast<long long>(r) * HD + 4 * j;
+    const float2* ml_at = p.ws_ml + r;
+    auto load_o = [&](int i) {
+      return *reinterpret_cast<const float4*>(o_at + slot(i) * (kDecRows * HD));
+    };
+    float4 o[kJoinBatch];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const float mref = m == -INFINITY ? 0.f : m;
-      for (int i = tid; i < pieces; i += 32) {
-        const float2 ml = p.ws_ml[slot(i) * kDecRows + r];
-        const float w = ex2_approx(ml.x - mref);
-        weight[i] = w;
-        l = fmaf(w, ml.y, l);
-      }
+    for (int k = 0; k < kJoinBatch; ++k)
+      if (y + k * GROUPS < pieces) o[k] = load_o(y + k * GROUPS);
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml_at[slot(i) * kDecRows].x);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-      if (tid == 0) {
-        stats[0] = m;
-        stats[1] = l;
-      }
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    const float mref = m == -INFINITY ? 0.f : m;
+    for (int i = lane; i < pieces; i += 32) {
+      const float2 ml = ml_at[slot(i) * kDecRows];
+      l = fmaf(ex2_approx(ml.x - mref), ml.y, l);
     }
-    __syncthreads();
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = y; i < pieces; i += GROUPS) {
-      const float4 o = *reinterpret_cast<const float4*>(
-          p.ws_o + (static_cast<long long>(slot(i)) * kDecRows + r) * HD + 4 * j);
-      const float w = weight[i];
-      acc.x = fmaf(w, o.x, acc.x);
-      acc.y = fmaf(w, o.y, acc.y);
-      acc.z = fmaf(w, o.z, acc.z);
-      acc.w = fmaf(w, o.w, acc.w);
+    for (int i = y; i < pieces; i += kJoinBatch * GROUPS) {
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const int ii = i + k * GROUPS;
+        if (ii >= pieces) break;
+        const float w = ex2_approx(ml_at[slot(ii) * kDecRows].x - mref);
+        acc.x = fmaf(w, o[k].x, acc.x);
+        acc.y = fmaf(w, o[k].y, acc.y);
+        acc.z = fmaf(w, o[k].z, acc.z);
+        acc.w = fmaf(w, o[k].w, acc.w);
+        if (ii + kJoinBatch * GROUPS < pieces) o[k] = load_o(ii + kJoinBatch * GROUPS);
+      }
     }
     part[y][j] = acc;
     __syncthreads();
@@ -974,15 +1053,14 @@ __global__ void __launch_bounds__(kJoinThreads)
         acc.z += part[k][j].z;
         acc.w += part[k][j].w;
       }
-      const float m = stats[0], l = stats[1];
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const long long orow = static_cast<long long>(d.x) * p.nq + h0 + r;
+      const long long orow = static_cast<long long>(c.b) * p.nq + h0 + r;
       *reinterpret_cast<uint2*>(p.out + orow * HD + 4 * j) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (j == 0 && p.lse != nullptr)
         p.lse[orow] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
     }
-    __syncthreads();  // weight, stats and part are reused by the next head
+    __syncthreads();  // part is reused by the next head
   }
 }
 

@@ -60,23 +60,21 @@ int copy_grid(const cpattn_ctx* ctx, long long tokens, int hpi) {
 }
 
 // CTAs of a decode launch: at most one per SM.
-int decode_max_ctas(const cpattn_ctx* ctx) {
-  return std::min(ctx->num_sms > 0 ? ctx->num_sms : 152, cpattn::kJoinMaxPieces);
-}
+int decode_max_ctas(const cpattn_ctx* ctx) { return ctx->num_sms > 0 ? ctx->num_sms : 152; }
 
-// Workspace of a decode: O, then (m, l) of every CTA's first and last row,
-// then the CTAs' descriptions of the rows they began.  It depends on neither
-// the lengths nor the number of sequences.
+// Workspace of a decode: O, then (m, l) of every warp's first and last row,
+// then the rows that were cut.  It depends on neither the lengths nor the
+// number of sequences.
 struct DecodeWorkspace {
-  uint64_t ml, desc, total;  // byte offsets
+  uint64_t ml, cut, total;  // byte offsets
 };
 DecodeWorkspace decode_workspace(const cpattn_ctx* ctx) {
-  const uint64_t ctas = static_cast<uint64_t>(decode_max_ctas(ctx));
-  const uint64_t rows = 2 * ctas * cpattn::kDecRows;
+  const uint64_t warps = static_cast<uint64_t>(decode_max_ctas(ctx)) * cpattn::kDecWarps;
+  const uint64_t rows = 2 * warps * cpattn::kDecRows;
   DecodeWorkspace w;
   w.ml = cpattn::align256(rows * ctx->cfg.head_dim * sizeof(float));
-  w.desc = w.ml + cpattn::align256(rows * sizeof(float2));
-  w.total = w.desc + cpattn::align256(ctas * sizeof(int4));
+  w.cut = w.ml + cpattn::align256(rows * sizeof(float2));
+  w.total = w.cut + cpattn::align256(warps * sizeof(cpattn::DecodeCut));
   return w;
 }
 
@@ -106,13 +104,13 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
   const long long tiles =
       (static_cast<long long>(pages->max_pages) * pages->page_size + Ly::WT - 1) / Ly::WT;
   p->num_ctas = static_cast<int>(std::min<long long>(
-      decode_max_ctas(ctx),
-      (rows_all * std::min(tiles, 1LL << 20) + Ly::NW - 1) / Ly::NW));
+      decode_max_ctas(ctx), (rows_all * std::min(tiles, 1LL << 20) + Ly::NW - 1) / Ly::NW));
+  p->by_row = rows_all <= p->num_ctas ? 1 : 0;
   cpattn::paged_decode_kernel<HD, Q8, NB><<<p->num_ctas, Ly::THREADS, Ly::SMEM_BYTES, st>>>(*p);
   cpattn_status s = after_launch(ctx, st, "paged decode launch");
-  if (s != CPATTN_OK || tiles == 1 || p->num_ctas == 1) return s;  // no row can be cut
+  if (s != CPATTN_OK || tiles == 1) return s;  // rows of one tile are never cut
   // Blocks: one per row that may have been cut, times heads where those are few.
-  const int cut = static_cast<int>(std::min<long long>(rows_all, p->num_ctas));
+  const int cut = p->by_row ? static_cast<int>(rows_all) : p->num_ctas * Ly::NW;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cut),
                      static_cast<unsigned>(std::min({std::max(1, 2 * ctx->num_sms / cut), p->group,
@@ -249,7 +247,7 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
   p.lse = lse;
   p.ws_o = reinterpret_cast<float*>(ws);
   p.ws_ml = reinterpret_cast<float2*>(ws + w.ml);
-  p.ws_desc = reinterpret_cast<int4*>(ws + w.desc);
+  p.ws_cut = reinterpret_cast<cpattn::DecodeCut*>(ws + w.cut);
   p.status = ctx->d_status;
   p.timeout_ns = ctx->timeout_ns;
   p.debug_flags = ctx->debug_flags;
