@@ -15,23 +15,27 @@
 //
 // Work split.  The cache is cut into tiles of WT tokens of one row = (sequence,
 // kv head, block of up to 16 q heads).  All tiles of all rows form one list
-// (sequence-major, then kv head), and each WARP of the grid takes an equal,
+// (sequence-major, then kv head), and each WORKER of the grid takes an equal,
 // contiguous slice of it, whatever the lengths are: one long sequence and many
 // ragged ones are balanced alike, and nothing depends on lengths the host does
-// not know.  A warp works alone: it issues its own TMA copies into its own
+// not know.  A worker works alone: it issues its own TMA copies into its own
 // ring of slots (K and V tiles alternate, the next copy goes out as soon as a
 // slot is read), holds Q, m, l and O (all HD columns) in registers, and turns
 // the accumulators of K Q^T into the operand of V^T P^T there (movmatrix).  A
 // row inside its slice it finishes by itself.  At most its first and its last
-// row are shared with other warps; their (m, l, O) go to the workspace as
+// row are shared with other workers; their (m, l, O) go to the workspace as
 // pieces, which a second kernel joins in list order, so that results do not
 // depend on timing:
 //   m = max m_i,  O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
-// A CTA whose whole slice lies in one row (long contexts) sums its warps' O in
-// shared memory first, in warp order, and leaves one piece.  (With the tiles
-// of a row dealt to the warps of a CTA in turn, the warps met at every row's
-// end: 4 us per row, 85 us for 64 ragged sequences where this takes the time
-// in the table of the documentation.)
+// A CTA whose whole slice lies in one row (long contexts) deals its tiles to
+// the workers in turn, sums their O in shared memory, in worker order, and
+// leaves one piece.
+//
+// A worker is one warp for up to 8 q heads per kv head, and two (each with 8
+// heads, on the same slots) for up to 16: a warp's O then takes HD / 4
+// registers and 12 to 16 warps fit an SM.  Latency of dependent instructions
+// bounds a warp here, so warps count for more than the conversions that a
+// pair does twice: with 8 warps of 16 heads, 1x128k e4m3 took 59 us.
 //
 // e4m3 (Q8): K and V are converted to fp16 (exact) in registers; mma.sync on
 // e4m3 operands takes the same conversions and adds fp32 additions (measured
@@ -57,32 +61,31 @@
 
 namespace cpattn {
 
-constexpr int kDecWarps = 8;                     // per CTA, one CTA per SM
-constexpr int kDecRows = 16;                     // most q heads of a row
 constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7
 constexpr float kMinSref = 7.888609052210118e-31f;  // 2^-100: kPScale / s_ref stays finite
 constexpr float kRaise = 8.f;                    // m is raised when a logit exceeds it by this
 constexpr int kDecStages = 8;                    // tiles whose pages a warp remembers (power of two)
 constexpr int kMaxBoxes = 4;                     // page pieces of a tile
 
-// NB: blocks of 8 q heads of a row (1: groups of up to 8 heads; 2: the rest).
-template <int HD, bool Q8, int NB>
+// PW: warps per worker, 8 q heads each.  NW workers per CTA with NSLOT slots
+// of SLOT bytes each, 192 KB in all; WT tokens per tile.  Registers set the
+// number of warps: 16 at HD = 128, 12 at HD = 256 -- 8 for bf16 and one warp
+// per worker, whose tiles of 16 tokens (the least) take 8 KB.
+template <int HD, bool Q8, int PW>
 struct DecodeLayout {
   static constexpr int ESZ = Q8 ? 1 : 2;
-  static constexpr int NW = kDecWarps;
-  static constexpr int THREADS = 32 * NW;
-  // 16 .. 64 tokens per tile, 24 KB of slots per warp and 192 KB per CTA.  At
-  // HD = 256 and NB = 2, O and Q take 192 registers, which leaves room for
-  // tiles of 16 tokens.
-  static constexpr int SLOT = Q8 && HD * NB == 512 ? 4096 : 8192;
-  static constexpr int NSLOT = 24576 / SLOT;
+  static constexpr bool WIDE = HD == 256 && !Q8 && PW == 1;
+  static constexpr int NW = HD == 128 ? 16 / PW : (WIDE ? 8 : 12 / PW);
+  static constexpr int THREADS = 32 * NW * PW;
+  static constexpr int SLOT = PW == 2 || WIDE ? 8192 : 4096;
+  static constexpr int NSLOT = 196608 / (NW * SLOT);
   static constexpr int WT = SLOT / (HD * ESZ);
   static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : 6);
   static constexpr int BOXW = 128 / ESZ;         // values per 128-byte box row
   static constexpr int NBOX = HD / BOXW;         // column blocks of a tile
   static constexpr int MT = WT / 16;             // m-tiles of K Q^T
   static constexpr int MO = HD / 16;             // m-tiles of V^T P^T
-  static constexpr int HEADS = 8 * NB;
+  static constexpr int HEADS = 8 * PW;
   static constexpr int CD = 32;                  // columns summed over the warps at a time
   static constexpr int C_STRIDE = CD + 8;
   static constexpr int OFF_SCALE = NW * NSLOT * SLOT;
@@ -90,10 +93,10 @@ struct DecodeLayout {
   static constexpr int OFF_ML = OFF_SUM + NW * HEADS * C_STRIDE * 4;  // [NW][HEADS] (m, l)
   static constexpr int OFF_BAR = OFF_ML + NW * HEADS * 8;
   // [NW][kDecStages] pool rows of the tile's boxes, and the mask of absent pages
-  static constexpr int OFF_ROWS = OFF_BAR + NW * NSLOT * 8;
+  static constexpr int OFF_ROWS = OFF_BAR + 2 * NW * NSLOT * 8;  // (full, and empty for pairs)
   static constexpr int OFF_BAD = OFF_ROWS + NW * kDecStages * kMaxBoxes * 4;
   static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;  // scan, spots, abort flag
-  static constexpr int SMEM_BYTES = OFF_MISC + NW * 8 + NW * 16 + 16;
+  static constexpr int SMEM_BYTES = OFF_MISC + NW * 16 + THREADS / 32 * 8 + 16;
   static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0 && OFF_SUM % 16 == 0,
                 "shared memory alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -102,7 +105,7 @@ struct DecodeLayout {
 };
 
 // A row that several warps share: list indices [first, end) of its tiles, the
-// list's length and the warps that share it.  end == 0: there is none.
+// list's length and the workers that share it.  end == 0: there is none.
 struct DecodeCut {
   long long first, end, total;
   int b, rr, active, pad;
@@ -116,22 +119,24 @@ struct PagedDecodeParams {
   const __nv_bfloat16* q;     // [num_seqs][NQ][HD]
   __nv_bfloat16* out;
   float* lse;                 // or null
-  float* ws_o;                // [2 * warps][16][HD] O of a warp's first / last row
-  float2* ws_ml;              // [2 * warps][16] its m and l
-  // The cut row that begins in a warp's slice; by row, where there are no more
-  // rows than CTAs, else by warp.
-  DecodeCut* ws_cut;          // [warps]
+  float* ws_o;                // [2 * workers][8 PW][HD] O of a worker's first / last row
+  float2* ws_ml;              // [2 * workers][8 PW] its m and l
+  // The cut row that begins in a worker's slice; by row, where there are no
+  // more rows than CTAs, else by worker.
+  DecodeCut* ws_cut;          // [workers]
   int* status;
   unsigned long long timeout_ns;
   int pool_rows;              // num_pages * NKV * page_size
   int debug_flags;
   int by_row;                 // ws_cut is indexed by row
+  int workers;                // per CTA
+  int piece_rows;             // 8 PW
   int num_ctas;               // CTAs of the decode kernel
-  int num_seqs, nq, group, hblocks;  // hblocks: blocks of 16 q heads per kv head
+  int num_seqs, nq, group, hblocks;  // hblocks: blocks of 8 PW q heads per kv head
   float scale_log2;
 };
 
-enum : int { kSiteDecFull = 9 };  // after the prefill's sites
+enum : int { kSiteDecFull = 9, kSiteDecEmpty = 10 };  // after the prefill's sites
 
 // ------------------------------------------------------------------ mma.sync
 // c (16 x 8) = (ZERO ? 0 : c) + A (16 x 16) B (16 x 8).
@@ -215,8 +220,8 @@ __device__ __forceinline__ int decode_len(const PagedDecodeParams& p, int b) {
   return static_cast<int>(max(0LL, min(static_cast<long long>(__ldg(p.lens + b)), room)));
 }
 
-// Slices: warp w of the `active` ones that share the list takes the tiles
-// [start(w), start(w + 1)); tile i belongs to warp owner(i).
+// Slices: worker w of the `active` ones that share the list takes the tiles
+// [start(w), start(w + 1)); tile i belongs to worker owner(i).
 __device__ __forceinline__ long long slice_start(long long total, int active, int w) {
   return total * w / active;
 }
@@ -224,12 +229,12 @@ __device__ __forceinline__ int slice_owner(long long total, int active, long lon
   return static_cast<int>(((i + 1) * active - 1) / total);
 }
 
-// A warp's way through its slice [s, s1) of the tile list, one row segment at a
-// time: tiles tile0 .. tile0 + tiles - 1 of row rr = kv head * hblocks + head
-// block of sequence b.  tiles == 0: the slice is done.
+// A worker's way through its slice [s, s1) of the tile list, one row segment
+// at a time: tiles tile0, tile0 + step, .. (`tiles` of them) of row rr = kv head
+// * hblocks + head block of sequence b.  tiles == 0: the slice is done.
 struct DecodeWalk {
   long long s, s1;
-  int b, rr, tile0, tiles, nt, n;
+  int b, rr, tile0, tiles, step, nt, n;
 
   template <int WT>
   __device__ __forceinline__ void enter(const PagedDecodeParams& p) {
@@ -256,13 +261,13 @@ struct DecodeWalk {
   }
 };
 
-// Whole block: the list's length, the warps that share it (one tile each at
-// least), and where each warp's slice begins: spot[w] = (b, rr, tile0).
-template <int WT, int NW>
+// Whole block: the list's length, the workers that share it (one tile each at
+// least), and where each one's slice begins: spot[w] = (b, rr, tile0).
+template <int WT, int NW, int WARPS>
 __device__ __forceinline__ long long decode_slices(const PagedDecodeParams& p, int rows_per_seq,
                                                    long long* warp_sum, int4* spot, int* active) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.num_seqs + 32 * NW - 1) / (32 * NW);
+  const int per = (p.num_seqs + 32 * WARPS - 1) / (32 * WARPS);
   const int b0 = min(p.num_seqs, tid * per), b1 = min(p.num_seqs, b0 + per);
   const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
   long long sum = 0;
@@ -281,7 +286,7 @@ __device__ __forceinline__ long long decode_slices(const PagedDecodeParams& p, i
   __syncthreads();
   long long base = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) base += warp_sum[w];
     total += warp_sum[w];
   }
@@ -313,63 +318,76 @@ __device__ __forceinline__ long long decode_slices(const PagedDecodeParams& p, i
 }
 
 // ------------------------------------------------------------------ kernel
-template <int HD, bool Q8, int NB>
-__global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
+template <int HD, bool Q8, int PW>
+__global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
-  using Ly = DecodeLayout<HD, Q8, NB>;
+  using Ly = DecodeLayout<HD, Q8, PW>;
   constexpr int WT = Ly::WT, MT = Ly::MT, MO = Ly::MO, NSLOT = Ly::NSLOT, NW = Ly::NW;
-  constexpr int HEADS = Ly::HEADS;
+  constexpr int HEADS = Ly::HEADS, NB = 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int wk = (tid >> 5) / PW;    // worker of the CTA
+  const int half = (tid >> 5) % PW;  // which 8 heads; warp 0 of a pair issues the copies
   griddep_launch_dependents();
   // Swizzled copies need a 1024-byte aligned base (which the launch gives).
   if ((sbase & 1023u) != 0) {
     if (tid == 0 && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusLayout);
     // Nothing to join (by row: no more rows than CTAs).
-    if (p.by_row ? tid == 0 : lane == 0) p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * NW + warp].end = 0;
+    if (p.by_row ? tid == 0 : lane == 0 && half == 0)
+      p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * NW + wk].end = 0;
     return;
   }
-  const uint32_t ring = sbase + warp * (NSLOT * Ly::SLOT);
-  auto full = [&](int s) {
-    return sbase + Ly::OFF_BAR + 8u * static_cast<uint32_t>(warp * NSLOT + s);
-  };
+  const uint32_t ring = sbase + wk * (NSLOT * Ly::SLOT);
+  const uint32_t full0 = sbase + Ly::OFF_BAR + wk * (16 * NSLOT), empty0 = full0 + 8 * NSLOT;
   int4* spots = reinterpret_cast<int4*>(smem + Ly::OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::OFF_MISC + NW * 24);
-  if (lane == 0) {
-    // (Q8: every lane's copies of the scales arrive too.)
-    for (int s = 0; s < NSLOT; ++s) mbar_init(full(s), Q8 ? 33 : 1);
-    if (warp == 0) *abort_flag = 0;
+  volatile int* abort_flag =
+      reinterpret_cast<volatile int*>(smem + Ly::OFF_MISC + NW * 16 + Ly::THREADS / 4);
+  if (lane == 0 && half == 0) {
+    for (int s = 0; s < NSLOT; ++s) {
+      mbar_init(full0 + 8 * s, Q8 ? 33 : 1);  // (Q8: every lane's copies of the scales arrive too)
+      mbar_init(empty0 + 8 * s, 1);           // the other warp of a pair has read the slot
+    }
+    if (wk == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   const int rows_per_seq = p.pool.nkv * p.hblocks;
-  const int worker = blockIdx.x * NW + warp;
+  const int worker = blockIdx.x * NW + wk;
   int active;
-  const long long total = decode_slices<WT, NW>(
+  const long long total = decode_slices<WT, NW, NW * PW>(
       p, rows_per_seq, reinterpret_cast<long long*>(smem + Ly::OFF_MISC + NW * 16), spots, &active);
   const BoundedWait wait{abort_flag, p.status, p.timeout_ns, nullptr, 0u, 0};
 
   DecodeWalk at;
   at.s = at.s1 = 0;
   at.b = at.rr = at.tile0 = at.tiles = at.nt = at.n = 0;
+  at.step = 1;
   if (worker < active) {
     at.s = slice_start(total, active, worker);
     at.s1 = slice_start(total, active, worker + 1);
-    at.b = spots[warp].x;
-    at.rr = spots[warp].y;
-    at.tile0 = spots[warp].z;
+    at.b = spots[wk].x;
+    at.rr = spots[wk].y;
+    at.tile0 = spots[wk].z;
     at.template enter<WT>(p);
   }
-  // Whether the CTA's whole slice lies in one row (and all its warps have one).
+  // Whether the CTA's whole slice lies in one row (and every worker has tiles):
+  // the workers then take its tiles in turn, neighbours at the same time.
+  const long long cta_s0 = slice_start(total, active, min(static_cast<int>(blockIdx.x) * NW, active));
   bool uniform = false;
-  if (blockIdx.x * NW + NW <= active) {
+  if (static_cast<int>(blockIdx.x) * NW + NW <= active) {
+    const long long cta_s1 = slice_start(total, active, blockIdx.x * NW + NW);
     const int nt0 = (decode_len(p, spots[0].x) + WT - 1) / WT;
-    uniform = spots[0].z + slice_start(total, active, blockIdx.x * NW + NW) -
-                  slice_start(total, active, blockIdx.x * NW) <= nt0;
+    uniform = spots[0].z + cta_s1 - cta_s0 <= nt0;
+    if (uniform) {
+      at.s = at.s1 = 0;  // (one segment)
+      at.tile0 = spots[0].z + wk;
+      at.step = NW;
+      at.tiles = static_cast<int>((cta_s1 - cta_s0 - wk + NW - 1) / NW);
+    }
   }
 
-  // ------------------------------------------- this warp's stream of copies
-  // Copy u of the warp is K (u even) or V (u odd) of its tile u / 2, in slot
+  // ------------------------------------------- the worker's stream of copies
+  // Copy u of the worker is K (u even) or V (u odd) of its tile u / 2, in slot
   // u % NSLOT.  Where K of a tile goes out, its page ids were loaded one tile
   // before (and are looked at only now, so that nothing waits for them); the
   // rows they give are kept for V.
@@ -377,15 +395,15 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   const int box = min(ps, WT), box_shift = min(p.pool.page_shift, Ly::WT_SHIFT);
   const int boxes = WT >> box_shift;
   volatile int* my_rows =
-      reinterpret_cast<volatile int*>(smem + Ly::OFF_ROWS) + warp * (kDecStages * kMaxBoxes);
+      reinterpret_cast<volatile int*>(smem + Ly::OFF_ROWS) + wk * (kDecStages * kMaxBoxes);
   volatile uint32_t* my_bad =
-      reinterpret_cast<volatile uint32_t*>(smem + Ly::OFF_BAD) + warp * kDecStages;
+      reinterpret_cast<volatile uint32_t*>(smem + Ly::OFF_BAD) + wk * kDecStages;
   DecodeWalk ahead = at;  // the tile whose K goes out next
   int aj = 0;             // its index in ahead's segment
   int issued = 0, slot_out = 0;
   int next_t = -1, next_id = 0;  // lane i: first token of its box i (-1: none), and its page
   int next_g = 0;
-  bool more = at.s < at.s1;
+  bool more = at.tiles > 0;
   auto look_up = [&]() {
     // To the next segment, or to the end of the slice.
     if (more && aj >= ahead.tiles) {
@@ -394,7 +412,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       more = ahead.tiles > 0;
     }
     next_t = -1;
-    const int t = (ahead.tile0 + aj) * WT + (lane << box_shift);
+    const int t = (ahead.tile0 + aj * ahead.step) * WT + (lane << box_shift);
     if (more && lane < boxes && t < ahead.n) {
       next_t = t;
       next_id = __ldg(p.pool.table + ahead.b * p.pool.table_stride + (t >> p.pool.page_shift));
@@ -402,7 +420,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     next_g = ahead.rr / p.hblocks;
   };
   auto send = [&](const CUtensorMap* m, const float* scales, int stage) {
-    const uint32_t bar = full(slot_out), dst = ring + slot_out * Ly::SLOT;
+    const uint32_t bar = full0 + 8 * slot_out, dst = ring + slot_out * Ly::SLOT;
     if (lane == 0) mbar_arrive_expect_tx(bar, Ly::SLOT);
     if (lane < boxes) {
       const int row = my_rows[stage * kMaxBoxes + lane];
@@ -417,7 +435,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         if (WT >= 32 || tok < WT) {
           const int row = my_rows[stage * kMaxBoxes + (tok >> box_shift)];
           if (row < p.pool_rows)
-            copy4_async(sbase + Ly::OFF_SCALE + (warp * NSLOT + slot_out) * (WT * 4) + tok * 4,
+            copy4_async(sbase + Ly::OFF_SCALE + (wk * NSLOT + slot_out) * (WT * 4) + tok * 4,
                         scales + row + (tok & (box - 1)));
         }
       }
@@ -455,18 +473,20 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       look_up();
     }
   };
-  look_up();
-  if ((p.debug_flags & kDebugDropArrive) && blockIdx.x == 0 && warp == 0 && more) {
-    // Fault injection: the warp's first copy is never sent.
-    take_rows(0);
-    slot_out = 1;
-    issued = 1;
-    ++aj;
+  if (half == 0) {
     look_up();
-  }
+    if ((p.debug_flags & kDebugDropArrive) && blockIdx.x == 0 && wk == 0 && more) {
+      // Fault injection: the worker's first copy is never sent.
+      take_rows(0);
+      slot_out = 1;
+      issued = 1;
+      ++aj;
+      look_up();
+    }
 #pragma unroll 1
-  for (int i = 0; i < NSLOT; ++i)
-    if (issued == i) issue();
+    for (int i = 0; i < NSLOT; ++i)
+      if (issued == i) issue();
+  }
 
   // Sequences without tokens: zeros, and an LSE of -infinity.
   for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
@@ -479,7 +499,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     if (p.by_row)
       for (int r = tid; r < rows_per_seq; r += Ly::THREADS) p.ws_cut[b * rows_per_seq + r].end = 0;
   }
-  if (!p.by_row && lane == 0) p.ws_cut[worker].end = 0;
+  if (!p.by_row && lane == 0 && half == 0) p.ws_cut[worker].end = 0;
 
   // Accumulator fragments (16 x 8): rows r0 and r0 + 8 (tokens or columns of
   // V), columns 2 quad and 2 quad + 1 (q heads of the block).
@@ -491,22 +511,34 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   // tells the host.
   bool ok = true;
   auto await = [&]() {
-    if (ok) ok = __all_sync(0xFFFFFFFFu, wait(full(slot), phase, kSiteDecFull));
+    if (ok && !mbar_try_wait(full0 + 8 * slot, phase)) ok = wait(full0 + 8 * slot, phase, kSiteDecFull);
     __syncwarp();
   };
-  auto release = [&]() {  // the slot has been read by every lane
+  // The slot has been read by every lane: the next copy goes out (of a pair,
+  // the first warp sends it once the second has read the slot too).
+  auto release = [&]() {
     __syncwarp();
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (PW == 2 && half == 1) {
+      if (lane == 0) mbar_arrive(empty0 + 8 * slot);
+    } else if (PW == 2) {
+      if (ok && !mbar_try_wait(empty0 + 8 * slot, phase))
+        ok = wait(empty0 + 8 * slot, phase, kSiteDecEmpty);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    }
     if (++slot == NSLOT) {
       slot = 0;
       phase ^= 1u;
     }
     ++used;
-    if (ok) issue();
+    if (half == 0 && ok) issue();
   };
 
   for (; at.tiles > 0; at.template next<WT>(p, rows_per_seq)) {
-    const int g = at.rr / p.hblocks, h0 = g * p.group + (at.rr % p.hblocks) * kDecRows;
-    const int heads = min(HEADS, (g + 1) * p.group - h0);
+    const int g = at.rr / p.hblocks;
+    const int hrow = g * p.group + (at.rr % p.hblocks) * HEADS;  // the row's first q head
+    const int h0 = hrow + 8 * half;                             // this warp's
+    const int heads = min(8, (g + 1) * p.group - h0);           // (may be negative: none)
 
     // B fragments of Q^T, this lane's head (r0 of each block of 8): bf16 as it
     // is, dims 16 ks + 2 quad + {0, 1} and + 8; or (Q8) fp16 scaled by a power
@@ -518,7 +550,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     for (int nb = 0; nb < NB; ++nb) {
       const bool here = 8 * nb + r0 < heads;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          p.q + (static_cast<long long>(at.b) * p.nq + h0 + (here ? 8 * nb + r0 : 0)) * HD);
+          p.q + (static_cast<long long>(at.b) * p.nq + (here ? h0 + 8 * nb + r0 : hrow)) * HD);
       uint32_t big = 0;
 #pragma unroll
       for (int ks = 0; ks < HD / 16; ++ks) {
@@ -578,12 +610,12 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         for (int j = 0; j < 4; ++j) o[i][nb][j] = 0.f;
 
     for (int v = 0; v < at.tiles; ++v) {
-      const int valid = min(WT, at.n - (at.tile0 + v) * WT);  // tokens of the tile
-      const uint32_t bad = my_bad[(used >> 1) & (kDecStages - 1)];
-      const bool partial = valid < WT || bad != 0u;
+      const int valid = min(WT, at.n - (at.tile0 + v * at.step) * WT);  // tokens of the tile
 
       // ---- S^T = K Q^T
       await();
+      const uint32_t bad = my_bad[(used >> 1) & (kDecStages - 1)];
+      const bool partial = valid < WT || bad != 0u;
       const uint32_t kb = ring + slot * Ly::SLOT;
       float c[MT][NB][4];
       if constexpr (Q8) {
@@ -630,7 +662,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       // c becomes <q, k> times the token's scale; what is no token is -infinity,
       // by value.  The logits (log2 units) are c sl, taken with m below.
       const float* ksc = reinterpret_cast<const float*>(
-          smem + Ly::OFF_SCALE + (warp * NSLOT + slot) * (WT * 4));
+          smem + Ly::OFF_SCALE + (wk * NSLOT + slot) * (WT * 4));
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -676,7 +708,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       float smx = 0.f;
       if constexpr (Q8) {
         const float* vsc = reinterpret_cast<const float*>(
-            smem + Ly::OFF_SCALE + (warp * NSLOT + slot) * (WT * 4));
+            smem + Ly::OFF_SCALE + (wk * NSLOT + slot) * (WT * 4));
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -810,12 +842,15 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][j], d);
-    const long long row0 = at.s - at.tile0;  // list index of the row's first tile
-    const bool begins = at.tile0 == 0, ends = at.tile0 + at.tiles == at.nt;
-    if (begins && lane == 0) {
-      // The warp in whose slice a row begins says who shares it.
-      const bool cut = !(ends || (uniform && row0 + at.nt <= slice_start(total, active,
-                                                                         (blockIdx.x + 1) * NW)));
+    // List index of the row's first tile; whether the row begins and ends here.
+    const long long row0 = uniform ? cta_s0 - spots[0].z : at.s - at.tile0;
+    const bool begins = at.tile0 == 0, ends = !uniform && at.tile0 + at.tiles == at.nt;
+    const bool cta_whole =
+        uniform && spots[0].z == 0 &&
+        row0 + at.nt == slice_start(total, active, (blockIdx.x + 1) * NW);
+    if (begins && lane == 0 && half == 0) {
+      // The worker in whose slice a row begins says who shares it.
+      const bool cut = !(ends || cta_whole);
       DecodeCut d;
       d.first = row0;
       d.end = cut ? row0 + at.nt : 0;
@@ -831,71 +866,63 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     }
     const float oscale = Q8 ? sref * (1.f / kPScale) : 1.f;
     if (uniform) {
-      // One piece for the CTA: the warps' m and l, then their O, 32 columns at
-      // a time, summed in warp order.  (The only row of every warp here.)
+      // One piece for the CTA: the workers' m and l, then their O, 32 columns
+      // at a time, summed in worker order.  (The only row of every warp here.)
       float2* mls = reinterpret_cast<float2*>(smem + Ly::OFF_ML);
       float* summed = reinterpret_cast<float*>(smem + Ly::OFF_SUM);
       if (r0 == 0) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            mls[warp * HEADS + 8 * nb + 2 * quad + j] = make_float2(m[nb][j], l[nb][j]);
+        for (int j = 0; j < 2; ++j)
+          mls[wk * HEADS + 8 * half + 2 * quad + j] = make_float2(m[0][j], l[0][j]);
       }
       __syncthreads();
-      const long long c0 = slice_start(total, active, blockIdx.x * NW);
-      const bool whole = spots[0].z == 0 &&
-                         c0 + at.nt == slice_start(total, active, (blockIdx.x + 1) * NW);
       const long long piece = 2LL * blockIdx.x * NW;
-      float f[NB][2];
+      const int row_heads = min(HEADS, (g + 1) * p.group - hrow);
+      float f[2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * half + 2 * quad + j;
+        float mm = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = 8 * nb + 2 * quad + j;
-          float mm = -INFINITY, sum = 0.f;
+        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mls[w * HEADS + r].x);
+        const float mref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-          for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mls[w * HEADS + r].x);
-          const float mref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const float2 ml = mls[w * HEADS + r];
-            sum = fmaf(ex2_approx(ml.x - mref), ml.y, sum);
-          }
-          f[nb][j] = ex2_approx(m[nb][j] - mref) * oscale;
-          // sum = 0: every page of the row was absent.
-          if (whole) f[nb][j] = sum == 0.f ? 0.f : f[nb][j] / sum;
-          if (warp == 0 && r0 == 0 && r < heads) {
-            const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
-            if (!whole)
-              p.ws_ml[piece * kDecRows + r] = make_float2(mm, sum);
-            else if (p.lse != nullptr)
-              p.lse[orow] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.69314718055994531f;
-          }
+        for (int w = 0; w < NW; ++w) {
+          const float2 ml = mls[w * HEADS + r];
+          sum = fmaf(ex2_approx(ml.x - mref), ml.y, sum);
         }
+        f[j] = ex2_approx(m[0][j] - mref) * oscale;
+        // sum = 0: every page of the row was absent.
+        if (cta_whole) f[j] = sum == 0.f ? 0.f : f[j] / sum;
+        if (wk == 0 && r0 == 0 && r < row_heads) {
+          const long long orow = static_cast<long long>(at.b) * p.nq + hrow + r;
+          if (!cta_whole)
+            p.ws_ml[piece * HEADS + r] = make_float2(mm, sum);
+          else if (p.lse != nullptr)
+            p.lse[orow] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.69314718055994531f;
+        }
+      }
 #pragma unroll
       for (int cc = 0; cc < HD / Ly::CD; ++cc) {
         if (cc > 0) __syncthreads();
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int j = 0; j < 2; ++j) {
+          float* dst = summed + (wk * HEADS + 8 * half + 2 * quad + j) * Ly::C_STRIDE;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float* dst = summed + (warp * HEADS + 8 * nb + 2 * quad + j) * Ly::C_STRIDE;
-#pragma unroll
-            for (int k = 0; k < Ly::CD / 16; ++k) {
-              const float* a = o[cc * (Ly::CD / 16) + k][nb];
-              if constexpr (Q8) {  // rows r0, r0 + 8 of the m-tile: columns 2 r0 and 2 r0 + 1
-                *reinterpret_cast<float2*>(dst + 16 * k + 2 * r0) =
-                    make_float2(a[j] * f[nb][j], a[2 + j] * f[nb][j]);
-              } else {
-                dst[16 * k + r0] = a[j] * f[nb][j];
-                dst[16 * k + 8 + r0] = a[2 + j] * f[nb][j];
-              }
+          for (int k = 0; k < Ly::CD / 16; ++k) {
+            const float* a = o[cc * (Ly::CD / 16) + k][0];
+            if constexpr (Q8) {  // rows r0, r0 + 8 of the m-tile: columns 2 r0 and 2 r0 + 1
+              *reinterpret_cast<float2*>(dst + 16 * k + 2 * r0) =
+                  make_float2(a[j] * f[j], a[2 + j] * f[j]);
+            } else {
+              dst[16 * k + r0] = a[j] * f[j];
+              dst[16 * k + 8 + r0] = a[2 + j] * f[j];
             }
           }
+        }
         __syncthreads();
         const int r = tid / (Ly::CD / 2), d = 2 * (tid % (Ly::CD / 2));  // column pairs
-        if (r < heads) {
+        if (r < row_heads) {
           float2 y = make_float2(0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < NW; ++w) {
@@ -904,12 +931,12 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
             y.x += z.x;
             y.y += z.y;
           }
-          if (whole)
+          if (cta_whole)
             *reinterpret_cast<uint32_t*>(
-                p.out + (static_cast<long long>(at.b) * p.nq + h0 + r) * HD + cc * Ly::CD + d) =
+                p.out + (static_cast<long long>(at.b) * p.nq + hrow + r) * HD + cc * Ly::CD + d) =
                 pack_bf16x2(y.x, y.y);
           else
-            *reinterpret_cast<float2*>(p.ws_o + (piece * kDecRows + r) * HD + cc * Ly::CD + d) = y;
+            *reinterpret_cast<float2*>(p.ws_o + (piece * HEADS + r) * HD + cc * Ly::CD + d) = y;
         }
       }
     } else {
@@ -917,45 +944,44 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       const bool whole = begins && ends;
       const long long piece = 2LL * worker + (begins ? 1 : 0);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int j = 0; j < 2; ++j) {
+        const int r = 2 * quad + j;  // of this warp's 8 heads
+        const float sum = l[0][j];
+        const float f = whole ? (sum == 0.f ? 0.f : oscale / sum) : oscale;
+        const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
+        const long long prow = piece * HEADS + 8 * half + r;
+        if (r0 == 0 && r < heads) {
+          if (!whole)
+            p.ws_ml[prow] = make_float2(m[0][j], sum);
+          else if (p.lse != nullptr)
+            p.lse[orow] = sum == 0.f ? -INFINITY : (m[0][j] + __log2f(sum)) * 0.69314718055994531f;
+        }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = 8 * nb + 2 * quad + j;
-          const float sum = l[nb][j];
-          const float f = whole ? (sum == 0.f ? 0.f : oscale / sum) : oscale;
-          const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
-          if (r0 == 0 && r < heads) {
-            if (!whole)
-              p.ws_ml[piece * kDecRows + r] = make_float2(m[nb][j], sum);
-            else if (p.lse != nullptr)
-              p.lse[orow] = sum == 0.f ? -INFINITY
-                                       : (m[nb][j] + __log2f(sum)) * 0.69314718055994531f;
+        for (int i = 0; i < MO; ++i) {
+          float2 y = make_float2(o[i][0][j] * f, o[i][0][2 + j] * f);
+          int d = 16 * i + 2 * r0;
+          if constexpr (!Q8) {
+            // Rows r0 and r0 + 8 are columns r0 and r0 + 8: a neighbour's value
+            // makes a pair.
+            const bool odd = (r0 & 1) != 0;
+            const float z = __shfl_xor_sync(0xFFFFFFFFu, odd ? y.x : y.y, 4);
+            y = odd ? make_float2(z, y.y) : make_float2(y.x, z);
+            d = 16 * i + (odd ? r0 + 7 : r0);
           }
-#pragma unroll
-          for (int i = 0; i < MO; ++i) {
-            float2 y = make_float2(o[i][nb][j] * f, o[i][nb][2 + j] * f);
-            int d = 16 * i + 2 * r0;
-            if constexpr (!Q8) {
-              // Rows r0 and r0 + 8 are columns r0 and r0 + 8: a neighbour's
-              // value makes a pair.
-              const bool odd = (r0 & 1) != 0;
-              const float z = __shfl_xor_sync(0xFFFFFFFFu, odd ? y.x : y.y, 4);
-              y = odd ? make_float2(z, y.y) : make_float2(y.x, z);
-              d = 16 * i + (odd ? r0 + 7 : r0);
-            }
-            if (r >= heads) continue;
+          if (r < heads) {
             if (whole)
               *reinterpret_cast<uint32_t*>(p.out + orow * HD + d) = pack_bf16x2(y.x, y.y);
             else
-              *reinterpret_cast<float2*>(p.ws_o + (piece * kDecRows + r) * HD + d) = y;
+              *reinterpret_cast<float2*>(p.ws_o + prow * HD + d) = y;
           }
         }
+      }
     }
   }
-  if (!ok) {
+  if (!ok && half == 0) {
     // Let copies already sent land before this CTA can exit.
     for (; used < issued; ++used) {
-      mbar_wait_drain(full(slot), phase, 200ull * 1000 * 1000);
+      mbar_wait_drain(full0 + 8 * slot, phase, 200ull * 1000 * 1000);
       if (++slot == NSLOT) {
         slot = 0;
         phase ^= 1u;
@@ -965,102 +991,112 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 }
 
 // Joins the pieces of the rows that were cut.  Block (x, y): row x of the
-// batch, or (where there are more rows than CTAs) the row that begins in warp
-// x's slice; q heads y, y + gridDim.y, ... of it.  Most blocks of a large batch
-// find nothing to do.  A programmatic dependent of the decode kernel.  Thread
-// (j, y): output elements 4j .. 4j+3 over the pieces y, y + GROUPS, ..., summed
-// over y in shared memory.  Each warp reads all pieces' (m, l) itself, while
-// its first loads of O are in flight: two round trips to L2 in all.
-constexpr int kJoinThreads = 512;
+// batch, or (where there are more rows than CTAs) the row that begins in worker
+// x's slice; and of its q heads the y-th part.  Most blocks of a large batch
+// find nothing to do.  A programmatic dependent of the decode kernel.  A unit of
+// HD / 4 threads takes one head and every `groups`-th of its pieces, each
+// thread 4 columns; the groups are summed in shared memory.  Each warp reads
+// the pieces' (m, l) itself, while its first loads of O are in flight: two
+// round trips to L2 in all.
 constexpr int kJoinBatch = 4;  // loads of O in flight per thread
 
 template <int HD>
-__global__ void __launch_bounds__(kJoinThreads)
-    paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
-  constexpr int GROUPS = kJoinThreads / (HD / 4);
-  __shared__ float4 part[GROUPS][HD / 4];
-  const int tid = threadIdx.x, lane = tid & 31, j = tid % (HD / 4), y = tid / (HD / 4);
+__global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+  constexpr int COLS = HD / 4;
+  __shared__ float4 part[512];
+  const int tid = threadIdx.x, lane = tid & 31, j = tid % COLS, unit = tid / COLS;
+  const int units = blockDim.x / COLS;
   griddep_wait();
   const DecodeCut c = p.ws_cut[blockIdx.x];
   if (c.end == 0) return;
-  const int g = c.rr / p.hblocks, h0 = g * p.group + (c.rr % p.hblocks) * kDecRows;
-  const int heads = min(kDecRows, (g + 1) * p.group - h0);
-  // The pieces, in list order: of the row's first CTA, one per warp from the
-  // row's first warp on (one in all if the CTA lies in the row altogether);
-  // one of each CTA between; and of its last CTA again one per warp, or one.
+  const int nw = p.workers;
+  const int g = c.rr / p.hblocks, hrow = g * p.group + (c.rr % p.hblocks) * p.piece_rows;
+  const int heads = min(p.piece_rows, (g + 1) * p.group - hrow);
+  // The pieces, in list order: of the row's first CTA, one per worker from the
+  // row's first worker on (one in all if the CTA lies in the row altogether);
+  // one of each CTA between; and of its last CTA again one per worker, or one.
   const int w0 = slice_owner(c.total, c.active, c.first), w1 = slice_owner(c.total, c.active, c.end - 1);
-  const int cta0 = w0 / kDecWarps, cta1 = w1 / kDecWarps;
-  const bool one0 = w0 % kDecWarps == 0 && slice_start(c.total, c.active, w0) == c.first;
-  const bool one1 = w1 % kDecWarps == kDecWarps - 1 && slice_start(c.total, c.active, w1 + 1) == c.end;
-  int head_n, tail_n;  // pieces of the first and the last CTA (apart from the first)
-  if (cta0 == cta1) {
-    head_n = w1 - w0 + 1;
-    tail_n = 0;
-  } else {
-    head_n = one0 ? 1 : kDecWarps - w0 % kDecWarps;
-    tail_n = one1 ? 1 : w1 % kDecWarps + 1;
-  }
-  const int mid_n = max(cta1 - cta0 - 1, 0), pieces = head_n + mid_n + tail_n;
-  const bool first_own = !(cta0 != cta1 && one0);  // the first piece is a warp's last row
+  const int cta0 = w0 / nw, cta1 = w1 / nw;
+  const bool one0 = cta0 != cta1 && w0 % nw == 0 && slice_start(c.total, c.active, w0) == c.first;
+  const bool one1 = w1 % nw == nw - 1 && slice_start(c.total, c.active, w1 + 1) == c.end;
+  const int head_n = cta0 == cta1 ? w1 - w0 + 1 : (one0 ? 1 : nw - w0 % nw);
+  const int mid_n = max(cta1 - cta0 - 1, 0);
+  const int tail_n = cta0 == cta1 ? 0 : (one1 ? 1 : w1 % nw + 1);
+  const int pieces = head_n + mid_n + tail_n;
   auto slot = [&](int i) -> long long {
-    if (i < head_n) return 2LL * (w0 + i) + (i == 0 && first_own ? 1 : 0);
+    if (i < head_n) return 2LL * (w0 + i) + (i == 0 && !one0 ? 1 : 0);  // (0: a worker's last row)
     i -= head_n;
-    if (i < mid_n) return 2LL * (cta0 + 1 + i) * kDecWarps;
-    return 2LL * (cta1 * kDecWarps + i - mid_n);
+    if (i < mid_n) return 2LL * (cta0 + 1 + i) * nw;
+    return 2LL * (cta1 * nw + i - mid_n);
   };
-  for (int r = blockIdx.y; r < heads; r += gridDim.y) {
+  // This block's heads, and how many groups share the pieces of one.
+  const int per = (heads + gridDim.y - 1) / gridDim.y;
+  const int ra = blockIdx.y * per, rb = min(heads, ra + per);
+  int groups = 1;
+  while (2 * groups * per <= units && 2 * groups <= pieces) groups *= 2;
+  const int y = unit % groups;
+  for (int base = ra; base < rb; base += units / groups) {
+    const int r = base + unit / groups;
+    const bool mine = r < rb;
     const float* o_at = p.ws_o + static_cast<long long>(r) * HD + 4 * j;
     const float2* ml_at = p.ws_ml + r;
-    auto load_o = [&](int i) {
-      return *reinterpret_cast<const float4*>(o_at + slot(i) * (kDecRows * HD));
-    };
-    float4 o[kJoinBatch];
-#pragma unroll
-    for (int k = 0; k < kJoinBatch; ++k)
-      if (y + k * GROUPS < pieces) o[k] = load_o(y + k * GROUPS);
+    const long long rows = p.piece_rows;
     float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml_at[slot(i) * kDecRows].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    const float mref = m == -INFINITY ? 0.f : m;
-    for (int i = lane; i < pieces; i += 32) {
-      const float2 ml = ml_at[slot(i) * kDecRows];
-      l = fmaf(ex2_approx(ml.x - mref), ml.y, l);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = y; i < pieces; i += kJoinBatch * GROUPS) {
+    if (mine) {
+      float4 o[kJoinBatch];
 #pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k) {
-        const int ii = i + k * GROUPS;
-        if (ii >= pieces) break;
-        const float w = ex2_approx(ml_at[slot(ii) * kDecRows].x - mref);
-        acc.x = fmaf(w, o[k].x, acc.x);
-        acc.y = fmaf(w, o[k].y, acc.y);
-        acc.z = fmaf(w, o[k].z, acc.z);
-        acc.w = fmaf(w, o[k].w, acc.w);
-        if (ii + kJoinBatch * GROUPS < pieces) o[k] = load_o(ii + kJoinBatch * GROUPS);
+      for (int k = 0; k < kJoinBatch; ++k)
+        if (y + k * groups < pieces)
+          o[k] = *reinterpret_cast<const float4*>(o_at + slot(y + k * groups) * rows * HD);
+      for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml_at[slot(i) * rows].x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+      const float mref = m == -INFINITY ? 0.f : m;
+      for (int i = lane; i < pieces; i += 32) {
+        const float2 ml = ml_at[slot(i) * rows];
+        l = fmaf(ex2_approx(ml.x - mref), ml.y, l);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+      for (int i = y; i < pieces; i += kJoinBatch * groups) {
+#pragma unroll
+        for (int k = 0; k < kJoinBatch; ++k) {
+          const int ii = i + k * groups;
+          if (ii < pieces) {
+            const float w = ex2_approx(ml_at[slot(ii) * rows].x - mref);
+            acc.x = fmaf(w, o[k].x, acc.x);
+            acc.y = fmaf(w, o[k].y, acc.y);
+            acc.z = fmaf(w, o[k].z, acc.z);
+            acc.w = fmaf(w, o[k].w, acc.w);
+            const int in = ii + kJoinBatch * groups;
+            if (in < pieces) o[k] = *reinterpret_cast<const float4*>(o_at + slot(in) * rows * HD);
+          }
+        }
       }
     }
-    part[y][j] = acc;
-    __syncthreads();
-    if (y == 0) {
-#pragma unroll
-      for (int k = 1; k < GROUPS; ++k) {
-        acc.x += part[k][j].x;
-        acc.y += part[k][j].y;
-        acc.z += part[k][j].z;
-        acc.w += part[k][j].w;
+    if (groups > 1) {
+      __syncthreads();
+      part[tid] = acc;
+      __syncthreads();
+      if (y == 0) {
+        for (int k = 1; k < groups; ++k) {
+          const float4 z = part[tid + k * COLS];
+          acc.x += z.x;
+          acc.y += z.y;
+          acc.z += z.z;
+          acc.w += z.w;
+        }
       }
+    }
+    if (mine && y == 0) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const long long orow = static_cast<long long>(c.b) * p.nq + h0 + r;
+      const long long orow = static_cast<long long>(c.b) * p.nq + hrow + r;
       *reinterpret_cast<uint2*>(p.out + orow * HD + 4 * j) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (j == 0 && p.lse != nullptr)
         p.lse[orow] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
     }
-    __syncthreads();  // part is reused by the next head
   }
 }
 

@@ -62,29 +62,31 @@ int copy_grid(const cpattn_ctx* ctx, long long tokens, int hpi) {
 // CTAs of a decode launch: at most one per SM.
 int decode_max_ctas(const cpattn_ctx* ctx) { return ctx->num_sms > 0 ? ctx->num_sms : 152; }
 
-// Workspace of a decode: O, then (m, l) of every warp's first and last row,
+// Workspace of a decode: O, then (m, l) of every worker's first and last row,
 // then the rows that were cut.  It depends on neither the lengths nor the
 // number of sequences.
 struct DecodeWorkspace {
   uint64_t ml, cut, total;  // byte offsets
 };
 DecodeWorkspace decode_workspace(const cpattn_ctx* ctx) {
-  const uint64_t warps = static_cast<uint64_t>(decode_max_ctas(ctx)) * cpattn::kDecWarps;
-  const uint64_t rows = 2 * warps * cpattn::kDecRows;
+  // At most 16 workers per CTA with 8 rows per piece, or 8 with 16.
+  const uint64_t workers = static_cast<uint64_t>(decode_max_ctas(ctx)) * 16;
+  const uint64_t rows = 2 * workers * 8;
   DecodeWorkspace w;
   w.ml = cpattn::align256(rows * ctx->cfg.head_dim * sizeof(float));
   w.cut = w.ml + cpattn::align256(rows * sizeof(float2));
-  w.total = w.cut + cpattn::align256(warps * sizeof(cpattn::DecodeCut));
+  w.total = w.cut + cpattn::align256(workers * sizeof(cpattn::DecodeCut));
   return w;
 }
 
-template <int HD, bool Q8, int NB>
+template <int HD, bool Q8, int PW>
 cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
                             cpattn::PagedDecodeParams* p, cudaStream_t st) {
-  using Ly = cpattn::DecodeLayout<HD, Q8, NB>;
+  using Ly = cpattn::DecodeLayout<HD, Q8, PW>;
+  static_assert(Ly::NW <= 16 && Ly::NW * Ly::HEADS <= 128, "decode_workspace");
   bool& ready = ctx->decode_ready[HD == 256][Q8];
   if (!ready) {
-    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8, NB>,
+    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8, PW>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Ly::SMEM_BYTES);
     if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaFuncSetAttribute(paged decode)");
@@ -105,17 +107,20 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
       (static_cast<long long>(pages->max_pages) * pages->page_size + Ly::WT - 1) / Ly::WT;
   p->num_ctas = static_cast<int>(std::min<long long>(
       decode_max_ctas(ctx), (rows_all * std::min(tiles, 1LL << 20) + Ly::NW - 1) / Ly::NW));
+  p->workers = Ly::NW;
+  p->piece_rows = Ly::HEADS;
   p->by_row = rows_all <= p->num_ctas ? 1 : 0;
-  cpattn::paged_decode_kernel<HD, Q8, NB><<<p->num_ctas, Ly::THREADS, Ly::SMEM_BYTES, st>>>(*p);
+  cpattn::paged_decode_kernel<HD, Q8, PW><<<p->num_ctas, Ly::THREADS, Ly::SMEM_BYTES, st>>>(*p);
   cpattn_status s = after_launch(ctx, st, "paged decode launch");
   if (s != CPATTN_OK || tiles == 1) return s;  // rows of one tile are never cut
-  // Blocks: one per row that may have been cut, times heads where those are few.
-  const int cut = p->by_row ? static_cast<int>(rows_all) : p->num_ctas * Ly::NW;
+  // Few rows: one block per row and as many heads as fill the GPU, each with
+  // the threads for many pieces.  Many rows have few pieces each.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(cut),
-                     static_cast<unsigned>(std::min({std::max(1, 2 * ctx->num_sms / cut), p->group,
-                                                     cpattn::kDecRows})));
-  cfg.blockDim = dim3(cpattn::kJoinThreads);
+  const int blocks = p->by_row ? static_cast<int>(rows_all) : p->num_ctas * Ly::NW;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks),
+                     static_cast<unsigned>(std::min({std::max(1, 2 * ctx->num_sms / blocks), p->group,
+                                                     Ly::HEADS})));
+  cfg.blockDim = dim3(p->by_row ? 512 : 256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -255,11 +260,12 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
   p.num_seqs = num_seqs;
   p.nq = c.num_q_heads;
   p.group = c.num_q_heads / c.num_kv_heads;
-  p.hblocks = (p.group + cpattn::kDecRows - 1) / cpattn::kDecRows;
+  // Up to 8 q heads per kv head: one warp each worker; else two, 16 heads.
+  const bool one = p.group <= 8;
+  p.hblocks = one ? 1 : (p.group + 15) / 16;
   p.scale_log2 = c.softmax_scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool q8 = pages->format == CPATTN_PAGES_E4M3;
-  const bool one = p.group <= 8;
   if (c.head_dim == 128) {
     if (one)
       return q8 ? launch_decode<128, true, 1>(ctx, pages, &p, st)
