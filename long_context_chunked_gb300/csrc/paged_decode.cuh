@@ -95,8 +95,9 @@ struct DecodeLayout {
   // [NW][kDecStages] pool rows of the tile's boxes, and the mask of absent pages
   static constexpr int OFF_ROWS = OFF_BAR + 2 * NW * NSLOT * 8;  // (full, and empty for pairs)
   static constexpr int OFF_BAD = OFF_ROWS + NW * kDecStages * kMaxBoxes * 4;
-  static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;  // scan, spots, abort flag
+  static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;  // spots, scan, abort flag
   static constexpr int SMEM_BYTES = OFF_MISC + NW * 16 + THREADS / 32 * 8 + 16;
+  static_assert(THREADS * 8 <= NW * HEADS * C_STRIDE * 4, "the scan's ends lie where O is summed later");
   static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0 && OFF_SUM % 16 == 0,
                 "shared memory alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -104,11 +105,11 @@ struct DecodeLayout {
   static_assert(WT / 16 <= kMaxBoxes && NSLOT / 2 + 2 <= kDecStages, "page table of a warp");
 };
 
-// A row that several warps share: list indices [first, end) of its tiles, the
-// list's length and the workers that share it.  end == 0: there is none.
+// A row that the workers first .. last share.  one_first, one_last: the whole
+// slice of first's CTA (of last's CTA) lies in the row and is one piece.
+// first < 0: there is none.
 struct DecodeCut {
-  long long first, end, total;
-  int b, rr, active, pad;
+  int b, rr, first, last, one_first, one_last, pad[2];
 };
 
 struct PagedDecodeParams {
@@ -186,10 +187,10 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-// Asynchronous copy of 4 bytes, and an arrival on `bar` once this thread's
+// Asynchronous copy of 16 bytes, and an arrival on `bar` once this thread's
 // copies so far have landed.
-__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(src))
                : "memory");
 }
@@ -220,14 +221,32 @@ __device__ __forceinline__ int decode_len(const PagedDecodeParams& p, int b) {
   return static_cast<int>(max(0LL, min(static_cast<long long>(__ldg(p.lens + b)), room)));
 }
 
+// Quotients of tile counts, which hardly ever pass 32 bits: a 64-bit division
+// takes far longer than a 32-bit one, and every warp waits for a few of these.
+__device__ __forceinline__ long long div_count(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // Slices: worker w of the `active` ones that share the list takes the tiles
-// [start(w), start(w + 1)); tile i belongs to worker owner(i).
-__device__ __forceinline__ long long slice_start(long long total, int active, int w) {
-  return total * w / active;
-}
-__device__ __forceinline__ int slice_owner(long long total, int active, long long i) {
-  return static_cast<int>(((i + 1) * active - 1) / total);
-}
+// [start(w), start(w + 1)), q of them and one more for w < r; tile i belongs to
+// worker owner(i).
+struct DecodeSlices {
+  long long total, q;
+  int active, r;
+
+  __device__ __forceinline__ void init(long long total_, long long workers) {
+    total = total_;
+    active = static_cast<int>(min(total, workers));
+    q = active > 0 ? div_count(total, active) : 0;
+    r = static_cast<int>(total - q * active);
+  }
+  __device__ __forceinline__ long long start(int w) const { return q * w + min(w, r); }
+  __device__ __forceinline__ int owner(long long i) const {
+    const long long big = (q + 1) * r;  // tiles of the slices with q + 1
+    return static_cast<int>(i < big ? div_count(i, q + 1) : r + div_count(i - big, q));
+  }
+};
 
 // A worker's way through its slice [s, s1) of the tile list, one row segment
 // at a time: tiles tile0, tile0 + step, .. (`tiles` of them) of row rr = kv head
@@ -261,11 +280,14 @@ struct DecodeWalk {
   }
 };
 
-// Whole block: the list's length, the workers that share it (one tile each at
-// least), and where each one's slice begins: spot[w] = (b, rr, tile0).
-template <int WT, int NW, int WARPS>
-__device__ __forceinline__ long long decode_slices(const PagedDecodeParams& p, int rows_per_seq,
-                                                   long long* warp_sum, int4* spot, int* active) {
+// Whole block: the slices, and where each worker's one begins: spot[w] =
+// (b, rr, tile0).  `ends` (shared memory): per thread, the list index behind
+// its sequences.
+template <int WT, int NW, int PW>
+__device__ __forceinline__ void decode_slices(const PagedDecodeParams& p, int rows_per_seq,
+                                              long long* warp_sum, long long* ends, int4* spot,
+                                              DecodeSlices* out) {
+  constexpr int WARPS = NW * PW;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.num_seqs + 32 * WARPS - 1) / (32 * WARPS);
   const int b0 = min(p.num_seqs, tid * per), b1 = min(p.num_seqs, b0 + per);
@@ -290,31 +312,36 @@ __device__ __forceinline__ long long decode_slices(const PagedDecodeParams& p, i
     if (w < warp) base += warp_sum[w];
     total += warp_sum[w];
   }
-  total *= rows_per_seq;
-  *active = static_cast<int>(min(total, static_cast<long long>(gridDim.x) * NW));
-  long long at = (base + inc - sum) * rows_per_seq;  // list index of sequence b0's first tile
-  const long long end = at + sum * rows_per_seq;
-  if (sum > 0) {
-#pragma unroll 1
-    for (int w = 0; w < NW; ++w) {
-      const int worker = blockIdx.x * NW + w;
-      if (worker >= *active) break;
-      const long long s0 = slice_start(total, *active, worker);
-      if (s0 < at || s0 >= end) continue;
-      long long a = at;
-      for (int b = b0; b < b1; ++b) {
-        const int nt = (decode_len(p, b) + WT - 1) / WT;
-        const long long n = static_cast<long long>(nt) * rows_per_seq;
-        if (s0 < a + n) {
-          spot[w] = make_int4(b, static_cast<int>((s0 - a) / nt), static_cast<int>((s0 - a) % nt), 0);
-          break;
-        }
-        a += n;
+  ends[tid] = (base + inc) * rows_per_seq;
+  out->init(total * rows_per_seq, static_cast<long long>(gridDim.x) * NW);
+  __syncthreads();
+  // The first warp of each worker looks for its slice's first tile: the first
+  // thread whose sequences end behind it, then among that thread's sequences.
+  const int worker = blockIdx.x * NW + warp / PW;
+  if (warp % PW == 0 && worker < out->active) {
+    const long long s0 = out->start(worker);
+    int t = 0;
+    for (int k = 0; k < WARPS; ++k) {
+      const uint32_t behind = __ballot_sync(0xFFFFFFFFu, ends[32 * k + lane] > s0);
+      if (behind != 0u) {
+        t = 32 * k + __ffs(static_cast<int>(behind)) - 1;
+        break;
       }
+    }
+    long long a = t > 0 ? ends[t - 1] : 0;
+    for (int b = t * per; b < p.num_seqs; ++b) {
+      const int nt = (decode_len(p, b) + WT - 1) / WT;
+      const long long n = static_cast<long long>(nt) * rows_per_seq;
+      if (s0 < a + n) {
+        const int rr = static_cast<int>(div_count(s0 - a, nt));
+        if (lane == 0)
+          spot[warp / PW] = make_int4(b, rr, static_cast<int>(s0 - a - static_cast<long long>(rr) * nt), 0);
+        break;
+      }
+      a += n;
     }
   }
   __syncthreads();
-  return total;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -335,7 +362,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
     if (tid == 0 && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusLayout);
     // Nothing to join (by row: no more rows than CTAs).
     if (p.by_row ? tid == 0 : lane == 0 && half == 0)
-      p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * NW + wk].end = 0;
+      p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * NW + wk].first = -1;
     return;
   }
   const uint32_t ring = sbase + wk * (NSLOT * Ly::SLOT);
@@ -345,7 +372,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
       reinterpret_cast<volatile int*>(smem + Ly::OFF_MISC + NW * 16 + Ly::THREADS / 4);
   if (lane == 0 && half == 0) {
     for (int s = 0; s < NSLOT; ++s) {
-      mbar_init(full0 + 8 * s, Q8 ? 33 : 1);  // (Q8: every lane's copies of the scales arrive too)
+      mbar_init(full0 + 8 * s, Q8 ? 1 + WT / 4 : 1);  // (Q8: the copies of the scales arrive too)
       mbar_init(empty0 + 8 * s, 1);           // the other warp of a pair has read the slot
     }
     if (wk == 0) *abort_flag = 0;
@@ -353,18 +380,21 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
   }
   const int rows_per_seq = p.pool.nkv * p.hblocks;
   const int worker = blockIdx.x * NW + wk;
-  int active;
-  const long long total = decode_slices<WT, NW, NW * PW>(
-      p, rows_per_seq, reinterpret_cast<long long*>(smem + Ly::OFF_MISC + NW * 16), spots, &active);
+  DecodeSlices sl_;
+  decode_slices<WT, NW, PW>(p, rows_per_seq,
+                            reinterpret_cast<long long*>(smem + Ly::OFF_MISC + NW * 16),
+                            reinterpret_cast<long long*>(smem + Ly::OFF_SUM), spots, &sl_);
+  const DecodeSlices slices = sl_;
+  const int cta_w0 = static_cast<int>(blockIdx.x) * NW;
   const BoundedWait wait{abort_flag, p.status, p.timeout_ns, nullptr, 0u, 0};
 
   DecodeWalk at;
   at.s = at.s1 = 0;
   at.b = at.rr = at.tile0 = at.tiles = at.nt = at.n = 0;
   at.step = 1;
-  if (worker < active) {
-    at.s = slice_start(total, active, worker);
-    at.s1 = slice_start(total, active, worker + 1);
+  if (worker < slices.active) {
+    at.s = slices.start(worker);
+    at.s1 = slices.start(worker + 1);
     at.b = spots[wk].x;
     at.rr = spots[wk].y;
     at.tile0 = spots[wk].z;
@@ -372,10 +402,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
   }
   // Whether the CTA's whole slice lies in one row (and every worker has tiles):
   // the workers then take its tiles in turn, neighbours at the same time.
-  const long long cta_s0 = slice_start(total, active, min(static_cast<int>(blockIdx.x) * NW, active));
+  const long long cta_s0 = slices.start(cta_w0), cta_s1 = slices.start(cta_w0 + NW);
   bool uniform = false;
-  if (static_cast<int>(blockIdx.x) * NW + NW <= active) {
-    const long long cta_s1 = slice_start(total, active, blockIdx.x * NW + NW);
+  if (cta_w0 + NW <= slices.active) {
     const int nt0 = (decode_len(p, spots[0].x) + WT - 1) / WT;
     uniform = spots[0].z + cta_s1 - cta_s0 <= nt0;
     if (uniform) {
@@ -429,17 +458,14 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
         tma_load_3d(dst + c * (WT * 128) + (lane << box_shift) * 128, m, bar, c * Ly::BOXW, 0, row);
     }
     if constexpr (Q8) {
-#pragma unroll
-      for (int j = 0; j < WT; j += 32) {
-        const int tok = j + lane;
-        if (WT >= 32 || tok < WT) {
-          const int row = my_rows[stage * kMaxBoxes + (tok >> box_shift)];
-          if (row < p.pool_rows)
-            copy4_async(sbase + Ly::OFF_SCALE + (wk * NSLOT + slot_out) * (WT * 4) + tok * 4,
-                        scales + row + (tok & (box - 1)));
-        }
+      if (lane < WT / 4) {  // four tokens' scales (a page holds 16 or more)
+        const int tok = 4 * lane;
+        const int row = my_rows[stage * kMaxBoxes + (tok >> box_shift)];
+        if (row < p.pool_rows)
+          copy16_async(sbase + Ly::OFF_SCALE + (wk * NSLOT + slot_out) * (WT * 4) + tok * 4,
+                       scales + row + (tok & (box - 1)));
+        copies_arrive(bar);
       }
-      copies_arrive(bar);
     }
     __syncwarp();
     if (++slot_out == NSLOT) slot_out = 0;
@@ -497,9 +523,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
       for (int h = tid; h < p.nq; h += Ly::THREADS)
         p.lse[static_cast<long long>(b) * p.nq + h] = -INFINITY;
     if (p.by_row)
-      for (int r = tid; r < rows_per_seq; r += Ly::THREADS) p.ws_cut[b * rows_per_seq + r].end = 0;
+      for (int r = tid; r < rows_per_seq; r += Ly::THREADS) p.ws_cut[b * rows_per_seq + r].first = -1;
   }
-  if (!p.by_row && lane == 0 && half == 0) p.ws_cut[worker].end = 0;
+  if (!p.by_row && lane == 0 && half == 0) p.ws_cut[worker].first = -1;
 
   // Accumulator fragments (16 x 8): rows r0 and r0 + 8 (tokens or columns of
   // V), columns 2 quad and 2 quad + 1 (q heads of the block).
@@ -847,21 +873,23 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
     const bool begins = at.tile0 == 0, ends = !uniform && at.tile0 + at.tiles == at.nt;
     const bool cta_whole =
         uniform && spots[0].z == 0 &&
-        row0 + at.nt == slice_start(total, active, (blockIdx.x + 1) * NW);
+        row0 + at.nt == cta_s1;
     if (begins && lane == 0 && half == 0) {
       // The worker in whose slice a row begins says who shares it.
-      const bool cut = !(ends || cta_whole);
       DecodeCut d;
-      d.first = row0;
-      d.end = cut ? row0 + at.nt : 0;
-      d.total = total;
       d.b = at.b;
       d.rr = at.rr;
-      d.active = active;
-      d.pad = 0;
+      d.first = d.last = d.one_first = d.one_last = -1;
+      if (!(ends || cta_whole)) {
+        d.first = worker;
+        d.last = slices.owner(row0 + at.nt - 1);
+        d.one_first = uniform;
+        d.one_last = d.last % NW == NW - 1 && slices.start(d.last + 1) == row0 + at.nt &&
+                     slices.start(d.last - NW + 1) >= row0;
+      }
       if (p.by_row)
         p.ws_cut[at.b * rows_per_seq + at.rr] = d;
-      else if (cut)
+      else if (d.first >= 0)
         p.ws_cut[worker] = d;
     }
     const float oscale = Q8 ? sref * (1.f / kPScale) : 1.f;
@@ -1008,17 +1036,15 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__
   const int units = blockDim.x / COLS;
   griddep_wait();
   const DecodeCut c = p.ws_cut[blockIdx.x];
-  if (c.end == 0) return;
-  const int nw = p.workers;
+  if (c.first < 0) return;
+  const int nw = p.workers, w0 = c.first, w1 = c.last;
   const int g = c.rr / p.hblocks, hrow = g * p.group + (c.rr % p.hblocks) * p.piece_rows;
   const int heads = min(p.piece_rows, (g + 1) * p.group - hrow);
   // The pieces, in list order: of the row's first CTA, one per worker from the
   // row's first worker on (one in all if the CTA lies in the row altogether);
   // one of each CTA between; and of its last CTA again one per worker, or one.
-  const int w0 = slice_owner(c.total, c.active, c.first), w1 = slice_owner(c.total, c.active, c.end - 1);
   const int cta0 = w0 / nw, cta1 = w1 / nw;
-  const bool one0 = cta0 != cta1 && w0 % nw == 0 && slice_start(c.total, c.active, w0) == c.first;
-  const bool one1 = w1 % nw == nw - 1 && slice_start(c.total, c.active, w1 + 1) == c.end;
+  const bool one0 = cta0 != cta1 && c.one_first > 0, one1 = c.one_last > 0;
   const int head_n = cta0 == cta1 ? w1 - w0 + 1 : (one0 ? 1 : nw - w0 % nw);
   const int mid_n = max(cta1 - cta0 - 1, 0);
   const int tail_n = cta0 == cta1 ? 0 : (one1 ? 1 : w1 % nw + 1);
