@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(256)
     paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
   constexpr int VECS = HD / 8;        // 16-byte vectors per row
   constexpr int LOADS = HD / 128;     // rows (K, V) a warp takes one after the other
+  griddep_launch_dependents();        // a decode that follows may be set up meanwhile
   const int lane = threadIdx.x & 31;
   const int nkv = p.pool.nkv;
   const int groups = (nkv + p.heads_per_item - 1) / p.heads_per_item;

@@ -86,22 +86,20 @@ struct DecodeLayout {
   static constexpr int MT = WT / 16;             // m-tiles of K Q^T
   static constexpr int MO = HD / 16;             // m-tiles of V^T P^T
   static constexpr int HEADS = 8 * PW;
-  static constexpr int CD = 32;                  // columns summed over the warps at a time
-  static constexpr int C_STRIDE = CD + 8;
+  static constexpr int C_STRIDE = HD + 8;        // floats of a head's O where workers sum theirs
   static constexpr int OFF_SCALE = NW * NSLOT * SLOT;
-  static constexpr int OFF_SUM = OFF_SCALE + (Q8 ? NW * NSLOT * WT * 4 : 0);  // [NW][HEADS][C_STRIDE]
-  static constexpr int OFF_ML = OFF_SUM + NW * HEADS * C_STRIDE * 4;  // [NW][HEADS] (m, l)
+  static constexpr int OFF_ENDS = OFF_SCALE + (Q8 ? NW * NSLOT * WT * 4 : 0);  // [THREADS] 64-bit
+  static constexpr int OFF_ML = OFF_ENDS + THREADS * 8;  // [NW][HEADS] (m, l)
   static constexpr int OFF_BAR = OFF_ML + NW * HEADS * 8;
   // [NW][kDecStages] pool rows of the tile's boxes, and the mask of absent pages
   static constexpr int OFF_ROWS = OFF_BAR + 2 * NW * NSLOT * 8;  // (full, and empty for pairs)
   static constexpr int OFF_BAD = OFF_ROWS + NW * kDecStages * kMaxBoxes * 4;
   static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;  // spots, scan, abort flag
   static constexpr int SMEM_BYTES = OFF_MISC + NW * 16 + THREADS / 32 * 8 + 16;
-  static_assert(THREADS * 8 <= NW * HEADS * C_STRIDE * 4, "the scan's ends lie where O is summed later");
-  static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0 && OFF_SUM % 16 == 0,
+  static_assert(HEADS * C_STRIDE * 4 <= NSLOT * SLOT, "a worker's O fits its slots");
+  static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0,
                 "shared memory alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-  static_assert(HEADS * (CD / 2) <= THREADS, "a thread per column pair");
   static_assert(WT / 16 <= kMaxBoxes && NSLOT / 2 + 2 <= kDecStages, "page table of a warp");
 };
 
@@ -359,6 +357,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
   griddep_launch_dependents();
   // Swizzled copies need a 1024-byte aligned base (which the launch gives).
   if ((sbase & 1023u) != 0) {
+    griddep_wait();
     if (tid == 0 && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusLayout);
     // Nothing to join (by row: no more rows than CTAs).
     if (p.by_row ? tid == 0 : lane == 0 && half == 0)
@@ -378,12 +377,19 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
     if (wk == 0) *abort_flag = 0;
     fence_mbar_init();
   }
+  if (tid == 0) {
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+  }
+  // Launched as a programmatic dependent of whatever is ahead on the stream:
+  // nothing above reads or writes global memory that another kernel does.
+  griddep_wait();
   const int rows_per_seq = p.pool.nkv * p.hblocks;
   const int worker = blockIdx.x * NW + wk;
   DecodeSlices sl_;
   decode_slices<WT, NW, PW>(p, rows_per_seq,
                             reinterpret_cast<long long*>(smem + Ly::OFF_MISC + NW * 16),
-                            reinterpret_cast<long long*>(smem + Ly::OFF_SUM), spots, &sl_);
+                            reinterpret_cast<long long*>(smem + Ly::OFF_ENDS), spots, &sl_);
   const DecodeSlices slices = sl_;
   const int cta_w0 = static_cast<int>(blockIdx.x) * NW;
   const BoundedWait wait{abort_flag, p.status, p.timeout_ns, nullptr, 0u, 0};
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
 
   // ------------------------------------------- the worker's stream of copies
   // Copy u of the worker is K (u even) or V (u odd) of its tile u / 2, in slot
-  // u % NSLOT.  Where K of a tile goes out, its page ids were loaded one tile
+  // u % NSLOT.  Where K of a tile goes out, its page ids were loaded two tiles
   // before (and are looked at only now, so that nothing waits for them); the
   // rows they give are kept for V.
   const int ps = 1 << p.pool.page_shift;
@@ -430,23 +436,30 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
   DecodeWalk ahead = at;  // the tile whose K goes out next
   int aj = 0;             // its index in ahead's segment
   int issued = 0, slot_out = 0;
-  int next_t = -1, next_id = 0;  // lane i: first token of its box i (-1: none), and its page
-  int next_g = 0;
+  // Lane i: first token of box i (-1: none), its page id and the kv head, for
+  // the next two tiles whose K goes out.
+  int next_t[2] = {-1, -1}, next_id[2] = {0, 0}, next_g[2] = {0, 0};
+  int queued = 0;         // of them
   bool more = at.tiles > 0;
   auto look_up = [&]() {
-    // To the next segment, or to the end of the slice.
-    if (more && aj >= ahead.tiles) {
+    next_t[0] = next_t[1];
+    next_id[0] = next_id[1];
+    next_g[0] = next_g[1];
+    next_t[1] = -1;
+    if (!more) return;
+    const int t = (ahead.tile0 + aj * ahead.step) * WT + (lane << box_shift);
+    if (lane < boxes && t < ahead.n) {
+      next_t[1] = t;
+      next_id[1] = __ldg(p.pool.table + ahead.b * p.pool.table_stride + (t >> p.pool.page_shift));
+    }
+    next_g[1] = ahead.rr / p.hblocks;
+    ++queued;
+    // To the next tile: of the segment, of the next one, or there is none.
+    if (++aj >= ahead.tiles) {
       ahead.template next<WT>(p, rows_per_seq);
       aj = 0;
       more = ahead.tiles > 0;
     }
-    next_t = -1;
-    const int t = (ahead.tile0 + aj * ahead.step) * WT + (lane << box_shift);
-    if (more && lane < boxes && t < ahead.n) {
-      next_t = t;
-      next_id = __ldg(p.pool.table + ahead.b * p.pool.table_stride + (t >> p.pool.page_shift));
-    }
-    next_g = ahead.rr / p.hblocks;
   };
   auto send = [&](const CUtensorMap* m, const float* scales, int stage) {
     const uint32_t bar = full0 + 8 * slot_out, dst = ring + slot_out * Ly::SLOT;
@@ -476,10 +489,11 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
   auto take_rows = [&](int stage) {
     int row = p.pool_rows;
     bool bad = false;
-    if (next_t >= 0) {
-      bad = static_cast<unsigned>(next_id) >= static_cast<unsigned>(p.pool.num_pages);
-      if (!bad) row = static_cast<int>(pool_row(p.pool, next_id, next_g, next_t & (ps - 1)));
+    if (next_t[0] >= 0) {
+      bad = static_cast<unsigned>(next_id[0]) >= static_cast<unsigned>(p.pool.num_pages);
+      if (!bad) row = static_cast<int>(pool_row(p.pool, next_id[0], next_g[0], next_t[0] & (ps - 1)));
     }
+    --queued;
     const uint32_t badm = __ballot_sync(0xFFFFFFFFu, bad);
     if (badm != 0u && bad && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusPage);
     if (lane < boxes) my_rows[stage * kMaxBoxes + lane] = row;
@@ -492,21 +506,20 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
     const int stage = (issued >> 1) & (kDecStages - 1);
     if (issued & 1) {
       send(&p.tm_v, p.pool.v_scales, stage);
-    } else if (more) {
+    } else if (queued > 0) {
       take_rows(stage);
       send(&p.tm_k, p.pool.k_scales, stage);
-      ++aj;
       look_up();
     }
   };
   if (half == 0) {
     look_up();
-    if ((p.debug_flags & kDebugDropArrive) && blockIdx.x == 0 && wk == 0 && more) {
+    look_up();
+    if ((p.debug_flags & kDebugDropArrive) && blockIdx.x == 0 && wk == 0 && queued > 0) {
       // Fault injection: the worker's first copy is never sent.
       take_rows(0);
       slot_out = 1;
       issued = 1;
-      ++aj;
       look_up();
     }
 #pragma unroll 1
@@ -894,10 +907,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
     }
     const float oscale = Q8 ? sref * (1.f / kPScale) : 1.f;
     if (uniform) {
-      // One piece for the CTA: the workers' m and l, then their O, 32 columns
-      // at a time, summed in worker order.  (The only row of every warp here.)
+      // One piece for the CTA: the workers' m and l, then their O, summed in
+      // worker order.  (The only row of every warp here.)
       float2* mls = reinterpret_cast<float2*>(smem + Ly::OFF_ML);
-      float* summed = reinterpret_cast<float*>(smem + Ly::OFF_SUM);
       if (r0 == 0) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -930,42 +942,43 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
             p.lse[orow] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.69314718055994531f;
         }
       }
+      // The slots have been read (the barrier above): worker w's O goes there.
+      constexpr int RING = NSLOT * Ly::SLOT;
 #pragma unroll
-      for (int cc = 0; cc < HD / Ly::CD; ++cc) {
-        if (cc > 0) __syncthreads();
+      for (int j = 0; j < 2; ++j) {
+        float* dst = reinterpret_cast<float*>(smem + wk * RING) +
+                     (8 * half + 2 * quad + j) * Ly::C_STRIDE;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float* dst = summed + (wk * HEADS + 8 * half + 2 * quad + j) * Ly::C_STRIDE;
-#pragma unroll
-          for (int k = 0; k < Ly::CD / 16; ++k) {
-            const float* a = o[cc * (Ly::CD / 16) + k][0];
-            if constexpr (Q8) {  // rows r0, r0 + 8 of the m-tile: columns 2 r0 and 2 r0 + 1
-              *reinterpret_cast<float2*>(dst + 16 * k + 2 * r0) =
-                  make_float2(a[j] * f[j], a[2 + j] * f[j]);
-            } else {
-              dst[16 * k + r0] = a[j] * f[j];
-              dst[16 * k + 8 + r0] = a[2 + j] * f[j];
-            }
+        for (int i = 0; i < MO; ++i) {
+          if constexpr (Q8) {  // rows r0, r0 + 8 of the m-tile: columns 2 r0 and 2 r0 + 1
+            *reinterpret_cast<float2*>(dst + 16 * i + 2 * r0) =
+                make_float2(o[i][0][j] * f[j], o[i][0][2 + j] * f[j]);
+          } else {
+            dst[16 * i + r0] = o[i][0][j] * f[j];
+            dst[16 * i + 8 + r0] = o[i][0][2 + j] * f[j];
           }
         }
-        __syncthreads();
-        const int r = tid / (Ly::CD / 2), d = 2 * (tid % (Ly::CD / 2));  // column pairs
-        if (r < row_heads) {
-          float2 y = make_float2(0.f, 0.f);
+      }
+      __syncthreads();
+      for (int i = tid; i < HEADS * (HD / 4); i += Ly::THREADS) {
+        const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
+        if (r >= row_heads) break;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const float2 z =
-                *reinterpret_cast<const float2*>(summed + (w * HEADS + r) * Ly::C_STRIDE + d);
-            y.x += z.x;
-            y.y += z.y;
-          }
-          if (cta_whole)
-            *reinterpret_cast<uint32_t*>(
-                p.out + (static_cast<long long>(at.b) * p.nq + hrow + r) * HD + cc * Ly::CD + d) =
-                pack_bf16x2(y.x, y.y);
-          else
-            *reinterpret_cast<float2*>(p.ws_o + (piece * HEADS + r) * HD + cc * Ly::CD + d) = y;
+        for (int w = 0; w < NW; ++w) {
+          const float4 z = *reinterpret_cast<const float4*>(
+              smem + w * RING + (r * Ly::C_STRIDE + d) * sizeof(float));
+          y.x += z.x;
+          y.y += z.y;
+          y.z += z.z;
+          y.w += z.w;
         }
+        if (cta_whole)
+          *reinterpret_cast<uint2*>(
+              p.out + (static_cast<long long>(at.b) * p.nq + hrow + r) * HD + d) =
+              make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+        else
+          *reinterpret_cast<float4*>(p.ws_o + (piece * HEADS + r) * HD + d) = y;
       }
     } else {
       // This warp's own row, or its piece of one: straight from the registers.
@@ -1019,24 +1032,21 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
 }
 
 // Joins the pieces of the rows that were cut.  Block (x, y): row x of the
-// batch, or (where there are more rows than CTAs) the row that begins in worker
-// x's slice; and of its q heads the y-th part.  Most blocks of a large batch
-// find nothing to do.  A programmatic dependent of the decode kernel.  A unit of
-// HD / 4 threads takes one head and every `groups`-th of its pieces, each
-// thread 4 columns; the groups are summed in shared memory.  Each warp reads
-// the pieces' (m, l) itself, while its first loads of O are in flight: two
-// round trips to L2 in all.
+// batch, and of its q heads the y-th part; or, where there are more rows than
+// CTAs, every gridDim.y-th of the rows that begin in the slices of CTA x's
+// workers.  A programmatic dependent of the decode kernel.  A unit of HD / 4
+// threads takes one head and every `groups`-th of its pieces, each thread 4
+// columns; the groups are summed in shared memory.  Each warp reads the
+// pieces' (m, l) itself, while its first loads of O are in flight: two round
+// trips to L2 per row.
 constexpr int kJoinBatch = 4;  // loads of O in flight per thread
 
 template <int HD>
-__global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+__device__ __forceinline__ void join_row(const PagedDecodeParams& p, const DecodeCut& c, int part_of,
+                                         int parts, float4* sums) {
   constexpr int COLS = HD / 4;
-  __shared__ float4 part[512];
   const int tid = threadIdx.x, lane = tid & 31, j = tid % COLS, unit = tid / COLS;
   const int units = blockDim.x / COLS;
-  griddep_wait();
-  const DecodeCut c = p.ws_cut[blockIdx.x];
-  if (c.first < 0) return;
   const int nw = p.workers, w0 = c.first, w1 = c.last;
   const int g = c.rr / p.hblocks, hrow = g * p.group + (c.rr % p.hblocks) * p.piece_rows;
   const int heads = min(p.piece_rows, (g + 1) * p.group - hrow);
@@ -1056,8 +1066,8 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__
     return 2LL * (cta1 * nw + i - mid_n);
   };
   // This block's heads, and how many groups share the pieces of one.
-  const int per = (heads + gridDim.y - 1) / gridDim.y;
-  const int ra = blockIdx.y * per, rb = min(heads, ra + per);
+  const int per = (heads + parts - 1) / parts;
+  const int ra = part_of * per, rb = min(heads, ra + per);
   int groups = 1;
   while (2 * groups * per <= units && 2 * groups <= pieces) groups *= 2;
   const int y = unit % groups;
@@ -1103,11 +1113,11 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__
     }
     if (groups > 1) {
       __syncthreads();
-      part[tid] = acc;
+      sums[tid] = acc;
       __syncthreads();
       if (y == 0) {
         for (int k = 1; k < groups; ++k) {
-          const float4 z = part[tid + k * COLS];
+          const float4 z = sums[tid + k * COLS];
           acc.x += z.x;
           acc.y += z.y;
           acc.z += z.z;
@@ -1123,6 +1133,25 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__
       if (j == 0 && p.lse != nullptr)
         p.lse[orow] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
     }
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+  __shared__ float4 part[512];
+  const int lane = threadIdx.x & 31;
+  const int nw = p.workers;
+  griddep_launch_dependents();
+  griddep_wait();
+  // By CTA: lane i looks at worker i's row.
+  uint32_t mine = 1u;
+  if (!p.by_row)
+    mine = __ballot_sync(0xFFFFFFFFu, lane < nw && p.ws_cut[blockIdx.x * nw + lane].first >= 0);
+  for (int turn = 0; mine != 0u; mine &= mine - 1u, ++turn) {
+    if (!p.by_row && turn % static_cast<int>(gridDim.y) != static_cast<int>(blockIdx.y)) continue;
+    const DecodeCut c = p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * nw + __ffs(static_cast<int>(mine)) - 1];
+    if (c.first < 0) return;
+    join_row<HD>(p, c, p.by_row ? blockIdx.y : 0, p.by_row ? gridDim.y : 1, part);
   }
 }
 

@@ -89,6 +89,12 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
     cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8, PW>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Ly::SMEM_BYTES);
+    // The join asks for the decode kernel's division of the SM's memory, so
+    // that the SMs need not change it between the two.
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(cpattn::paged_join_kernel<HD>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaFuncSetAttribute(paged decode)");
     ready = true;
   }
@@ -110,24 +116,33 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
   p->workers = Ly::NW;
   p->piece_rows = Ly::HEADS;
   p->by_row = rows_all <= p->num_ctas ? 1 : 0;
-  cpattn::paged_decode_kernel<HD, Q8, PW><<<p->num_ctas, Ly::THREADS, Ly::SMEM_BYTES, st>>>(*p);
-  cpattn_status s = after_launch(ctx, st, "paged decode launch");
-  if (s != CPATTN_OK || tiles == 1) return s;  // rows of one tile are never cut
-  // Few rows: one block per row and as many heads as fill the GPU, each with
-  // the threads for many pieces.  Many rows have few pieces each.
-  cudaLaunchConfig_t cfg = {};
-  const int blocks = p->by_row ? static_cast<int>(rows_all) : p->num_ctas * Ly::NW;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks),
-                     static_cast<unsigned>(std::min({std::max(1, 2 * ctx->num_sms / blocks), p->group,
-                                                     Ly::HEADS})));
-  cfg.blockDim = dim3(p->by_row ? 512 : 256);
-  cfg.stream = st;
+  // Both kernels are programmatic dependents of what is ahead of them: their
+  // launch overlaps its end, and they wait for it before they touch memory.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p->num_ctas));
+  cfg.blockDim = dim3(Ly::THREADS);
+  cfg.dynamicSmemBytes = Ly::SMEM_BYTES;
+  cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, cpattn::paged_join_kernel<HD>, *p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, cpattn::paged_decode_kernel<HD, Q8, PW>, *p);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "paged decode launch");
+  cpattn_status s = after_launch(ctx, st, "paged decode launch");
+  if (s != CPATTN_OK || tiles == 1) return s;  // rows of one tile are never cut
+  // Few rows: one block per row and as many parts of its heads as fill the
+  // GPU, each with the threads for many pieces.  Many rows have few pieces
+  // each: four blocks per CTA of the decode share the rows that begin there.
+  const int blocks = p->by_row ? static_cast<int>(rows_all) : p->num_ctas;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks),
+                     p->by_row ? static_cast<unsigned>(std::min(
+                                     {std::max(1, 2 * ctx->num_sms / blocks), p->group, Ly::HEADS}))
+                               : 4u);
+  cfg.blockDim = dim3(p->by_row ? 512 : 256);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, cpattn::paged_join_kernel<HD>, *p);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "paged join launch");
   return after_launch(ctx, st, "paged join launch");
 }
