@@ -31,11 +31,10 @@
 // the workers in turn, sums their O in shared memory, in worker order, and
 // leaves one piece.
 //
-// A worker is one warp for up to 8 q heads per kv head, and two (each with 8
-// heads, on the same slots) for up to 16: a warp's O then takes HD / 4
-// registers and 12 to 16 warps fit an SM.  Latency of dependent instructions
-// bounds a warp here, so warps count for more than the conversions that a
-// pair does twice: with 8 warps of 16 heads, 1x128k e4m3 took 59 us.
+// A worker is one warp, and a row up to 16 q heads of a kv head: its O then
+// takes up to HD / 2 registers, and 8 to 16 warps fit an SM.  (Two warps of 8
+// heads on the same slots convert everything twice: 1x128k e4m3 took 40 us
+// where one warp of 16 heads takes 28.)
 //
 // e4m3 (Q8): K and V are converted to fp16 (exact) in registers; mma.sync on
 // e4m3 operands takes the same conversions and adds fp32 additions (measured
@@ -64,20 +63,24 @@ namespace cpattn {
 constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7
 constexpr float kMinSref = 7.888609052210118e-31f;  // 2^-100: kPScale / s_ref stays finite
 constexpr float kRaise = 8.f;                    // m is raised when a logit exceeds it by this
-constexpr int kDecStages = 8;                    // tiles whose pages a warp remembers (power of two)
-constexpr int kMaxBoxes = 4;                     // page pieces of a tile
+constexpr int kDecStages = 8;                    // tiles whose absent pages a worker remembers
+#ifndef CPATTN_NW128
+#define CPATTN_NW128 8
+#endif
+constexpr int kNw128 = CPATTN_NW128;
 
-// PW: warps per worker, 8 q heads each.  NW workers per CTA with NSLOT slots
-// of SLOT bytes each, 192 KB in all; WT tokens per tile.  Registers set the
-// number of warps: 16 at HD = 128, 12 at HD = 256 -- 8 for bf16 and one warp
-// per worker, whose tiles of 16 tokens (the least) take 8 KB.
-template <int HD, bool Q8, int PW>
+// NB: blocks of 8 q heads of a row (1: groups of up to 8 heads; 2: the rest).
+// NW workers per CTA with NSLOT slots of SLOT bytes each, 192 KB in all; WT
+// tokens per tile.  Registers set the number of warps: with NB = 1, 16 at
+// HD = 128 and 12 at HD = 256; else 8, as for bf16 at HD = 256, whose tiles of
+// 16 tokens (the least) take 8 KB.
+template <int HD, bool Q8, int NB>
 struct DecodeLayout {
   static constexpr int ESZ = Q8 ? 1 : 2;
-  static constexpr bool WIDE = HD == 256 && !Q8 && PW == 1;
-  static constexpr int NW = HD == 128 ? 16 / PW : (WIDE ? 8 : 12 / PW);
-  static constexpr int THREADS = 32 * NW * PW;
-  static constexpr int SLOT = PW == 2 || WIDE ? 8192 : 4096;
+  static constexpr bool BIG = NB == 2 || (HD == 256 && !Q8);
+  static constexpr int NW = BIG ? 8 : (HD == 128 ? kNw128 : 12);
+  static constexpr int THREADS = 32 * NW;
+  static constexpr int SLOT = BIG || NW == 8 ? 8192 : 4096;
   static constexpr int NSLOT = 196608 / (NW * SLOT);
   static constexpr int WT = SLOT / (HD * ESZ);
   static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : 6);
@@ -85,22 +88,20 @@ struct DecodeLayout {
   static constexpr int NBOX = HD / BOXW;         // column blocks of a tile
   static constexpr int MT = WT / 16;             // m-tiles of K Q^T
   static constexpr int MO = HD / 16;             // m-tiles of V^T P^T
-  static constexpr int HEADS = 8 * PW;
+  static constexpr int HEADS = 8 * NB;
   static constexpr int C_STRIDE = HD + 8;        // floats of a head's O where workers sum theirs
   static constexpr int OFF_SCALE = NW * NSLOT * SLOT;
   static constexpr int OFF_ENDS = OFF_SCALE + (Q8 ? NW * NSLOT * WT * 4 : 0);  // [THREADS] 64-bit
   static constexpr int OFF_ML = OFF_ENDS + THREADS * 8;  // [NW][HEADS] (m, l)
   static constexpr int OFF_BAR = OFF_ML + NW * HEADS * 8;
-  // [NW][kDecStages] pool rows of the tile's boxes, and the mask of absent pages
-  static constexpr int OFF_ROWS = OFF_BAR + 2 * NW * NSLOT * 8;  // (full, and empty for pairs)
-  static constexpr int OFF_BAD = OFF_ROWS + NW * kDecStages * kMaxBoxes * 4;
+  static constexpr int OFF_BAD = OFF_BAR + NW * NSLOT * 8;  // [NW][kDecStages] absent boxes of a tile
   static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;  // spots, scan, abort flag
   static constexpr int SMEM_BYTES = OFF_MISC + NW * 16 + THREADS / 32 * 8 + 16;
   static_assert(HEADS * C_STRIDE * 4 <= NSLOT * SLOT, "a worker's O fits its slots");
   static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0,
                 "shared memory alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-  static_assert(WT / 16 <= kMaxBoxes && NSLOT / 2 + 2 <= kDecStages, "page table of a warp");
+  static_assert(NSLOT / 2 + 3 <= kDecStages, "tiles between their look-up and their use");
 };
 
 // A row that the workers first .. last share.  one_first, one_last: the whole
@@ -118,8 +119,8 @@ struct PagedDecodeParams {
   const __nv_bfloat16* q;     // [num_seqs][NQ][HD]
   __nv_bfloat16* out;
   float* lse;                 // or null
-  float* ws_o;                // [2 * workers][8 PW][HD] O of a worker's first / last row
-  float2* ws_ml;              // [2 * workers][8 PW] its m and l
+  float* ws_o;                // [2 * workers][8 NB][HD] O of a worker's first / last row
+  float2* ws_ml;              // [2 * workers][8 NB] its m and l
   // The cut row that begins in a worker's slice; by row, where there are no
   // more rows than CTAs, else by worker.
   DecodeCut* ws_cut;          // [workers]
@@ -129,13 +130,13 @@ struct PagedDecodeParams {
   int debug_flags;
   int by_row;                 // ws_cut is indexed by row
   int workers;                // per CTA
-  int piece_rows;             // 8 PW
+  int piece_rows;             // 8 NB
   int num_ctas;               // CTAs of the decode kernel
-  int num_seqs, nq, group, hblocks;  // hblocks: blocks of 8 PW q heads per kv head
+  int num_seqs, nq, group, hblocks;  // hblocks: blocks of 8 NB q heads per kv head
   float scale_log2;
 };
 
-enum : int { kSiteDecFull = 9, kSiteDecEmpty = 10 };  // after the prefill's sites
+enum : int { kSiteDecFull = 9 };  // after the prefill's sites
 
 // ------------------------------------------------------------------ mma.sync
 // c (16 x 8) = (ZERO ? 0 : c) + A (16 x 16) B (16 x 8).
@@ -281,13 +282,12 @@ struct DecodeWalk {
 // Whole block: the slices, and where each worker's one begins: spot[w] =
 // (b, rr, tile0).  `ends` (shared memory): per thread, the list index behind
 // its sequences.
-template <int WT, int NW, int PW>
+template <int WT, int NW>
 __device__ __forceinline__ void decode_slices(const PagedDecodeParams& p, int rows_per_seq,
                                               long long* warp_sum, long long* ends, int4* spot,
                                               DecodeSlices* out) {
-  constexpr int WARPS = NW * PW;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.num_seqs + 32 * WARPS - 1) / (32 * WARPS);
+  const int per = (p.num_seqs + 32 * NW - 1) / (32 * NW);
   const int b0 = min(p.num_seqs, tid * per), b1 = min(p.num_seqs, b0 + per);
   const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
   long long sum = 0;
@@ -306,20 +306,20 @@ __device__ __forceinline__ void decode_slices(const PagedDecodeParams& p, int ro
   __syncthreads();
   long long base = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
+  for (int w = 0; w < NW; ++w) {
     if (w < warp) base += warp_sum[w];
     total += warp_sum[w];
   }
   ends[tid] = (base + inc) * rows_per_seq;
   out->init(total * rows_per_seq, static_cast<long long>(gridDim.x) * NW);
   __syncthreads();
-  // The first warp of each worker looks for its slice's first tile: the first
+  // Each worker looks for its slice's first tile: the first
   // thread whose sequences end behind it, then among that thread's sequences.
-  const int worker = blockIdx.x * NW + warp / PW;
-  if (warp % PW == 0 && worker < out->active) {
+  const int worker = blockIdx.x * NW + warp;
+  if (worker < out->active) {
     const long long s0 = out->start(worker);
     int t = 0;
-    for (int k = 0; k < WARPS; ++k) {
+    for (int k = 0; k < NW; ++k) {
       const uint32_t behind = __ballot_sync(0xFFFFFFFFu, ends[32 * k + lane] > s0);
       if (behind != 0u) {
         t = 32 * k + __ffs(static_cast<int>(behind)) - 1;
@@ -333,7 +333,7 @@ __device__ __forceinline__ void decode_slices(const PagedDecodeParams& p, int ro
       if (s0 < a + n) {
         const int rr = static_cast<int>(div_count(s0 - a, nt));
         if (lane == 0)
-          spot[warp / PW] = make_int4(b, rr, static_cast<int>(s0 - a - static_cast<long long>(rr) * nt), 0);
+          spot[warp] = make_int4(b, rr, static_cast<int>(s0 - a - static_cast<long long>(rr) * nt), 0);
         break;
       }
       a += n;
@@ -343,36 +343,33 @@ __device__ __forceinline__ void decode_slices(const PagedDecodeParams& p, int ro
 }
 
 // ------------------------------------------------------------------ kernel
-template <int HD, bool Q8, int PW>
-__global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
+template <int HD, bool Q8, int NB>
+__global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
-  using Ly = DecodeLayout<HD, Q8, PW>;
+  using Ly = DecodeLayout<HD, Q8, NB>;
   constexpr int WT = Ly::WT, MT = Ly::MT, MO = Ly::MO, NSLOT = Ly::NSLOT, NW = Ly::NW;
-  constexpr int HEADS = Ly::HEADS, NB = 1;
+  constexpr int HEADS = Ly::HEADS;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int wk = (tid >> 5) / PW;    // worker of the CTA
-  const int half = (tid >> 5) % PW;  // which 8 heads; warp 0 of a pair issues the copies
+  const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5;  // wk: worker of the CTA
   griddep_launch_dependents();
   // Swizzled copies need a 1024-byte aligned base (which the launch gives).
   if ((sbase & 1023u) != 0) {
     griddep_wait();
     if (tid == 0 && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusLayout);
     // Nothing to join (by row: no more rows than CTAs).
-    if (p.by_row ? tid == 0 : lane == 0 && half == 0)
+    if (p.by_row ? tid == 0 : lane == 0)
       p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * NW + wk].first = -1;
     return;
   }
   const uint32_t ring = sbase + wk * (NSLOT * Ly::SLOT);
-  const uint32_t full0 = sbase + Ly::OFF_BAR + wk * (16 * NSLOT), empty0 = full0 + 8 * NSLOT;
+  const uint32_t full0 = sbase + Ly::OFF_BAR + wk * (8 * NSLOT);
   int4* spots = reinterpret_cast<int4*>(smem + Ly::OFF_MISC);
   volatile int* abort_flag =
       reinterpret_cast<volatile int*>(smem + Ly::OFF_MISC + NW * 16 + Ly::THREADS / 4);
-  if (lane == 0 && half == 0) {
+  if (lane == 0) {
     for (int s = 0; s < NSLOT; ++s) {
       mbar_init(full0 + 8 * s, Q8 ? 1 + WT / 4 : 1);  // (Q8: the copies of the scales arrive too)
-      mbar_init(empty0 + 8 * s, 1);           // the other warp of a pair has read the slot
     }
     if (wk == 0) *abort_flag = 0;
     fence_mbar_init();
@@ -387,7 +384,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
   const int rows_per_seq = p.pool.nkv * p.hblocks;
   const int worker = blockIdx.x * NW + wk;
   DecodeSlices sl_;
-  decode_slices<WT, NW, PW>(p, rows_per_seq,
+  decode_slices<WT, NW>(p, rows_per_seq,
                             reinterpret_cast<long long*>(smem + Ly::OFF_MISC + NW * 16),
                             reinterpret_cast<long long*>(smem + Ly::OFF_ENDS), spots, &sl_);
   const DecodeSlices slices = sl_;
@@ -423,109 +420,120 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
 
   // ------------------------------------------- the worker's stream of copies
   // Copy u of the worker is K (u even) or V (u odd) of its tile u / 2, in slot
-  // u % NSLOT.  Where K of a tile goes out, its page ids were loaded two tiles
-  // before (and are looked at only now, so that nothing waits for them); the
-  // rows they give are kept for V.
+  // u % NSLOT.  A slot should be refilled the moment it has been read, so what
+  // the next copy needs is in registers by then: `cur` is the tile whose V goes
+  // out next, `next` the one whose K does, and `raw` the page ids of the tile
+  // behind it, loaded but not looked at.
   const int ps = 1 << p.pool.page_shift;
   const int box = min(ps, WT), box_shift = min(p.pool.page_shift, Ly::WT_SHIFT);
   const int boxes = WT >> box_shift;
-  volatile int* my_rows =
-      reinterpret_cast<volatile int*>(smem + Ly::OFF_ROWS) + wk * (kDecStages * kMaxBoxes);
   volatile uint32_t* my_bad =
       reinterpret_cast<volatile uint32_t*>(smem + Ly::OFF_BAD) + wk * kDecStages;
-  DecodeWalk ahead = at;  // the tile whose K goes out next
+  DecodeWalk ahead = at;  // the tile whose page ids are loaded next
   int aj = 0;             // its index in ahead's segment
-  int issued = 0, slot_out = 0;
-  // Lane i: first token of box i (-1: none), its page id and the kv head, for
-  // the next two tiles whose K goes out.
-  int next_t[2] = {-1, -1}, next_id[2] = {0, 0}, next_g[2] = {0, 0};
-  int queued = 0;         // of them
-  bool more = at.tiles > 0;
-  auto look_up = [&]() {
-    next_t[0] = next_t[1];
-    next_id[0] = next_id[1];
-    next_g[0] = next_g[1];
-    next_t[1] = -1;
-    if (!more) return;
+  // Lane i: first token of box i (-1: none), its page id, and the kv head.
+  int raw_t = -1, raw_id = 0, raw_g = 0;
+  bool raw_any = false, next_any = false;
+  int next_row = 0, cur_row = 0;      // lane i: pool row of box i
+  int next_scale = 0, cur_scale = 0;  // Q8: lane i: pool row of tokens 4 i .., or -1
+  int resolved = 0, issued = 0, slot_out = 0;
+  auto load_raw = [&]() {
+    raw_any = ahead.tiles > 0;
+    raw_t = -1;
+    if (!raw_any) return;
     const int t = (ahead.tile0 + aj * ahead.step) * WT + (lane << box_shift);
+    raw_g = ahead.rr / p.hblocks;
     if (lane < boxes && t < ahead.n) {
-      next_t[1] = t;
-      next_id[1] = __ldg(p.pool.table + ahead.b * p.pool.table_stride + (t >> p.pool.page_shift));
+      raw_t = t;
+      raw_id = __ldg(p.pool.table + ahead.b * p.pool.table_stride + (t >> p.pool.page_shift));
     }
-    next_g[1] = ahead.rr / p.hblocks;
-    ++queued;
-    // To the next tile: of the segment, of the next one, or there is none.
     if (++aj >= ahead.tiles) {
       ahead.template next<WT>(p, rows_per_seq);
       aj = 0;
-      more = ahead.tiles > 0;
     }
   };
-  auto send = [&](const CUtensorMap* m, const float* scales, int stage) {
-    const uint32_t bar = full0 + 8 * slot_out, dst = ring + slot_out * Ly::SLOT;
-    if (lane == 0) mbar_arrive_expect_tx(bar, Ly::SLOT);
-    if (lane < boxes) {
-      const int row = my_rows[stage * kMaxBoxes + lane];
-#pragma unroll
-      for (int c = 0; c < Ly::NBOX; ++c)
-        tma_load_3d(dst + c * (WT * 128) + (lane << box_shift) * 128, m, bar, c * Ly::BOXW, 0, row);
+  // raw becomes next.  A box's row is where it starts, or p.pool_rows (out of
+  // range: TMA fills zeros) when it lies behind the last token or its page is
+  // absent.
+  auto resolve = [&]() {
+    next_any = raw_any;
+    bool bad = false;
+    next_row = p.pool_rows;
+    if (raw_t >= 0) {
+      bad = static_cast<unsigned>(raw_id) >= static_cast<unsigned>(p.pool.num_pages);
+      if (!bad) next_row = static_cast<int>(pool_row(p.pool, raw_id, raw_g, raw_t & (ps - 1)));
     }
-    if constexpr (Q8) {
-      if (lane < WT / 4) {  // four tokens' scales (a page holds 16 or more)
-        const int tok = 4 * lane;
-        const int row = my_rows[stage * kMaxBoxes + (tok >> box_shift)];
-        if (row < p.pool_rows)
-          copy16_async(sbase + Ly::OFF_SCALE + (wk * NSLOT + slot_out) * (WT * 4) + tok * 4,
-                       scales + row + (tok & (box - 1)));
-        copies_arrive(bar);
+    const uint32_t badm = __ballot_sync(0xFFFFFFFFu, bad);
+    if (bad && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusPage);
+    if (lane == 0) my_bad[resolved & (kDecStages - 1)] = badm;
+    ++resolved;
+    if (Q8) {
+      const int tok = 4 * lane;
+      const int row = __shfl_sync(0xFFFFFFFFu, next_row, (tok & (WT - 1)) >> box_shift);
+      next_scale = tok < WT && row < p.pool_rows ? row + (tok & (box - 1)) : -1;
+    }
+  };
+  auto send = [&](const CUtensorMap* m, const float* scales, int row, int scale_row) {
+    const uint32_t bar = full0 + 8 * slot_out, dst = ring + slot_out * Ly::SLOT;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, Ly::SLOT);
+#pragma unroll
+      for (int c = 0; c < Ly::NBOX; ++c) tma_load_3d(dst + c * (WT * 128), m, bar, c * Ly::BOXW, 0, row);
+    }
+    if (boxes > 1) {
+      if (lane > 0 && lane < boxes) {
+#pragma unroll
+        for (int c = 0; c < Ly::NBOX; ++c)
+          tma_load_3d(dst + c * (WT * 128) + (lane << box_shift) * 128, m, bar, c * Ly::BOXW, 0, row);
       }
     }
-    __syncwarp();
+    if (Q8 && lane < WT / 4) {  // four tokens' scales (a page holds 16 or more)
+      if (scale_row >= 0)
+        copy16_async(sbase + Ly::OFF_SCALE + (wk * NSLOT + slot_out) * (WT * 4) + 16 * lane,
+                     scales + scale_row);
+      copies_arrive(bar);
+    }
     if (++slot_out == NSLOT) slot_out = 0;
     ++issued;
   };
-  // The row of a lane's box: where it starts, or p.pool_rows (out of range:
-  // TMA fills zeros) when it lies behind the last token or its page is absent.
-  auto take_rows = [&](int stage) {
-    int row = p.pool_rows;
-    bool bad = false;
-    if (next_t[0] >= 0) {
-      bad = static_cast<unsigned>(next_id[0]) >= static_cast<unsigned>(p.pool.num_pages);
-      if (!bad) row = static_cast<int>(pool_row(p.pool, next_id[0], next_g[0], next_t[0] & (ps - 1)));
-    }
-    --queued;
-    const uint32_t badm = __ballot_sync(0xFFFFFFFFu, bad);
-    if (badm != 0u && bad && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusPage);
-    if (lane < boxes) my_rows[stage * kMaxBoxes + lane] = row;
-    if (lane == 0) my_bad[stage] = badm;
-    __syncwarp();
+  auto advance = [&]() {
+    cur_row = next_row;
+    cur_scale = next_scale;
+    resolve();
+    load_raw();
   };
   // The next copy, if there is one: called NSLOT times at first, then once for
   // every slot read.
   auto issue = [&]() {
-    const int stage = (issued >> 1) & (kDecStages - 1);
     if (issued & 1) {
-      send(&p.tm_v, p.pool.v_scales, stage);
-    } else if (queued > 0) {
-      take_rows(stage);
-      send(&p.tm_k, p.pool.k_scales, stage);
-      look_up();
+      send(&p.tm_v, p.pool.v_scales, cur_row, cur_scale);
+    } else if (next_any) {
+      send(&p.tm_k, p.pool.k_scales, next_row, next_scale);
+      advance();
     }
   };
-  if (half == 0) {
-    look_up();
-    look_up();
-    if ((p.debug_flags & kDebugDropArrive) && blockIdx.x == 0 && wk == 0 && queued > 0) {
-      // Fault injection: the worker's first copy is never sent.
-      take_rows(0);
-      slot_out = 1;
-      issued = 1;
-      look_up();
-    }
-#pragma unroll 1
-    for (int i = 0; i < NSLOT; ++i)
-      if (issued == i) issue();
+  load_raw();
+  {
+    // (The second tile's page ids are on their way before the first's are
+    // looked at.)
+    const int t0 = raw_t, id0 = raw_id, g0 = raw_g;
+    const bool any0 = raw_any;
+    load_raw();
+    const int t1 = raw_t, id1 = raw_id, g1 = raw_g;
+    const bool any1 = raw_any;
+    raw_t = t0, raw_id = id0, raw_g = g0, raw_any = any0;
+    resolve();
+    raw_t = t1, raw_id = id1, raw_g = g1, raw_any = any1;
   }
+  if ((p.debug_flags & kDebugDropArrive) && blockIdx.x == 0 && wk == 0 && next_any) {
+    // Fault injection: the worker's first copy is never sent.
+    slot_out = 1;
+    issued = 1;
+    advance();
+  }
+#pragma unroll 1
+  for (int i = 0; i < NSLOT; ++i)
+    if (issued == i) issue();
 
   // Sequences without tokens: zeros, and an LSE of -infinity.
   for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
@@ -538,7 +546,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
     if (p.by_row)
       for (int r = tid; r < rows_per_seq; r += Ly::THREADS) p.ws_cut[b * rows_per_seq + r].first = -1;
   }
-  if (!p.by_row && lane == 0 && half == 0) p.ws_cut[worker].first = -1;
+  if (!p.by_row && lane == 0) p.ws_cut[worker].first = -1;
 
   // Accumulator fragments (16 x 8): rows r0 and r0 + 8 (tokens or columns of
   // V), columns 2 quad and 2 quad + 1 (q heads of the block).
@@ -553,31 +561,20 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
     if (ok && !mbar_try_wait(full0 + 8 * slot, phase)) ok = wait(full0 + 8 * slot, phase, kSiteDecFull);
     __syncwarp();
   };
-  // The slot has been read by every lane: the next copy goes out (of a pair,
-  // the first warp sends it once the second has read the slot too).
-  auto release = [&]() {
-    __syncwarp();
+  auto release = [&]() {  // the slot has been read by every lane
     ok = __all_sync(0xFFFFFFFFu, ok);
-    if (PW == 2 && half == 1) {
-      if (lane == 0) mbar_arrive(empty0 + 8 * slot);
-    } else if (PW == 2) {
-      if (ok && !mbar_try_wait(empty0 + 8 * slot, phase))
-        ok = wait(empty0 + 8 * slot, phase, kSiteDecEmpty);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-    }
     if (++slot == NSLOT) {
       slot = 0;
       phase ^= 1u;
     }
     ++used;
-    if (half == 0 && ok) issue();
+    if (ok) issue();
   };
 
   for (; at.tiles > 0; at.template next<WT>(p, rows_per_seq)) {
     const int g = at.rr / p.hblocks;
-    const int hrow = g * p.group + (at.rr % p.hblocks) * HEADS;  // the row's first q head
-    const int h0 = hrow + 8 * half;                             // this warp's
-    const int heads = min(8, (g + 1) * p.group - h0);           // (may be negative: none)
+    const int h0 = g * p.group + (at.rr % p.hblocks) * HEADS;  // the row's first q head
+    const int heads = min(HEADS, (g + 1) * p.group - h0);
 
     // B fragments of Q^T, this lane's head (r0 of each block of 8): bf16 as it
     // is, dims 16 ks + 2 quad + {0, 1} and + 8; or (Q8) fp16 scaled by a power
@@ -589,7 +586,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
     for (int nb = 0; nb < NB; ++nb) {
       const bool here = 8 * nb + r0 < heads;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          p.q + (static_cast<long long>(at.b) * p.nq + (here ? h0 + 8 * nb + r0 : hrow)) * HD);
+          p.q + (static_cast<long long>(at.b) * p.nq + (here ? h0 + 8 * nb + r0 : h0)) * HD);
       uint32_t big = 0;
 #pragma unroll
       for (int ks = 0; ks < HD / 16; ++ks) {
@@ -887,7 +884,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
     const bool cta_whole =
         uniform && spots[0].z == 0 &&
         row0 + at.nt == cta_s1;
-    if (begins && lane == 0 && half == 0) {
+    if (begins && lane == 0) {
       // The worker in whose slice a row begins says who shares it.
       DecodeCut d;
       d.b = at.b;
@@ -912,57 +909,55 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
       float2* mls = reinterpret_cast<float2*>(smem + Ly::OFF_ML);
       if (r0 == 0) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          mls[wk * HEADS + 8 * half + 2 * quad + j] = make_float2(m[0][j], l[0][j]);
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            mls[wk * HEADS + 8 * nb + 2 * quad + j] = make_float2(m[nb][j], l[nb][j]);
       }
       __syncthreads();
       const long long piece = 2LL * blockIdx.x * NW;
-      const int row_heads = min(HEADS, (g + 1) * p.group - hrow);
-      float f[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = 8 * half + 2 * quad + j;
-        float mm = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mls[w * HEADS + r].x);
-        const float mref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float2 ml = mls[w * HEADS + r];
-          sum = fmaf(ex2_approx(ml.x - mref), ml.y, sum);
-        }
-        f[j] = ex2_approx(m[0][j] - mref) * oscale;
-        // sum = 0: every page of the row was absent.
-        if (cta_whole) f[j] = sum == 0.f ? 0.f : f[j] / sum;
-        if (wk == 0 && r0 == 0 && r < row_heads) {
-          const long long orow = static_cast<long long>(at.b) * p.nq + hrow + r;
-          if (!cta_whole)
-            p.ws_ml[piece * HEADS + r] = make_float2(mm, sum);
-          else if (p.lse != nullptr)
-            p.lse[orow] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.69314718055994531f;
-        }
-      }
       // The slots have been read (the barrier above): worker w's O goes there.
       constexpr int RING = NSLOT * Ly::SLOT;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float* dst = reinterpret_cast<float*>(smem + wk * RING) +
-                     (8 * half + 2 * quad + j) * Ly::C_STRIDE;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < MO; ++i) {
-          if constexpr (Q8) {  // rows r0, r0 + 8 of the m-tile: columns 2 r0 and 2 r0 + 1
-            *reinterpret_cast<float2*>(dst + 16 * i + 2 * r0) =
-                make_float2(o[i][0][j] * f[j], o[i][0][2 + j] * f[j]);
-          } else {
-            dst[16 * i + r0] = o[i][0][j] * f[j];
-            dst[16 * i + 8 + r0] = o[i][0][2 + j] * f[j];
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * nb + 2 * quad + j;
+          float mm = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mls[w * HEADS + r].x);
+          const float mref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const float2 ml = mls[w * HEADS + r];
+            sum = fmaf(ex2_approx(ml.x - mref), ml.y, sum);
+          }
+          float f = ex2_approx(m[nb][j] - mref) * oscale;
+          // sum = 0: every page of the row was absent.
+          if (cta_whole) f = sum == 0.f ? 0.f : f / sum;
+          if (wk == 0 && r0 == 0 && r < heads) {
+            const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
+            if (!cta_whole)
+              p.ws_ml[piece * HEADS + r] = make_float2(mm, sum);
+            else if (p.lse != nullptr)
+              p.lse[orow] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.69314718055994531f;
+          }
+          float* dst = reinterpret_cast<float*>(smem + wk * RING) + r * Ly::C_STRIDE;
+#pragma unroll
+          for (int i = 0; i < MO; ++i) {
+            if constexpr (Q8) {  // rows r0, r0 + 8 of the m-tile: columns 2 r0 and 2 r0 + 1
+              *reinterpret_cast<float2*>(dst + 16 * i + 2 * r0) =
+                  make_float2(o[i][nb][j] * f, o[i][nb][2 + j] * f);
+            } else {
+              dst[16 * i + r0] = o[i][nb][j] * f;
+              dst[16 * i + 8 + r0] = o[i][nb][2 + j] * f;
+            }
           }
         }
-      }
       __syncthreads();
       for (int i = tid; i < HEADS * (HD / 4); i += Ly::THREADS) {
         const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
-        if (r >= row_heads) break;
+        if (r >= heads) break;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
@@ -975,7 +970,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
         }
         if (cta_whole)
           *reinterpret_cast<uint2*>(
-              p.out + (static_cast<long long>(at.b) * p.nq + hrow + r) * HD + d) =
+              p.out + (static_cast<long long>(at.b) * p.nq + h0 + r) * HD + d) =
               make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
         else
           *reinterpret_cast<float4*>(p.ws_o + (piece * HEADS + r) * HD + d) = y;
@@ -985,41 +980,44 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
       const bool whole = begins && ends;
       const long long piece = 2LL * worker + (begins ? 1 : 0);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = 2 * quad + j;  // of this warp's 8 heads
-        const float sum = l[0][j];
-        const float f = whole ? (sum == 0.f ? 0.f : oscale / sum) : oscale;
-        const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
-        const long long prow = piece * HEADS + 8 * half + r;
-        if (r0 == 0 && r < heads) {
-          if (!whole)
-            p.ws_ml[prow] = make_float2(m[0][j], sum);
-          else if (p.lse != nullptr)
-            p.lse[orow] = sum == 0.f ? -INFINITY : (m[0][j] + __log2f(sum)) * 0.69314718055994531f;
-        }
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < MO; ++i) {
-          float2 y = make_float2(o[i][0][j] * f, o[i][0][2 + j] * f);
-          int d = 16 * i + 2 * r0;
-          if constexpr (!Q8) {
-            // Rows r0 and r0 + 8 are columns r0 and r0 + 8: a neighbour's value
-            // makes a pair.
-            const bool odd = (r0 & 1) != 0;
-            const float z = __shfl_xor_sync(0xFFFFFFFFu, odd ? y.x : y.y, 4);
-            y = odd ? make_float2(z, y.y) : make_float2(y.x, z);
-            d = 16 * i + (odd ? r0 + 7 : r0);
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * nb + 2 * quad + j;
+          const float sum = l[nb][j];
+          const float f = whole ? (sum == 0.f ? 0.f : oscale / sum) : oscale;
+          const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
+          const long long prow = piece * HEADS + r;
+          if (r0 == 0 && r < heads) {
+            if (!whole)
+              p.ws_ml[prow] = make_float2(m[nb][j], sum);
+            else if (p.lse != nullptr)
+              p.lse[orow] =
+                  sum == 0.f ? -INFINITY : (m[nb][j] + __log2f(sum)) * 0.69314718055994531f;
           }
-          if (r < heads) {
-            if (whole)
-              *reinterpret_cast<uint32_t*>(p.out + orow * HD + d) = pack_bf16x2(y.x, y.y);
-            else
-              *reinterpret_cast<float2*>(p.ws_o + prow * HD + d) = y;
+#pragma unroll
+          for (int i = 0; i < MO; ++i) {
+            float2 y = make_float2(o[i][nb][j] * f, o[i][nb][2 + j] * f);
+            int d = 16 * i + 2 * r0;
+            if constexpr (!Q8) {
+              // Rows r0 and r0 + 8 are columns r0 and r0 + 8: a neighbour's
+              // value makes a pair.
+              const bool odd = (r0 & 1) != 0;
+              const float z = __shfl_xor_sync(0xFFFFFFFFu, odd ? y.x : y.y, 4);
+              y = odd ? make_float2(z, y.y) : make_float2(y.x, z);
+              d = 16 * i + (odd ? r0 + 7 : r0);
+            }
+            if (r < heads) {
+              if (whole)
+                *reinterpret_cast<uint32_t*>(p.out + orow * HD + d) = pack_bf16x2(y.x, y.y);
+              else
+                *reinterpret_cast<float2*>(p.ws_o + prow * HD + d) = y;
+            }
           }
         }
-      }
     }
   }
-  if (!ok && half == 0) {
+  if (!ok) {
     // Let copies already sent land before this CTA can exit.
     for (; used < issued; ++used) {
       mbar_wait_drain(full0 + 8 * slot, phase, 200ull * 1000 * 1000);
@@ -1039,7 +1037,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, PW>::THREADS, 1)
 // columns; the groups are summed in shared memory.  Each warp reads the
 // pieces' (m, l) itself, while its first loads of O are in flight: two round
 // trips to L2 per row.
-constexpr int kJoinBatch = 4;  // loads of O in flight per thread
+constexpr int kJoinBatch = 8;  // loads of O in flight per thread
+constexpr int kJoinThreads = 1024;
 
 template <int HD>
 __device__ __forceinline__ void join_row(const PagedDecodeParams& p, const DecodeCut& c, int part_of,
@@ -1137,8 +1136,8 @@ __device__ __forceinline__ void join_row(const PagedDecodeParams& p, const Decod
 }
 
 template <int HD>
-__global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
-  __shared__ float4 part[512];
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+  __shared__ float4 part[kJoinThreads];
   const int lane = threadIdx.x & 31;
   const int nw = p.workers;
   griddep_launch_dependents();

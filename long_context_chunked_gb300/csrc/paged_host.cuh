@@ -79,14 +79,14 @@ DecodeWorkspace decode_workspace(const cpattn_ctx* ctx) {
   return w;
 }
 
-template <int HD, bool Q8, int PW>
+template <int HD, bool Q8, int NB>
 cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
                             cpattn::PagedDecodeParams* p, cudaStream_t st) {
-  using Ly = cpattn::DecodeLayout<HD, Q8, PW>;
+  using Ly = cpattn::DecodeLayout<HD, Q8, NB>;
   static_assert(Ly::NW <= 16 && Ly::NW * Ly::HEADS <= 128, "decode_workspace");
   bool& ready = ctx->decode_ready[HD == 256][Q8];
   if (!ready) {
-    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8, PW>,
+    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8, NB>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Ly::SMEM_BYTES);
     // The join asks for the decode kernel's division of the SM's memory, so
@@ -128,7 +128,7 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, cpattn::paged_decode_kernel<HD, Q8, PW>, *p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, cpattn::paged_decode_kernel<HD, Q8, NB>, *p);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "paged decode launch");
   cpattn_status s = after_launch(ctx, st, "paged decode launch");
   if (s != CPATTN_OK || tiles == 1) return s;  // rows of one tile are never cut
@@ -140,7 +140,7 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
                      p->by_row ? static_cast<unsigned>(std::min(
                                      {std::max(1, 2 * ctx->num_sms / blocks), p->group, Ly::HEADS}))
                                : 4u);
-  cfg.blockDim = dim3(p->by_row ? 512 : 256);
+  cfg.blockDim = dim3(p->by_row ? cpattn::kJoinThreads : 256);
   cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, cpattn::paged_join_kernel<HD>, *p);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "paged join launch");
@@ -275,7 +275,6 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
   p.num_seqs = num_seqs;
   p.nq = c.num_q_heads;
   p.group = c.num_q_heads / c.num_kv_heads;
-  // Up to 8 q heads per kv head: one warp each worker; else two, 16 heads.
   const bool one = p.group <= 8;
   p.hblocks = one ? 1 : (p.group + 15) / 16;
   p.scale_log2 = c.softmax_scale * 1.4426950408889634f;
