@@ -27,9 +27,11 @@
 // pieces, which a second kernel joins in list order, so that results do not
 // depend on timing:
 //   m = max m_i,  O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
-// A CTA whose whole slice lies in one row (long contexts) deals its tiles to
-// the workers in turn, sums their O in shared memory, in worker order, and
-// leaves one piece.
+// A CTA whose whole slice lies in one row deals its tiles to the workers in
+// turn, sums their O in shared memory, in worker order, and leaves one piece:
+// neighbouring tiles read at the same time keep DRAM 15 % faster than 8 streams
+// per SM.  So where there are few rows and every one is worth a CTA or more,
+// the CTAs are dealt to the rows first (each row a whole number of them).
 //
 // A worker is one warp, and a row up to 16 q heads of a kv head: its O then
 // takes up to HD / 2 registers, and 8 to 16 warps fit an SM.  (Two warps of 8
@@ -63,6 +65,7 @@ namespace cpattn {
 constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7
 constexpr float kMinSref = 7.888609052210118e-31f;  // 2^-100: kPScale / s_ref stays finite
 constexpr float kRaise = 8.f;                    // m is raised when a logit exceeds it by this
+constexpr int kDecMaxHeads = 16;                 // of a row
 constexpr int kDecStages = 8;                    // tiles whose absent pages a worker remembers
 #ifndef CPATTN_NW128
 #define CPATTN_NW128 8
@@ -104,11 +107,12 @@ struct DecodeLayout {
   static_assert(NSLOT / 2 + 3 <= kDecStages, "tiles between their look-up and their use");
 };
 
-// A row that the workers first .. last share.  one_first, one_last: the whole
-// slice of first's CTA (of last's CTA) lies in the row and is one piece.
-// first < 0: there is none.
+// A row in several pieces, by their places in the workspace, in list order:
+// head0, then the first places of the workers head_w + 1 .. (n_head in all),
+// those of the CTAs mid_cta .. (n_mid) and of the workers tail_w .. (n_tail).
+// n_head + n_mid + n_tail == 0: not in pieces.
 struct DecodeCut {
-  int b, rr, first, last, one_first, one_last, pad[2];
+  int b, rr, head0, head_w, n_head, mid_cta, n_mid, tail_w, n_tail, pad[3];
 };
 
 struct PagedDecodeParams {
@@ -280,10 +284,15 @@ struct DecodeWalk {
 };
 
 // Whole block: the slices, and where each worker's one begins: spot[w] =
-// (b, rr, tile0).  `ends` (shared memory): per thread, the list index behind
-// its sequences.
+// (b, rr, tile0); or, where the CTAs are dealt to the rows, this CTA's row and
+// share: spot[0] = (b, rr, its number among the row's CTAs, their number),
+// and true is returned.  `ends` (shared memory): per thread, the list index
+// behind its sequences.
+//   Dealt to the rows: row r takes the CTAs round(P_r n / total) ..
+// round(P_r+1 n / total) - 1 of n, P the tiles of the rows before it, if that
+// leaves every row a CTA and no CTA more than 1.2 times the mean.
 template <int WT, int NW>
-__device__ __forceinline__ void decode_slices(const PagedDecodeParams& p, int rows_per_seq,
+__device__ __forceinline__ bool decode_slices(const PagedDecodeParams& p, int rows_per_seq,
                                               long long* warp_sum, long long* ends, int4* spot,
                                               DecodeSlices* out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -312,7 +321,22 @@ __device__ __forceinline__ void decode_slices(const PagedDecodeParams& p, int ro
   }
   ends[tid] = (base + inc) * rows_per_seq;
   out->init(total * rows_per_seq, static_cast<long long>(gridDim.x) * NW);
-  __syncthreads();
+  bool dealt = p.by_row != 0;  // (one thread per sequence then)
+  if (p.by_row) {
+    const long long all = out->total;
+    const int n = static_cast<int>(min(div_count(all + NW - 1, NW), static_cast<long long>(gridDim.x)));
+    const long long before = (base + inc - sum) * rows_per_seq;
+    int a = sum > 0 ? static_cast<int>(div_count(2 * before * n + all, 2 * all)) : 0;
+    for (int rr = 0; rr < rows_per_seq && sum > 0; ++rr) {
+      const int e = static_cast<int>(div_count(2 * (before + (rr + 1) * sum) * n + all, 2 * all));
+      dealt = dealt && e > a && 5 * sum * n <= 6 * all * (e - a);
+      if (a <= static_cast<int>(blockIdx.x) && static_cast<int>(blockIdx.x) < e)
+        spot[0] = make_int4(tid, rr, static_cast<int>(blockIdx.x) - a, e - a);
+      a = e;
+    }
+    if (tid == 0 && static_cast<int>(blockIdx.x) >= n) spot[0] = make_int4(0, 0, 0, 0);
+  }
+  if (__syncthreads_and(dealt)) return true;
   // Each worker looks for its slice's first tile: the first
   // thread whose sequences end behind it, then among that thread's sequences.
   const int worker = blockIdx.x * NW + warp;
@@ -340,6 +364,7 @@ __device__ __forceinline__ void decode_slices(const PagedDecodeParams& p, int ro
     }
   }
   __syncthreads();
+  return false;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -359,7 +384,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     if (tid == 0 && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusLayout);
     // Nothing to join (by row: no more rows than CTAs).
     if (p.by_row ? tid == 0 : lane == 0)
-      p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * NW + wk].first = -1;
+      p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * NW + wk] = DecodeCut{};
     return;
   }
   const uint32_t ring = sbase + wk * (NSLOT * Ly::SLOT);
@@ -384,7 +409,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   const int rows_per_seq = p.pool.nkv * p.hblocks;
   const int worker = blockIdx.x * NW + wk;
   DecodeSlices sl_;
-  decode_slices<WT, NW>(p, rows_per_seq,
+  const bool dealt = decode_slices<WT, NW>(p, rows_per_seq,
                             reinterpret_cast<long long*>(smem + Ly::OFF_MISC + NW * 16),
                             reinterpret_cast<long long*>(smem + Ly::OFF_ENDS), spots, &sl_);
   const DecodeSlices slices = sl_;
@@ -395,27 +420,42 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   at.s = at.s1 = 0;
   at.b = at.rr = at.tile0 = at.tiles = at.nt = at.n = 0;
   at.step = 1;
-  if (worker < slices.active) {
-    at.s = slices.start(worker);
-    at.s1 = slices.start(worker + 1);
-    at.b = spots[wk].x;
-    at.rr = spots[wk].y;
-    at.tile0 = spots[wk].z;
-    at.template enter<WT>(p);
-  }
-  // Whether the CTA's whole slice lies in one row (and every worker has tiles):
-  // the workers then take its tiles in turn, neighbours at the same time.
-  const long long cta_s0 = slices.start(cta_w0), cta_s1 = slices.start(cta_w0 + NW);
-  bool uniform = false;
-  if (cta_w0 + NW <= slices.active) {
-    const int nt0 = (decode_len(p, spots[0].x) + WT - 1) / WT;
-    uniform = spots[0].z + cta_s1 - cta_s0 <= nt0;
-    if (uniform) {
-      at.s = at.s1 = 0;  // (one segment)
-      at.tile0 = spots[0].z + wk;
-      at.step = NW;
-      at.tiles = static_cast<int>((cta_s1 - cta_s0 - wk + NW - 1) / NW);
+  // `uniform`: the CTA's whole slice, tiles [cta_t0, cta_t1) of its row, lies
+  // in one row; the workers take its tiles in turn.
+  bool uniform = dealt;
+  int cta_t0 = 0, cta_t1 = 0;
+  if (dealt) {
+    const int4 mine = spots[0];
+    at.b = mine.x;
+    at.rr = mine.y;
+    if (mine.w > 0) {
+      at.n = decode_len(p, at.b);
+      at.nt = (at.n + WT - 1) / WT;
+      cta_t0 = static_cast<int>(div_count(static_cast<long long>(at.nt) * mine.z, mine.w));
+      cta_t1 = static_cast<int>(div_count(static_cast<long long>(at.nt) * (mine.z + 1), mine.w));
     }
+  } else {
+    if (worker < slices.active) {
+      at.s = slices.start(worker);
+      at.s1 = slices.start(worker + 1);
+      at.b = spots[wk].x;
+      at.rr = spots[wk].y;
+      at.tile0 = spots[wk].z;
+      at.template enter<WT>(p);
+    }
+    if (cta_w0 + NW <= slices.active) {
+      const long long cta_tiles = slices.start(cta_w0 + NW) - slices.start(cta_w0);
+      const int nt0 = (decode_len(p, spots[0].x) + WT - 1) / WT;
+      uniform = spots[0].z + cta_tiles <= nt0;
+      cta_t0 = spots[0].z;
+      cta_t1 = static_cast<int>(cta_t0 + cta_tiles);
+    }
+  }
+  if (uniform) {
+    at.s = at.s1 = 0;  // (one segment)
+    at.tile0 = cta_t0 + wk;
+    at.step = NW;
+    at.tiles = max(0, (cta_t1 - at.tile0 + NW - 1) / NW);
   }
 
   // ------------------------------------------- the worker's stream of copies
@@ -544,9 +584,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       for (int h = tid; h < p.nq; h += Ly::THREADS)
         p.lse[static_cast<long long>(b) * p.nq + h] = -INFINITY;
     if (p.by_row)
-      for (int r = tid; r < rows_per_seq; r += Ly::THREADS) p.ws_cut[b * rows_per_seq + r].first = -1;
+      for (int r = tid; r < rows_per_seq; r += Ly::THREADS) p.ws_cut[b * rows_per_seq + r] = DecodeCut{};
   }
-  if (!p.by_row && lane == 0) p.ws_cut[worker].first = -1;
+  if (!p.by_row && lane == 0) p.ws_cut[worker] = DecodeCut{};
 
   // Accumulator fragments (16 x 8): rows r0 and r0 + 8 (tokens or columns of
   // V), columns 2 quad and 2 quad + 1 (q heads of the block).
@@ -571,7 +611,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     if (ok) issue();
   };
 
-  for (; at.tiles > 0; at.template next<WT>(p, rows_per_seq)) {
+  // (A worker without tiles still takes part in its CTA's sum.)
+  for (bool once = uniform && cta_t1 > cta_t0; at.tiles > 0 || once;
+       once = false, at.template next<WT>(p, rows_per_seq)) {
     const int g = at.rr / p.hblocks;
     const int h0 = g * p.group + (at.rr % p.hblocks) * HEADS;  // the row's first q head
     const int heads = min(HEADS, (g + 1) * p.group - h0);
@@ -878,29 +920,38 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nb][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nb][j], d);
-    // List index of the row's first tile; whether the row begins and ends here.
-    const long long row0 = uniform ? cta_s0 - spots[0].z : at.s - at.tile0;
-    const bool begins = at.tile0 == 0, ends = !uniform && at.tile0 + at.tiles == at.nt;
-    const bool cta_whole =
-        uniform && spots[0].z == 0 &&
-        row0 + at.nt == cta_s1;
+    // Whether the row begins and ends here, and whether it is the CTA's alone.
+    const bool begins = uniform ? cta_t0 == 0 && wk == 0 : at.tile0 == 0;
+    const bool ends = !uniform && at.tile0 + at.tiles == at.nt;
+    const bool cta_whole = uniform && cta_t0 == 0 && cta_t1 == at.nt;
     if (begins && lane == 0) {
-      // The worker in whose slice a row begins says who shares it.
-      DecodeCut d;
+      // The worker in whose slice a row begins says where its pieces are.
+      DecodeCut d = {};
       d.b = at.b;
       d.rr = at.rr;
-      d.first = d.last = d.one_first = d.one_last = -1;
-      if (!(ends || cta_whole)) {
-        d.first = worker;
-        d.last = slices.owner(row0 + at.nt - 1);
-        d.one_first = uniform;
-        d.one_last = d.last % NW == NW - 1 && slices.start(d.last + 1) == row0 + at.nt &&
-                     slices.start(d.last - NW + 1) >= row0;
+      if (dealt) {
+        if (!cta_whole) {
+          d.mid_cta = blockIdx.x;
+          d.n_mid = spots[0].w;
+        }
+      } else if (!(ends || cta_whole)) {
+        const long long row0 = (uniform ? slices.start(cta_w0) : at.s), end = row0 + at.nt;
+        const int last = slices.owner(end - 1), cta1 = last / NW;
+        const bool one_last = last % NW == NW - 1 && slices.start(last + 1) == end;
+        d.head0 = uniform ? 2 * worker : 2 * worker + 1;
+        d.head_w = worker;
+        d.n_head = uniform ? 1 : min(last, cta_w0 + NW - 1) - worker + 1;
+        if (cta1 > static_cast<int>(blockIdx.x)) {
+          d.mid_cta = blockIdx.x + 1;
+          d.n_mid = cta1 - d.mid_cta + (one_last ? 1 : 0);
+          d.tail_w = cta1 * NW;
+          d.n_tail = one_last ? 0 : last - d.tail_w + 1;
+        }
       }
       if (p.by_row)
         p.ws_cut[at.b * rows_per_seq + at.rr] = d;
-      else if (d.first >= 0)
-        p.ws_cut[worker] = d;
+      else if (d.n_head > 0)
+        p.ws_cut[worker] = d;  // (at most one row that begins here is cut: the last)
     }
     const float oscale = Q8 ? sref * (1.f / kPScale) : 1.f;
     if (uniform) {
@@ -1037,94 +1088,105 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 // columns; the groups are summed in shared memory.  Each warp reads the
 // pieces' (m, l) itself, while its first loads of O are in flight: two round
 // trips to L2 per row.
-constexpr int kJoinBatch = 8;  // loads of O in flight per thread
 constexpr int kJoinThreads = 1024;
+constexpr int kJoinPieces = 288;  // most pieces of a row: one per CTA, and the workers of two
+constexpr int kJoinBatch = 4;     // loads of O in flight per thread
+
+struct JoinShared {
+  float4 sums[kJoinThreads];
+  float weight[kDecMaxHeads][kJoinPieces];
+  float stats[kDecMaxHeads][2];  // m, l
+  int place[kJoinPieces];
+};
 
 template <int HD>
 __device__ __forceinline__ void join_row(const PagedDecodeParams& p, const DecodeCut& c, int part_of,
-                                         int parts, float4* sums) {
+                                         int parts, JoinShared& sh) {
   constexpr int COLS = HD / 4;
-  const int tid = threadIdx.x, lane = tid & 31, j = tid % COLS, unit = tid / COLS;
-  const int units = blockDim.x / COLS;
-  const int nw = p.workers, w0 = c.first, w1 = c.last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int j = tid % COLS, unit = tid / COLS, units = blockDim.x / COLS;
   const int g = c.rr / p.hblocks, hrow = g * p.group + (c.rr % p.hblocks) * p.piece_rows;
   const int heads = min(p.piece_rows, (g + 1) * p.group - hrow);
-  // The pieces, in list order: of the row's first CTA, one per worker from the
-  // row's first worker on (one in all if the CTA lies in the row altogether);
-  // one of each CTA between; and of its last CTA again one per worker, or one.
-  const int cta0 = w0 / nw, cta1 = w1 / nw;
-  const bool one0 = cta0 != cta1 && c.one_first > 0, one1 = c.one_last > 0;
-  const int head_n = cta0 == cta1 ? w1 - w0 + 1 : (one0 ? 1 : nw - w0 % nw);
-  const int mid_n = max(cta1 - cta0 - 1, 0);
-  const int tail_n = cta0 == cta1 ? 0 : (one1 ? 1 : w1 % nw + 1);
-  const int pieces = head_n + mid_n + tail_n;
-  auto slot = [&](int i) -> long long {
-    if (i < head_n) return 2LL * (w0 + i) + (i == 0 && !one0 ? 1 : 0);  // (0: a worker's last row)
-    i -= head_n;
-    if (i < mid_n) return 2LL * (cta0 + 1 + i) * nw;
-    return 2LL * (cta1 * nw + i - mid_n);
-  };
+  const int pieces = c.n_head + c.n_mid + c.n_tail;
+  for (int i = tid; i < pieces; i += blockDim.x) {
+    int at = i < c.n_head ? 2 * (c.head_w + i) : 2 * p.workers * (c.mid_cta + i - c.n_head);
+    if (i == 0 && c.n_head > 0) at = c.head0;
+    if (i >= c.n_head + c.n_mid) at = 2 * (c.tail_w + i - c.n_head - c.n_mid);
+    sh.place[i] = at * p.piece_rows;
+  }
+  __syncthreads();
   // This block's heads, and how many groups share the pieces of one.
   const int per = (heads + parts - 1) / parts;
   const int ra = part_of * per, rb = min(heads, ra + per);
   int groups = 1;
   while (2 * groups * per <= units && 2 * groups <= pieces) groups *= 2;
-  const int y = unit % groups;
-  for (int base = ra; base < rb; base += units / groups) {
-    const int r = base + unit / groups;
-    const bool mine = r < rb;
-    const float* o_at = p.ws_o + static_cast<long long>(r) * HD + 4 * j;
-    const float2* ml_at = p.ws_ml + r;
-    const long long rows = p.piece_rows;
+  const int y = unit % groups, step = units / groups;
+  // The first loads of O are in flight while the weights are made.
+  float4 o[kJoinBatch];
+  auto load = [&](int r, int i) {
+    return *reinterpret_cast<const float4*>(p.ws_o + static_cast<long long>(sh.place[i] + r) * HD + 4 * j);
+  };
+  const int r0 = ra + unit / groups;
+  if (r0 < rb) {
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k)
+      if (y + k * groups < pieces) o[k] = load(r0, y + k * groups);
+  }
+  for (int r = ra + warp; r < rb; r += blockDim.x / 32) {  // one warp per head
     float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, p.ws_ml[sh.place[i] + r].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    const float mref = m == -INFINITY ? 0.f : m;
+    for (int i = lane; i < pieces; i += 32) {
+      const float2 ml = p.ws_ml[sh.place[i] + r];
+      const float w = ex2_approx(ml.x - mref);
+      sh.weight[r][i] = w;
+      l = fmaf(w, ml.y, l);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    if (lane == 0) {
+      sh.stats[r][0] = m;
+      sh.stats[r][1] = l;
+    }
+  }
+  __syncthreads();
+  for (int base = ra; base < rb; base += step) {
+    const int r = base + unit / groups;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mine) {
-      float4 o[kJoinBatch];
-#pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k)
-        if (y + k * groups < pieces)
-          o[k] = *reinterpret_cast<const float4*>(o_at + slot(y + k * groups) * rows * HD);
-      for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml_at[slot(i) * rows].x);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-      const float mref = m == -INFINITY ? 0.f : m;
-      for (int i = lane; i < pieces; i += 32) {
-        const float2 ml = ml_at[slot(i) * rows];
-        l = fmaf(ex2_approx(ml.x - mref), ml.y, l);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    if (r < rb) {
       for (int i = y; i < pieces; i += kJoinBatch * groups) {
 #pragma unroll
         for (int k = 0; k < kJoinBatch; ++k) {
           const int ii = i + k * groups;
           if (ii < pieces) {
-            const float w = ex2_approx(ml_at[slot(ii) * rows].x - mref);
+            if (base > ra || i > y) o[k] = load(r, ii);
+            const float w = sh.weight[r][ii];
             acc.x = fmaf(w, o[k].x, acc.x);
             acc.y = fmaf(w, o[k].y, acc.y);
             acc.z = fmaf(w, o[k].z, acc.z);
             acc.w = fmaf(w, o[k].w, acc.w);
-            const int in = ii + kJoinBatch * groups;
-            if (in < pieces) o[k] = *reinterpret_cast<const float4*>(o_at + slot(in) * rows * HD);
           }
         }
       }
     }
     if (groups > 1) {
-      __syncthreads();
-      sums[tid] = acc;
+      sh.sums[tid] = acc;
       __syncthreads();
       if (y == 0) {
         for (int k = 1; k < groups; ++k) {
-          const float4 z = sums[tid + k * COLS];
+          const float4 z = sh.sums[tid + k * COLS];
           acc.x += z.x;
           acc.y += z.y;
           acc.z += z.z;
           acc.w += z.w;
         }
       }
+      __syncthreads();
     }
-    if (mine && y == 0) {
+    if (r < rb && y == 0) {
+      const float m = sh.stats[r][0], l = sh.stats[r][1];
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const long long orow = static_cast<long long>(c.b) * p.nq + hrow + r;
       *reinterpret_cast<uint2*>(p.out + orow * HD + 4 * j) =
@@ -1133,25 +1195,26 @@ __device__ __forceinline__ void join_row(const PagedDecodeParams& p, const Decod
         p.lse[orow] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
     }
   }
+  __syncthreads();  // the shared tables are reused by the next row
 }
 
 template <int HD>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
-  __shared__ float4 part[kJoinThreads];
-  const int lane = threadIdx.x & 31;
-  const int nw = p.workers;
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_join_kernel(const __grid_constant__ PagedDecodeParams p) {
+  __shared__ JoinShared sh;
+  const int lane = threadIdx.x & 31, nw = p.workers;
   griddep_launch_dependents();
   griddep_wait();
-  // By CTA: lane i looks at worker i's row.
-  uint32_t mine = 1u;
-  if (!p.by_row)
-    mine = __ballot_sync(0xFFFFFFFFu, lane < nw && p.ws_cut[blockIdx.x * nw + lane].first >= 0);
-  for (int turn = 0; mine != 0u; mine &= mine - 1u, ++turn) {
-    if (!p.by_row && turn % static_cast<int>(gridDim.y) != static_cast<int>(blockIdx.y)) continue;
-    const DecodeCut c = p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * nw + __ffs(static_cast<int>(mine)) - 1];
-    if (c.first < 0) return;
-    join_row<HD>(p, c, p.by_row ? blockIdx.y : 0, p.by_row ? gridDim.y : 1, part);
+  if (p.by_row) {
+    const DecodeCut c = p.ws_cut[blockIdx.x];
+    if (c.n_head + c.n_mid + c.n_tail > 0) join_row<HD>(p, c, blockIdx.y, gridDim.y, sh);
+    return;
   }
+  // Lane i looks at the row of worker i.
+  uint32_t some = __ballot_sync(0xFFFFFFFFu, lane < nw && p.ws_cut[blockIdx.x * nw + lane].n_head > 0);
+  for (int turn = 0; some != 0u; some &= some - 1u, ++turn)
+    if (turn % static_cast<int>(gridDim.y) == static_cast<int>(blockIdx.y))
+      join_row<HD>(p, p.ws_cut[blockIdx.x * nw + __ffs(static_cast<int>(some)) - 1], 0, 1, sh);
 }
 
 }  // namespace cpattn

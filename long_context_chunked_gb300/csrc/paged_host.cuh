@@ -59,8 +59,10 @@ int copy_grid(const cpattn_ctx* ctx, long long tokens, int hpi) {
                                                             static_cast<long long>(ctx->num_sms) * 8)));
 }
 
-// CTAs of a decode launch: at most one per SM.
-int decode_max_ctas(const cpattn_ctx* ctx) { return ctx->num_sms > 0 ? ctx->num_sms : 152; }
+// CTAs of a decode launch: at most one per SM (and the join's table of pieces).
+int decode_max_ctas(const cpattn_ctx* ctx) {
+  return std::min(ctx->num_sms > 0 ? ctx->num_sms : 152, cpattn::kJoinPieces - 32);
+}
 
 // Workspace of a decode: O, then (m, l) of every worker's first and last row,
 // then the rows that were cut.  It depends on neither the lengths nor the
