@@ -92,16 +92,24 @@ struct DecodeLayout {
   static constexpr int MT = WT / 16;             // m-tiles of K Q^T
   static constexpr int MO = HD / 16;             // m-tiles of V^T P^T
   static constexpr int HEADS = 8 * NB;
+  // Where O leaves no registers for Q, Q is read from shared memory: once for
+  // the CTA if it is uniform, else each worker has its own in the place of its
+  // third slot.
+  static constexpr bool Q_SMEM = HD * NB == 512;
+  static constexpr int Q_BYTES = HEADS * HD * 2;
   static constexpr int C_STRIDE = HD + 8;        // floats of a head's O where workers sum theirs
   static constexpr int OFF_SCALE = NW * NSLOT * SLOT;
-  static constexpr int OFF_ENDS = OFF_SCALE + (Q8 ? NW * NSLOT * WT * 4 : 0);  // [THREADS] 64-bit
+  static constexpr int OFF_Q = OFF_SCALE + (Q8 ? NW * NSLOT * WT * 4 : 0);
+  static constexpr int OFF_QEXP = OFF_Q + (Q_SMEM ? Q_BYTES : 0);  // [NW][HEADS] 2^e of each Q row
+  static constexpr int OFF_ENDS = OFF_QEXP + (Q_SMEM ? NW * HEADS * 4 : 0);  // [THREADS] 64-bit
   static constexpr int OFF_ML = OFF_ENDS + THREADS * 8;  // [NW][HEADS] (m, l)
   static constexpr int OFF_BAR = OFF_ML + NW * HEADS * 8;
   static constexpr int OFF_BAD = OFF_BAR + NW * NSLOT * 8;  // [NW][kDecStages] absent boxes of a tile
   static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;  // spots, scan, abort flag
   static constexpr int SMEM_BYTES = OFF_MISC + NW * 16 + THREADS / 32 * 8 + 16;
   static_assert(HEADS * C_STRIDE * 4 <= NSLOT * SLOT, "a worker's O fits its slots");
-  static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0,
+  static_assert(!Q_SMEM || (NSLOT == 3 && Q_BYTES <= SLOT), "a worker's Q fits a slot");
+  static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0 && OFF_Q % 16 == 0 && OFF_ENDS % 8 == 0,
                 "shared memory alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(NSLOT / 2 + 3 <= kDecStages, "tiles between their look-up and their use");
@@ -387,7 +395,6 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       p.ws_cut[p.by_row ? blockIdx.x : blockIdx.x * NW + wk] = DecodeCut{};
     return;
   }
-  const uint32_t ring = sbase + wk * (NSLOT * Ly::SLOT);
   const uint32_t full0 = sbase + Ly::OFF_BAR + wk * (8 * NSLOT);
   int4* spots = reinterpret_cast<int4*>(smem + Ly::OFF_MISC);
   volatile int* abort_flag =
@@ -451,6 +458,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       cta_t1 = static_cast<int>(cta_t0 + cta_tiles);
     }
   }
+  const int nslot = Ly::Q_SMEM && !uniform ? NSLOT - 1 : NSLOT;  // (see Q_SMEM)
+  const uint32_t ring = sbase + wk * (nslot * Ly::SLOT);
   if (uniform) {
     at.s = at.s1 = 0;  // (one segment)
     at.tile0 = cta_t0 + wk;
@@ -460,7 +469,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 
   // ------------------------------------------- the worker's stream of copies
   // Copy u of the worker is K (u even) or V (u odd) of its tile u / 2, in slot
-  // u % NSLOT.  A slot should be refilled the moment it has been read, so what
+  // u % nslot.  A slot should be refilled the moment it has been read, so what
   // the next copy needs is in registers by then: `cur` is the tile whose V goes
   // out next, `next` the one whose K does, and `raw` the page ids of the tile
   // behind it, loaded but not looked at.
@@ -533,7 +542,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
                      scales + scale_row);
       copies_arrive(bar);
     }
-    if (++slot_out == NSLOT) slot_out = 0;
+    if (++slot_out == nslot) slot_out = 0;
     ++issued;
   };
   auto advance = [&]() {
@@ -542,7 +551,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     resolve();
     load_raw();
   };
-  // The next copy, if there is one: called NSLOT times at first, then once for
+  // The next copy, if there is one: called nslot times at first, then once for
   // every slot read.
   auto issue = [&]() {
     if (issued & 1) {
@@ -572,7 +581,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     advance();
   }
 #pragma unroll 1
-  for (int i = 0; i < NSLOT; ++i)
+  for (int i = 0; i < nslot; ++i)
     if (issued == i) issue();
 
   // Sequences without tokens: zeros, and an LSE of -infinity.
@@ -603,7 +612,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   };
   auto release = [&]() {  // the slot has been read by every lane
     ok = __all_sync(0xFFFFFFFFu, ok);
-    if (++slot == NSLOT) {
+    if (++slot == nslot) {
       slot = 0;
       phase ^= 1u;
     }
@@ -618,55 +627,118 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     const int h0 = g * p.group + (at.rr % p.hblocks) * HEADS;  // the row's first q head
     const int heads = min(HEADS, (g + 1) * p.group - h0);
 
-    // B fragments of Q^T, this lane's head (r0 of each block of 8): bf16 as it
-    // is, dims 16 ks + 2 quad + {0, 1} and + 8; or (Q8) fp16 scaled by a power
-    // of two, dims 16 ks + 4 quad + {0 .. 3}, the order in which the e4m3 K
+    // B fragments of Q^T, 16 dims a step.  bf16: as it is, dims 16 ks + 2 quad +
+    // {0, 1} and + 8 of head r0 of each block.  Q8: fp16, scaled by a power of
+    // two, dims 16 ks + 4 quad + {0 .. 3}, the order in which the e4m3 K
     // fragments come out of ldmatrix.
-    uint32_t q[HD / 16][2 * NB];
+    // For the largest magnitude `big` of a head (bf16 bits): e, the exponent of
+    // the head's largest value (zeros and subnormals: -126), down = 2^-e, and
+    // 2^e, which gives it back to the logits; 2^-127, 2^-128 and 2^128 are made
+    // in two steps.
+    auto scaling = [](uint32_t big, float* down, float* up) {
+      const int e = max(static_cast<int>(big >> 7), 1) - 127;
+      const int e1 = min(e, 126), e2 = e - e1;
+      *down = __int_as_float((127 - e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 0.5f : 0.25f));
+      *up = __int_as_float((127 + e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 2.f : 4.f));
+    };
+    uint32_t q[Ly::Q_SMEM ? 1 : HD / 16][2 * NB];
     float qexp[NB];
+    // Q_SMEM: rows of HD 16-bit values, 16-byte chunks swizzled by the row.
+    const uint32_t q_at = uniform ? Ly::OFF_Q : NW * (NSLOT - 1) * Ly::SLOT + wk * Ly::Q_BYTES;
+    if constexpr (Ly::Q_SMEM) {
+      float* exps = reinterpret_cast<float*>(smem + Ly::OFF_QEXP) + (uniform ? 0 : wk * HEADS);
+      for (int r = uniform ? wk : 0; r < HEADS; r += uniform ? NW : 1) {
+        const uint2* src = reinterpret_cast<const uint2*>(
+            p.q + (static_cast<long long>(at.b) * p.nq + (r < heads ? h0 + r : h0)) * HD);
+        uint2 w[HD / 128];
+        uint32_t big = 0;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const bool here = 8 * nb + r0 < heads;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          p.q + (static_cast<long long>(at.b) * p.nq + (here ? h0 + 8 * nb + r0 : h0)) * HD);
-      uint32_t big = 0;
-#pragma unroll
-      for (int ks = 0; ks < HD / 16; ++ks) {
-        uint2 w;
-        if constexpr (Q8) {
-          w = __ldg(reinterpret_cast<const uint2*>(src) + 4 * ks + quad);
-        } else {
-          w.x = __ldg(src + 8 * ks + quad);
-          w.y = __ldg(src + 8 * ks + 4 + quad);
+        for (int i = 0; i < HD / 128; ++i) {
+          w[i] = r < heads ? __ldg(src + 32 * i + lane) : make_uint2(0u, 0u);
+          big = __vmaxu2(big, __vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu));
         }
-        if (!here) w = make_uint2(0u, 0u);
-        q[ks][2 * nb] = w.x;
-        q[ks][2 * nb + 1] = w.y;
-        if (Q8) big = __vmaxu2(big, __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu));
-      }
-      qexp[nb] = 1.f;
-      if constexpr (Q8) {
-        big = max(big & 0xFFFFu, big >> 16);
-        big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-        big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-        // e: the exponent of the head's largest value (zeros and subnormals:
-        // -126), down = 2^-e, and qexp = 2^e gives it back to the logits.
-        // 2^-127, 2^-128 and 2^128 are made in two steps.
-        const int e = max(static_cast<int>(big >> 7), 1) - 127;
-        const int e1 = min(e, 126), e2 = e - e1;
-        const float down =
-            __int_as_float((127 - e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 0.5f : 0.25f));
-        qexp[nb] = __int_as_float((127 + e1) << 23) * (e2 == 0 ? 1.f : (e2 == 1 ? 2.f : 4.f));
+        if constexpr (Q8) {
+          big = __reduce_max_sync(0xFFFFFFFFu, max(big & 0xFFFFu, big >> 16));
+          float down, up;
+          scaling(big, &down, &up);
+          if (lane == 0) exps[r] = up;
 #pragma unroll
-        for (int ks = 0; ks < HD / 16; ++ks)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t w = q[ks][2 * nb + j];
-            q[ks][2 * nb + j] = pack_f16x2(__uint_as_float(w << 16) * down,
-                                           __uint_as_float(w & 0xFFFF0000u) * down);
+          for (int i = 0; i < HD / 128; ++i) {
+            w[i].x = pack_f16x2(__uint_as_float(w[i].x << 16) * down,
+                                __uint_as_float(w[i].x & 0xFFFF0000u) * down);
+            w[i].y = pack_f16x2(__uint_as_float(w[i].y << 16) * down,
+                                __uint_as_float(w[i].y & 0xFFFF0000u) * down);
           }
+        }
+#pragma unroll
+        for (int i = 0; i < HD / 128; ++i) {
+          // Dims 4 k .. 4 k + 3, k = 32 i + lane: 8 bytes.  Q8: dims 4 a + 2 c of
+          // a 16-block go to position 2 a + 8 c.
+          const int k = 32 * i + lane;
+          const int c0 = Q8 ? 2 * (k >> 2) : k >> 1;
+          uint8_t* row = smem + q_at + r * (2 * HD);
+          if constexpr (Q8) {
+            *reinterpret_cast<uint32_t*>(row + ((c0 ^ (r & 7)) << 4) + (k & 3) * 4) = w[i].x;
+            *reinterpret_cast<uint32_t*>(row + (((c0 + 1) ^ (r & 7)) << 4) + (k & 3) * 4) = w[i].y;
+          } else {
+            *reinterpret_cast<uint2*>(row + ((c0 ^ (r & 7)) << 4) + (k & 1) * 8) = w[i];
+          }
+        }
+      }
+      if (uniform)
+        __syncthreads();
+      else
+        __syncwarp();
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) qexp[nb] = Q8 ? exps[8 * nb + r0] : 1.f;
+    } else {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const bool here = 8 * nb + r0 < heads;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+            p.q + (static_cast<long long>(at.b) * p.nq + (here ? h0 + 8 * nb + r0 : h0)) * HD);
+        uint32_t big = 0;
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          uint2 w;
+          if constexpr (Q8) {
+            w = __ldg(reinterpret_cast<const uint2*>(src) + 4 * ks + quad);
+          } else {
+            w.x = __ldg(src + 8 * ks + quad);
+            w.y = __ldg(src + 8 * ks + 4 + quad);
+          }
+          if (!here) w = make_uint2(0u, 0u);
+          q[ks][2 * nb] = w.x;
+          q[ks][2 * nb + 1] = w.y;
+          if (Q8) big = __vmaxu2(big, __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu));
+        }
+        qexp[nb] = 1.f;
+        if constexpr (Q8) {
+          big = max(big & 0xFFFFu, big >> 16);
+          big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+          big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+          float down;
+          scaling(big, &down, &qexp[nb]);
+#pragma unroll
+          for (int ks = 0; ks < HD / 16; ++ks)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t w = q[ks][2 * nb + j];
+              q[ks][2 * nb + j] = pack_f16x2(__uint_as_float(w << 16) * down,
+                                             __uint_as_float(w & 0xFFFF0000u) * down);
+            }
+        }
       }
     }
+    const uint32_t q_row = sbase + q_at + ((NB == 2 ? (oct >> 1) * 8 : 0) + r8) * (2 * HD);
+    auto q_frag = [&](int ks, uint32_t (&f)[4]) {  // [nb][b0, b1]
+      if constexpr (Ly::Q_SMEM) {
+        ldsm4(f, q_row + (((2 * ks + (oct & 1)) ^ r8) << 4));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i) f[i] = q[ks][i];
+      }
+    };
     float sl[NB][2], m[NB][2], l[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -699,6 +771,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       if constexpr (Q8) {
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ks += 2) {  // 32 dims: chunks ks and ks + 1
+          uint32_t qa[4], qb[4];
+          q_frag(ks, qa);
+          q_frag(ks + 1, qb);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             uint32_t kr[4], a[4];  // token half, then chunk, by lane octet
@@ -709,19 +784,21 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               if (ks == 0)
-                mma16816<true, true>(c[t][nb], a, q[ks][2 * nb], q[ks][2 * nb + 1]);
+                mma16816<true, true>(c[t][nb], a, qa[2 * nb], qa[2 * nb + 1]);
               else
-                mma16816<true>(c[t][nb], a, q[ks][2 * nb], q[ks][2 * nb + 1]);
+                mma16816<true>(c[t][nb], a, qa[2 * nb], qa[2 * nb + 1]);
             }
             e4m3x4_to_f16x4(kr[2], &a[0], &a[2]);
             e4m3x4_to_f16x4(kr[3], &a[1], &a[3]);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma16816<true>(c[t][nb], a, q[ks + 1][2 * nb], q[ks + 1][2 * nb + 1]);
+            for (int nb = 0; nb < NB; ++nb) mma16816<true>(c[t][nb], a, qb[2 * nb], qb[2 * nb + 1]);
           }
         }
       } else {
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {  // 16 dims: chunks 2 ks and 2 ks + 1
+          uint32_t qf[4];
+          q_frag(ks, qf);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             uint32_t a[4];
@@ -730,9 +807,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               if (ks == 0)
-                mma16816<false, true>(c[t][nb], a, q[ks][2 * nb], q[ks][2 * nb + 1]);
+                mma16816<false, true>(c[t][nb], a, qf[2 * nb], qf[2 * nb + 1]);
               else
-                mma16816<false>(c[t][nb], a, q[ks][2 * nb], q[ks][2 * nb + 1]);
+                mma16816<false>(c[t][nb], a, qf[2 * nb], qf[2 * nb + 1]);
             }
           }
         }
@@ -1072,7 +1149,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     // Let copies already sent land before this CTA can exit.
     for (; used < issued; ++used) {
       mbar_wait_drain(full0 + 8 * slot, phase, 200ull * 1000 * 1000);
-      if (++slot == NSLOT) {
+      if (++slot == nslot) {
         slot = 0;
         phase ^= 1u;
       }
