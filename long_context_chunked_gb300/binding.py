@@ -92,7 +92,7 @@ class PagedKV:
             raise ValueError("pages, scales and block_table must be on one CUDA device")
         self.k_pages, self.v_pages, self.block_table = k_pages, v_pages, block_table
         self.k_scales, self.v_scales = k_scales, v_scales
-        self.device = k_pages.device
+        self.device = k_pages.get_device()
         self.num_seqs, cols = block_table.shape
         self.num_kv_heads, self.head_dim = k_pages.shape[1], k_pages.shape[3]
         self.c = Pages(int(e4m3), k_pages.shape[2], k_pages.shape[0], cols,
@@ -184,18 +184,28 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
-def _want(name, t, dtype, shape, like=None):
-    """A contiguous CUDA tensor of this dtype and shape, on `like`'s device."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous() or (
-            like is not None and t.device != like.device):
-        raise ValueError(f"{name}: expected a contiguous {dtype} CUDA tensor {list(shape)}, got "
-                         f"{t.dtype} {list(t.shape)} on {t.device}")
+def _want(name, t, dtype, shape, device: int):
+    """A contiguous CUDA tensor of this dtype and shape, on CUDA device `device`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or device < 0 \
+            or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on CUDA device "
+                         f"{device}, got {t.dtype} {list(t.shape)} on {t.device}")
 
 
-def _workspace_bytes(workspace, like) -> int:
-    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != like.device:
+def _workspace_bytes(workspace, device: int) -> int:
+    if workspace.get_device() != device or device < 0 or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous CUDA tensor on the inputs' device")
     return workspace.numel() * workspace.element_size()
+
+
+def _stream_on(stream, device: int) -> int:
+    """`stream`, or the current stream of CUDA device `device`."""
+    if stream is None:
+        import torch
+        # (What torch.cuda.current_stream wraps in an object, at a tenth of the time.)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+    return _stream(stream)
 
 
 def _stream(stream) -> int:
@@ -222,6 +232,7 @@ class Context:
                           chunk_size, softmax_scale, int(bool(fast_p)), int(bool(v_cache_f16)),
                           PAIRING[pairing], 0 if gqa_packing else 1)
         self.v_cache_f16 = bool(v_cache_f16)
+        self.dims = (int(num_q_heads), int(num_kv_heads), int(head_dim))
         h = ctypes.c_void_p()
         st = self.lib.cpattn_create(ctypes.byref(self.cfg), ctypes.byref(h))
         if st != OK:
@@ -345,19 +356,20 @@ class Context:
     def prefill_packed(self, seq_lens, q, k, v, out, workspace, lse=None, stream=None):
         """Causal attention over whole prompts packed one behind the other:
         q, out [sum(seq_lens), NQ, HD], k, v [sum(seq_lens), NKV, HD], bf16."""
-        sl, slp = _i32(seq_lens)
-        rows = int(sl.sum(dtype=np.int64))
-        nq, nkv, hd = self.cfg.num_q_heads, self.cfg.num_kv_heads, self.cfg.head_dim
         import torch
-        _want("q", q, torch.bfloat16, (rows, nq, hd))
-        _want("k", k, torch.bfloat16, (rows, nkv, hd), q)
-        _want("v", v, torch.bfloat16, (rows, nkv, hd), q)
-        _want("out", out, torch.bfloat16, (rows, nq, hd), q)
+        n = len(seq_lens)
+        sl = (ctypes.c_int32 * n)(*[int(x) for x in seq_lens])
+        rows, dev = sum(sl), q.get_device()
+        nq, nkv, hd = self.dims
+        _want("q", q, torch.bfloat16, (rows, nq, hd), dev)
+        _want("k", k, torch.bfloat16, (rows, nkv, hd), dev)
+        _want("v", v, torch.bfloat16, (rows, nkv, hd), dev)
+        _want("out", out, torch.bfloat16, (rows, nq, hd), dev)
         if lse is not None:
-            _want("lse", lse, torch.float32, (rows, nq), q)
+            _want("lse", lse, torch.float32, (rows, nq), dev)
         self._check(self.lib.cpattn_prefill_packed(
-            self._h, len(sl), slp, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-            _ptr(workspace), _workspace_bytes(workspace, q), _stream(stream)))
+            self._h, n, sl, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse),
+            workspace.data_ptr(), _workspace_bytes(workspace, dev), _stream_on(stream, dev)))
 
     def paged_write_kv(self, pages: PagedKV, cache_lens, k_new, v_new, row_starts=None,
                        stream=None):
@@ -367,33 +379,32 @@ class Context:
         token per sequence.  cache_lens and row_starts: int32 CUDA tensors."""
         import torch
         self._check_pages(pages)
-        b = pages.num_seqs
-        rows = k_new.shape[0]
+        b, dev, rows = pages.num_seqs, pages.device, k_new.shape[0]
         shape = (rows, pages.num_kv_heads, pages.head_dim)
-        _want("k_new", k_new, torch.bfloat16, shape, pages)
-        _want("v_new", v_new, torch.bfloat16, shape, pages)
-        _want("cache_lens", cache_lens, torch.int32, (b,), pages)
+        _want("k_new", k_new, torch.bfloat16, shape, dev)
+        _want("v_new", v_new, torch.bfloat16, shape, dev)
+        _want("cache_lens", cache_lens, torch.int32, (b,), dev)
         if row_starts is not None:
-            _want("row_starts", row_starts, torch.int32, (b + 1,), pages)
+            _want("row_starts", row_starts, torch.int32, (b + 1,), dev)
         self._check(self.lib.cpattn_paged_write_kv(
-            self._h, pages.ref, b, rows, _ptr(cache_lens), _ptr(row_starts), _ptr(k_new),
-            _ptr(v_new), _stream(stream)))
+            self._h, pages.ref, b, rows, cache_lens.data_ptr(), _ptr(row_starts), k_new.data_ptr(),
+            v_new.data_ptr(), _stream_on(stream, dev)))
 
     def paged_read_kv(self, pages: PagedKV, lens, k_cache, v_cache, first=None, stream=None):
         """Read tokens first[b] (None: 0) .. lens[b] - 1 back into the striped
         caches [num_seqs, NKV, P, S, HD] of the chunked prefill."""
         import torch
         self._check_pages(pages)
-        c, b = self.cfg, pages.num_seqs
-        shape = (b, c.num_kv_heads, c.num_shards, c.shard_capacity, c.head_dim)
-        _want("k_cache", k_cache, torch.bfloat16, shape, pages)
-        _want("v_cache", v_cache, torch.float16 if self.v_cache_f16 else torch.bfloat16, shape,
-              pages)
-        _want("lens", lens, torch.int32, (b,), pages)
+        c, b, dev = self.cfg, pages.num_seqs, pages.device
+        shape = (b, pages.num_kv_heads, c.num_shards, c.shard_capacity, pages.head_dim)
+        _want("k_cache", k_cache, torch.bfloat16, shape, dev)
+        _want("v_cache", v_cache, torch.float16 if self.v_cache_f16 else torch.bfloat16, shape, dev)
+        _want("lens", lens, torch.int32, (b,), dev)
         if first is not None:
-            _want("first", first, torch.int32, (b,), pages)
-        self._check(self.lib.cpattn_paged_read_kv(self._h, pages.ref, b, _ptr(first), _ptr(lens),
-                                                  _ptr(k_cache), _ptr(v_cache), _stream(stream)))
+            _want("first", first, torch.int32, (b,), dev)
+        self._check(self.lib.cpattn_paged_read_kv(
+            self._h, pages.ref, b, _ptr(first), lens.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), _stream_on(stream, dev)))
 
     def paged_decode_workspace(self, num_seqs: int) -> int:
         """Workspace bytes of paged_decode for a batch of num_seqs sequences."""
@@ -406,20 +417,20 @@ class Context:
         the first lens[b] (int32 CUDA tensor) tokens of its pages."""
         import torch
         self._check_pages(pages)
-        b, nq = pages.num_seqs, self.cfg.num_q_heads
-        _want("q", q, torch.bfloat16, (b, nq, pages.head_dim), pages)
-        _want("out", out, torch.bfloat16, (b, nq, pages.head_dim), pages)
-        _want("lens", lens, torch.int32, (b,), pages)
+        b, nq, hd, dev = pages.num_seqs, self.dims[0], pages.head_dim, pages.device
+        _want("q", q, torch.bfloat16, (b, nq, hd), dev)
+        _want("out", out, torch.bfloat16, (b, nq, hd), dev)
+        _want("lens", lens, torch.int32, (b,), dev)
         if lse is not None:
-            _want("lse", lse, torch.float32, (b, nq), pages)
+            _want("lse", lse, torch.float32, (b, nq), dev)
         self._check(self.lib.cpattn_paged_decode(
-            self._h, pages.ref, b, _ptr(lens), _ptr(q), _ptr(out), _ptr(lse), _ptr(workspace),
-            _workspace_bytes(workspace, pages), _stream(stream)))
+            self._h, pages.ref, b, lens.data_ptr(), q.data_ptr(), out.data_ptr(), _ptr(lse),
+            workspace.data_ptr(), _workspace_bytes(workspace, dev), _stream_on(stream, dev)))
 
     def _check_pages(self, pages: PagedKV):
-        if (pages.num_kv_heads, pages.head_dim) != (self.cfg.num_kv_heads, self.cfg.head_dim):
+        if pages.num_kv_heads != self.dims[1] or pages.head_dim != self.dims[2]:
             raise ValueError(f"pages hold {pages.num_kv_heads} kv heads of {pages.head_dim}, the "
-                             f"context {self.cfg.num_kv_heads} of {self.cfg.head_dim}")
+                             f"context {self.dims[1]} of {self.dims[2]}")
 
     def sync_status(self, stream=None) -> int:
         """Synchronise and return the status code (E_TIMEOUT if a device wait expired)."""

@@ -44,19 +44,28 @@ cpattn_status check_pages(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t nu
   return check_device(ctx);
 }
 
-// kv heads a warp of the paged copies takes of one token: one while there are
-// fewer than 32 warps per SM for them, else up to four, which share the
-// token's table lookups.
-int heads_per_item(const cpattn_ctx* ctx, long long tokens) {
-  const long long rows = tokens * ctx->cfg.num_kv_heads;
-  const long long h = rows / (static_cast<long long>(std::max(ctx->num_sms, 1)) * 32);
+// kv heads a warp of the paged copies takes of its rows (`units` of them): one
+// while there are fewer than 32 warps per SM for them, else up to four, which
+// share the look-ups.
+int heads_per_item(const cpattn_ctx* ctx, long long units) {
+  const long long h = units * ctx->cfg.num_kv_heads / (static_cast<long long>(std::max(ctx->num_sms, 1)) * 32);
   return static_cast<int>(std::max(1LL, std::min<long long>({h, 4, ctx->cfg.num_kv_heads})));
 }
 
-int copy_grid(const cpattn_ctx* ctx, long long tokens, int hpi) {
-  const long long items = tokens * ((ctx->cfg.num_kv_heads + hpi - 1) / hpi);
+int copy_grid(const cpattn_ctx* ctx, long long units, int hpi) {
+  const long long items = units * ((ctx->cfg.num_kv_heads + hpi - 1) / hpi);
   return static_cast<int>(std::max(1LL, std::min<long long>((items + 7) / 8,
                                                             static_cast<long long>(ctx->num_sms) * 8)));
+}
+
+template <int ROWS>
+void launch_paged_write(const cpattn::PagedWriteParams& p, int hd, bool q8, int grid, cudaStream_t st) {
+  if (hd == 128)
+    q8 ? cpattn::paged_write_kernel<128, true, ROWS><<<grid, 256, 0, st>>>(p)
+       : cpattn::paged_write_kernel<128, false, ROWS><<<grid, 256, 0, st>>>(p);
+  else
+    q8 ? cpattn::paged_write_kernel<256, true, ROWS><<<grid, 256, 0, st>>>(p)
+       : cpattn::paged_write_kernel<256, false, ROWS><<<grid, 256, 0, st>>>(p);
 }
 
 // CTAs of a decode launch: at most one per SM (and the join's table of pieces).
@@ -177,16 +186,16 @@ cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, 
   p.status = ctx->d_status;
   p.num_seqs = num_seqs;
   p.rows = num_rows;
-  p.heads_per_item = heads_per_item(ctx, num_rows);
-  const int grid = copy_grid(ctx, num_rows, p.heads_per_item);
+  // Four rows a warp where that leaves 16 warps per SM, else one.
+  const int per = static_cast<long long>(num_rows) * ctx->cfg.num_kv_heads >=
+                          4LL * 16 * std::max(ctx->num_sms, 1) ? 4 : 1;
+  const long long units = (static_cast<long long>(num_rows) + per - 1) / per;
+  p.heads_per_item = heads_per_item(ctx, units);
+  const int grid = copy_grid(ctx, units, p.heads_per_item);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool q8 = pages->format == CPATTN_PAGES_E4M3;
-  if (ctx->cfg.head_dim == 128)
-    q8 ? cpattn::paged_write_kernel<128, true><<<grid, 256, 0, st>>>(p)
-       : cpattn::paged_write_kernel<128, false><<<grid, 256, 0, st>>>(p);
-  else
-    q8 ? cpattn::paged_write_kernel<256, true><<<grid, 256, 0, st>>>(p)
-       : cpattn::paged_write_kernel<256, false><<<grid, 256, 0, st>>>(p);
+  per == 4 ? launch_paged_write<4>(p, ctx->cfg.head_dim, q8, grid, st)
+           : launch_paged_write<1>(p, ctx->cfg.head_dim, q8, grid, st);
   return after_launch(ctx, st, "paged write launch");
 } catch (...) {
   return CPATTN_E_NOMEM;
@@ -220,8 +229,9 @@ cpattn_status cpattn_paged_read_kv(cpattn_ctx* ctx, const cpattn_pages* pages, i
   // The most tokens the lengths can ask for (they are known on the device only).
   const long long most = std::min<long long>(
       tokens, static_cast<long long>(num_seqs) * pages->max_pages * pages->page_size);
-  p.heads_per_item = heads_per_item(ctx, most);
-  const int grid = copy_grid(ctx, most, p.heads_per_item);
+  const long long runs = most / cpattn::kReadRun + num_seqs;
+  p.heads_per_item = heads_per_item(ctx, runs);
+  const int grid = copy_grid(ctx, runs, p.heads_per_item);
   const size_t smem = (static_cast<size_t>(num_seqs) + 1) * sizeof(int);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool q8 = pages->format == CPATTN_PAGES_E4M3;

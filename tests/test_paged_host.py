@@ -159,7 +159,7 @@ def test_binding_checks_tensors():
             cp.PagedKV(kw.get("k", kp), kw.get("v", kp), kw.get("table", table), kw.get("ks"),
                        kw.get("vs"))
     with pytest.raises(ValueError):
-        binding._want("q", torch.zeros(2, 3, dtype=bf), bf, (2, 3))     # not on a GPU
+        binding._want("q", torch.zeros(2, 3, dtype=bf), bf, (2, 3), -1)  # not on a GPU
 
 
 # ------------------------------------------------------------------ oracle pins
