@@ -67,26 +67,27 @@ constexpr float kMinSref = 7.888609052210118e-31f;  // 2^-100: kPScale / s_ref s
 constexpr float kRaise = 8.f;                    // m is raised when a logit exceeds it by this
 constexpr int kDecMaxHeads = 16;                 // of a row
 constexpr int kDecStages = 8;                    // tiles whose absent pages a worker remembers
-#ifndef CPATTN_NW128
-#define CPATTN_NW128 8
-#endif
-constexpr int kNw128 = CPATTN_NW128;
 
 // NB: blocks of 8 q heads of a row (1: groups of up to 8 heads; 2: the rest).
 // NW workers per CTA with NSLOT slots of SLOT bytes each, 192 KB in all; WT
-// tokens per tile.  Registers set the number of warps: with NB = 1, 16 at
-// HD = 128 and 12 at HD = 256; else 8, as for bf16 at HD = 256, whose tiles of
-// 16 tokens (the least) take 8 KB.
+// tokens per tile.  8 KB slots and 8 workers: more and smaller ones pay the
+// fixed cost of a tile more often (64 ragged at HD = 128: 16 workers with 4 KB
+// slots 80 us, 12 68 us, 8 with 8 KB 66 us) -- but for e4m3 at HD = 256 and
+// NB = 1 registers allow 12.
 template <int HD, bool Q8, int NB>
 struct DecodeLayout {
   static constexpr int ESZ = Q8 ? 1 : 2;
   static constexpr bool BIG = NB == 2 || (HD == 256 && !Q8);
-  static constexpr int NW = BIG ? 8 : (HD == 128 ? kNw128 : 12);
+  static constexpr int NW = HD == 256 && !BIG ? 12 : 8;
   static constexpr int THREADS = 32 * NW;
   static constexpr int SLOT = BIG || NW == 8 ? 8192 : 4096;
   static constexpr int NSLOT = 196608 / (NW * SLOT);
   static constexpr int WT = SLOT / (HD * ESZ);
   static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : 6);
+  // Beginning and ending a row costs a worker about as much as 40 KB of tiles;
+  // the list counts them before the row's first tile (64 ragged sequences,
+  // tiles of 16 KB: 70 us without, 62.9 with one, 59.3 with two, 58.9 with three).
+  static constexpr int ROW = 40960 / (2 * SLOT);
   static constexpr int BOXW = 128 / ESZ;         // values per 128-byte box row
   static constexpr int NBOX = HD / BOXW;         // column blocks of a tile
   static constexpr int MT = WT / 16;             // m-tiles of K Q^T
@@ -232,6 +233,13 @@ __device__ __forceinline__ int decode_len(const PagedDecodeParams& p, int b) {
   return static_cast<int>(max(0LL, min(static_cast<long long>(__ldg(p.lens + b)), room)));
 }
 
+// Units of the list that a row of sequence b takes.
+template <int WT, int ROW>
+__device__ __forceinline__ int row_units(const PagedDecodeParams& p, int b) {
+  const int n = decode_len(p, b);
+  return n > 0 ? (n + WT - 1) / WT + ROW : 0;
+}
+
 // Quotients of tile counts, which hardly ever pass 32 bits: a 64-bit division
 // takes far longer than a 32-bit one, and every warp waits for a few of these.
 __device__ __forceinline__ long long div_count(long long a, long long b) {
@@ -259,35 +267,45 @@ struct DecodeSlices {
   }
 };
 
-// A worker's way through its slice [s, s1) of the tile list, one row segment
-// at a time: tiles tile0, tile0 + step, .. (`tiles` of them) of row rr = kv head
+// A worker's way through its slice [s, s1) of the list, one row segment (`units`
+// of the list) at a time: tiles tile0, tile0 + step, .. (`tiles` of them) of row rr = kv head
 // * hblocks + head block of sequence b.  tiles == 0: the slice is done.
 struct DecodeWalk {
   long long s, s1;
-  int b, rr, tile0, tiles, step, nt, n;
+  int b, rr, tile0, tiles, units, step, nt, n;
 
-  template <int WT>
-  __device__ __forceinline__ void enter(const PagedDecodeParams& p) {
+  // To the segment that begins at unit u of row (b, rr), or behind it to the
+  // first one with tiles.
+  template <int WT, int ROW>
+  __device__ __forceinline__ void enter(const PagedDecodeParams& p, int rows_per_seq, int u) {
     n = decode_len(p, b);
     nt = (n + WT - 1) / WT;
-    tiles = static_cast<int>(min(static_cast<long long>(nt - tile0), s1 - s));
+    while (true) {
+      units = static_cast<int>(min(static_cast<long long>(nt + ROW - u), s1 - s));
+      tile0 = max(u - ROW, 0);
+      tiles = max(u + units - ROW, 0) - tile0;
+      if (tiles > 0 || s + units >= s1) return;
+      s += units;
+      u = 0;
+      step_row<WT, ROW>(p, rows_per_seq);
+    }
   }
-  template <int WT>
+  template <int WT, int ROW>
+  __device__ __forceinline__ void step_row(const PagedDecodeParams& p, int rows_per_seq) {
+    if (++rr < rows_per_seq) return;
+    rr = 0;
+    do {
+      n = decode_len(p, ++b);
+    } while (n == 0);
+    nt = (n + WT - 1) / WT;
+  }
+  template <int WT, int ROW>
   __device__ __forceinline__ void next(const PagedDecodeParams& p, int rows_per_seq) {
-    s += tiles;
-    if (s >= s1) {
-      tiles = 0;
-      return;
-    }
-    tile0 = 0;
-    if (++rr == rows_per_seq) {
-      rr = 0;
-      do {
-        n = decode_len(p, ++b);
-      } while (n == 0);
-      nt = (n + WT - 1) / WT;
-    }
-    tiles = static_cast<int>(min(static_cast<long long>(nt), s1 - s));
+    s += units;
+    tiles = 0;
+    if (s >= s1) return;
+    step_row<WT, ROW>(p, rows_per_seq);
+    enter<WT, ROW>(p, rows_per_seq, 0);
   }
 };
 
@@ -299,7 +317,7 @@ struct DecodeWalk {
 //   Dealt to the rows: row r takes the CTAs round(P_r n / total) ..
 // round(P_r+1 n / total) - 1 of n, P the tiles of the rows before it, if that
 // leaves every row a CTA and no CTA more than 1.2 times the mean.
-template <int WT, int NW>
+template <int WT, int ROW, int NW>
 __device__ __forceinline__ bool decode_slices(const PagedDecodeParams& p, int rows_per_seq,
                                               long long* warp_sum, long long* ends, int4* spot,
                                               DecodeSlices* out) {
@@ -309,7 +327,7 @@ __device__ __forceinline__ bool decode_slices(const PagedDecodeParams& p, int ro
   const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
   long long sum = 0;
   for (int b = b0; b < b1; ++b) {
-    sum += (decode_len(p, b) + WT - 1) / WT;
+    sum += row_units<WT, ROW>(p, b);
     if (p.lens[b] > room && blockIdx.x == 0 && p.status != nullptr)
       atomicCAS(p.status, kStatusOk, kStatusPage);
   }
@@ -360,7 +378,7 @@ __device__ __forceinline__ bool decode_slices(const PagedDecodeParams& p, int ro
     }
     long long a = t > 0 ? ends[t - 1] : 0;
     for (int b = t * per; b < p.num_seqs; ++b) {
-      const int nt = (decode_len(p, b) + WT - 1) / WT;
+      const int nt = row_units<WT, ROW>(p, b);
       const long long n = static_cast<long long>(nt) * rows_per_seq;
       if (s0 < a + n) {
         const int rr = static_cast<int>(div_count(s0 - a, nt));
@@ -380,7 +398,7 @@ template <int HD, bool Q8, int NB>
 __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   using Ly = DecodeLayout<HD, Q8, NB>;
-  constexpr int WT = Ly::WT, MT = Ly::MT, MO = Ly::MO, NSLOT = Ly::NSLOT, NW = Ly::NW;
+  constexpr int WT = Ly::WT, ROW = Ly::ROW, MT = Ly::MT, MO = Ly::MO, NSLOT = Ly::NSLOT, NW = Ly::NW;
   constexpr int HEADS = Ly::HEADS;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -416,7 +434,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   const int rows_per_seq = p.pool.nkv * p.hblocks;
   const int worker = blockIdx.x * NW + wk;
   DecodeSlices sl_;
-  const bool dealt = decode_slices<WT, NW>(p, rows_per_seq,
+  const bool dealt = decode_slices<WT, ROW, NW>(p, rows_per_seq,
                             reinterpret_cast<long long*>(smem + Ly::OFF_MISC + NW * 16),
                             reinterpret_cast<long long*>(smem + Ly::OFF_ENDS), spots, &sl_);
   const DecodeSlices slices = sl_;
@@ -425,7 +443,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 
   DecodeWalk at;
   at.s = at.s1 = 0;
-  at.b = at.rr = at.tile0 = at.tiles = at.nt = at.n = 0;
+  at.b = at.rr = at.tile0 = at.tiles = at.units = at.nt = at.n = 0;
   at.step = 1;
   // `uniform`: the CTA's whole slice, tiles [cta_t0, cta_t1) of its row, lies
   // in one row; the workers take its tiles in turn.
@@ -447,21 +465,26 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       at.s1 = slices.start(worker + 1);
       at.b = spots[wk].x;
       at.rr = spots[wk].y;
-      at.tile0 = spots[wk].z;
-      at.template enter<WT>(p);
+      at.template enter<WT, ROW>(p, rows_per_seq, spots[wk].z);
     }
     if (cta_w0 + NW <= slices.active) {
-      const long long cta_tiles = slices.start(cta_w0 + NW) - slices.start(cta_w0);
-      const int nt0 = (decode_len(p, spots[0].x) + WT - 1) / WT;
-      uniform = spots[0].z + cta_tiles <= nt0;
-      cta_t0 = spots[0].z;
-      cta_t1 = static_cast<int>(cta_t0 + cta_tiles);
+      const long long cta_units = slices.start(cta_w0 + NW) - slices.start(cta_w0);
+      const int4 first = spots[0];
+      if (first.z + cta_units <= row_units<WT, ROW>(p, first.x)) {
+        uniform = true;
+        at.b = first.x;
+        at.rr = first.y;
+        at.n = decode_len(p, at.b);
+        at.nt = (at.n + WT - 1) / WT;
+        cta_t0 = max(first.z - ROW, 0);
+        cta_t1 = max(static_cast<int>(first.z + cta_units) - ROW, 0);
+      }
     }
   }
   const int nslot = Ly::Q_SMEM && !uniform ? NSLOT - 1 : NSLOT;  // (see Q_SMEM)
   const uint32_t ring = sbase + wk * (nslot * Ly::SLOT);
   if (uniform) {
-    at.s = at.s1 = 0;  // (one segment)
+    at.s = at.s1 = at.units = 0;  // (one segment)
     at.tile0 = cta_t0 + wk;
     at.step = NW;
     at.tiles = max(0, (cta_t1 - at.tile0 + NW - 1) / NW);
@@ -497,7 +520,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       raw_id = __ldg(p.pool.table + ahead.b * p.pool.table_stride + (t >> p.pool.page_shift));
     }
     if (++aj >= ahead.tiles) {
-      ahead.template next<WT>(p, rows_per_seq);
+      ahead.template next<WT, ROW>(p, rows_per_seq);
       aj = 0;
     }
   };
@@ -622,7 +645,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 
   // (A worker without tiles still takes part in its CTA's sum.)
   for (bool once = uniform && cta_t1 > cta_t0; at.tiles > 0 || once;
-       once = false, at.template next<WT>(p, rows_per_seq)) {
+       once = false, at.template next<WT, ROW>(p, rows_per_seq)) {
     const int g = at.rr / p.hblocks;
     const int h0 = g * p.group + (at.rr % p.hblocks) * HEADS;  // the row's first q head
     const int heads = min(HEADS, (g + 1) * p.group - h0);
@@ -1012,7 +1035,10 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
           d.n_mid = spots[0].w;
         }
       } else if (!(ends || cta_whole)) {
-        const long long row0 = (uniform ? slices.start(cta_w0) : at.s), end = row0 + at.nt;
+        // List index behind the row's last tile.
+        const long long end =
+            uniform ? slices.start(cta_w0) - spots[0].z + ROW + at.nt
+                    : at.s + at.units + (at.nt - at.tiles);
         const int last = slices.owner(end - 1), cta1 = last / NW;
         const bool one_last = last % NW == NW - 1 && slices.start(last + 1) == end;
         d.head0 = uniform ? 2 * worker : 2 * worker + 1;
