@@ -1193,7 +1193,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 // trips to L2 per row.
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinPieces = 288;  // most pieces of a row: one per CTA, and the workers of two
-constexpr int kJoinBatch = 4;     // loads of O in flight per thread
+constexpr int kJoinBatch = 5;     // loads of O in flight per thread
 
 struct JoinShared {
   float4 sums[kJoinThreads];
@@ -1224,7 +1224,35 @@ __device__ __forceinline__ void join_row(const PagedDecodeParams& p, const Decod
   int groups = 1;
   while (2 * groups * per <= units && 2 * groups <= pieces) groups *= 2;
   const int y = unit % groups, step = units / groups;
-  // The first loads of O are in flight while the weights are made.
+  // One warp per head makes its weights; the others' first loads of O are in
+  // flight meanwhile.
+  for (int r = ra + warp; r < rb; r += blockDim.x / 32) {
+    float2 ml[kJoinPieces / 32];
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinPieces / 32; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (32 * k + lane < pieces) ml[k] = p.ws_ml[sh.place[32 * k + lane] + r];
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinPieces / 32; ++k) m = fmaxf(m, ml[k].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    const float mref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int k = 0; k < kJoinPieces / 32; ++k) {
+      if (32 * k >= pieces) break;
+      const float w = ex2_approx(ml[k].x - mref);
+      sh.weight[r][32 * k + lane] = w;
+      l = fmaf(w, ml[k].y, l);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    if (lane == 0) {
+      sh.stats[r][0] = m;
+      sh.stats[r][1] = l;
+    }
+  }
   float4 o[kJoinBatch];
   auto load = [&](int r, int i) {
     return *reinterpret_cast<const float4*>(p.ws_o + static_cast<long long>(sh.place[i] + r) * HD + 4 * j);
@@ -1234,25 +1262,6 @@ __device__ __forceinline__ void join_row(const PagedDecodeParams& p, const Decod
 #pragma unroll
     for (int k = 0; k < kJoinBatch; ++k)
       if (y + k * groups < pieces) o[k] = load(r0, y + k * groups);
-  }
-  for (int r = ra + warp; r < rb; r += blockDim.x / 32) {  // one warp per head
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, p.ws_ml[sh.place[i] + r].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    const float mref = m == -INFINITY ? 0.f : m;
-    for (int i = lane; i < pieces; i += 32) {
-      const float2 ml = p.ws_ml[sh.place[i] + r];
-      const float w = ex2_approx(ml.x - mref);
-      sh.weight[r][i] = w;
-      l = fmaf(w, ml.y, l);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-    if (lane == 0) {
-      sh.stats[r][0] = m;
-      sh.stats[r][1] = l;
-    }
   }
   __syncthreads();
   for (int base = ra; base < rb; base += step) {

@@ -151,7 +151,7 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
   const int blocks = p->by_row ? static_cast<int>(rows_all) : p->num_ctas;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks),
                      p->by_row ? static_cast<unsigned>(std::min(
-                                     {std::max(1, 2 * ctx->num_sms / blocks), p->group, Ly::HEADS}))
+                                     {std::max(1, ctx->num_sms / blocks), p->group, Ly::HEADS}))
                                : 4u);
   cfg.blockDim = dim3(p->by_row ? cpattn::kJoinThreads : 256);
   cfg.dynamicSmemBytes = 0;

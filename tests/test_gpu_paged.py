@@ -226,6 +226,29 @@ def test_decode_many_sequences(e4m3):
     _decode(c.upload(), 4, lens)
 
 
+SPLITS = [  # nq, nkv, hd, page, lens: every way in which the rows share the GPU
+    (16, 4, 128, 64, [5000, 7001, 6000, 8123, 4999, 9000, 100, 7777]),   # ends and beginnings in one CTA
+    (32, 2, 256, 128, [3000, 4100, 2999, 3500, 0, 1, 6001, 2500]),
+    (4, 2, 256, 32, [9001, 9001]),                                        # CTAs dealt evenly
+    (16, 1, 256, 64, [20000]),
+    (8, 4, 128, 32, [700 + 13 * i for i in range(60)]),                   # more rows than CTAs
+    (32, 2, 256, 16, [1200, 900, 3] * 40),
+    (8, 8, 128, 16, [2400, 2300, 2500, 2600] * 6),
+    (4, 4, 256, 64, [1500, 20, 1700] * 20),
+]
+
+
+@FORMATS
+@pytest.mark.parametrize("nq,nkv,hd,page,lens", SPLITS, ids=[f"{s[:4]}x{len(s[4])}" for s in SPLITS])
+def test_decode_work_splits(nq, nkv, hd, page, lens, e4m3):
+    c = Paged(nkv, hd, page, lens, e4m3, seed=nq + hd)
+    c.fill(np.random.default_rng(nq + hd), lens)
+    c.upload()
+    a = _decode(c, nq, lens)
+    b = _decode(c, nq, lens)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
 @FORMATS
 @pytest.mark.parametrize("q_scale", [2.0 ** -120, 2.0 ** 60, 30.0])
 def test_decode_extreme_queries(q_scale, e4m3):
