@@ -124,6 +124,8 @@ struct DecodeCut {
   int b, rr, head0, head_w, n_head, mid_cta, n_mid, tail_w, n_tail, pad[3];
 };
 
+constexpr int kBriefRounds = 3;  // rounds of tiles that a CTA alone does for a short row
+
 struct PagedDecodeParams {
   CUtensorMap tm_k;  // [pool rows][HD], box BOXW x 1 x min(page_size, WT)
   CUtensorMap tm_v;
@@ -314,6 +316,9 @@ struct DecodeWalk {
 // share: spot[0] = (b, rr, its number among the row's CTAs, their number),
 // and true is returned.  `ends` (shared memory): per thread, the list index
 // behind its sequences.
+//   Few short rows (no more rows than CTAs, none of more than three tiles per
+// worker) take a CTA each: nothing is left to join (1x500: 10.9 us joined from
+// two CTAs per row).
 //   Dealt to the rows: row r takes the CTAs round(P_r n / total) ..
 // round(P_r+1 n / total) - 1 of n, P the tiles of the rows before it, if that
 // leaves every row a CTA and no CTA more than 1.2 times the mean.
@@ -326,8 +331,10 @@ __device__ __forceinline__ bool decode_slices(const PagedDecodeParams& p, int ro
   const int b0 = min(p.num_seqs, tid * per), b1 = min(p.num_seqs, b0 + per);
   const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
   long long sum = 0;
+  bool brief = p.by_row != 0;
   for (int b = b0; b < b1; ++b) {
     sum += row_units<WT, ROW>(p, b);
+    brief = brief && decode_len(p, b) <= kBriefRounds * NW * WT;
     if (p.lens[b] > room && blockIdx.x == 0 && p.status != nullptr)
       atomicCAS(p.status, kStatusOk, kStatusPage);
   }
@@ -338,7 +345,15 @@ __device__ __forceinline__ bool decode_slices(const PagedDecodeParams& p, int ro
     if (lane >= o) inc += y;
   }
   if (lane == 31) warp_sum[warp] = inc;
-  __syncthreads();
+  if (__syncthreads_and(brief)) {
+    const int b = static_cast<int>(blockIdx.x) / rows_per_seq;
+    if (tid == 0)
+      spot[0] = make_int4(b, static_cast<int>(blockIdx.x) % rows_per_seq, 0,
+                          b < p.num_seqs && decode_len(p, b) > 0 ? 1 : 0);
+    out->init(0, 0);
+    __syncthreads();
+    return true;
+  }
   long long base = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {

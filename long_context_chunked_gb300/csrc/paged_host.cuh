@@ -144,7 +144,8 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
   cudaError_t e = cudaLaunchKernelEx(&cfg, cpattn::paged_decode_kernel<HD, Q8, NB>, *p);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "paged decode launch");
   cpattn_status s = after_launch(ctx, st, "paged decode launch");
-  if (s != CPATTN_OK || tiles == 1) return s;  // rows of one tile are never cut
+  // Rows of one tile are never cut, nor are few short ones (decode_slices).
+  if (s != CPATTN_OK || tiles == 1 || (p->by_row && tiles <= cpattn::kBriefRounds * Ly::NW)) return s;
   // Few rows: one block per row and as many parts of its heads as fill the
   // GPU, each with the threads for many pieces.  Many rows have few pieces
   // each: four blocks per CTA of the decode share the rows that begin there.
