@@ -336,8 +336,10 @@ cpattn_status cpattn_sync_status(cpattn_ctx* ctx, void* stream);
  * Testing hook for the bounded-wait failure path.  flags = 1 makes one thread
  * of the first CTA of later cpattn_prefill launches skip one internal
  * arrival, so that CTA's waits expire after timeout_ms and it returns early;
- * cpattn_sync_status then reports E_TIMEOUT.  flags = 0 restores normal
- * operation.  timeout_ms <= 0 restores the default limit of 1000 ms per wait.
+ * cpattn_sync_status then reports E_TIMEOUT.  Later cpattn_paged_decode
+ * launches skip one copy of their first CTA, with the same effect.  flags = 0
+ * restores normal operation.  timeout_ms <= 0 restores the default limit of
+ * 1000 ms per wait.
  */
 cpattn_status cpattn_set_fault_injection(cpattn_ctx* ctx, int32_t flags, int32_t timeout_ms);
 
@@ -451,7 +453,8 @@ void cpattn_destroy(cpattn_ctx* ctx);
  * With cpattn_config.v_cache_f16 the staged V is fp16 and P.V one product of
  * fp16 P (a value beyond 65504 is reported by cpattn_sync_status as E_RANGE);
  * otherwise V stays bf16 and P is a bf16 hi + lo pair (fast_p: bf16).  Short
- * prompts run GQA-packed and units are dealt as in cpattn_prefill.  Two
+ * prompts run GQA-packed and units are dealt as in cpattn_prefill.  out, lse
+ * and workspace must not overlap the inputs or one another.  Two
  * launches (the staging, then the prefill kernel); a walk is never split.
  * Errors: E_INVALID, E_UNSUPPORTED (more than CPATTN_MAX_SEQS sequences or
  * CPATTN_MAX_ROW_BLOCKS row blocks of 128 tokens), E_CUDA, E_NOMEM (host).
@@ -561,6 +564,10 @@ cpattn_status cpattn_paged_read_kv(cpattn_ctx* ctx, const cpattn_pages* pages, i
  *               cpattn_paged_decode_workspace() bytes, used by the call's
  *               kernels only; its contents need no preparation.  Calls that
  *               overlap on the GPU must not share one.
+ * out, lse and workspace must not overlap the inputs, the pool or one another.
+ * Two launches (the attention, then the join of rows that were split), or one
+ * where max_pages leaves nothing to split.  Results do not depend on timing:
+ * the same call gives the same bits.
  * Errors: as cpattn_paged_write_kv; E_INVALID also for a small or misaligned
  * workspace.  After E_PAGE the outputs of the sequences concerned lack the
  * skipped tokens.

@@ -34,9 +34,9 @@
 // the CTAs are dealt to the rows first (each row a whole number of them).
 //
 // A worker is one warp, and a row up to 16 q heads of a kv head: its O then
-// takes up to HD / 2 registers, and 8 to 16 warps fit an SM.  (Two warps of 8
+// takes up to HD / 2 registers, and 8 or 12 warps fit an SM.  (Two warps of 8
 // heads on the same slots convert everything twice: 1x128k e4m3 took 40 us
-// where one warp of 16 heads takes 28.)
+// where one warp of 16 heads took 28, both without the join.)
 //
 // e4m3 (Q8): K and V are converted to fp16 (exact) in registers; mma.sync on
 // e4m3 operands takes the same conversions and adds fp32 additions (measured
@@ -235,11 +235,17 @@ __device__ __forceinline__ int decode_len(const PagedDecodeParams& p, int b) {
   return static_cast<int>(max(0LL, min(static_cast<long long>(__ldg(p.lens + b)), room)));
 }
 
+// Tiles of n tokens (unsigned: n may end less than a tile below 2^31).
+template <int WT>
+__device__ __forceinline__ int tile_count(int n) {
+  return static_cast<int>((static_cast<uint32_t>(n) + WT - 1) / WT);
+}
+
 // Units of the list that a row of sequence b takes.
 template <int WT, int ROW>
 __device__ __forceinline__ int row_units(const PagedDecodeParams& p, int b) {
   const int n = decode_len(p, b);
-  return n > 0 ? (n + WT - 1) / WT + ROW : 0;
+  return n > 0 ? tile_count<WT>(n) + ROW : 0;
 }
 
 // Quotients of tile counts, which hardly ever pass 32 bits: a 64-bit division
@@ -281,7 +287,7 @@ struct DecodeWalk {
   template <int WT, int ROW>
   __device__ __forceinline__ void enter(const PagedDecodeParams& p, int rows_per_seq, int u) {
     n = decode_len(p, b);
-    nt = (n + WT - 1) / WT;
+    nt = tile_count<WT>(n);
     while (true) {
       units = static_cast<int>(min(static_cast<long long>(nt + ROW - u), s1 - s));
       tile0 = max(u - ROW, 0);
@@ -299,7 +305,7 @@ struct DecodeWalk {
     do {
       n = decode_len(p, ++b);
     } while (n == 0);
-    nt = (n + WT - 1) / WT;
+    nt = tile_count<WT>(n);
   }
   template <int WT, int ROW>
   __device__ __forceinline__ void next(const PagedDecodeParams& p, int rows_per_seq) {
@@ -470,7 +476,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     at.rr = mine.y;
     if (mine.w > 0) {
       at.n = decode_len(p, at.b);
-      at.nt = (at.n + WT - 1) / WT;
+      at.nt = tile_count<WT>(at.n);
       cta_t0 = static_cast<int>(div_count(static_cast<long long>(at.nt) * mine.z, mine.w));
       cta_t1 = static_cast<int>(div_count(static_cast<long long>(at.nt) * (mine.z + 1), mine.w));
     }
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         at.b = first.x;
         at.rr = first.y;
         at.n = decode_len(p, at.b);
-        at.nt = (at.n + WT - 1) / WT;
+        at.nt = tile_count<WT>(at.n);
         cta_t0 = max(first.z - ROW, 0);
         cta_t1 = max(static_cast<int>(first.z + cta_units) - ROW, 0);
       }

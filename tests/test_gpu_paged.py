@@ -249,6 +249,71 @@ def test_decode_work_splits(nq, nkv, hd, page, lens, e4m3):
     assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
 
 
+BRIEF = [  # nq, nkv, hd, page, lens: around the longest rows that a CTA takes alone
+    (8, 2, 128, 16, [768, 767, 1, 0]), (8, 2, 128, 16, [769, 3]),
+    (8, 2, 128, 64, [1536, 1500]), (8, 2, 128, 64, [1537, 0]),
+    (16, 1, 128, 32, [769]), (16, 1, 256, 32, [384, 383]), (16, 1, 256, 32, [385, 768]),
+    (4, 2, 256, 16, [384, 5]), (4, 2, 256, 16, [577, 576]), (4, 2, 256, 16, [576, 0, 1]),
+]
+
+
+@FORMATS
+@pytest.mark.parametrize("spare", [0, 2000])
+@pytest.mark.parametrize("nq,nkv,hd,page,lens", BRIEF, ids=[f"{s[:4]}-{s[4][0]}" for s in BRIEF])
+def test_decode_few_short_rows(nq, nkv, hd, page, lens, spare, e4m3):
+    """With a table that ends behind them, and with one that could hold far more."""
+    c = Paged(nkv, hd, page, [n + spare for n in lens], e4m3, seed=lens[0])
+    c.fill(np.random.default_rng(lens[0]), lens)
+    _decode(c.upload(), nq, lens)
+
+
+@FORMATS
+def test_decode_of_the_largest_batch(e4m3):
+    """CPATTN_MAX_PAGED_SEQS sequences, most of them padding, some sharing pages."""
+    rng = np.random.default_rng(16)
+    B = cp.MAX_PAGED_SEQS
+    lens = np.full(B, -1)
+    used = rng.choice(B, 40, replace=False)
+    lens[used] = rng.integers(1, 70, 40)
+    lens[B - 1] = 33
+    c = Paged(1, 128, 16, np.maximum(lens, 0), e4m3, seed=16)
+    c.fill(rng, np.maximum(lens, 0))
+    twin = int(used[0]) if used[0] != B - 1 else int(used[1])
+    c.table[0], lens[0] = c.table[twin], lens[twin]       # a shared prefix
+    c.upload()
+    out, _ = _decode(c, 2, [int(n) for n in lens])
+    assert np.all(out[lens <= 0] == 0)
+
+
+@FORMATS
+def test_decode_one_page_named_again_and_again(e4m3):
+    """The longest sequence a table can name, every entry the same page: the
+    page's own softmax, and an LSE that counts the copies.  Tokens are counted
+    to less than a tile below 2^31.  A lane adds up 2^31 / (152 CTAs x 8 warps x
+    8 lanes) = 2.2e5 probabilities at most in one fp32 sum, O as many products:
+    each is off by at most 2.2e5 x 2^-24 = 1.4 % of A."""
+    page, cols = 256, (1 << 31) // 256 - 1
+    c = Paged(1, 128, page, [page], e4m3, seed=17)
+    c.fill(np.random.default_rng(17), [page])
+    c.upload()
+    table = torch.full((1, cols), int(c.table[0, 0]), dtype=torch.int32, device="cuda")
+    kv = cp.PagedKV(c.d_pools[0].t, c.d_pools[1].t, table,
+                    *((s.t for s in c.d_scales) if e4m3 else (None, None)))
+    q = bf16_normal(np.random.default_rng(18), 1, 4, 128)
+    out = torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(1, 4, device="cuda")
+    ctx = cp.Context(4, 1, 128, 1, 1, 1)
+    ws = torch.empty(ctx.paged_decode_workspace(1), dtype=torch.uint8, device="cuda")
+    ctx.paged_decode(kv, i32([2 ** 31 - 1]), Buffer(q, torch.bfloat16).t, out, ws, lse=lse)
+    assert ctx.sync_status() == cp.E_PAGE                 # cut at the table's row
+    ctx.paged_decode(kv, i32([cols * page]), Buffer(q, torch.bfloat16).t, out, ws, lse=lse)
+    _ok(ctx)
+    ref, ref_lse, A, X = oracle.paged_decode_ref(oracle.bits_to_f64(q), c.pools, c.scales, c.table, page,
+                                                 [page], 128 ** -0.5)
+    assert np.all(np.abs(out.double().cpu().numpy() - ref) <= 2 ** -8 * np.abs(ref) + 0.03 * A)
+    assert np.all(np.abs(lse.double().cpu().numpy() - ref_lse - np.log(cols)) <= 0.02)
+
+
 @FORMATS
 @pytest.mark.parametrize("q_scale", [2.0 ** -120, 2.0 ** 60, 30.0])
 def test_decode_extreme_queries(q_scale, e4m3):
@@ -425,6 +490,77 @@ def test_captured_step_replays_with_new_lengths(e4m3):
         ref = oracle.paged_decode_ref(oracle.bits_to_f64(qb), c.pools, c.scales, c.table, page,
                                       list(have + i + 1), hd ** -0.5)
         check_decode(out.double().cpu().numpy(), lse.double().cpu().numpy(), *ref, hd)
+
+
+def test_captured_forks_copies_and_shared_workspace():
+    """A captured step whose decode follows a copy, then a fork of two streams,
+    twice on one workspace; and an eager decode between its replays."""
+    lens = [3000, 500, 17]
+    ctx = cp.Context(16, 2, 128, 1, 1, 1)
+    cs = [Paged(2, 128, 32, lens, bool(s), seed=50 + s) for s in range(2)]
+    for s, c in enumerate(cs):
+        c.fill(np.random.default_rng(50 + s), lens)
+        c.upload()
+    qs = [bf16_normal(np.random.default_rng(60 + s), 3, 16, 128) for s in range(2)]
+    src = [Buffer(q, torch.bfloat16).t for q in qs]
+    q = [torch.zeros_like(x) for x in src]
+    out = [torch.zeros_like(x) for x in src]
+    ws = [torch.empty(ctx.paged_decode_workspace(3), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    d_lens = i32([0] * 3)
+    true_lens = i32(lens)
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        q[0].copy_(src[0], non_blocking=True)
+        ctx.paged_decode(cs[0].kv, d_lens, q[0], out[0], ws[0])   # behind a copy
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            q[1].copy_(src[1])
+            d_side.copy_(true_lens)
+        here.wait_stream(side)
+        ctx.paged_decode(cs[1].kv, d_side, q[1], out[1], ws[0])   # behind a join, same workspace
+
+    d_side = i32([0] * 3)
+    d_lens.copy_(true_lens)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    first = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(first):
+        ctx.paged_decode(cs[0].kv, d_lens, q[0], out[0], ws[0])   # the first node
+    refs = [oracle.paged_decode_ref(oracle.bits_to_f64(x), c.pools, c.scales, c.table, 32, lens, 128 ** -0.5)
+            for x, c in zip(qs, cs)]
+    for _ in range(5):
+        for t in out + q + [d_side]:
+            t.zero_()
+        graph.replay()
+        ctx.paged_decode(cs[1].kv, true_lens, q[1], out[1], ws[0])
+        got = [o.clone() for o in out]
+        out[0].zero_()
+        first.replay()
+        _ok(ctx)
+        for o, ref in ((got[0], refs[0]), (got[1], refs[1]), (out[0], refs[0])):
+            check_decode(o.double().cpu().numpy(), None, *ref, 128)
+
+
+def test_read_serves_shared_pages():
+    """Two sequences whose tables name the same pages, read from odd places."""
+    c = Paged(2, 128, 16, [50, 50], False, seed=70)
+    c.fill(np.random.default_rng(70), [50, 50])
+    c.table[1] = c.table[0]
+    c.upload()
+    ctx = cp.Context(2, 2, 128, 3, 17, 1)
+    k, v = (torch.zeros(2, 2, 3, 17, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ctx.paged_read_kv(c.kv, i32([50, 50]), k, v, first=i32([1, 47]))
+    _ok(ctx)
+    for i, x in enumerate((k, v)):
+        rows = torch.from_numpy(oracle.paged_rows(c.pools[i], None, c.table[0], 16, 0, 50)).to(torch.bfloat16)
+        for b, first in enumerate((1, 47)):
+            for t in range(51):
+                want = rows[t] if first <= t < 50 else torch.zeros(2, 128, dtype=torch.bfloat16)
+                assert torch.equal(x[b, :, t % 3, t // 3].cpu(), want), (i, b, t)
 
 
 def test_two_streams_with_their_own_workspaces():
