@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(256)
     paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
   constexpr int VECS = HD / 8;        // 16-byte vectors per row
   constexpr int LOADS = HD / 128;     // loads of a row: K and V together, or one after the other
-  griddep_launch_dependents();        // a decode that follows may be set up meanwhile
+  griddep_launch_dependents();
+  griddep_wait();
   const int lane = threadIdx.x & 31;
   const int nkv = p.pool.nkv;
   const int groups = (nkv + p.heads_per_item - 1) / p.heads_per_item;
@@ -295,6 +296,8 @@ __global__ void __launch_bounds__(256)
   constexpr int LOADS = HD / 128;
   constexpr int RUN = kReadRun;
   extern __shared__ int prefix[];
+  griddep_launch_dependents();
+  griddep_wait();
   const int lane = threadIdx.x & 31;
   const int nkv = p.pool.nkv;
   // Tokens that both the striped cache and the table's row can hold.

@@ -60,14 +60,34 @@ int copy_grid(const cpattn_ctx* ctx, long long units, int hpi) {
                                                             static_cast<long long>(ctx->num_sms) * 8)));
 }
 
+// Launch as a programmatic dependent of what is ahead on the stream: the launch
+// overlaps its end, and the kernel waits for it before it touches memory.
+template <class Params>
+cpattn_status launch_dependent(cpattn_ctx* ctx, void (*kernel)(Params), dim3 grid, int threads,
+                               size_t smem, cudaStream_t st, const Params& p, const char* what) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, what);
+  return after_launch(ctx, st, what);
+}
+
 template <int ROWS>
-void launch_paged_write(const cpattn::PagedWriteParams& p, int hd, bool q8, int grid, cudaStream_t st) {
-  if (hd == 128)
-    q8 ? cpattn::paged_write_kernel<128, true, ROWS><<<grid, 256, 0, st>>>(p)
-       : cpattn::paged_write_kernel<128, false, ROWS><<<grid, 256, 0, st>>>(p);
-  else
-    q8 ? cpattn::paged_write_kernel<256, true, ROWS><<<grid, 256, 0, st>>>(p)
-       : cpattn::paged_write_kernel<256, false, ROWS><<<grid, 256, 0, st>>>(p);
+cpattn_status launch_paged_write(cpattn_ctx* ctx, const cpattn::PagedWriteParams& p, bool q8, int grid,
+                                 cudaStream_t st) {
+  const auto kernel = ctx->cfg.head_dim == 128 ? (q8 ? cpattn::paged_write_kernel<128, true, ROWS>
+                                                     : cpattn::paged_write_kernel<128, false, ROWS>)
+                                               : (q8 ? cpattn::paged_write_kernel<256, true, ROWS>
+                                                     : cpattn::paged_write_kernel<256, false, ROWS>);
+  return launch_dependent(ctx, kernel, dim3(grid), 256, 0, st, p, "paged write launch");
 }
 
 // CTAs of a decode launch: at most one per SM (and the join's table of pieces).
@@ -129,36 +149,17 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
   p->workers = Ly::NW;
   p->piece_rows = Ly::HEADS;
   p->by_row = rows_all <= p->num_ctas ? 1 : 0;
-  // Both kernels are programmatic dependents of what is ahead of them: their
-  // launch overlaps its end, and they wait for it before they touch memory.
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p->num_ctas));
-  cfg.blockDim = dim3(Ly::THREADS);
-  cfg.dynamicSmemBytes = Ly::SMEM_BYTES;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, cpattn::paged_decode_kernel<HD, Q8, NB>, *p);
-  if (e != cudaSuccess) return cuda_fail(ctx, e, "paged decode launch");
-  cpattn_status s = after_launch(ctx, st, "paged decode launch");
+  cpattn_status s = launch_dependent(ctx, cpattn::paged_decode_kernel<HD, Q8, NB>, dim3(p->num_ctas),
+                                     Ly::THREADS, Ly::SMEM_BYTES, st, *p, "paged decode launch");
   // Rows of one tile are never cut, nor are few short ones (decode_slices).
   if (s != CPATTN_OK || tiles == 1 || (p->by_row && tiles <= cpattn::kBriefRounds * Ly::NW)) return s;
   // Few rows: one block per row and as many parts of its heads as fill the
   // GPU, each with the threads for many pieces.  Many rows have few pieces
   // each: four blocks per CTA of the decode share the rows that begin there.
   const int blocks = p->by_row ? static_cast<int>(rows_all) : p->num_ctas;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks),
-                     p->by_row ? static_cast<unsigned>(std::min(
-                                     {std::max(1, ctx->num_sms / blocks), p->group, Ly::HEADS}))
-                               : 4u);
-  cfg.blockDim = dim3(p->by_row ? cpattn::kJoinThreads : 256);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, cpattn::paged_join_kernel<HD>, *p);
-  if (e != cudaSuccess) return cuda_fail(ctx, e, "paged join launch");
-  return after_launch(ctx, st, "paged join launch");
+  const int parts = p->by_row ? std::min({std::max(1, ctx->num_sms / blocks), p->group, Ly::HEADS}) : 4;
+  return launch_dependent(ctx, cpattn::paged_join_kernel<HD>, dim3(blocks, parts),
+                          p->by_row ? cpattn::kJoinThreads : 256, 0, st, *p, "paged join launch");
 }
 
 }  // namespace
@@ -197,9 +198,8 @@ cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, 
   const int grid = copy_grid(ctx, units, p.heads_per_item);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool q8 = pages->format == CPATTN_PAGES_E4M3;
-  per == 4 ? launch_paged_write<4>(p, ctx->cfg.head_dim, q8, grid, st)
-           : launch_paged_write<1>(p, ctx->cfg.head_dim, q8, grid, st);
-  return after_launch(ctx, st, "paged write launch");
+  return per == 4 ? launch_paged_write<4>(ctx, p, q8, grid, st)
+                  : launch_paged_write<1>(ctx, p, q8, grid, st);
 } catch (...) {
   return CPATTN_E_NOMEM;
 }
@@ -238,13 +238,11 @@ cpattn_status cpattn_paged_read_kv(cpattn_ctx* ctx, const cpattn_pages* pages, i
   const size_t smem = (static_cast<size_t>(num_seqs) + 1) * sizeof(int);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool q8 = pages->format == CPATTN_PAGES_E4M3;
-  if (c.head_dim == 128)
-    q8 ? cpattn::paged_read_kernel<128, true><<<grid, 256, smem, st>>>(p)
-       : cpattn::paged_read_kernel<128, false><<<grid, 256, smem, st>>>(p);
-  else
-    q8 ? cpattn::paged_read_kernel<256, true><<<grid, 256, smem, st>>>(p)
-       : cpattn::paged_read_kernel<256, false><<<grid, 256, smem, st>>>(p);
-  return after_launch(ctx, st, "paged read launch");
+  const auto kernel = c.head_dim == 128 ? (q8 ? cpattn::paged_read_kernel<128, true>
+                                              : cpattn::paged_read_kernel<128, false>)
+                                        : (q8 ? cpattn::paged_read_kernel<256, true>
+                                              : cpattn::paged_read_kernel<256, false>);
+  return launch_dependent(ctx, kernel, dim3(grid), 256, smem, st, p, "paged read launch");
 } catch (...) {
   return CPATTN_E_NOMEM;
 }
