@@ -109,7 +109,8 @@ struct DecodeLayout {
   static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;  // spots, scan, abort flag
   static constexpr int SMEM_BYTES = OFF_MISC + NW * 16 + THREADS / 32 * 8 + 16;
   static_assert(HEADS * C_STRIDE * 4 <= NSLOT * SLOT, "a worker's O fits its slots");
-  static_assert(!Q_SMEM || (NSLOT == 3 && Q_BYTES <= SLOT), "a worker's Q fits a slot");
+  static_assert(!Q_SMEM || (NSLOT == 3 && Q_BYTES <= SLOT && OFF_Q % 512 == 0),
+                "a worker's Q fits a slot, and chunks can be XORed into a row's address");
   static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0 && OFF_Q % 16 == 0 && OFF_ENDS % 8 == 0,
                 "shared memory alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -421,6 +422,13 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   using Ly = DecodeLayout<HD, Q8, NB>;
   constexpr int WT = Ly::WT, ROW = Ly::ROW, MT = Ly::MT, MO = Ly::MO, NSLOT = Ly::NSLOT, NW = Ly::NW;
   constexpr int HEADS = Ly::HEADS;
+  // Where Q is in shared memory, K Q^T can be a loop that holds the code of KU
+  // steps.  With e4m3's conversions a whole tile's code is more than the
+  // instruction cache feeds without pauses (1x128k: 38.7 us unrolled, 37.4 by
+  // twos, 38.6 by ones with the loop over V's halves rolled up too); with bf16
+  // it is not (8x32k: 96.5 us unrolled, 99 by twos).
+  constexpr bool ROLL = Ly::Q_SMEM && Q8;
+  constexpr int KU = ROLL ? 2 : HD / 16;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5;  // wk: worker of the CTA
@@ -774,10 +782,11 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         }
       }
     }
-    const uint32_t q_row = sbase + q_at + ((NB == 2 ? (oct >> 1) * 8 : 0) + r8) * (2 * HD);
+    const uint32_t q_row = sbase + q_at + ((NB == 2 ? (oct >> 1) * 8 : 0) + r8) * (2 * HD) +
+                           (((oct & 1) ^ r8) << 4);
     auto q_frag = [&](int ks, uint32_t (&f)[4]) {  // [nb][b0, b1]
       if constexpr (Ly::Q_SMEM) {
-        ldsm4(f, q_row + (((2 * ks + (oct & 1)) ^ r8) << 4));
+        ldsm4(f, q_row ^ (ks << 5));
       } else {
 #pragma unroll
         for (int i = 0; i < 2 * NB; ++i) f[i] = q[ks][i];
@@ -812,8 +821,17 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       const bool partial = valid < WT || bad != 0u;
       const uint32_t kb = ring + slot * Ly::SLOT;
       float c[MT][NB][4];
-      if constexpr (Q8) {
+      if constexpr (ROLL) {
 #pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[t][nb][j] = 0.f;
+      }
+      const uint32_t k_at = sw128(kb, (oct & 1) * 8 + r8, oct >> 1);  // (chunks are XORed in)
+      if constexpr (Q8) {
+#pragma unroll KU
         for (int ks = 0; ks < HD / 16; ks += 2) {  // 32 dims: chunks ks and ks + 1
           uint32_t qa[4], qb[4];
           q_frag(ks, qa);
@@ -821,13 +839,12 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             uint32_t kr[4], a[4];  // token half, then chunk, by lane octet
-            ldsm4(kr, sw128(kb + (ks >> 3) * (WT * 128), t * 16 + (oct & 1) * 8 + r8,
-                            (ks & 7) + (oct >> 1)));
+            ldsm4(kr, (k_at ^ ((ks & 7) << 4)) + (ks >> 3) * (WT * 128) + t * 2048);
             e4m3x4_to_f16x4(kr[0], &a[0], &a[2]);
             e4m3x4_to_f16x4(kr[1], &a[1], &a[3]);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              if (ks == 0)
+              if (ks == 0 && !ROLL)
                 mma16816<true, true>(c[t][nb], a, qa[2 * nb], qa[2 * nb + 1]);
               else
                 mma16816<true>(c[t][nb], a, qa[2 * nb], qa[2 * nb + 1]);
@@ -839,18 +856,17 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
           }
         }
       } else {
-#pragma unroll
+#pragma unroll KU
         for (int ks = 0; ks < HD / 16; ++ks) {  // 16 dims: chunks 2 ks and 2 ks + 1
           uint32_t qf[4];
           q_frag(ks, qf);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             uint32_t a[4];
-            ldsm4(a, sw128(kb + (ks >> 2) * (WT * 128), t * 16 + (oct & 1) * 8 + r8,
-                           (2 * ks & 7) + (oct >> 1)));
+            ldsm4(a, (k_at ^ ((2 * ks & 7) << 4)) + (ks >> 2) * (WT * 128) + t * 2048);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              if (ks == 0)
+              if (ks == 0 && !ROLL)
                 mma16816<false, true>(c[t][nb], a, qf[2 * nb], qf[2 * nb + 1]);
               else
                 mma16816<false>(c[t][nb], a, qf[2 * nb], qf[2 * nb + 1]);
