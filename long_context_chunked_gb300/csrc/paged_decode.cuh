@@ -51,6 +51,17 @@
 // m and s_ref are references, not exact maxima: they are raised (and O and l
 // rescaled) only when a logit exceeds m by 8 or a scale exceeds s_ref, which
 // after a row's first tile hardly happens; p then stays below 2^8.
+//
+// Measured (both launches): 8 x 32768 tokens, bf16, 32 q heads on 2 kv heads of
+// 256: 96.5 us for 537 MB (5.6 TB/s, 82 % of a copy's rate); 64 ragged
+// sequences of 1 to 8191 tokens, e4m3, 32 on 4 of 128: 57.9 us for 275 MB
+// (4.8 TB/s, 70 %); 1 x 126977, e4m3, 32 on 2 of 256: 37.4 us for 132 MB (3.5
+// TB/s, 52 %); 1 x 500, bf16, 8 on 2 of 128: 7.9 us.  What lies between them
+// and the copy's rate: about 7 us until the first tile is in (lengths, page
+// ids, tile: three round trips, one after the other), 4 to 5 us of join, and
+// CTAs that end apart (9 or 10 to a row of the first case).  While tiles flow,
+// bf16 is bound by DRAM, and e4m3 by the latency of conversions and products
+// in 8 warps (a quarter to a third of the issue slots are used).
 #pragma once
 
 #include <cuda_bf16.h>
