@@ -83,8 +83,9 @@ constexpr int kDecStages = 8;                    // tiles whose absent pages a w
 // NW workers per CTA with NSLOT slots of SLOT bytes each, 192 KB in all; WT
 // tokens per tile.  8 KB slots and 8 workers: more and smaller ones pay the
 // fixed cost of a tile more often (64 ragged at HD = 128: 16 workers with 4 KB
-// slots 80 us, 12 68 us, 8 with 8 KB 66 us) -- but for e4m3 at HD = 256 and
-// NB = 1 registers allow 12.
+// slots 80 us, 12 68 us, 8 with 8 KB 66 us; later, 12 workers with two slots of
+// 8 KB 60.7 us, 8 with three 58.0) -- but for e4m3 at HD = 256 and NB = 1,
+// whose registers allow 12.
 template <int HD, bool Q8, int NB>
 struct DecodeLayout {
   static constexpr int ESZ = Q8 ? 1 : 2;

@@ -46,7 +46,8 @@ cpattn_status check_pages(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t nu
 
 // kv heads a warp of the paged copies takes of its rows (`units` of them): 4 or
 // 2, which share the look-ups, where that leaves 16 warps per SM, else 1.
-// (varlen e4m3 write: 4 heads 16.4 us, 2 heads 16.8, 1 head 18.3.)
+// (e4m3 write of 17421 tokens, 4 heads of 128: 16.4 us by 4 heads, 16.8 by 2, 18.3
+// by 1, before launches overlapped.)
 int heads_per_item(const cpattn_ctx* ctx, long long units) {
   const int nkv = ctx->cfg.num_kv_heads;
   for (int h = 4; h > 1; h /= 2)
@@ -190,7 +191,8 @@ cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, 
   p.status = ctx->d_status;
   p.num_seqs = num_seqs;
   p.rows = num_rows;
-  // Four rows a warp where that leaves 16 warps per SM, else one.
+  // Four rows a warp where that leaves 16 warps per SM, else one (the same
+  // write: 22.5 us by single rows, 19.7 by four).
   const int per = static_cast<long long>(num_rows) * ctx->cfg.num_kv_heads >=
                           4LL * 16 * std::max(ctx->num_sms, 1) ? 4 : 1;
   const long long units = (static_cast<long long>(num_rows) + per - 1) / per;

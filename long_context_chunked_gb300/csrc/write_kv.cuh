@@ -114,7 +114,9 @@ __global__ void __launch_bounds__(256) stage_v_f16_kernel(const __grid_constant_
 // rows, and a NaN or infinity there would reach this sequence as 0 * NaN in
 // the masked columns of P.V; a staged tile holds one sequence only.  f16:
 // converted to fp16 as stage_v_f16_kernel converts (one P.V product of fp16
-// P per tile), else copied.  HBM-bound: one 16-byte vector per thread.
+// P per tile), else copied.  HBM-bound: one 16-byte vector per thread (20161
+// rows of 2 x 256: 13 us of a 2.57 ms prefill, 0.5 %; four vectors in flight
+// and no search per vector left the whole call as it was).
 struct StagePackedParams {
   const uint4* v;
   uint4* staged;
