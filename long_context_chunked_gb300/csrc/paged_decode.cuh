@@ -674,7 +674,11 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     if (ok && !mbar_try_wait(full0 + 8 * slot, phase)) ok = wait(full0 + 8 * slot, phase, kSiteDecFull);
     __syncwarp();
   };
-  auto release = [&]() {  // the slot has been read by every lane
+  // The slot has been read by every lane.  __syncwarp, and not the vote, orders
+  // the lanes' reads (and clears) of it before the copies that a few of them
+  // send into it, and of Q before the next row's.
+  auto release = [&]() {
+    __syncwarp();
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (++slot == nslot) {
       slot = 0;
