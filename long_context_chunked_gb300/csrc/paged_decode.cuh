@@ -153,6 +153,7 @@ struct PagedDecodeParams {
   // more rows than CTAs, else by worker.
   DecodeCut* ws_cut;          // [workers]
   int* status;
+  uint32_t* bar_counts;       // barrier-count build: by CTA and worker, else unused
   unsigned long long timeout_ns;
   int pool_rows;              // num_pages * NKV * page_size
   int debug_flags;
@@ -165,6 +166,9 @@ struct PagedDecodeParams {
 };
 
 enum : int { kSiteDecFull = 9 };  // after the prefill's sites
+// Barrier-count build, by worker: copies sent (row kCountRowArrive) and copies
+// seen to have landed, which have to be as many.
+constexpr int kCountRowLanded = 1;
 
 // ------------------------------------------------------------------ mma.sync
 // c (16 x 8) = (ZERO ? 0 : c) + A (16 x 16) B (16 x 8).
@@ -589,6 +593,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   auto send = [&](const CUtensorMap* m, const float* scales, int row, int scale_row) {
     const uint32_t bar = full0 + 8 * slot_out, dst = ring + slot_out * Ly::SLOT;
     if (lane == 0) {
+      count_arrive(p.bar_counts, 1u, wk, 1);
       mbar_arrive_expect_tx(bar, Ly::SLOT);
 #pragma unroll
       for (int c = 0; c < Ly::NBOX; ++c) tma_load_3d(dst + c * (WT * 128), m, bar, c * Ly::BOXW, 0, row);
@@ -666,26 +671,43 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   const int quad = lane & 3, r0 = lane >> 2, r8 = lane & 7, oct = lane >> 3;
   int slot = 0, used = 0;  // the next slot to read, and copies read so far
   uint32_t phase = 0;
-  // A warp whose wait expired (ok = false) waits for no more copies: it runs
-  // to its end on stale data, still meets every barrier, and the status word
-  // tells the host.
+  // A warp whose wait expired, or that another warp's expired wait ends, is
+  // through with its tiles (ok = false): it lets its copies in flight land,
+  // still says where its rows' pieces are and meets every barrier, and the
+  // status word tells the host.
   bool ok = true;
-  auto await = [&]() {
-    if (ok && !mbar_try_wait(full0 + 8 * slot, phase)) ok = wait(full0 + 8 * slot, phase, kSiteDecFull);
+  auto await = [&]() {  // whether the copy in `slot` has landed, alike in the warp
+    bool in = mbar_try_wait(full0 + 8 * slot, phase);
+    if (!in) in = wait(full0 + 8 * slot, phase, kSiteDecFull);
+    ok = __all_sync(0xFFFFFFFFu, in);
     __syncwarp();
+    if (ok) count_wait(p.bar_counts, kCountRowLanded, wk);
+    return ok;
   };
   // The slot has been read by every lane.  __syncwarp, and not the vote, orders
   // the lanes' reads (and clears) of it before the copies that a few of them
   // send into it, and of Q before the next row's.
   auto release = [&]() {
     __syncwarp();
-    ok = __all_sync(0xFFFFFFFFu, ok);
     if (++slot == nslot) {
       slot = 0;
       phase ^= 1u;
     }
     ++used;
-    if (ok) issue();
+    issue();
+  };
+  // Copies used .. issued - 1 are in flight: they land before the ring is used
+  // for something else and before the CTA exits.
+  auto drain = [&]() {
+    for (; used < issued; ++used) {
+      if (mbar_wait_drain(full0 + 8 * slot, phase, 200ull * 1000 * 1000))
+        count_wait(p.bar_counts, kCountRowLanded, wk);
+      if (++slot == nslot) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+    __syncwarp();
   };
 
   // (A worker without tiles still takes part in its CTA's sum.)
@@ -828,11 +850,11 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][nb][j] = 0.f;
 
-    for (int v = 0; v < at.tiles; ++v) {
+    for (int v = 0; ok && v < at.tiles; ++v) {
       const int valid = min(WT, at.n - (at.tile0 + v * at.step) * WT);  // tokens of the tile
 
       // ---- S^T = K Q^T
-      await();
+      if (!await()) break;
       const uint32_t bad = my_bad[(used >> 1) & (kDecStages - 1)];
       const bool partial = valid < WT || bad != 0u;
       const uint32_t kb = ring + slot * Ly::SLOT;
@@ -933,7 +955,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       release();
 
       // ---- references: m, and (Q8) s_ref
-      await();
+      if (!await()) break;
       const uint32_t vb = ring + slot * Ly::SLOT;
       float vs[MT][2];
       float smx = 0.f;
@@ -1065,6 +1087,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       if (valid < WT) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       release();
     }
+
+    if (!ok) drain();
 
     // ---- the end of the row, or of this warp's part of it
 #pragma unroll
@@ -1222,16 +1246,6 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
             }
           }
         }
-    }
-  }
-  if (!ok) {
-    // Let copies already sent land before this CTA can exit.
-    for (; used < issued; ++used) {
-      mbar_wait_drain(full0 + 8 * slot, phase, 200ull * 1000 * 1000);
-      if (++slot == nslot) {
-        slot = 0;
-        phase ^= 1u;
-      }
     }
   }
 }

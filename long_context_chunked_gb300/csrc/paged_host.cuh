@@ -150,6 +150,11 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
   p->workers = Ly::NW;
   p->piece_rows = Ly::HEADS;
   p->by_row = rows_all <= p->num_ctas ? 1 : 0;
+  if (ctx->bar_counts != nullptr) {
+    if (ctx->bar_counts_bytes < static_cast<size_t>(p->num_ctas) * cpattn::kCountRecord * 4)
+      return fail(ctx, CPATTN_E_INVALID, "barrier-count records smaller than the launch");
+    p->bar_counts = ctx->bar_counts;
+  }
   cpattn_status s = launch_dependent(ctx, cpattn::paged_decode_kernel<HD, Q8, NB>, dim3(p->num_ctas),
                                      Ly::THREADS, Ly::SMEM_BYTES, st, *p, "paged decode launch");
   // Rows of one tile are never cut, nor are few short ones (decode_slices).
@@ -286,6 +291,7 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
   p.status = ctx->d_status;
   p.timeout_ns = ctx->timeout_ns;
   p.debug_flags = ctx->debug_flags;
+  p.bar_counts = nullptr;
   p.pool_rows = pages->num_pages * pages->page_size * c.num_kv_heads;
   p.num_seqs = num_seqs;
   p.nq = c.num_q_heads;

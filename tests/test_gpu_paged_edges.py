@@ -3,8 +3,12 @@ row after row, copies in flight when a wait expires, V rows of very different
 magnitudes, infinities.  Against the oracle, as tests/test_gpu_paged.py."""
 import numpy as np
 import pytest
+import torch
 
-from paged_helpers import Paged
+import long_context_chunked_gb300 as cp
+from long_context_chunked_gb300 import build as cpbuild
+from long_context_chunked_gb300.binding import COUNT_BARS, COUNT_RECORD
+from paged_helpers import Paged, i32
 from test_gpu_paged import FORMATS, _decode
 
 pytestmark = pytest.mark.gpu
@@ -13,16 +17,90 @@ pytestmark = pytest.mark.gpu
 @FORMATS
 @pytest.mark.parametrize("nq,hd", [(8, 128), (16, 256)])
 def test_slots_and_queries_reused_by_row_after_row(nq, hd, e4m3):
-    """More rows than warps, nearly all of which end inside a tile: each warp
-    clears the tail of a V slot, refills the slot and (16 heads of 256) takes
-    the next row's Q into shared memory, again and again.  The same bits every
-    time, within the bound."""
+    """Several rows for every warp, nearly all of which end inside a tile: each
+    warp clears the tail of a V slot, refills the slot and (16 heads of 256)
+    takes the next row's Q into shared memory, again and again.  The same bits
+    every time, within the bound.  (All sequences share eight pages.)"""
     rng = np.random.default_rng(31)
-    lens = [int(n) for n in rng.integers(1, 150, 1400)]
-    c = Paged(1, hd, 16, lens, e4m3, seed=31)
-    c.fill(rng, lens)
+    c = Paged(1, hd, 16, [128], e4m3, seed=31)
+    c.fill(rng, [128])
+    c.table = np.stack([rng.permutation(c.table[0, :8]) for _ in range(4000)]).astype(np.int32)
     c.upload()
+    lens = [int(n) for n in rng.integers(1, 129, 4000)]
     first = _decode(c, nq, lens)
-    for _ in range(5):
-        again = _decode(c, nq, lens)
-        assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+    again = _decode(c, nq, lens)
+    assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
+@pytest.fixture(scope="module")
+def counted_lib():
+    return cpbuild.build(variant="counted")
+
+
+def _tile(hd, e4m3, group):
+    """Tokens of a tile (DecodeLayout::WT)."""
+    wide = group > 8 or (hd == 256 and not e4m3)
+    slot = 4096 if hd == 256 and not wide else 8192
+    return slot // (hd * (1 if e4m3 else 2))
+
+
+# nq, nkv, hd, lens.  The first slice of the list is long enough for a tile: the
+# hook withholds the first copy of the first warp.
+COPIES = [
+    (8, 2, 128, [20001, 5]),             # a row that its whole CTA works on, cut across CTAs
+    (8, 2, 256, [9001, 5]),
+    (16, 1, 256, [9001]),                # the same, Q in shared memory
+    (8, 2, 128, [300]),                  # a short row, alone in its CTA
+    (16, 1, 256, [140] * 350),            # rows of its own, whole and cut
+    (4, 4, 128, [600 + 13 * i for i in range(40)]),
+]
+
+
+@FORMATS
+@pytest.mark.parametrize("drop", [False, True], ids=["healthy", "expired"])
+@pytest.mark.parametrize("nq,nkv,hd,lens", COPIES, ids=[f"{s[:3]}x{len(s[3])}" for s in COPIES])
+def test_every_copy_lands_before_the_kernel_ends(counted_lib, nq, nkv, hd, lens, drop, e4m3):
+    """Every copy that a warp sends is seen to land, also where its first copy
+    is withheld, so that its first wait runs into its limit with copies in
+    flight behind it: the kernel then ends, the status says so, and the next
+    call is right."""
+    c = Paged(nkv, hd, 64, lens, e4m3, seed=33)
+    if not drop:
+        c.fill(np.random.default_rng(33), lens)
+    c.upload()
+    ctx = cp.Context(nq, nkv, hd, 1, 1, 1, library=counted_lib)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rec = torch.zeros(sms * COUNT_RECORD, dtype=torch.int32, device="cuda")
+    ctx.set_barrier_counts(rec)
+    tiles = sum(-(-n // _tile(hd, e4m3, nq // nkv)) for n in lens) * nkv
+    if not drop:
+        _decode(c, nq, lens, ctx=ctx)
+    else:
+        ctx.set_fault_injection(1, 50)
+        q = torch.zeros(len(lens), nq, hd, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(ctx.paged_decode_workspace(len(lens)), dtype=torch.uint8, device="cuda")
+        ctx.paged_decode(c.kv, i32(lens), q, torch.zeros_like(q), ws)
+        assert ctx.sync_status() == cp.E_TIMEOUT
+    counts = rec.cpu().numpy().reshape(sms, -1, COUNT_BARS)
+    sent, landed = counts[:, 0], counts[:, 1]
+    assert np.array_equal(sent, landed)
+    if not drop:
+        assert sent.sum() == 2 * tiles
+    else:
+        assert 0 < sent[0, 0] and sent.sum() < 2 * tiles
+        ctx.set_fault_injection(0)
+        rec.zero_()
+        ctx.paged_decode(c.kv, i32(lens), q, torch.zeros_like(q), ws)
+        assert ctx.sync_status() == cp.OK
+        counts = rec.cpu().numpy().reshape(sms, -1, COUNT_BARS)
+        assert counts[:, 0].sum() == 2 * tiles and np.array_equal(counts[:, 0], counts[:, 1])
+
+
+def test_counting_refuses_a_short_record(counted_lib):
+    c = Paged(2, 128, 16, [4000] * 8, False, seed=34).upload()
+    ctx = cp.Context(4, 2, 128, 1, 1, 1, library=counted_lib)
+    ctx.set_barrier_counts(torch.zeros(COUNT_RECORD, dtype=torch.int32, device="cuda"))
+    q = torch.zeros(8, 4, 128, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(ctx.paged_decode_workspace(8), dtype=torch.uint8, device="cuda")
+    with pytest.raises(cp.CpattnError):
+        ctx.paged_decode(c.kv, i32([4000] * 8), q, torch.zeros_like(q), ws)
