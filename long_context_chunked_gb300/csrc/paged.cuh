@@ -27,6 +27,15 @@
 
 namespace cpattn {
 
+// Every load of the paged kernels from memory that a kernel ahead of them on the
+// stream may write (pages, tables, lengths, rows): an ordinary one.  They are
+// programmatic dependents, which may start while that kernel still writes, and
+// the non-coherent __ldg is for what nobody writes while the grid runs.
+template <class T>
+__device__ __forceinline__ T load_now(const T* p) {
+  return *p;
+}
+
 struct PagedPool {
   void* k;           // bf16 or e4m3 [num_pages][NKV][page_size][HD]
   void* v;
@@ -41,7 +50,7 @@ struct PagedPool {
 __device__ __forceinline__ int page_id(const PagedPool& c, int b, int idx, int* status) {
   int id = -1;
   if (idx < c.max_pages) {
-    id = __ldg(c.table + b * c.table_stride + idx);
+    id = load_now(c.table + b * c.table_stride + idx);
     if (id >= c.num_pages) id = -1;
   }
   if (id < 0) {
@@ -101,7 +110,7 @@ __device__ __forceinline__ int write_seq(const PagedWriteParams& p, int row, int
   while (n > 1) {
     const int step = (n + 31) / 32, at = lane * step;
     const uint32_t m =
-        __ballot_sync(0xFFFFFFFFu, at < n && __ldg(p.row_starts + lo + min(at, n - 1)) <= row);
+        __ballot_sync(0xFFFFFFFFu, at < n && load_now(p.row_starts + lo + min(at, n - 1)) <= row);
     const int k = m == 0u ? 0 : 31 - __clz(static_cast<int>(m));
     lo += k * step;
     n = min(step, n - k * step);
@@ -116,16 +125,16 @@ __device__ __forceinline__ long long write_place(const PagedWriteParams& p, int 
   if (row >= p.rows) return -1;
   int i = 0;
   if (p.row_starts != nullptr) {
-    int begin = __ldg(p.row_starts + b), end = __ldg(p.row_starts + b + 1);
+    int begin = load_now(p.row_starts + b), end = load_now(p.row_starts + b + 1);
     while (row >= end && b + 1 < p.num_seqs) {
       ++b;
       begin = end;
-      end = __ldg(p.row_starts + b + 1);
+      end = load_now(p.row_starts + b + 1);
     }
     if (row < begin || row >= end) return -1;
     i = row - begin;
   }
-  const int have = __ldg(p.cache_lens + b);
+  const int have = load_now(p.cache_lens + b);
   if (have < 0) return -1;
   const long long t = static_cast<long long>(have) + i;
   const int page =
@@ -171,7 +180,7 @@ __global__ void __launch_bounds__(256)
         for (int l = 0; l < LOADS; ++l) {
           const int row = min(row0 + r, p.rows - 1);
           const bool is_k = LOADS == 1 ? k_lane : l == 0;
-          x[r][l] = __ldg((is_k ? p.k_new : p.v_new) + (static_cast<long long>(row) * nkv + g) * VECS + vec);
+          x[r][l] = load_now((is_k ? p.k_new : p.v_new) + (static_cast<long long>(row) * nkv + g) * VECS + vec);
         }
     };
     load(g0);
@@ -264,10 +273,10 @@ __device__ __forceinline__ void block_prefix(int n, int* prefix, Count count) {
 // Eight values of a pool row, e4m3 or bf16, and the same in the cache's type
 // (f16: fp16, else bf16).
 __device__ __forceinline__ void load_vec(uint2& x, const void* pool, long long at) {
-  x = __ldg(reinterpret_cast<const uint2*>(pool) + at);
+  x = load_now(reinterpret_cast<const uint2*>(pool) + at);
 }
 __device__ __forceinline__ void load_vec(uint4& x, const void* pool, long long at) {
-  x = __ldg(reinterpret_cast<const uint4*>(pool) + at);
+  x = load_now(reinterpret_cast<const uint4*>(pool) + at);
 }
 __device__ __forceinline__ uint4 widen_vec(uint2 x, float s, bool f16, bool* overflow) {
   const uint32_t w[2] = {x.x, x.y};
@@ -312,9 +321,9 @@ __global__ void __launch_bounds__(256)
   // Tokens that both the striped cache and the table's row can hold.
   const long long room = min(static_cast<long long>(p.P) * p.S,
                              static_cast<long long>(p.pool.max_pages) << p.pool.page_shift);
-  auto start = [&](int b) { return p.first != nullptr ? max(__ldg(p.first + b), 0) : 0; };
+  auto start = [&](int b) { return p.first != nullptr ? max(load_now(p.first + b), 0) : 0; };
   auto stop = [&](int b) {
-    return static_cast<int>(min(static_cast<long long>(__ldg(p.lens + b)), room));
+    return static_cast<int>(min(static_cast<long long>(load_now(p.lens + b)), room));
   };
   block_prefix(p.num_seqs, prefix, [&](int b) {  // runs of each sequence
     if (p.lens[b] > room && p.status != nullptr) atomicCAS(p.status, kStatusOk, kStatusPage);
@@ -360,7 +369,7 @@ __global__ void __launch_bounds__(256)
         for (int l = 0; l < LOADS; ++l) {
           const bool is_k = LOADS == 1 ? k_lane : l == 0;
           load_vec(x[r][l], is_k ? p.pool.k : p.pool.v, (src + r) * VECS + vec);
-          if (Q8) sc[r][l] = __ldg((is_k ? p.pool.k_scales : p.pool.v_scales) + src + r);
+          if (Q8) sc[r][l] = load_now((is_k ? p.pool.k_scales : p.pool.v_scales) + src + r);
         }
 #pragma unroll
       for (int r = 0; r < RUN; ++r)

@@ -249,7 +249,7 @@ __device__ __forceinline__ uint32_t sw128(uint32_t base, int row, int chunk) {
 // Tokens of sequence b, cut to what its table row can name.
 __device__ __forceinline__ int decode_len(const PagedDecodeParams& p, int b) {
   const long long room = static_cast<long long>(p.pool.max_pages) << p.pool.page_shift;
-  return static_cast<int>(max(0LL, min(static_cast<long long>(__ldg(p.lens + b)), room)));
+  return static_cast<int>(max(0LL, min(static_cast<long long>(load_now(p.lens + b)), room)));
 }
 
 // Tiles of n tokens (unsigned: n may end less than a tile below 2^31).
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     raw_g = ahead.rr / p.hblocks;
     if (lane < boxes && t < ahead.n) {
       raw_t = t;
-      raw_id = __ldg(p.pool.table + ahead.b * p.pool.table_stride + (t >> p.pool.page_shift));
+      raw_id = load_now(p.pool.table + ahead.b * p.pool.table_stride + (t >> p.pool.page_shift));
     }
     if (++aj >= ahead.tiles) {
       ahead.template next<WT, ROW>(p, rows_per_seq);
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         uint32_t big = 0;
 #pragma unroll
         for (int i = 0; i < HD / 128; ++i) {
-          w[i] = r < heads ? __ldg(src + 32 * i + lane) : make_uint2(0u, 0u);
+          w[i] = r < heads ? load_now(src + 32 * i + lane) : make_uint2(0u, 0u);
           big = __vmaxu2(big, __vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu));
         }
         if constexpr (Q8) {
@@ -792,10 +792,10 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         for (int ks = 0; ks < HD / 16; ++ks) {
           uint2 w;
           if constexpr (Q8) {
-            w = __ldg(reinterpret_cast<const uint2*>(src) + 4 * ks + quad);
+            w = load_now(reinterpret_cast<const uint2*>(src) + 4 * ks + quad);
           } else {
-            w.x = __ldg(src + 8 * ks + quad);
-            w.y = __ldg(src + 8 * ks + 4 + quad);
+            w.x = load_now(src + 8 * ks + quad);
+            w.y = load_now(src + 8 * ks + 4 + quad);
           }
           if (!here) w = make_uint2(0u, 0u);
           q[ks][2 * nb] = w.x;

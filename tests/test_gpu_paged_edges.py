@@ -6,10 +6,11 @@ import pytest
 import torch
 
 import long_context_chunked_gb300 as cp
+import oracle
 from long_context_chunked_gb300 import build as cpbuild
 from long_context_chunked_gb300.binding import COUNT_BARS, COUNT_RECORD
-from paged_helpers import Paged, i32
-from test_gpu_paged import FORMATS, _decode
+from paged_helpers import Buffer, Paged, bf16_normal, i32
+from test_gpu_paged import FORMATS, _decode, _ok
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +105,45 @@ def test_counting_refuses_a_short_record(counted_lib):
     ws = torch.empty(ctx.paged_decode_workspace(8), dtype=torch.uint8, device="cuda")
     with pytest.raises(cp.CpattnError):
         ctx.paged_decode(c.kv, i32([4000] * 8), q, torch.zeros_like(q), ws)
+
+
+@FORMATS
+@pytest.mark.parametrize("captured", [False, True], ids=["eager", "captured"])
+@pytest.mark.parametrize("hd,page", [(128, 16), (256, 64)])
+def test_reads_between_writes_of_the_same_slots(hd, page, captured, e4m3):
+    """Read, write, read, write .. of the same slots with nothing between the
+    launches, each of which may start while the one ahead still runs: every
+    read has the values (and scales) of the write before it."""
+    rng = np.random.default_rng(35)
+    nkv, n, turns = 2, 40, 12
+    c = Paged(nkv, hd, page, [n, n], e4m3, seed=35).upload()
+    ctx = cp.Context(nkv, nkv, hd, 1, n, 1)
+    new = [[bf16_normal(rng, 2 * n, nkv, hd) for _ in range(2)] for _ in range(turns)]
+    d_new = [[Buffer(x, torch.bfloat16).t for x in pair] for pair in new]
+    got = torch.zeros(turns, 2, 2, nkv, 1, n, hd, dtype=torch.bfloat16, device="cuda")
+    none, all_, starts = i32([0, 0]), i32([n, n]), i32([0, n, 2 * n])
+
+    def chain():
+        for (k, v), out in zip(d_new, got):
+            ctx.paged_write_kv(c.kv, none, k, v, row_starts=starts)
+            ctx.paged_read_kv(c.kv, all_, out[0], out[1])
+
+    if captured:
+        chain()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chain()
+        got.zero_()
+        graph.replay()
+    else:
+        chain()
+    _ok(ctx)
+    for pair, out in zip(new, got.cpu()):
+        oracle.paged_write_ref(c.pools, c.scales, c.table, page, [0, 0], [0, n, 2 * n], pair)
+        for i in range(2):
+            for b in range(2):
+                want = oracle.paged_rows(c.pools[i], c.scales and c.scales[i], c.table[b], page, 0, n)
+                want = torch.from_numpy(want).float().to(torch.bfloat16)
+                assert torch.equal(out[i, b, :, 0].transpose(0, 1), want)
+    c.check_pools()
