@@ -43,14 +43,20 @@
 // by instruction counters).  Q is fp16, scaled by a power of two per head so
 // that its largest element is in [1, 2): elements below 2^-14 of it lose bits,
 // at most 2^-25 of the largest.  A K row's scale multiplies its logit.  A V
-// row's scale multiplies its probability: P is stored as p_t (s_t / s_ref) 2^7,
-// rounded once to fp16's 11 bits, with s_ref at least every scale so far and
-// at least 2^-100.
+// row's scale multiplies its probability: P is stored as p_t s_t 2^7 / W,
+// rounded once to fp16.  W is a power of two, at most twice the largest product
+// p_t s_t that the head has met in the slice (or 2^-100), and no product passes
+// 448 W.  So a scale counts as far as its token's probability goes: below a
+// reference that is at least every scale, one V row of 1e10 at a logit of -50
+// left nothing of rows of 1.  fp16 holds 11 bits of products down to 2^-21 W,
+// fewer below, and none below 2^-32 W.  (Against one reference per warp, which
+// was wrong: 1x128k 37.8 -> 38.9 us, 64 ragged 59.0 -> 58.3.  The largest product
+// found by a bound from p and s apart, and then once more token by token: 39.2.)
 // bf16: P is carried as a bf16 hi + lo pair (16 bits) against bf16 V.
 //
-// m and s_ref are references, not exact maxima: they are raised (and O and l
-// rescaled) only when a logit exceeds m by 8 or a scale exceeds s_ref, which
-// after a row's first tile hardly happens; p then stays below 2^8.
+// m and W are references, not exact maxima: they are raised only when a logit
+// exceeds m by 8, so p stays below 2^8, or a P would pass 57344, which after a
+// row's first tile hardly happens.  O is in units of W / 2^7.
 //
 // Measured (both launches): 8 x 32768 tokens, bf16, 32 q heads on 2 kv heads of
 // 256: 96.5 us for 537 MB (5.6 TB/s, 82 % of a copy's rate); 64 ragged
@@ -73,9 +79,11 @@
 
 namespace cpattn {
 
-constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7
-constexpr float kMinSref = 7.888609052210118e-31f;  // 2^-100: kPScale / s_ref stays finite
 constexpr float kRaise = 8.f;                    // m is raised when a logit exceeds it by this
+constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7 / W
+constexpr float kMinW = 7.888609052210118e-31f;  // 2^-100: kPScale / W stays finite
+constexpr float kMaxW = 8.507059173023462e+37f;  // 2^126, far above the largest scale of 2^119
+constexpr float kPMax = 57344.f;                 // Q8: W is raised where a P would pass this
 constexpr int kDecMaxHeads = 16;                 // of a row
 constexpr int kDecStages = 8;                    // tiles whose absent pages a worker remembers
 
@@ -227,6 +235,15 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The power of two at or above x, 2^-126 <= x <= 2^127, and 1 / x of a power of
+// two x, 2^-126 <= x <= 2^126: W's arithmetic, exact.
+__device__ __forceinline__ float pow2_above(float x) {
+  return __uint_as_float((__float_as_uint(x) + 0x7FFFFFu) & 0x7F800000u);
+}
+__device__ __forceinline__ float pow2_inverse(float x) {
+  return __uint_as_float(0x7F000000u - __float_as_uint(x));
 }
 
 // Four e4m3 values as two fp16 pairs (exact).
@@ -841,7 +858,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         m[nb][j] = -INFINITY;
         l[nb][j] = 0.f;
       }
-    float sref = kMinSref, pscale = kPScale / kMinSref;
+    float ps[NB][2];  // Q8: 2^7 / W
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) ps[nb][0] = ps[nb][1] = kPScale / kMinW;
     float o[MO][NB][4];
 #pragma unroll
     for (int i = 0; i < MO; ++i)
@@ -954,11 +973,10 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         }
       release();
 
-      // ---- references: m, and (Q8) s_ref
+      // ---- m
       if (!await()) break;
       const uint32_t vb = ring + slot * Ly::SLOT;
       float vs[MT][2];
-      float smx = 0.f;
       if constexpr (Q8) {
         const float* vsc = reinterpret_cast<const float*>(
             smem + Ly::OFF_SCALE + (wk * NSLOT + slot) * (WT * 4));
@@ -968,26 +986,19 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
           for (int i = 0; i < 2; ++i) {
             vs[t][i] = vsc[16 * t + 8 * i + r0];
             if (partial && !seen[t][i]) vs[t][i] = 0.f;
-            smx = fmaxf(smx, fabsf(vs[t][i]));
           }
       }
-      bool raise = Q8 && smx > sref;
+      float a[NB][2];  // 2^(m before - m)
+      bool raise = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) raise |= mx[nb][j] > m[nb][j] + kRaise;
-      if (__any_sync(0xFFFFFFFFu, raise)) {
-        float shrink = 1.f;
-        if constexpr (Q8) {
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) smx = fmaxf(smx, __shfl_xor_sync(0xFFFFFFFFu, smx, d));
-          if (smx > sref) {  // (every quad of lanes holds the same tokens: alike in the warp)
-            const float up = 2.f * smx;  // twice: the next scales are likely to fit
-            shrink = sref / up;
-            sref = up;
-            pscale = kPScale / up;
-          }
+        for (int j = 0; j < 2; ++j) {
+          a[nb][j] = 1.f;
+          raise |= mx[nb][j] > m[nb][j] + kRaise;
         }
+      raise = __any_sync(0xFFFFFFFFu, raise);
+      if (raise) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -996,35 +1007,82 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
             const float mn = fmaxf(m[nb][j], x);
-            const float a = m[nb][j] == mn ? 1.f : ex2_approx(m[nb][j] - mn);
+            if (m[nb][j] != mn) a[nb][j] = ex2_approx(m[nb][j] - mn);
             m[nb][j] = mn;
-            l[nb][j] *= a;
-            const float as = a * shrink;
+            l[nb][j] *= a[nb][j];
+            if constexpr (!Q8) {
 #pragma unroll
-            for (int i = 0; i < MO; ++i) {
-              o[i][nb][j] *= as;
-              o[i][nb][2 + j] *= as;
+              for (int i = 0; i < MO; ++i) {
+                o[i][nb][j] *= a[nb][j];
+                o[i][nb][2 + j] *= a[nb][j];
+              }
             }
           }
       }
 
-      // ---- P, transposed into the B operand of V^T P^T (16 tokens per step)
-      uint32_t ph[MT][NB][2], pl[Q8 ? 1 : MT][NB][2];
+      // ---- p (Q8: times the V row's scale), and l
+      float wx[NB][2];  // Q8: the lane's largest product
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
+        wx[nb][0] = wx[nb][1] = 0.f;
         const float m0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0];
         const float m1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float e0 = ex2_approx(fmaf(c[t][nb][2 * i], sl[nb][0], -m0));
-            const float e1 = ex2_approx(fmaf(c[t][nb][2 * i + 1], sl[nb][1], -m1));
+            float& e0 = c[t][nb][2 * i];
+            float& e1 = c[t][nb][2 * i + 1];
+            e0 = ex2_approx(fmaf(e0, sl[nb][0], -m0));
+            e1 = ex2_approx(fmaf(e1, sl[nb][1], -m1));
             l[nb][0] += e0;
             l[nb][1] += e1;
             if constexpr (Q8) {
-              const float f = vs[t][i] * pscale;
-              ph[t][nb][i] = transpose8(pack_f16x2(e0 * f, e1 * f));
+              e0 *= vs[t][i];
+              e1 *= vs[t][i];
+              wx[nb][0] = fmaxf(wx[nb][0], fabsf(e0));
+              wx[nb][1] = fmaxf(wx[nb][1], fabsf(e1));
+            }
+          }
+      }
+      if constexpr (Q8) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) raise |= wx[nb][j] * ps[nb][j] > kPMax;
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float w = wx[nb][j];
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) w = fmaxf(w, __shfl_xor_sync(0xFFFFFFFFu, w, d));
+              // W falls with p where m has risen, or rises to the tile's largest product.
+              const float was = kPScale * pow2_inverse(ps[nb][j]) * a[nb][j];
+              const float inv = pow2_inverse(pow2_above(fminf(fmaxf(fmaxf(was, w), kMinW), kMaxW)));
+              const float as = was * inv;
+              ps[nb][j] = kPScale * inv;
+#pragma unroll
+              for (int i = 0; i < MO; ++i) {
+                o[i][nb][j] *= as;
+                o[i][nb][2 + j] *= as;
+              }
+            }
+        }
+      }
+
+      // ---- P, transposed into the B operand of V^T P^T (16 tokens per step)
+      uint32_t ph[MT][NB][2], pl[Q8 ? 1 : MT][NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float e0 = c[t][nb][2 * i], e1 = c[t][nb][2 * i + 1];
+            if constexpr (Q8) {
+              ph[t][nb][i] = transpose8(pack_f16x2(e0 * ps[nb][0], e1 * ps[nb][1]));
             } else {
               const uint32_t hi = pack_bf16x2(e0, e1);
               ph[t][nb][i] = transpose8(hi);
@@ -1032,7 +1090,6 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
                                                     e1 - __uint_as_float(hi & 0xFFFF0000u)));
             }
           }
-      }
 
       // ---- O^T += V^T P^T
       if (valid < WT) {
@@ -1133,7 +1190,11 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       else if (d.n_head > 0)
         p.ws_cut[worker] = d;  // (at most one row that begins here is cut: the last)
     }
-    const float oscale = Q8 ? sref * (1.f / kPScale) : 1.f;
+    float oscale[NB][2];  // of the O in registers
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) oscale[nb][j] = Q8 ? pow2_inverse(ps[nb][j]) : 1.f;
     if (uniform) {
       // One piece for the CTA: the workers' m and l, then their O, summed in
       // worker order.  (The only row of every warp here.)
@@ -1163,7 +1224,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
             const float2 ml = mls[w * HEADS + r];
             sum = fmaf(ex2_approx(ml.x - mref), ml.y, sum);
           }
-          float f = ex2_approx(m[nb][j] - mref) * oscale;
+          float f = ex2_approx(m[nb][j] - mref) * oscale[nb][j];
           // sum = 0: every page of the row was absent.
           if (cta_whole) f = sum == 0.f ? 0.f : f / sum;
           if (wk == 0 && r0 == 0 && r < heads) {
@@ -1216,7 +1277,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         for (int j = 0; j < 2; ++j) {
           const int r = 8 * nb + 2 * quad + j;
           const float sum = l[nb][j];
-          const float f = whole ? (sum == 0.f ? 0.f : oscale / sum) : oscale;
+          const float f = whole ? (sum == 0.f ? 0.f : oscale[nb][j] / sum) : oscale[nb][j];
           const long long orow = static_cast<long long>(at.b) * p.nq + h0 + r;
           const long long prow = piece * HEADS + r;
           if (r0 == 0 && r < heads) {

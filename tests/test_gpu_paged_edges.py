@@ -9,7 +9,7 @@ import long_context_chunked_gb300 as cp
 import oracle
 from long_context_chunked_gb300 import build as cpbuild
 from long_context_chunked_gb300.binding import COUNT_BARS, COUNT_RECORD
-from paged_helpers import Buffer, Paged, bf16_normal, i32
+from paged_helpers import Buffer, Paged, bf16_normal, check_decode, i32
 from test_gpu_paged import FORMATS, _decode, _ok
 
 pytestmark = pytest.mark.gpu
@@ -147,3 +147,56 @@ def test_reads_between_writes_of_the_same_slots(hd, page, captured, e4m3):
                 want = torch.from_numpy(want).float().to(torch.bfloat16)
                 assert torch.equal(out[i, b, :, 0].transpose(0, 1), want)
     c.check_pools()
+
+
+def _bits(x):
+    return oracle.bf16_bits(torch.from_numpy(np.asarray(x, dtype=np.float64)).to(torch.bfloat16))
+
+
+# Which tokens of n differ, by which logit (the others' are within a few units
+# of 0) and which factor of V.  The e4m3 scales of V differ as much: a token's
+# scale may count only as far as its probability goes.
+UNLIKE = {
+    "first": lambda n, r: (np.arange(n) == 0, -50, 1e10),
+    "last": lambda n, r: (np.arange(n) == n - 1, -50, 1e10),
+    "middle": lambda n, r: (np.arange(n) == n // 2, -50, 1e10),
+    "every 16th": lambda n, r: (np.arange(n) % 16 == 3, -50, 1e10),
+    "every 2nd": lambda n, r: (np.arange(n) % 2 == 0, -60, 1e12),
+    # one token has nearly all the probability and next to no V
+    "sink": lambda n, r: (np.arange(n) == 0, 40, 1e-10),
+    "late sink": lambda n, r: (np.arange(n) == n - 1, 40, 1e-10),
+    # every product of a probability and a V is about as large as the others
+    "balanced": lambda n, r: (np.ones(n, bool), (x := r.uniform(-30, 30, n)), np.exp(-x)),
+}
+
+
+@FORMATS
+@pytest.mark.parametrize("where", UNLIKE)
+@pytest.mark.parametrize("nq,nkv,hd,lens", [(8, 2, 128, [300, 40]), (32, 2, 256, [700, 33]), (4, 2, 256, [500]),
+                                            (20, 1, 128, [5000])])
+def test_v_magnitudes_against_probabilities(nq, nkv, hd, lens, where, e4m3):
+    """Within check_decode's bound.  (P drops what is below 2^-31 of the largest
+    product of a probability and a scale; here no product that A counts on is.)"""
+    rng = np.random.default_rng(41)
+    B = len(lens)
+    base = rng.standard_normal((B, nkv, 1, hd))
+    q = _bits((base + 0.02 * rng.standard_normal((B, nkv, nq // nkv, hd))).reshape(B, nq, hd))
+    c = Paged(nkv, hd, 32, lens, e4m3, seed=41)
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    k, v = (rng.standard_normal((starts[-1], nkv, hd)) for _ in range(2))
+    for b, n in enumerate(lens):
+        hit, logit, factor = UNLIKE[where](n, rng)
+        at = starts[b] + np.flatnonzero(hit)
+        unit = hd ** 0.5 * base[b, :, 0] / (base[b, :, 0] ** 2).sum(-1, keepdims=True)  # logit 1
+        k[at] = np.broadcast_to(np.asarray(logit, float), n)[hit][:, None, None] * unit
+        v[at] *= np.broadcast_to(np.asarray(factor, float), n)[hit][:, None, None]
+    oracle.paged_write_ref(c.pools, c.scales, c.table, 32, [0] * B, starts, [_bits(k), _bits(v)])
+    c.upload()
+    out = torch.zeros(B, nq, hd, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(B, nq, device="cuda")
+    ctx = cp.Context(nq, nkv, hd, 1, 1, 1)
+    ws = torch.empty(ctx.paged_decode_workspace(B), dtype=torch.uint8, device="cuda")
+    ctx.paged_decode(c.kv, i32(lens), Buffer(q, torch.bfloat16).t, out, ws, lse=lse)
+    _ok(ctx)
+    ref = oracle.paged_decode_ref(oracle.bits_to_f64(q), c.pools, c.scales, c.table, 32, lens, hd ** -0.5)
+    check_decode(out.double().cpu().numpy(), lse.double().cpu().numpy(), *ref, hd)
