@@ -52,7 +52,10 @@
 // fewer below, and none below 2^-32 W.  (Against one reference per warp, which
 // was wrong: 1x128k 37.8 -> 38.9 us, 64 ragged 59.0 -> 58.3.  The largest product
 // found by a bound from p and s apart, and then once more token by token: 39.2.)
-// bf16: P is carried as a bf16 hi + lo pair (16 bits) against bf16 V.
+// bf16: P is carried as a bf16 hi + lo pair against bf16 V.  hi is cut, not
+// rounded, and lo takes 2^-22 p besides (far below its own rounding, 2^-16 p), so
+// that both are positive wherever p is: an infinite v_t stays infinite, where a lo
+// of 0 or below would make NaN of it.
 //
 // m and W are references, not exact maxima: they are raised only when a logit
 // exceeds m by 8, so p stays below 2^8, or a P would pass 57344, which after a
@@ -84,6 +87,7 @@ constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7 / 
 constexpr float kMinW = 7.888609052210118e-31f;  // 2^-100: kPScale / W stays finite
 constexpr float kMaxW = 8.507059173023462e+37f;  // 2^126, far above the largest scale of 2^119
 constexpr float kPMax = 57344.f;                 // Q8: W is raised where a P would pass this
+constexpr float kAboveOne = 1.00000023841857910f;  // 1 + 2^-22 (bf16: P's lo)
 constexpr int kDecMaxHeads = 16;                 // of a row
 constexpr int kDecStages = 8;                    // tiles whose absent pages a worker remembers
 
@@ -1084,10 +1088,12 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
             if constexpr (Q8) {
               ph[t][nb][i] = transpose8(pack_f16x2(e0 * ps[nb][0], e1 * ps[nb][1]));
             } else {
-              const uint32_t hi = pack_bf16x2(e0, e1);
-              ph[t][nb][i] = transpose8(hi);
-              pl[t][nb][i] = transpose8(pack_bf16x2(e0 - __uint_as_float(hi << 16),
-                                                    e1 - __uint_as_float(hi & 0xFFFF0000u)));
+              // hi: the upper 16 bits; lo: the rest, and 2^-22 of the whole (kAboveOne).
+              const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+              ph[t][nb][i] = transpose8(__byte_perm(b0, b1, 0x7632));
+              pl[t][nb][i] =
+                  transpose8(pack_bf16x2(fmaf(e0, kAboveOne, -__uint_as_float(b0 & 0xFFFF0000u)),
+                                         fmaf(e1, kAboveOne, -__uint_as_float(b1 & 0xFFFF0000u))));
             }
           }
 

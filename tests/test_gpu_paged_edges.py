@@ -200,3 +200,34 @@ def test_v_magnitudes_against_probabilities(nq, nkv, hd, lens, where, e4m3):
     _ok(ctx)
     ref = oracle.paged_decode_ref(oracle.bits_to_f64(q), c.pools, c.scales, c.table, 32, lens, hd ** -0.5)
     check_decode(out.double().cpu().numpy(), lse.double().cpu().numpy(), *ref, hd)
+
+
+@pytest.mark.parametrize("nq,nkv,hd,lens", [(8, 2, 128, [300, 40]), (32, 2, 256, [700, 33]), (4, 2, 256, [500]),
+                                            (20, 1, 128, [170]), (16, 1, 128, [9000])])
+def test_infinite_v_in_bf16_pages(nq, nkv, hd, lens):
+    """+inf or -inf where a column of V has one (the first token, the last one,
+    one between), NaN where it has both or a NaN; the other columns within the
+    bound."""
+    rng = np.random.default_rng(42)
+    c = Paged(nkv, hd, 16, lens, False, seed=42)
+    c.fill(rng, lens)
+    for b, n in enumerate(lens):
+        for t, d, x in ((0, 3, 0x7F80), (n - 1, 5, 0xFF80), (n // 4, 6, 0x7F80), (n // 2, 7, 0x7F80),
+                        (n // 3, 7, 0xFF80), (n // 5, 9, 0x7FC1)):
+            c.pools[1][c.table[b, t // 16], :, t % 16, d] = x
+    c.upload()
+    q = bf16_normal(rng, len(lens), nq, hd)
+    out = torch.zeros(*q.shape, dtype=torch.bfloat16, device="cuda")
+    ctx = cp.Context(nq, nkv, hd, 1, 1, 1)
+    ws = torch.empty(ctx.paged_decode_workspace(len(lens)), dtype=torch.uint8, device="cuda")
+    ctx.paged_decode(c.kv, i32(lens), Buffer(q, torch.bfloat16).t, out, ws)
+    _ok(ctx)
+    out = out.double().cpu().numpy()
+    for d, want in ((3, np.inf), (5, -np.inf), (6, np.inf), (7, np.nan), (9, np.nan)):
+        assert np.array_equal(out[..., d], np.full(out.shape[:2], want), equal_nan=True), d
+    for b, n in enumerate(lens):
+        for d in (3, 5, 6, 7, 9):
+            c.pools[1][c.table[b, np.arange(n) // 16], :, np.arange(n) % 16, d] = 0
+    keep = np.setdiff1d(np.arange(hd), (3, 5, 6, 7, 9))
+    ref, lse, A, X = oracle.paged_decode_ref(oracle.bits_to_f64(q), c.pools, None, c.table, 16, lens, hd ** -0.5)
+    check_decode(out[..., keep], None, ref[..., keep], lse, A[..., keep], X, hd)
