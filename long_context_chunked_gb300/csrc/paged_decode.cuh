@@ -34,7 +34,7 @@
 // the CTAs are dealt to the rows first (each row a whole number of them).
 //
 // A worker is one warp, and a row up to 16 q heads of a kv head: its O then
-// takes up to HD / 2 registers, and 8 or 12 warps fit an SM.  (Two warps of 8
+// takes up to HD / 2 registers, and 8 warps fit an SM.  (Two warps of 8
 // heads on the same slots convert everything twice: 1x128k e4m3 took 40 us
 // where one warp of 16 heads took 28, both without the join.)
 //
@@ -96,15 +96,15 @@ constexpr int kDecStages = 8;                    // tiles whose absent pages a w
 // tokens per tile.  8 KB slots and 8 workers: more and smaller ones pay the
 // fixed cost of a tile more often (64 ragged at HD = 128: 16 workers with 4 KB
 // slots 80 us, 12 68 us, 8 with 8 KB 66 us; later, 12 workers with two slots of
-// 8 KB 60.7 us, 8 with three 58.0) -- but for e4m3 at HD = 256 and NB = 1,
-// whose registers allow 12.
+// 8 KB 60.7 us, 8 with three 58.0), and at HD = 256 12 workers spill besides
+// (e4m3, NB = 1, four slots of 4 KB: 1x126977 36.6 us, 33.9 by 8; 64 ragged of 8
+// heads per kv head 64.5 and 59.3).
 template <int HD, bool Q8, int NB>
 struct DecodeLayout {
   static constexpr int ESZ = Q8 ? 1 : 2;
-  static constexpr bool BIG = NB == 2 || (HD == 256 && !Q8);
-  static constexpr int NW = HD == 256 && !BIG ? 12 : 8;
+  static constexpr int NW = 8;
   static constexpr int THREADS = 32 * NW;
-  static constexpr int SLOT = BIG || NW == 8 ? 8192 : 4096;
+  static constexpr int SLOT = 8192;
   static constexpr int NSLOT = 196608 / (NW * SLOT);
   static constexpr int WT = SLOT / (HD * ESZ);
   static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : 6);

@@ -103,9 +103,9 @@ struct DecodeWorkspace {
   uint64_t ml, cut, total;  // byte offsets
 };
 DecodeWorkspace decode_workspace(const cpattn_ctx* ctx) {
-  // At most 16 workers per CTA with 8 rows per piece, or 8 with 16.
-  const uint64_t workers = static_cast<uint64_t>(decode_max_ctas(ctx)) * 16;
-  const uint64_t rows = 2 * workers * 8;
+  // 8 workers per CTA, at most 16 rows per piece.
+  const uint64_t workers = static_cast<uint64_t>(decode_max_ctas(ctx)) * 8;
+  const uint64_t rows = 2 * workers * 16;
   DecodeWorkspace w;
   w.ml = cpattn::align256(rows * ctx->cfg.head_dim * sizeof(float));
   w.cut = w.ml + cpattn::align256(rows * sizeof(float2));
@@ -117,7 +117,7 @@ template <int HD, bool Q8, int NB>
 cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
                             cpattn::PagedDecodeParams* p, cudaStream_t st) {
   using Ly = cpattn::DecodeLayout<HD, Q8, NB>;
-  static_assert(Ly::NW <= 16 && Ly::NW * Ly::HEADS <= 128, "decode_workspace");
+  static_assert(Ly::NW <= 8 && Ly::HEADS <= 16, "decode_workspace");
   bool& ready = ctx->decode_ready[HD == 256][Q8];
   if (!ready) {
     cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8, NB>,

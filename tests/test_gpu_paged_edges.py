@@ -38,11 +38,9 @@ def counted_lib():
     return cpbuild.build(variant="counted")
 
 
-def _tile(hd, e4m3, group):
+def _tile(hd, e4m3):
     """Tokens of a tile (DecodeLayout::WT)."""
-    wide = group > 8 or (hd == 256 and not e4m3)
-    slot = 4096 if hd == 256 and not wide else 8192
-    return slot // (hd * (1 if e4m3 else 2))
+    return 8192 // (hd * (1 if e4m3 else 2))
 
 
 # nq, nkv, hd, lens.  The first slice of the list is long enough for a tile: the
@@ -73,7 +71,7 @@ def test_every_copy_lands_before_the_kernel_ends(counted_lib, nq, nkv, hd, lens,
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     rec = torch.zeros(sms * COUNT_RECORD, dtype=torch.int32, device="cuda")
     ctx.set_barrier_counts(rec)
-    tiles = sum(-(-n // _tile(hd, e4m3, nq // nkv)) for n in lens) * nkv
+    tiles = sum(-(-n // _tile(hd, e4m3)) for n in lens) * nkv
     if not drop:
         _decode(c, nq, lens, ctx=ctx)
     else:
