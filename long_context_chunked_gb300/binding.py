@@ -355,7 +355,9 @@ class Context:
 
     def prefill_packed(self, seq_lens, q, k, v, out, workspace, lse=None, stream=None):
         """Causal attention over whole prompts packed one behind the other:
-        q, out [sum(seq_lens), NQ, HD], k, v [sum(seq_lens), NKV, HD], bf16."""
+        q, out [sum(seq_lens), NQ, HD], k, v [sum(seq_lens), NKV, HD], bf16.  A
+        context made with v_cache_f16 takes V in fp16, with one P.V product
+        instead of two."""
         import torch
         n = len(seq_lens)
         sl = (ctypes.c_int32 * n)(*[int(x) for x in seq_lens])

@@ -149,10 +149,11 @@ __device__ __forceinline__ long long write_place(const PagedWriteParams& p, int 
 // loads the rows of its first head before it looks for their places (some
 // dependent loads, lane r for row r), and every head's ROWS rows together.
 // ROWS = 1 spreads few rows over more warps.
-//   64961 prompt tokens of 2 heads of 256 to bf16 pages: 41.1 us for 266 MB,
-// 6.5 TB/s.  17421 tokens of 4 heads of 128 to e4m3 pages: 14.1 us for 54 MB,
-// 3.8 TB/s: 8 us of traffic behind one launch and one look-up.  A decode step
-// of 7 tokens: 2.3 us as a node of a graph.
+//   64961 prompt tokens of 2 heads of 256 to bf16 pages: 41.8 us for 266 MB,
+// 6.4 TB/s.  To e4m3 pages a head's rows are quantised before the next head's are
+// loaded: 17421 tokens of 4 heads of 128 take 14.0 us for 54 MB, 3.9 TB/s, and
+// 40000 tokens of 2 heads of 256 37.7 us for 124 MB, 3.3 TB/s (108 registers, so
+// two blocks per SM).  A decode step of 7 tokens: 2.3 us as a node of a graph.
 template <int HD, bool Q8, int ROWS>
 __global__ void __launch_bounds__(256)
     paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
@@ -302,8 +303,8 @@ __device__ __forceinline__ uint4 widen_vec(uint4 x, float, bool f16, bool* overf
 // write; a run starts at a multiple of RUN, so it lies in one page and one
 // look-up serves it.  HBM-bound copy; the loads of a run's rows go out together
 // (one row at a time: 80 us where four took 60.5, the first case below).
-//   86970 tokens of 4 heads of 128 from bf16 pages: 58.1 us for 356 MB,
-// 6.1 TB/s.  28672 tokens of 2 heads of 256 from e4m3 pages of 16: 18.7 us for
+//   86970 tokens of 4 heads of 128 from bf16 pages: 58.9 us for 356 MB,
+// 6.0 TB/s.  28672 tokens of 2 heads of 256 from e4m3 pages of 16: 18.9 us for
 // 89 MB, 4.7 TB/s, the launch and the prefix sums of every block among them.
 constexpr int kReadRun = 4;
 

@@ -3,9 +3,11 @@
 //   m >= max_t x_t - 8,  l = sum_t p_t,  LSE = (m + log2 l) ln 2
 // over the cached tokens of kv head g = h / G.
 //
-// HBM-bound: every cached row is read once and used for the G q heads of its
-// kv head, 4 HD G flops per 4 HD bytes (bf16), far below what even the
-// legacy tensor path delivers per byte.  So the kernel is built around an
+// HBM-bound: a cached row is read once and used for the G q heads of its kv head,
+// 4 HD G flops per 4 HD bytes (bf16), far below what even the legacy tensor path
+// delivers per byte.  (Of more than 16 heads every further block of 16 copies
+// the rows again, mostly from L2: 8 x 32768 bf16 tokens of 32 heads on one kv
+// head of 128 move 171 MB of DRAM for 134 MB, 41.0 us; of 16 heads 32.6 us.)  So the kernel is built around an
 // unbroken stream of TMA copies, and computes with mma.sync, transposed:
 // S^T = K Q^T and O^T += V^T P^T put the cached rows on M = 16 and the q heads
 // on N = 8, so a group of up to 8 heads pays for 8.  tcgen05's M = 128 would
@@ -62,15 +64,17 @@
 // row's first tile hardly happens.  O is in units of W / 2^7.
 //
 // Measured (both launches): 8 x 32768 tokens, bf16, 32 q heads on 2 kv heads of
-// 256: 96.5 us for 537 MB (5.6 TB/s, 82 % of a copy's rate); 64 ragged
-// sequences of 1 to 8191 tokens, e4m3, 32 on 4 of 128: 57.9 us for 275 MB
-// (4.8 TB/s, 70 %); 1 x 126977, e4m3, 32 on 2 of 256: 37.4 us for 132 MB (3.5
-// TB/s, 52 %); 1 x 500, bf16, 8 on 2 of 128: 7.9 us.  What lies between them
+// 256: 97 us for 537 MB (5.5 TB/s, 82 % of a copy's rate); 64 ragged sequences
+// of 1 to 8191 tokens, e4m3, 32 on 4 of 128: 58.1 us for 275 MB (4.7 TB/s,
+// 70 %), 16 on 2 of 256: 59.3 us; 1 x 126977, e4m3, 32 on 2 of 256: 38.9 us for
+// 132 MB (3.4 TB/s, 50 %), 8 on 2 of 256: 33.9 us; 1 x 500, bf16, 8 on 2 of 128:
+// 8.0 us where the table's row names 768 tokens at most, 9.3 us where it has
+// room for more, so that the join has to be launched.  What lies between them
 // and the copy's rate: about 7 us until the first tile is in (lengths, page
 // ids, tile: three round trips, one after the other), 4 to 5 us of join, and
 // CTAs that end apart (9 or 10 to a row of the first case).  While tiles flow,
 // bf16 is bound by DRAM, and e4m3 by the latency of conversions and products
-// in 8 warps (a quarter to a third of the issue slots are used).
+// in 8 warps (a quarter of the issue slots is used).
 #pragma once
 
 #include <cuda_bf16.h>
