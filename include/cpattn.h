@@ -560,13 +560,14 @@ cpattn_status cpattn_paged_read_kv(cpattn_ctx* ctx, const cpattn_pages* pages, i
  *   O[b, h, :] = softmax_t( scale * <q_b, k_t> ) . v_t,  t in [0, lens[b])
  * over the cached tokens of kv head h/(NQ/NKV), the new one among them if it
  * was written before (cpattn_paged_write_kv).  Sums and softmax statistics in
- * fp32.  An infinite V value of a bf16 page makes its column of O infinite
- * (NaN with one of the other sign, or where its probability is below 2^-100 of
- * the largest); a NaN in V or K reaches its own sequence and kv head only, and a
- * row of e4m3 pages that held either is NaN.  For e4m3 pages a token's probability times its V scale is rounded to
- * fp16, with 11 bits where it is at least 2^-20 of the largest such product of
- * the q head, fewer below, and 0 below 2^-31.  A sequence without tokens (lens[b] <= 0) gets O = 0 and an LSE of
- * -infinity.
+ * fp32.  An infinite V value of a bf16 page makes its column of O infinite (NaN
+ * with one of the other sign, or where its probability is below 2^-100 of the
+ * largest); a NaN in V or K reaches its own sequence and kv head only, and a
+ * row of e4m3 pages that held either is NaN.  For e4m3 pages a token's
+ * probability times its V scale is rounded to fp16, with 11 bits where it is
+ * at least 2^-20 of the largest such product of the q head, fewer below, and 0
+ * below 2^-31.  A sequence without tokens (lens[b] <= 0) gets O = 0 and an LSE
+ * of -infinity.
  *   lens        device int32 [B], B in 1..CPATTN_MAX_PAGED_SEQS
  *   q, out      device bf16 [B, NQ, HD]
  *   lse         device fp32 [B, NQ] natural-log sum-exp, or NULL
