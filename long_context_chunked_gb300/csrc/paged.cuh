@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(256)
         for (int l = 0; l < LOADS; ++l) {
           const int row = min(row0 + r, p.rows - 1);
           const bool is_k = LOADS == 1 ? k_lane : l == 0;
-          x[r][l] = load_now((is_k ? p.k_new : p.v_new) + (static_cast<long long>(row) * nkv + g) * VECS + vec);
+          x[r][l] = load_now((is_k ? p.k_new : p.v_new) +
+                             (static_cast<long long>(row) * nkv + g) * VECS + vec);
         }
     };
     load(g0);

@@ -7,8 +7,9 @@
 // 4 HD G flops per 4 HD bytes (bf16), far below what even the legacy tensor path
 // delivers per byte.  (Of more than 16 heads every further block of 16 copies
 // the rows again, mostly from L2: 8 x 32768 bf16 tokens of 32 heads on one kv
-// head of 128 move 171 MB of DRAM for 134 MB, 41.0 us; of 16 heads 32.6 us.)  So the kernel is built around an
-// unbroken stream of TMA copies, and computes with mma.sync, transposed:
+// head of 128 move 171 MB of DRAM for 134 MB, 41.0 us; of 16 heads 32.6 us.)  So
+// the kernel is built around an unbroken stream of TMA copies, and computes with
+// mma.sync, transposed:
 // S^T = K Q^T and O^T += V^T P^T put the cached rows on M = 16 and the q heads
 // on N = 8, so a group of up to 8 heads pays for 8.  tcgen05's M = 128 would
 // leave most of its rows empty, or need e4m3 V converted to fp16 through
