@@ -215,6 +215,8 @@ def prepare(case, seed):
         import long_context_chunked_gb300 as cp
         s["ctx"] = cp.Context(nq, nkv, hd, case.get("shards", 1), case.get("capacity", 1), 1, s["scale"],
                               v_cache_f16=case.get("v_f16", False))
+        if case["op"] in ("keep4", "decode4"):       # (bytes, as the pages hold them)
+            s["kp"], s["vp"] = s["kp"].to(torch.uint8), s["vp"].to(torch.uint8)
         if "kp" in s:
             s["pages"] = cp.PagedKV(s["kp"], s["vp"], s["table"], s["ks"], s["vs"])
         if "inv_freq" in s:
