@@ -50,7 +50,8 @@ typedef enum {
   CPATTN_E_RANGE = 6,        /* a V value converted to fp16 (fp16 V cache or V staging)
                                 lies outside fp16's range */
   CPATTN_E_PAGE = 7          /* a paged call met a page id outside the pool, or a length
-                                beyond the block table or the striped cache */
+                                beyond the block table or the striped cache, or a step
+                                did not find pages or room for all of its tokens */
 } cpattn_status;
 
 typedef struct {
@@ -486,6 +487,19 @@ cpattn_status cpattn_prefill_packed(cpattn_ctx* ctx, int32_t num_seqs, const int
  *                        x8 = e4m3(x * (448 / max(amax, 2^-110)))   (fp32, nearest even)
  *                      and the value read back is s * x8.  A row that holds
  *                      an infinity or a NaN is stored with a NaN scale.
+ *   CPATTN_PAGES_E2M1  4-bit e2m1 values (magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6),
+ *                      two to a byte, the first in the lower half: k_pages and
+ *                      v_pages [num_pages, NKV, page_size, HD/2] bytes.  k_scales
+ *                      and v_scales hold one record of 4 + HD/32 bytes per token
+ *                      and kv head, [num_pages, NKV, page_size, 4 + HD/32]: s as
+ *                      fp32, then the e4m3 scale r_g of each group of 32 values:
+ *                        s = 2^(floor(log2(max(amax, 2^-117))) - 9)
+ *                        r_g = e4m3(amax_g / (6 s))
+ *                        x4 = e2m1((x / s) / r_g), 0 where r_g = 0
+ *                      (fp32, nearest even, x4 at most 6), and the value read
+ *                      back is s * r_g * x4.  A row that holds an infinity or a
+ *                      NaN is stored with s = NaN.  Readers take any r_g >= 0 and
+ *                      any s that is a power of two up to 2^118.
  * Lengths, row_starts and block_table are DEVICE arrays, read when the kernels
  * run: a captured graph of these calls can be replayed after they changed.
  * So they are checked on the device: a page id outside [0, num_pages), or a
@@ -498,23 +512,25 @@ cpattn_status cpattn_prefill_packed(cpattn_ctx* ctx, int32_t num_seqs, const int
  */
 #define CPATTN_PAGES_BF16 0
 #define CPATTN_PAGES_E4M3 1
+#define CPATTN_PAGES_E2M1 4
 #define CPATTN_MAX_PAGED_SEQS 4096
 
 typedef struct {
-  int32_t format;              /* CPATTN_PAGES_BF16 or CPATTN_PAGES_E4M3 */
+  int32_t format;              /* CPATTN_PAGES_BF16, _E4M3 or _E2M1 */
   int32_t page_size;           /* 16, 32, 64, 128 or 256 tokens */
   int32_t num_pages;           /* pages in the pool */
   int32_t max_pages;           /* columns of block_table in use, >= 1 */
   int64_t table_stride;        /* elements between its rows, >= max_pages */
   void* k_pages;               /* device, 16-byte aligned */
   void* v_pages;
-  float* k_scales;             /* device, 16-byte aligned; e4m3 only, else NULL */
+  float* k_scales;             /* device, 16-byte aligned: e4m3 scales, or e2m1
+                                  records (as bytes); bf16: NULL */
   float* v_scales;
   const int32_t* block_table;  /* device int32 [num_seqs][table_stride] */
 } cpattn_pages;
 
 /*
- * Write new tokens into their pages (quantising them for e4m3 pages): rows
+ * Write new tokens into their pages (quantising them for e4m3 and e2m1 pages): rows
  * row_starts[b] .. row_starts[b+1]-1 of k_new and v_new are tokens
  * cache_lens[b], cache_lens[b]+1, ... of sequence b.
  *   num_seqs     B, 1..CPATTN_MAX_PAGED_SEQS
@@ -563,10 +579,11 @@ cpattn_status cpattn_paged_read_kv(cpattn_ctx* ctx, const cpattn_pages* pages, i
  * fp32.  An infinite V value of a bf16 page makes its column of O infinite (NaN
  * with one of the other sign, or where its probability is below 2^-100 of the
  * largest); a NaN in V or K reaches its own sequence and kv head only, and a
- * row of e4m3 pages that held either is NaN.  For e4m3 pages a token's
+ * row of e4m3 or e2m1 pages that held either is NaN.  For e4m3 pages a token's
  * probability times its V scale is rounded to fp16, with 11 bits where it is
  * at least 2^-20 of the largest such product of the q head, fewer below, and 0
- * below 2^-31.  A sequence without tokens (lens[b] <= 0) gets O = 0 and an LSE
+ * below 2^-31.  For e2m1 pages the same is done with s, and the product times
+ * r_g / 256 is rounded to fp16 once more.  A sequence without tokens (lens[b] <= 0) gets O = 0 and an LSE
  * of -infinity.
  *   lens        device int32 [B], B in 1..CPATTN_MAX_PAGED_SEQS
  *   q, out      device bf16 [B, NQ, HD]
@@ -588,6 +605,124 @@ cpattn_status cpattn_paged_decode_workspace(const cpattn_ctx* ctx, int32_t num_s
 cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
                                   const int32_t* lens, const void* q, void* out, float* lse,
                                   void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * A serving step around the attention
+ * -----------------------------------
+ * plan (once per step), then in every layer norm_rope_write_kv and paged_decode
+ * (or norm_rope, prefill_packed and paged_write_kv for whole prompts), and trim
+ * when requests end or drafted tokens are rejected.  All of it is captured and
+ * replayed like the paged calls: lengths and lists are device arrays.
+ */
+
+/*
+ * Pages, places and positions of a step's new tokens, from the requests' lengths.
+ * Sequence b holds cache_lens[b] tokens and gets new_lens[b] more; its pages are
+ * extended off a list of free pages and written to block_table, which these two
+ * calls alone write.
+ *   num_seqs     B, 1..CPATTN_MAX_PAGED_SEQS
+ *   num_rows     rows that the step's arrays have room for, >= 0
+ *   cache_lens   device int32 [B] tokens held; negative: an empty place
+ *   new_lens     device int32 [B]; negative counts as 0
+ *   free_pages   device int32 [num_pages], a stack: entries 0 .. free_count - 1 are
+ *                the pages nobody holds, and the last of them goes first
+ *   free_count   device int32 [1], in and out
+ *   lens         device int32 [B], out: cache_lens[b] + new_lens[b], or cache_lens[b]
+ *                where the sequence is not served.  May be cache_lens.
+ *   row_starts   device int32 [B+1], out: rows row_starts[b] .. row_starts[b+1] - 1 are
+ *                the new tokens of sequence b
+ *   positions    device int32 [num_rows], out: each row's position in its sequence
+ *   slots        device int32 [num_rows], out: page * page_size + slot of each row
+ * A row of nobody's (behind the last sequence's, or of one that is not served) gets
+ * position and slot -1.  Sequences are served in order: one is not if its pages and
+ * those of all sequences before it, served or not, are more than the list has
+ * (one that needs no page always is), if its table row has no room, or if its rows
+ * pass num_rows; cpattn_sync_status then returns E_PAGE.  So does a page outside
+ * the pool, whose rows get slot -1, or a count outside [0, num_pages], which is
+ * cut.  Table entries behind a sequence's last page stay as they were.
+ * free_pages, block_table and the other arrays must not overlap one another, but
+ * for lens and cache_lens.  One launch.  Errors: as cpattn_paged_write_kv.
+ */
+cpattn_status cpattn_paged_plan(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                                int32_t num_rows, const int32_t* cache_lens,
+                                const int32_t* new_lens, int32_t* free_pages, int32_t* free_count,
+                                int32_t* lens, int32_t* row_starts, int32_t* positions,
+                                int32_t* slots, void* stream);
+
+/*
+ * Back to the list: the pages of sequence b behind those that its first keep[b]
+ * tokens need, of the lens[b] it holds (keep[b] = 0: all of them).  keep[b] < 0 or
+ * >= lens[b] leaves it alone.  A trim back to the lengths before a plan gives list
+ * and count back as they were.  The caller goes on with keep[b] as the length; a
+ * page that several sequences hold must not go back while one still needs it.
+ * More pages than the pool has left to give back (some would go back twice): none
+ * does, and cpattn_sync_status returns E_PAGE, as for a length beyond the table's
+ * row, which is cut there.
+ *   lens, keep   device int32 [B]
+ * One launch.  Errors: as cpattn_paged_write_kv.
+ */
+cpattn_status cpattn_paged_trim(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                                const int32_t* lens, const int32_t* keep, int32_t* free_pages,
+                                int32_t* free_count, void* stream);
+
+/* Norms and rotation of heads (cpattn_norm_rope, cpattn_norm_rope_write_kv). */
+typedef struct {
+  const void* q_weight;        /* device [HD] norm weights of queries, or NULL: no norm */
+  const void* k_weight;        /* the same of keys */
+  const uint64_t* rope_steps;  /* device [rotary_dim / 2], 8-byte aligned, of
+                                  cpattn_rope_steps; NULL if rotary_dim is 0 */
+  int32_t weight_f32;          /* 0: weights are bf16, 1: fp32; 4-byte aligned */
+  int32_t rotary_dim;          /* the first dims of a head that turn: a multiple of 8 in
+                                  [0, HD]; the others are left (normed) as they are */
+  int32_t interleaved;         /* 0: pairs (i, i + rotary_dim / 2), 1: pairs (2i, 2i + 1) */
+  float eps;                   /* >= 0, under the norm's root */
+  float rope_scale;            /* factor of the rotated dims, ordinarily 1 */
+} cpattn_norm_rope_desc;
+
+/*
+ * Turns per position of each pair in 64-bit fixed point, round(2^64 inv_freq / 2 pi)
+ * modulo 2^64: with them the angle of any position is reduced without rounding.
+ * Host arrays; |inv_freq| <= 2^20.  Error: E_INVALID.
+ */
+cpattn_status cpattn_rope_steps(const double* inv_freq, int32_t n, uint64_t* steps);
+
+/*
+ * Per-head norm and rotation of new tokens' queries and keys in one pass.  For
+ * each row r with positions[r] >= 0 and each head of HD values x of q (and k):
+ *   y = x / sqrt(mean(x^2) + eps) * weight           (no weight: y = x)
+ *   (y_a, y_b) <- rope_scale (y_a cos - y_b sin, y_b cos + y_a sin)
+ * for each pair i of the first rotary_dim values, at the angle positions[r] *
+ * inv_freq[i]; in fp32, rounded once.  Rows with a negative position are left as
+ * they are in q_out and k_out.
+ *   positions       device int32 [num_rows]
+ *   q, q_out        device bf16, NQ heads of HD per row, rows *_stride elements
+ *                   apart (a multiple of 8, at least NQ HD): so q and k may be
+ *                   parts of the rows of one projection
+ *   k, k_out        the same of NKV heads
+ * q_out may be q with the same stride, and k_out k; no other overlap.  A NaN or an
+ * infinity stays within its row and head.  One launch.  Errors: E_INVALID, E_CUDA.
+ */
+cpattn_status cpattn_norm_rope(cpattn_ctx* ctx, const cpattn_norm_rope_desc* desc, int32_t num_rows,
+                               const int32_t* positions, const void* q, int64_t q_stride,
+                               const void* k, int64_t k_stride, void* q_out, int64_t q_out_stride,
+                               void* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * The same, with K and V going straight into their pages, as cpattn_paged_write_kv
+ * writes them, but that K is rounded (e4m3, e2m1: quantised) from fp32 at once.
+ *   slots        device int32 [num_rows], page * page_size + slot of each row
+ *                (cpattn_paged_plan); negative: K and V are not stored; beyond
+ *                the pool: the same, and cpattn_sync_status returns E_PAGE
+ *   v            device bf16, as k
+ * The table plays no part and only has to be a valid pointer.  Two rows of a call
+ * must not name the same slot.  One launch.  Errors: E_INVALID, E_UNSUPPORTED, E_CUDA.
+ */
+cpattn_status cpattn_norm_rope_write_kv(cpattn_ctx* ctx, const cpattn_norm_rope_desc* desc,
+                                        const cpattn_pages* pages, int32_t num_rows,
+                                        const int32_t* positions, const int32_t* slots,
+                                        const void* q, int64_t q_stride, const void* k,
+                                        int64_t k_stride, const void* v, int64_t v_stride,
+                                        void* q_out, int64_t q_out_stride, void* stream);
 
 /* Static description of a status code. */
 const char* cpattn_status_string(cpattn_status s);

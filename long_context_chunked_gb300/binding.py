@@ -21,6 +21,8 @@ MAX_SEQS = 128
 MAX_ROW_BLOCKS = 2048
 MAX_PAGED_SEQS = 4096
 PAGE_SIZES = (16, 32, 64, 128, 256)
+PAGES_BF16, PAGES_E4M3, PAGES_E2M1 = 0, 1, 4  # CPATTN_PAGES_*
+GROUP4 = 32  # values of an e2m1 row that share a scale
 
 # Every symbol include/cpattn.h declares.
 EXPORTS = ("cpattn_create", "cpattn_write_kv", "cpattn_prefill", "cpattn_sync_status",
@@ -30,7 +32,9 @@ EXPORTS = ("cpattn_create", "cpattn_write_kv", "cpattn_prefill", "cpattn_sync_st
            "cpattn_splitkv_workspace", "cpattn_cache_walk_from", "cpattn_prefill_write_kv",
            "cpattn_set_barrier_counts", "cpattn_set_v_staging", "cpattn_v_staging_bytes",
            "cpattn_prefill_packed", "cpattn_prefill_packed_workspace", "cpattn_paged_write_kv",
-           "cpattn_paged_read_kv", "cpattn_paged_decode", "cpattn_paged_decode_workspace")
+           "cpattn_paged_read_kv", "cpattn_paged_decode", "cpattn_paged_decode_workspace",
+           "cpattn_paged_plan", "cpattn_paged_trim", "cpattn_rope_steps", "cpattn_norm_rope",
+           "cpattn_norm_rope_write_kv")
 
 # cpattn_config.pairing values, by name.
 PAIRING = {"mma2": 0, "none": 1, "pingpong": 2}
@@ -64,24 +68,31 @@ class Pages(ctypes.Structure):
 
 class PagedKV:
     """A paged KV cache: pools [num_pages, NKV, page_size, HD] of bf16, or of
-    torch.float8_e4m3fn with fp32 scales [num_pages, NKV, page_size], and the
+    torch.float8_e4m3fn with fp32 scales [num_pages, NKV, page_size], or 4-bit
+    pools [num_pages, NKV, page_size, HD // 2] of uint8 (two e2m1 values each)
+    with uint8 scale records [num_pages, NKV, page_size, 4 + HD // 32]; and the
     int32 block table [num_seqs, max_pages] (its rows may be a slice of a wider
     table).  Holds references to the tensors and checks them once; their
     contents are read by the kernels of each call."""
 
     def __init__(self, k_pages, v_pages, block_table, k_scales=None, v_scales=None):
         import torch
-        if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-            raise ValueError(f"pages must be bfloat16 or float8_e4m3fn, got {k_pages.dtype}")
+        formats = {torch.bfloat16: PAGES_BF16, torch.float8_e4m3fn: PAGES_E4M3, torch.uint8: PAGES_E2M1}
+        if k_pages.dtype not in formats:
+            raise ValueError(f"pages must be bfloat16, float8_e4m3fn or uint8 (e2m1), got {k_pages.dtype}")
         if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
             raise ValueError("k_pages and v_pages must be alike, [num_pages, NKV, page_size, HD]")
-        e4m3 = k_pages.dtype == torch.float8_e4m3fn
-        if (k_scales is None) != (not e4m3) or (v_scales is None) != (not e4m3):
-            raise ValueError("e4m3 pages need k_scales and v_scales, bf16 pages take none")
-        dense = [k_pages, v_pages] + ([k_scales, v_scales] if e4m3 else [])
+        fmt = formats[k_pages.dtype]
+        if (k_scales is None) != (fmt == PAGES_BF16) or (v_scales is None) != (fmt == PAGES_BF16):
+            raise ValueError("e4m3 and e2m1 pages need k_scales and v_scales, bf16 pages take none")
+        dense = [k_pages, v_pages] + ([] if fmt == PAGES_BF16 else [k_scales, v_scales])
+        hd = k_pages.shape[3] * (2 if fmt == PAGES_E2M1 else 1)
         for t in dense[2:]:
-            if t.dtype != torch.float32 or t.shape != k_pages.shape[:3]:
+            if fmt == PAGES_E4M3 and (t.dtype != torch.float32 or t.shape != k_pages.shape[:3]):
                 raise ValueError("scales must be float32 [num_pages, NKV, page_size]")
+            if fmt == PAGES_E2M1 and (t.dtype != torch.uint8 or
+                                      t.shape != (*k_pages.shape[:3], 4 + hd // GROUP4)):
+                raise ValueError("scales must be uint8 [num_pages, NKV, page_size, 4 + HD // 32]")
         if block_table.dim() != 2 or block_table.dtype != torch.int32 or (
                 block_table.shape[1] > 1 and block_table.stride(1) != 1) or (
                 block_table.shape[0] > 1 and block_table.stride(0) < block_table.shape[1]):
@@ -94,10 +105,56 @@ class PagedKV:
         self.k_scales, self.v_scales = k_scales, v_scales
         self.device = k_pages.get_device()
         self.num_seqs, cols = block_table.shape
-        self.num_kv_heads, self.head_dim = k_pages.shape[1], k_pages.shape[3]
-        self.c = Pages(int(e4m3), k_pages.shape[2], k_pages.shape[0], cols,
+        self.num_kv_heads, self.head_dim = k_pages.shape[1], hd
+        self.c = Pages(fmt, k_pages.shape[2], k_pages.shape[0], cols,
                        max(block_table.stride(0), cols), _ptr(k_pages), _ptr(v_pages),
                        _ptr(k_scales), _ptr(v_scales), _ptr(block_table))
+        self.ref = ctypes.byref(self.c)
+
+
+class NormRopeDesc(ctypes.Structure):
+    """cpattn_norm_rope_desc."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("rope_steps", ctypes.c_void_p), ("weight_f32", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("rope_scale", ctypes.c_float)]
+
+
+class NormRope:
+    """Norm weights and rotation of a layer's query and key heads: inv_freq, the
+    rotary_dim / 2 angles per position (host values, taken as float64; empty: no
+    rotation), q_weight and k_weight [HD] of bf16 or fp32 on the GPU (None: no
+    norm).  interleaved: pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2);
+    scale: a factor of the rotated values.  Holds the tensors; a context's calls
+    read them."""
+
+    def __init__(self, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, scale: float = 1.0, device=None):
+        import torch
+        freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+        if freq.ndim != 1 or freq.size % 4:
+            raise ValueError("inv_freq must be a vector of rotary_dim / 2 values, rotary_dim a multiple of 8")
+        steps = np.zeros(freq.size, dtype=np.uint64)
+        if load().cpattn_rope_steps(freq.ctypes.data, freq.size, steps.ctypes.data) != OK:
+            raise ValueError("inv_freq must be finite and within 2^20")
+        weights = [w for w in (q_weight, k_weight) if w is not None]
+        for w in weights:
+            if w.dtype not in (torch.bfloat16, torch.float32) or w.dtype != weights[0].dtype or \
+                    w.dim() != 1 or w.shape != weights[0].shape or not w.is_cuda or \
+                    not w.is_contiguous() or w.device != weights[0].device:
+                raise ValueError("weights must be alike, contiguous bfloat16 or float32 [HD] on one CUDA device")
+        if device is None:
+            device = weights[0].device if weights else torch.device("cuda", torch.cuda.current_device())
+        self.steps = torch.from_numpy(steps.view(np.int64)).to(device) if freq.size else None
+        self.q_weight, self.k_weight, self.rotary_dim = q_weight, k_weight, 2 * freq.size
+        held = weights + ([self.steps] if freq.size else [])
+        if any(w.device != held[0].device for w in held):
+            raise ValueError("weights and device must be the same CUDA device")
+        self.device = held[0].get_device() if held else torch.device(device).index
+        self.head_dim = weights[0].numel() if weights else None
+        f32 = bool(weights) and weights[0].dtype is torch.float32
+        self.c = NormRopeDesc(_ptr(q_weight), _ptr(k_weight), _ptr(self.steps), int(f32),
+                              self.rotary_dim, int(bool(interleaved)), float(eps), float(scale))
         self.ref = ctypes.byref(self.c)
 
 
@@ -166,6 +223,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                 ("cpattn_paged_decode", [P, PAGES, I32, P, P, P, P, P, U64, P])):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = I32
+    if hasattr(lib, "cpattn_paged_plan"):
+        I64, NR = ctypes.c_int64, ctypes.POINTER(NormRopeDesc)
+        for name, args in (
+                ("cpattn_paged_plan", [P, PAGES, I32, I32] + [P] * 9),
+                ("cpattn_paged_trim", [P, PAGES, I32] + [P] * 5),
+                ("cpattn_rope_steps", [P, I32, P]),
+                ("cpattn_norm_rope", [P, NR, I32, P] + [P, I64] * 4 + [P]),
+                ("cpattn_norm_rope_write_kv", [P, NR, PAGES, I32, P, P] + [P, I64] * 4 + [P])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = I32
     _libs[path] = lib
     return lib
 
@@ -190,6 +257,16 @@ def _want(name, t, dtype, shape, device: int):
             or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor {list(shape)} on CUDA device "
                          f"{device}, got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _want_rows(name, t, rows: int, heads: int, hd: int, device: int) -> int:
+    """The row stride of a bf16 CUDA tensor [rows, heads, hd] whose rows are dense."""
+    import torch
+    if t.dtype is not torch.bfloat16 or t.shape != (rows, heads, hd) or t.get_device() != device \
+            or device < 0 or (t.numel() > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != hd))):
+        raise ValueError(f"{name}: expected a bfloat16 tensor [{rows}, {heads}, {hd}] with dense rows on "
+                         f"CUDA device {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.stride(0) if rows > 1 else max(t.stride(0), heads * hd)
 
 
 def _workspace_bytes(workspace, device: int) -> int:
@@ -428,6 +505,82 @@ class Context:
         self._check(self.lib.cpattn_paged_decode(
             self._h, pages.ref, b, lens.data_ptr(), q.data_ptr(), out.data_ptr(), _ptr(lse),
             workspace.data_ptr(), _workspace_bytes(workspace, dev), _stream_on(stream, dev)))
+
+    # -- a serving step around the attention ------------------------------
+    def paged_plan(self, pages: PagedKV, cache_lens, new_lens, free_pages, free_count, lens,
+                   row_starts, positions, slots, stream=None):
+        """Pages, places and positions of a step's new tokens, from the requests'
+        lengths: new_lens[b] more for sequence b, which holds cache_lens[b] (< 0: an
+        empty place).  Takes pages off the stack free_pages [num_pages] (free_count
+        [1]: how many are free), extends pages.block_table and fills lens [num_seqs],
+        row_starts [num_seqs + 1] and each row's positions and slots [rows].  All int32
+        CUDA tensors; lens may be cache_lens.  What does not fit is not served."""
+        import torch
+        b, dev = pages.num_seqs, pages.device
+        for name, t, n in (("cache_lens", cache_lens, b), ("new_lens", new_lens, b), ("lens", lens, b),
+                           ("row_starts", row_starts, b + 1), ("free_pages", free_pages, pages.c.num_pages),
+                           ("free_count", free_count, 1), ("positions", positions, positions.numel()),
+                           ("slots", slots, positions.numel())):
+            _want(name, t, torch.int32, (n,), dev)
+        self._check_pages(pages)
+        self._check(self.lib.cpattn_paged_plan(
+            self._h, pages.ref, b, positions.numel(), cache_lens.data_ptr(), new_lens.data_ptr(),
+            free_pages.data_ptr(), free_count.data_ptr(), lens.data_ptr(), row_starts.data_ptr(),
+            positions.data_ptr(), slots.data_ptr(), _stream_on(stream, dev)))
+
+    def paged_trim(self, pages: PagedKV, lens, keep, free_pages, free_count, stream=None):
+        """Give back to the list the pages of sequence b behind those of its first
+        keep[b] tokens, of the lens[b] it holds (0: all of them; < 0: none)."""
+        import torch
+        b, dev = pages.num_seqs, pages.device
+        for name, t, n in (("lens", lens, b), ("keep", keep, b), ("free_pages", free_pages, pages.c.num_pages),
+                           ("free_count", free_count, 1)):
+            _want(name, t, torch.int32, (n,), dev)
+        self._check_pages(pages)
+        self._check(self.lib.cpattn_paged_trim(
+            self._h, pages.ref, b, lens.data_ptr(), keep.data_ptr(), free_pages.data_ptr(),
+            free_count.data_ptr(), _stream_on(stream, dev)))
+
+    def norm_rope(self, nr: NormRope, positions, q, k, q_out, k_out, stream=None):
+        """Per-head norm and rotation of q [rows, NQ, HD] and k [rows, NKV, HD] (bf16;
+        rows may lie apart, as in a projection's output) into q_out and k_out, which
+        may be q and k.  positions: int32 [rows]; < 0: the row is left alone."""
+        rows, nq, nkv, hd, dev = self._check_norm_rope(nr, positions)
+        args = []
+        for name, t, heads in (("q", q, nq), ("k", k, nkv), ("q_out", q_out, nq), ("k_out", k_out, nkv)):
+            args += [t.data_ptr(), _want_rows(name, t, rows, heads, hd, dev)]
+        if rows:
+            self._check(self.lib.cpattn_norm_rope(self._h, nr.ref, rows, positions.data_ptr(), *args,
+                                                  _stream_on(stream, dev)))
+
+    def norm_rope_write_kv(self, nr: NormRope, pages: PagedKV, positions, slots, q, k, v, q_out,
+                           stream=None):
+        """The same, with K and V [rows, NKV, HD] going straight into their pages: row r
+        to slots[r] = page * page_size + slot (int32, from paged_plan; < 0: not stored)."""
+        import torch
+        rows, nq, nkv, hd, dev = self._check_norm_rope(nr, positions)
+        self._check_pages(pages)
+        _want("slots", slots, torch.int32, (rows,), dev)
+        if pages.device != dev:
+            raise ValueError("pages and positions must be on one CUDA device")
+        args = []
+        for name, t, heads in (("q", q, nq), ("k", k, nkv), ("v", v, nkv), ("q_out", q_out, nq)):
+            args += [t.data_ptr(), _want_rows(name, t, rows, heads, hd, dev)]
+        if rows:
+            self._check(self.lib.cpattn_norm_rope_write_kv(
+                self._h, nr.ref, pages.ref, rows, positions.data_ptr(), slots.data_ptr(), *args,
+                _stream_on(stream, dev)))
+
+    def _check_norm_rope(self, nr: NormRope, positions):
+        import torch
+        nq, nkv, hd = self.dims
+        dev = positions.get_device()
+        _want("positions", positions, torch.int32, (positions.numel(),), dev)
+        if nr.device != dev:
+            raise ValueError("the norm's weights and positions must be on one CUDA device")
+        if nr.head_dim not in (None, hd):
+            raise ValueError(f"norm weights of {nr.head_dim} values, the context's heads have {hd}")
+        return positions.numel(), nq, nkv, hd, dev
 
     def _check_pages(self, pages: PagedKV):
         if pages.num_kv_heads != self.dims[1] or pages.head_dim != self.dims[2]:

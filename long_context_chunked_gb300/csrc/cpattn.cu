@@ -22,6 +22,8 @@
 #include "write_kv.cuh"
 #include "paged.cuh"
 #include "paged_decode.cuh"
+#include "paged_plan.cuh"
+#include "norm_rope.cuh"
 #include "merge.cuh"
 #include "plan.h"
 
@@ -56,7 +58,8 @@ struct cpattn_ctx {
   // GQA packing for short-chunk launches (cpattn_config.gqa_packing, or the
   // CPATTN_GQA_PACKING override).
   bool gqa_packing = true;
-  bool decode_ready[2][2] = {};  // [HD == 256][e4m3]: the decode kernel has been set up
+  bool plan_ready = false;  // the plan and trim kernels have been set up
+  bool decode_ready[2][2][3] = {};  // [HD == 256][head blocks - 1][format]: set up
   std::vector<int> block_lens;  // scratch of the unit-order choice
   // Unit order (test override CPATTN_UNIT_ORDER): 0 chosen by the cost
   // model, 1 longest first, 2 kv-head-major.
@@ -1320,3 +1323,4 @@ cpattn_status cpattn_prefill_packed(cpattn_ctx* ctx, int32_t num_seqs, const int
 }  // extern "C"
 
 #include "paged_host.cuh"
+#include "step_host.cuh"

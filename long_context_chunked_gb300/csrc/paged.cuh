@@ -1,5 +1,6 @@
 // The paged KV cache: writing new tokens into pages (as bf16, or quantised to
-// e4m3) and reading pages back into the striped cache of the chunked prefill.
+// e4m3 or e2m1) and reading pages back into the striped cache of the chunked
+// prefill.
 // The attention over the pages is in paged_decode.cuh.
 //
 // A page holds page_size consecutive tokens of one sequence for every kv
@@ -15,6 +16,18 @@
 // so that a token can be appended without touching the page's earlier ones.
 // The scale is one factor of a whole row: the attention multiplies it into a
 // logit (K) or a probability (V), never into the row's HD values.
+//
+// e2m1 pages hold 4-bit values (magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6), two to a
+// byte, and scales of two levels for each (token, kv head), K and V each:
+//   s = 2^(floor(log2 amax) - 9), amax at least 2^-117,
+//   r_g = e4m3(amax_g / (6 s)) of each group g of 32 values, at most 176,
+//   x4 = e2m1((x / s) / r_g), 0 where r_g = 0,   x ~ s r_g x4.
+// s is a power of two so that every one of these roundings is decided exactly in
+// fp32 for a bf16 x: x / s is exact, and a quotient of two numbers this short is
+// either a border between two codes or further from it than fp32 rounds.  r_g
+// keeps e4m3's precision for groups down to 2^-15 of the row's largest value.  A
+// row's scales are one record of 4 + HD / 32 bytes, s as fp32 and then the r_g,
+// so that one copy brings them.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -36,10 +49,20 @@ __device__ __forceinline__ T load_now(const T* p) {
   return *p;
 }
 
+// Page formats, as CPATTN_PAGES_*.
+constexpr int kBf16 = 0, kE4m3 = 1, kE2m1 = 4;
+
+constexpr int kGroup4 = 32;  // values of an e2m1 row that share an r_g
+__host__ __device__ constexpr int record_bytes(int hd) { return 4 + hd / kGroup4; }
+// Bytes of a row's values.
+__host__ __device__ constexpr int row_bytes(int hd, int fmt) {
+  return fmt == kBf16 ? 2 * hd : (fmt == kE4m3 ? hd : hd / 2);
+}
+
 struct PagedPool {
-  void* k;           // bf16 or e4m3 [num_pages][NKV][page_size][HD]
+  void* k;           // bf16, e4m3 or e2m1 [num_pages][NKV][page_size][HD]
   void* v;
-  float* k_scales;   // e4m3: [num_pages][NKV][page_size]
+  float* k_scales;   // e4m3: [num_pages][NKV][page_size]; e2m1: records, as many
   float* v_scales;
   const int* table;  // [num_seqs][table_stride], the first max_pages columns used
   long long table_stride;
@@ -82,6 +105,28 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
   return r;
 }
 
+// Two fp32 values as e2m1 (round to nearest even, saturating), lo in the low half
+// of the byte; and four bytes' values as fp16 pairs (exact).
+__device__ __forceinline__ uint32_t pack_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
+      "cvt.u32.u8 %0, b;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t x, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(x));
+}
+
 // Largest magnitude of eight bf16 values, as bf16 bits: for sign-less bf16
 // the order of the bit patterns is the order of the values, with infinities
 // and NaNs on top.
@@ -89,6 +134,97 @@ __device__ __forceinline__ uint32_t amax_bits(uint4 x) {
   const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
                               __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
   return max(m & 0xFFFFu, m >> 16);
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// A row of HD values in HD / 8 neighbouring lanes, eight each, as fp32: what the
+// page stores for it.  mag: the bits of the lane's largest magnitude.  Rows
+// that hold an infinity or a NaN have a NaN scale and read back as NaN.
+struct Row8 {
+  uint2 x8;  // the lane's values
+  float s;   // the row's scale
+};
+template <int HD>
+__device__ __forceinline__ Row8 quantise_e4m3(const float (&x)[8], uint32_t mag) {
+#pragma unroll
+  for (int o = HD / 16; o > 0; o >>= 1) mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, o));
+  const float amax = mag >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                        : fmaxf(__uint_as_float(mag), kTinyAmax);
+  const float inv = kE4m3Max / amax;
+  uint32_t h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) h[j] = pack_e4m3x2(x[2 * j] * inv, x[2 * j + 1] * inv);
+  return {make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16)), amax / kE4m3Max};
+}
+
+struct Row4 {
+  uint32_t x4;  // the lane's values, the first in the lowest bits
+  float s;      // the row's scale
+  uint32_t r;   // e4m3 scale of the lane's group (four lanes)
+};
+template <int HD>
+__device__ __forceinline__ Row4 quantise_e2m1(const float (&x)[8], uint32_t mag) {
+  mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
+  mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
+  uint32_t row = mag;
+#pragma unroll
+  for (int o = HD / 16; o >= 4; o >>= 1) row = max(row, __shfl_xor_sync(0xFFFFFFFFu, row, o));
+  if (row >= 0x7F800000u) return {0u, __uint_as_float(0x7FC00000u), 0u};
+  const uint32_t e = max(row >> 23, 10u);                     // exponent field of amax
+  const float inv_s = __uint_as_float((263u - e) << 23);      // 2^(9 - k), k = e - 127
+  const uint32_t r = pack_e4m3x2(__uint_as_float(mag) * inv_s / 6.f, 0.f) & 0xFFu;
+  Row4 out = {0u, __uint_as_float((e - 9u) << 23), r};
+  if (r != 0u) {
+    const float rf = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(r))).x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      out.x4 |= pack_e2m1x2(x[2 * j] * inv_s / rf, x[2 * j + 1] * inv_s / rf) << (8 * j);
+  }
+  return out;
+}
+
+// Eight values of lane `vec` of a row's HD / 8 lanes to row `dst` of the pool (and
+// their scales), if `dst` >= 0; mag: the bits of the largest magnitude among
+// them (not read for bf16).  All lanes of the warp call it.
+template <int HD, int FMT>
+__device__ __forceinline__ void store_row(const PagedPool& c, bool is_k, long long dst, int vec,
+                                          const float (&x)[8], uint32_t mag) {
+  constexpr int VECS = HD / 8;
+  void* pool = is_k ? c.k : c.v;
+  float* scales = is_k ? c.k_scales : c.v_scales;
+  if constexpr (FMT == kE4m3) {
+    const Row8 y = quantise_e4m3<HD>(x, mag);
+    if (dst < 0) return;
+    reinterpret_cast<uint2*>(pool)[dst * VECS + vec] = y.x8;
+    if (vec == 0) scales[dst] = y.s;
+  } else if constexpr (FMT == kE2m1) {
+    const Row4 y = quantise_e2m1<HD>(x, mag);
+    // The record's words: s from the first lane, then four r_g each.
+    uint32_t r = y.r;
+    r |= __shfl_down_sync(0xFFFFFFFFu, r, 4) << 8;
+    r |= __shfl_down_sync(0xFFFFFFFFu, r, 8) << 16;
+    if (dst < 0) return;
+    reinterpret_cast<uint32_t*>(pool)[dst * VECS + vec] = y.x4;
+    uint32_t* rec = reinterpret_cast<uint32_t*>(scales) + dst * (record_bytes(HD) / 4);
+    if (vec == 0) rec[0] = __float_as_uint(y.s);
+    if ((vec & 15) == 0) rec[1 + vec / 16] = r;
+  } else {
+    if (dst < 0) return;
+    reinterpret_cast<uint4*>(pool)[dst * VECS + vec] =
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                   pack_bf16x2(x[6], x[7]));
+  }
+}
+__device__ __forceinline__ void bf16x8_to_f32x8(uint4 x, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = __uint_as_float(w[j] << 16);
+    f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
 }
 
 // ------------------------------------------------------------------ write
@@ -154,7 +290,7 @@ __device__ __forceinline__ long long write_place(const PagedWriteParams& p, int 
 // loaded: 17421 tokens of 4 heads of 128 take 14.0 us for 54 MB, 3.9 TB/s, and
 // 40000 tokens of 2 heads of 256 37.7 us for 124 MB, 3.3 TB/s (108 registers, so
 // two blocks per SM).  A decode step of 7 tokens: 2.3 us as a node of a graph.
-template <int HD, bool Q8, int ROWS>
+template <int HD, int ROWS, int FMT>
 __global__ void __launch_bounds__(256)
     paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
   constexpr int VECS = HD / 8;        // 16-byte vectors per row
@@ -202,28 +338,13 @@ __global__ void __launch_bounds__(256)
           const bool is_k = LOADS == 1 ? k_lane : l == 0;
           const long long dst = pool_row(p.pool, static_cast<int>(place[r] >> 8), g,
                                          static_cast<int>(place[r] & 255));
-          void* pool = is_k ? p.pool.k : p.pool.v;
-          if constexpr (Q8) {
-            uint32_t m = amax_bits(x[r][l]);
-#pragma unroll
-            for (int o = VECS / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            // A row with an infinity or a NaN has no scale: all of it reads back as NaN.
-            float amax = __uint_as_float(m << 16);
-            amax = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : fmaxf(amax, kTinyAmax);
-            const float inv = kE4m3Max / amax;
-            const uint32_t w[4] = {x[r][l].x, x[r][l].y, x[r][l].z, x[r][l].w};
-            uint32_t h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              h[j] = pack_e4m3x2(__uint_as_float(w[j] << 16) * inv,
-                                 __uint_as_float(w[j] & 0xFFFF0000u) * inv);
-            if (place[r] >= 0) {
-              reinterpret_cast<uint2*>(pool)[dst * VECS + vec] =
-                  make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-              if (vec == 0) (is_k ? p.pool.k_scales : p.pool.v_scales)[dst] = amax / kE4m3Max;
-            }
+          if constexpr (FMT == kBf16) {
+            if (place[r] >= 0)
+              reinterpret_cast<uint4*>(is_k ? p.pool.k : p.pool.v)[dst * VECS + vec] = x[r][l];
           } else {
-            if (place[r] >= 0) reinterpret_cast<uint4*>(pool)[dst * VECS + vec] = x[r][l];
+            float f[8];
+            bf16x8_to_f32x8(x[r][l], f);
+            store_row<HD, FMT>(p.pool, is_k, place[r] < 0 ? -1 : dst, vec, f, amax_bits(x[r][l]) << 16);
           }
         }
       }
@@ -280,6 +401,26 @@ __device__ __forceinline__ void load_vec(uint2& x, const void* pool, long long a
 __device__ __forceinline__ void load_vec(uint4& x, const void* pool, long long at) {
   x = load_now(reinterpret_cast<const uint4*>(pool) + at);
 }
+__device__ __forceinline__ void load_vec(uint32_t& x, const void* pool, long long at) {
+  x = load_now(reinterpret_cast<const uint32_t*>(pool) + at);
+}
+// (s: e2m1: s r_g.  A row of ordinary magnitudes comes back exactly: s r_g x4 has
+// at most 6 significant bits.)
+__device__ __forceinline__ uint4 widen_vec(uint32_t x, float s, bool f16, bool* overflow) {
+  uint32_t h[4], o[4];
+  e2m1x8_to_f16x8(x, h);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = f16x2_to_f32x2(h[j]);
+    if (f16) {
+      o[j] = pack_f16x2(f.x * s, f.y * s);
+      if ((o[j] & 0x7C00u) == 0x7C00u || (o[j] & 0x7C000000u) == 0x7C000000u) *overflow = true;
+    } else {
+      o[j] = pack_bf16x2(f.x * s, f.y * s);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
 __device__ __forceinline__ uint4 widen_vec(uint2 x, float s, bool f16, bool* overflow) {
   const uint32_t w[2] = {x.x, x.y};
   uint32_t o[4];
@@ -309,7 +450,7 @@ __device__ __forceinline__ uint4 widen_vec(uint4 x, float, bool f16, bool* overf
 // 89 MB, 4.7 TB/s, the launch and the prefix sums of every block among them.
 constexpr int kReadRun = 4;
 
-template <int HD, bool Q8>
+template <int HD, int FMT>
 __global__ void __launch_bounds__(256)
     paged_read_kernel(const __grid_constant__ PagedReadParams p) {
   constexpr int VECS = HD / 8;
@@ -363,7 +504,9 @@ __global__ void __launch_bounds__(256)
     for (int g = g0; g < g1; ++g) {
       const long long src = pool_row(p.pool, page, g, slot0);
       const long long dst = (static_cast<long long>(lo) * nkv + g) * p.P * p.S;
-      typename std::conditional<Q8, uint2, uint4>::type x[RUN][LOADS];
+      typename std::conditional<FMT == kBf16, uint4,
+                                typename std::conditional<FMT == kE4m3, uint2, uint32_t>::type>::type
+          x[RUN][LOADS];
       float sc[RUN][LOADS];
 #pragma unroll
       for (int r = 0; r < RUN; ++r)
@@ -371,7 +514,13 @@ __global__ void __launch_bounds__(256)
         for (int l = 0; l < LOADS; ++l) {
           const bool is_k = LOADS == 1 ? k_lane : l == 0;
           load_vec(x[r][l], is_k ? p.pool.k : p.pool.v, (src + r) * VECS + vec);
-          if (Q8) sc[r][l] = load_now((is_k ? p.pool.k_scales : p.pool.v_scales) + src + r);
+          const float* scales = is_k ? p.pool.k_scales : p.pool.v_scales;
+          if (FMT == kE4m3) sc[r][l] = load_now(scales + src + r);
+          if (FMT == kE2m1) {
+            const float* rec = scales + (src + r) * (record_bytes(HD) / 4);
+            const uint8_t rg = load_now(reinterpret_cast<const uint8_t*>(rec) + 4 + vec / (kGroup4 / 8));
+            sc[r][l] = load_now(rec) * f16x2_to_f32x2(e4m3x2_to_f16x2(rg)).x;
+          }
         }
 #pragma unroll
       for (int r = 0; r < RUN; ++r)

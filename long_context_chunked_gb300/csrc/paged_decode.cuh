@@ -92,6 +92,7 @@ constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7 / 
 constexpr float kMinW = 7.888609052210118e-31f;  // 2^-100: kPScale / W stays finite
 constexpr float kMaxW = 8.507059173023462e+37f;  // 2^126, far above the largest scale of 2^119
 constexpr float kPMax = 57344.f;                 // Q8: W is raised where a P would pass this
+constexpr float kPMax4 = 32768.f;                // Q4: the same (r_g / 256 is 1.75 at most)
 constexpr float kAboveOne = 1.00000023841857910f;  // 1 + 2^-22 (bf16: P's lo)
 constexpr int kDecMaxHeads = 16;                 // of a row
 constexpr int kDecStages = 8;                    // tiles whose absent pages a worker remembers
@@ -104,21 +105,28 @@ constexpr int kDecStages = 8;                    // tiles whose absent pages a w
 // 8 KB 60.7 us, 8 with three 58.0), and at HD = 256 12 workers spill besides
 // (e4m3, NB = 1, four slots of 4 KB: 1x126977 36.6 us, 33.9 by 8; 64 ragged of 8
 // heads per kv head 64.5 and 59.3).
-template <int HD, bool Q8, int NB>
+template <int HD, int FMT, int NB>
 struct DecodeLayout {
-  static constexpr int ESZ = Q8 ? 1 : 2;
+  static constexpr bool QUANT = FMT != kBf16;
+  static constexpr int RB = row_bytes(HD, FMT);
   static constexpr int NW = 8;
   static constexpr int THREADS = 32 * NW;
   static constexpr int SLOT = 8192;
   static constexpr int NSLOT = 196608 / (NW * SLOT);
-  static constexpr int WT = SLOT / (HD * ESZ);
-  static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : 6);
+  static constexpr int WT = SLOT / RB;
+  static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : (WT == 64 ? 6 : 7));
   // Beginning and ending a row costs a worker about as much as 40 KB of tiles;
   // the list counts them before the row's first tile (64 ragged sequences,
   // tiles of 16 KB: 70 us without, 62.9 with one, 59.3 with two, 58.9 with three).
   static constexpr int ROW = 40960 / (2 * SLOT);
-  static constexpr int BOXW = 128 / ESZ;         // values per 128-byte box row
-  static constexpr int NBOX = HD / BOXW;         // column blocks of a tile
+  // A slot holds lines of 128 bytes: NBOX column blocks of them, or (e2m1 of HD =
+  // 128) two tokens to a line.
+  static constexpr int BOXW = FMT == kBf16 ? 64 : 128;  // elements per line, of 2 bytes or 1
+  static constexpr int NBOX = RB > 128 ? RB / 128 : 1;
+  static constexpr int LINE_TOKENS = RB < 128 ? 128 / RB : 1;
+  // Bytes of a token's scales (K's or V's), and the lanes that copy a tile's.
+  static constexpr int REC = FMT == kE2m1 ? record_bytes(HD) : 4;
+  static constexpr int SCALE_LANES = FMT == kE2m1 ? 32 : WT / 4;
   static constexpr int MT = WT / 16;             // m-tiles of K Q^T
   static constexpr int MO = HD / 16;             // m-tiles of V^T P^T
   static constexpr int HEADS = 8 * NB;
@@ -129,7 +137,7 @@ struct DecodeLayout {
   static constexpr int Q_BYTES = HEADS * HD * 2;
   static constexpr int C_STRIDE = HD + 8;        // floats of a head's O where workers sum theirs
   static constexpr int OFF_SCALE = NW * NSLOT * SLOT;
-  static constexpr int OFF_Q = OFF_SCALE + (Q8 ? NW * NSLOT * WT * 4 : 0);
+  static constexpr int OFF_Q = OFF_SCALE + (QUANT ? NW * NSLOT * WT * REC : 0);
   static constexpr int OFF_QEXP = OFF_Q + (Q_SMEM ? Q_BYTES : 0);  // [NW][HEADS] 2^e of each Q row
   static constexpr int OFF_ENDS = OFF_QEXP + (Q_SMEM ? NW * HEADS * 4 : 0);  // [THREADS] 64-bit
   static constexpr int OFF_ML = OFF_ENDS + THREADS * 8;  // [NW][HEADS] (m, l)
@@ -157,7 +165,7 @@ struct DecodeCut {
 constexpr int kBriefRounds = 3;  // rounds of tiles that a CTA alone does for a short row
 
 struct PagedDecodeParams {
-  CUtensorMap tm_k;  // [pool rows][HD], box BOXW x 1 x min(page_size, WT)
+  CUtensorMap tm_k;  // [pool rows][HD] (e2m1: lines of 128 bytes), box BOXW x 1 x a page's or a tile's lines
   CUtensorMap tm_v;
   PagedPool pool;
   const int* lens;            // [num_seqs]; <= 0: no tokens
@@ -263,6 +271,12 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t* lo, uint32
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(*lo), "=r"(*hi)
       : "r"(x));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Shared address of 16-byte chunk `chunk` of row `row` in the column block at
@@ -458,10 +472,11 @@ __device__ __forceinline__ bool decode_slices(const PagedDecodeParams& p, int ro
 }
 
 // ------------------------------------------------------------------ kernel
-template <int HD, bool Q8, int NB>
-__global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
+template <int HD, int FMT, int NB>
+__global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
-  using Ly = DecodeLayout<HD, Q8, NB>;
+  using Ly = DecodeLayout<HD, FMT, NB>;
+  constexpr bool Q8 = FMT == kE4m3, Q4 = FMT == kE2m1, QUANT = Ly::QUANT;
   constexpr int WT = Ly::WT, ROW = Ly::ROW, MT = Ly::MT, MO = Ly::MO, NSLOT = Ly::NSLOT, NW = Ly::NW;
   constexpr int HEADS = Ly::HEADS;
   // Where Q is in shared memory, K Q^T can be a loop that holds the code of KU
@@ -469,8 +484,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   // instruction cache feeds without pauses (1x128k: 38.7 us unrolled, 37.4 by
   // twos, 38.6 by ones with the loop over V's halves rolled up too); with bf16
   // it is not (8x32k: 96.5 us unrolled, 99 by twos).
-  constexpr bool ROLL = Ly::Q_SMEM && Q8;
-  constexpr int KU = ROLL ? 2 : HD / 16;
+  constexpr bool ROLL = Ly::Q_SMEM && QUANT;
+  constexpr int KU = ROLL ? (Q4 ? 1 : 2) : HD / 16;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5;  // wk: worker of the CTA
@@ -490,7 +505,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       reinterpret_cast<volatile int*>(smem + Ly::OFF_MISC + NW * 16 + Ly::THREADS / 4);
   if (lane == 0) {
     for (int s = 0; s < NSLOT; ++s) {
-      mbar_init(full0 + 8 * s, Q8 ? 1 + WT / 4 : 1);  // (Q8: the copies of the scales arrive too)
+      mbar_init(full0 + 8 * s, QUANT ? 1 + Ly::SCALE_LANES : 1);  // (the copies of the scales arrive too)
     }
     if (wk == 0) *abort_flag = 0;
     fence_mbar_init();
@@ -578,7 +593,11 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   int raw_t = -1, raw_id = 0, raw_g = 0;
   bool raw_any = false, next_any = false;
   int next_row = 0, cur_row = 0;      // lane i: pool row of box i
-  int next_scale = 0, cur_scale = 0;  // Q8: lane i: pool row of tokens 4 i .., or -1
+  // Of the scales: Q8: lane i: pool row of tokens 4 i .., or -1; Q4: the 16-byte
+  // pieces i and i + 32 of the tile's records, counted in the pool, or -1.
+  int next_scale = 0, cur_scale = 0, next_scale2 = -1, cur_scale2 = -1;
+  constexpr int PIECES = WT * Ly::REC / 16;
+  const int piece_shift = box_shift - 4;  // (a box of 16 tokens has REC pieces)
   int resolved = 0, issued = 0, slot_out = 0;
   auto load_raw = [&]() {
     raw_any = ahead.tiles > 0;
@@ -615,20 +634,31 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       const int row = __shfl_sync(0xFFFFFFFFu, next_row, (tok & (WT - 1)) >> box_shift);
       next_scale = tok < WT && row < p.pool_rows ? row + (tok & (box - 1)) : -1;
     }
+    if (Q4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int piece = lane + 32 * i, of = (piece >> piece_shift) / Ly::REC;
+        const int row = __shfl_sync(0xFFFFFFFFu, next_row, of & 31);
+        const int at = row / 16 * Ly::REC + piece - ((of * Ly::REC) << piece_shift);
+        (i == 0 ? next_scale : next_scale2) = piece < PIECES && row < p.pool_rows ? at : -1;
+      }
+    }
   };
-  auto send = [&](const CUtensorMap* m, const float* scales, int row, int scale_row) {
+  auto send = [&](const CUtensorMap* m, const float* scales, int row, int scale_row, int scale_row2) {
     const uint32_t bar = full0 + 8 * slot_out, dst = ring + slot_out * Ly::SLOT;
     if (lane == 0) {
       count_arrive(p.bar_counts, 1u, wk, 1);
       mbar_arrive_expect_tx(bar, Ly::SLOT);
 #pragma unroll
-      for (int c = 0; c < Ly::NBOX; ++c) tma_load_3d(dst + c * (WT * 128), m, bar, c * Ly::BOXW, 0, row);
+      for (int c = 0; c < Ly::NBOX; ++c)
+        tma_load_3d(dst + c * (WT * 128), m, bar, c * Ly::BOXW, 0, row / Ly::LINE_TOKENS);
     }
     if (boxes > 1) {
       if (lane > 0 && lane < boxes) {
 #pragma unroll
         for (int c = 0; c < Ly::NBOX; ++c)
-          tma_load_3d(dst + c * (WT * 128) + (lane << box_shift) * 128, m, bar, c * Ly::BOXW, 0, row);
+          tma_load_3d(dst + c * (WT * 128) + (lane << box_shift) * (128 / Ly::LINE_TOKENS), m, bar,
+                      c * Ly::BOXW, 0, row / Ly::LINE_TOKENS);
       }
     }
     if (Q8 && lane < WT / 4) {  // four tokens' scales (a page holds 16 or more)
@@ -637,12 +667,20 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
                      scales + scale_row);
       copies_arrive(bar);
     }
+    if (Q4) {
+      const uint32_t to = sbase + Ly::OFF_SCALE + (wk * NSLOT + slot_out) * (WT * Ly::REC) + 16 * lane;
+      const uint8_t* from = reinterpret_cast<const uint8_t*>(scales);
+      if (scale_row >= 0) copy16_async(to, from + 16LL * scale_row);
+      if (scale_row2 >= 0) copy16_async(to + 512, from + 16LL * scale_row2);
+      copies_arrive(bar);
+    }
     if (++slot_out == nslot) slot_out = 0;
     ++issued;
   };
   auto advance = [&]() {
     cur_row = next_row;
     cur_scale = next_scale;
+    cur_scale2 = next_scale2;
     resolve();
     load_raw();
   };
@@ -650,9 +688,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
   // every slot read.
   auto issue = [&]() {
     if (issued & 1) {
-      send(&p.tm_v, p.pool.v_scales, cur_row, cur_scale);
+      send(&p.tm_v, p.pool.v_scales, cur_row, cur_scale, cur_scale2);
     } else if (next_any) {
-      send(&p.tm_k, p.pool.k_scales, next_row, next_scale);
+      send(&p.tm_k, p.pool.k_scales, next_row, next_scale, next_scale2);
       advance();
     }
   };
@@ -746,7 +784,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
     // B fragments of Q^T, 16 dims a step.  bf16: as it is, dims 16 ks + 2 quad +
     // {0, 1} and + 8 of head r0 of each block.  Q8: fp16, scaled by a power of
     // two, dims 16 ks + 4 quad + {0 .. 3}, the order in which the e4m3 K
-    // fragments come out of ldmatrix.
+    // fragments come out of ldmatrix.  Q4: the same with dims 32 c + 8 quad +
+    // {0 .. 3} (ks = 2 c) and {4 .. 7} (ks = 2 c + 1).
     // For the largest magnitude `big` of a head (bf16 bits): e, the exponent of
     // the head's largest value (zeros and subnormals: -126), down = 2^-e, and
     // 2^e, which gives it back to the logits; 2^-127, 2^-128 and 2^128 are made
@@ -773,7 +812,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
           w[i] = r < heads ? load_now(src + 32 * i + lane) : make_uint2(0u, 0u);
           big = __vmaxu2(big, __vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu));
         }
-        if constexpr (Q8) {
+        if constexpr (QUANT) {
           big = __reduce_max_sync(0xFFFFFFFFu, max(big & 0xFFFFu, big >> 16));
           float down, up;
           scaling(big, &down, &up);
@@ -789,13 +828,15 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < HD / 128; ++i) {
           // Dims 4 k .. 4 k + 3, k = 32 i + lane: 8 bytes.  Q8: dims 4 a + 2 c of
-          // a 16-block go to position 2 a + 8 c.
+          // a 16-block go to position 2 a + 8 c.  Q4: dims 8 a + 2 c of a 32-block
+          // to position 2 a + 8 c.
           const int k = 32 * i + lane;
-          const int c0 = Q8 ? 2 * (k >> 2) : k >> 1;
+          const int c0 = Q8 ? 2 * (k >> 2) : (Q4 ? 4 * (k >> 3) + 2 * (k & 1) : k >> 1);
+          const int a4 = Q4 ? (k >> 1) & 3 : k & 3;
           uint8_t* row = smem + q_at + r * (2 * HD);
-          if constexpr (Q8) {
-            *reinterpret_cast<uint32_t*>(row + ((c0 ^ (r & 7)) << 4) + (k & 3) * 4) = w[i].x;
-            *reinterpret_cast<uint32_t*>(row + (((c0 + 1) ^ (r & 7)) << 4) + (k & 3) * 4) = w[i].y;
+          if constexpr (QUANT) {
+            *reinterpret_cast<uint32_t*>(row + ((c0 ^ (r & 7)) << 4) + a4 * 4) = w[i].x;
+            *reinterpret_cast<uint32_t*>(row + (((c0 + 1) ^ (r & 7)) << 4) + a4 * 4) = w[i].y;
           } else {
             *reinterpret_cast<uint2*>(row + ((c0 ^ (r & 7)) << 4) + (k & 1) * 8) = w[i];
           }
@@ -806,7 +847,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       else
         __syncwarp();
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) qexp[nb] = Q8 ? exps[8 * nb + r0] : 1.f;
+      for (int nb = 0; nb < NB; ++nb) qexp[nb] = QUANT ? exps[8 * nb + r0] : 1.f;
     } else {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -819,6 +860,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
           uint2 w;
           if constexpr (Q8) {
             w = load_now(reinterpret_cast<const uint2*>(src) + 4 * ks + quad);
+          } else if constexpr (Q4) {
+            w = load_now(reinterpret_cast<const uint2*>(src) + 8 * (ks >> 1) + 2 * quad + (ks & 1));
           } else {
             w.x = load_now(src + 8 * ks + quad);
             w.y = load_now(src + 8 * ks + 4 + quad);
@@ -826,10 +869,10 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
           if (!here) w = make_uint2(0u, 0u);
           q[ks][2 * nb] = w.x;
           q[ks][2 * nb + 1] = w.y;
-          if (Q8) big = __vmaxu2(big, __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu));
+          if (QUANT) big = __vmaxu2(big, __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu));
         }
         qexp[nb] = 1.f;
-        if constexpr (Q8) {
+        if constexpr (QUANT) {
           big = max(big & 0xFFFFu, big >> 16);
           big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
           big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
@@ -867,7 +910,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         m[nb][j] = -INFINITY;
         l[nb][j] = 0.f;
       }
-    float ps[NB][2];  // Q8: 2^7 / W
+    float ps[NB][2];  // QUANT: 2^7 / W
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) ps[nb][0] = ps[nb][1] = kPScale / kMinW;
     float o[MO][NB][4];
@@ -887,7 +930,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       const bool partial = valid < WT || bad != 0u;
       const uint32_t kb = ring + slot * Ly::SLOT;
       float c[MT][NB][4];
-      if constexpr (ROLL) {
+      if constexpr (ROLL || Q4) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -895,8 +938,50 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) c[t][nb][j] = 0.f;
       }
-      const uint32_t k_at = sw128(kb, (oct & 1) * 8 + r8, oct >> 1);  // (chunks are XORed in)
-      if constexpr (Q8) {
+      // (Chunks are XORed in.)
+      const uint32_t k_at = Ly::LINE_TOKENS == 2
+                                ? sw128(kb, (oct & 1) * 4 + (r8 >> 1), (r8 & 1) * 4 + (oct >> 1))
+                                : sw128(kb, (oct & 1) * 8 + r8, oct >> 1);
+      // This slot's scales.
+      const uint8_t* k_rec = smem + Ly::OFF_SCALE + (wk * NSLOT + slot) * (WT * Ly::REC);
+      if constexpr (Q4) {
+#pragma unroll KU
+        for (int ch = 0; ch < HD / 32; ch += 2) {  // 64 dims: chunks ch and ch + 1, a group each
+          uint32_t qf[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q_frag(2 * ch + i, qf[i]);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            uint32_t kr[4];  // token half, then chunk, by lane octet
+            ldsm4(kr, (k_at ^ (ch << 4)) + t * (2048 / Ly::LINE_TOKENS));
+            // r_g of the two chunks, tokens r0 and r0 + 8
+            const uint8_t* rec = k_rec + (16 * t + r0) * Ly::REC + 4 + ch;
+            const uint32_t g0 = *reinterpret_cast<const uint16_t*>(rec);
+            const uint32_t g8 = *reinterpret_cast<const uint16_t*>(rec + 8 * Ly::REC);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t lo[4], hi[4];
+              e2m1x8_to_f16x8(kr[2 * j], lo);
+              e2m1x8_to_f16x8(kr[2 * j + 1], hi);
+              // An e4m3 byte without its sign, in fp32's place: 2^-120 times its value.
+              const float f0 = __uint_as_float((j == 0 ? g0 << 20 : g0 << 12) & 0x07F00000u);
+              const float f8 = __uint_as_float((j == 0 ? g8 << 20 : g8 << 12) & 0x07F00000u);
+              const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
+              const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                float part[4];
+                mma16816<true, true>(part, a0, qf[2 * j][2 * nb], qf[2 * j][2 * nb + 1]);
+                mma16816<true>(part, a1, qf[2 * j + 1][2 * nb], qf[2 * j + 1][2 * nb + 1]);
+                c[t][nb][0] = fmaf(part[0], f0, c[t][nb][0]);
+                c[t][nb][1] = fmaf(part[1], f0, c[t][nb][1]);
+                c[t][nb][2] = fmaf(part[2], f8, c[t][nb][2]);
+                c[t][nb][3] = fmaf(part[3], f8, c[t][nb][3]);
+              }
+            }
+          }
+        }
+      } else if constexpr (Q8) {
 #pragma unroll KU
         for (int ks = 0; ks < HD / 16; ks += 2) {  // 32 dims: chunks ks and ks + 1
           uint32_t qa[4], qb[4];
@@ -942,18 +1027,17 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       }
       // c becomes <q, k> times the token's scale; what is no token is -infinity,
       // by value.  The logits (log2 units) are c sl, taken with m below.
-      const float* ksc = reinterpret_cast<const float*>(
-          smem + Ly::OFF_SCALE + (wk * NSLOT + slot) * (WT * 4));
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float ks = Q8 ? ksc[16 * t + 8 * i + r0] : 1.f;
+          const float ks =
+              QUANT ? *reinterpret_cast<const float*>(k_rec + (16 * t + 8 * i + r0) * Ly::REC) : 1.f;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              if (Q8) c[t][nb][2 * i + j] *= ks;
+              if (QUANT) c[t][nb][2 * i + j] = (Q4 ? c[t][nb][2 * i + j] * 0x1p120f : c[t][nb][2 * i + j]) * ks;
         }
       bool seen[MT][2];
       if (partial) {
@@ -986,14 +1070,13 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       if (!await()) break;
       const uint32_t vb = ring + slot * Ly::SLOT;
       float vs[MT][2];
-      if constexpr (Q8) {
-        const float* vsc = reinterpret_cast<const float*>(
-            smem + Ly::OFF_SCALE + (wk * NSLOT + slot) * (WT * 4));
+      const uint8_t* v_rec = smem + Ly::OFF_SCALE + (wk * NSLOT + slot) * (WT * Ly::REC);
+      if constexpr (QUANT) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            vs[t][i] = vsc[16 * t + 8 * i + r0];
+            vs[t][i] = *reinterpret_cast<const float*>(v_rec + (16 * t + 8 * i + r0) * Ly::REC);
             if (partial && !seen[t][i]) vs[t][i] = 0.f;
           }
       }
@@ -1019,7 +1102,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
             if (m[nb][j] != mn) a[nb][j] = ex2_approx(m[nb][j] - mn);
             m[nb][j] = mn;
             l[nb][j] *= a[nb][j];
-            if constexpr (!Q8) {
+            if constexpr (!QUANT) {
 #pragma unroll
               for (int i = 0; i < MO; ++i) {
                 o[i][nb][j] *= a[nb][j];
@@ -1029,8 +1112,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
           }
       }
 
-      // ---- p (Q8: times the V row's scale), and l
-      float wx[NB][2];  // Q8: the lane's largest product
+      // ---- p (QUANT: times the V row's scale), and l
+      float wx[NB][2];  // QUANT: the lane's largest product
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         wx[nb][0] = wx[nb][1] = 0.f;
@@ -1046,7 +1129,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
             e1 = ex2_approx(fmaf(e1, sl[nb][1], -m1));
             l[nb][0] += e0;
             l[nb][1] += e1;
-            if constexpr (Q8) {
+            if constexpr (QUANT) {
               e0 *= vs[t][i];
               e1 *= vs[t][i];
               wx[nb][0] = fmaxf(wx[nb][0], fabsf(e0));
@@ -1054,11 +1137,11 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
             }
           }
       }
-      if constexpr (Q8) {
+      if constexpr (QUANT) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) raise |= wx[nb][j] * ps[nb][j] > kPMax;
+          for (int j = 0; j < 2; ++j) raise |= wx[nb][j] * ps[nb][j] > (Q4 ? kPMax4 : kPMax);
         if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
@@ -1082,7 +1165,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       }
 
       // ---- P, transposed into the B operand of V^T P^T (16 tokens per step)
-      uint32_t ph[MT][NB][2], pl[Q8 ? 1 : MT][NB][2];
+      uint32_t ph[MT][NB][2], pl[QUANT ? 1 : MT][NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1090,7 +1173,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float e0 = c[t][nb][2 * i], e1 = c[t][nb][2 * i + 1];
-            if constexpr (Q8) {
+            if constexpr (QUANT) {
               ph[t][nb][i] = transpose8(pack_f16x2(e0 * ps[nb][0], e1 * ps[nb][1]));
             } else {
               // hi: the upper 16 bits; lo: the rest, and 2^-22 of the whole (kAboveOne).
@@ -1103,10 +1186,10 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
           }
 
       // ---- O^T += V^T P^T
-      if (valid < WT) {
+      if (!Q4 && valid < WT) {
         // Slots behind the last token may hold anything; 0 * NaN must not
-        // reach O.
-        constexpr int CH = HD * Ly::ESZ / 16;
+        // reach O.  (e2m1 values and r_g without their sign are all finite.)
+        constexpr int CH = Ly::RB / 16;
         for (int i = lane; i < (WT - valid) * CH; i += 32) {
           const int ch = i % CH;
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
@@ -1118,7 +1201,44 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       }
 #pragma unroll
       for (int k = 0; k < MT; ++k) {
-        if constexpr (Q8) {
+        if constexpr (Q4) {
+          const uint32_t v_at = Ly::LINE_TOKENS == 2
+                                    ? sw128(vb, (oct & 1) * 4 + (r8 >> 1), (r8 & 1) * 4 + (oct >> 1))
+                                    : sw128(vb, (oct & 1) * 8 + r8, oct >> 1);
+#pragma unroll
+          for (int ch = 0; ch < HD / 32; ch += 2) {  // two 16-byte chunks: 64 columns, two groups
+            uint32_t vr[4];  // token half, then chunk, by lane octet
+            ldsm4_t(vr, (v_at ^ (ch << 4)) + k * (2048 / Ly::LINE_TOKENS));
+            // r_g of the two chunks, tokens 2 quad and + 1, + 8 and + 9
+            const uint8_t* rec = v_rec + (16 * k + 2 * quad) * Ly::REC + 4 + ch;
+            const uint32_t g0 = *reinterpret_cast<const uint16_t*>(rec);
+            const uint32_t g1 = *reinterpret_cast<const uint16_t*>(rec + Ly::REC);
+            const uint32_t g8 = *reinterpret_cast<const uint16_t*>(rec + 8 * Ly::REC);
+            const uint32_t g9 = *reinterpret_cast<const uint16_t*>(rec + 9 * Ly::REC);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              // An e4m3 byte without its sign, in fp16's place: 2^-8 times its value.
+              const uint32_t sel = j == 0 ? 0x4202 : 0x5212;
+              const uint32_t f0 = (__byte_perm(g0, g1, sel) >> 1) & 0x3F803F80u;
+              const uint32_t f8 = (__byte_perm(g8, g9, sel) >> 1) & 0x3F803F80u;
+              // A register holds two tokens x four columns; regrouped, columns 4 r0 +
+              // {0, 1} and {2, 3} are rows r0 and r0 + 8 of two m-tiles.
+              uint32_t lo[4], hi[4];
+              e2m1x8_to_f16x8(vr[2 * j], lo);
+              e2m1x8_to_f16x8(vr[2 * j + 1], hi);
+              const uint32_t a0[4] = {__byte_perm(lo[0], lo[2], 0x5410), __byte_perm(lo[0], lo[2], 0x7632),
+                                      __byte_perm(hi[0], hi[2], 0x5410), __byte_perm(hi[0], hi[2], 0x7632)};
+              const uint32_t a1[4] = {__byte_perm(lo[1], lo[3], 0x5410), __byte_perm(lo[1], lo[3], 0x7632),
+                                      __byte_perm(hi[1], hi[3], 0x5410), __byte_perm(hi[1], hi[3], 0x7632)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                const uint32_t b0 = mul_f16x2(ph[k][nb][0], f0), b1 = mul_f16x2(ph[k][nb][1], f8);
+                mma16816<true>(o[2 * (ch + j)][nb], a0, b0, b1);
+                mma16816<true>(o[2 * (ch + j) + 1][nb], a1, b0, b1);
+              }
+            }
+          }
+        } else if constexpr (Q8) {
 #pragma unroll
           for (int ch = 0; ch < MO; ch += 2) {  // two 16-byte chunks: 32 columns
             uint32_t vr[4];  // token half, then chunk, by lane octet
@@ -1152,7 +1272,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
         }
       }
       // Cleared slots: these writes come before the copy that reuses the slot.
-      if (valid < WT) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      if (!Q4 && valid < WT) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       release();
     }
 
@@ -1201,11 +1321,15 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
       else if (d.n_head > 0)
         p.ws_cut[worker] = d;  // (at most one row that begins here is cut: the last)
     }
+    // QUANT: the column of row r0 of m-tile i; row r0 + 8 is the next one.
+    auto out_column = [&](int i) {
+      return Q4 ? 32 * (i >> 1) + 4 * r0 + 2 * (i & 1) : 16 * i + 2 * r0;
+    };
     float oscale[NB][2];  // of the O in registers
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) oscale[nb][j] = Q8 ? pow2_inverse(ps[nb][j]) : 1.f;
+      for (int j = 0; j < 2; ++j) oscale[nb][j] = QUANT ? (Q4 ? 256.f : 1.f) * pow2_inverse(ps[nb][j]) : 1.f;
     if (uniform) {
       // One piece for the CTA: the workers' m and l, then their O, summed in
       // worker order.  (The only row of every warp here.)
@@ -1248,8 +1372,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
           float* dst = reinterpret_cast<float*>(smem + wk * RING) + r * Ly::C_STRIDE;
 #pragma unroll
           for (int i = 0; i < MO; ++i) {
-            if constexpr (Q8) {  // rows r0, r0 + 8 of the m-tile: columns 2 r0 and 2 r0 + 1
-              *reinterpret_cast<float2*>(dst + 16 * i + 2 * r0) =
+            if constexpr (QUANT) {  // rows r0, r0 + 8 of the m-tile: neighbouring columns
+              *reinterpret_cast<float2*>(dst + out_column(i)) =
                   make_float2(o[i][nb][j] * f, o[i][nb][2 + j] * f);
             } else {
               dst[16 * i + r0] = o[i][nb][j] * f;
@@ -1301,8 +1425,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, Q8, NB>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < MO; ++i) {
             float2 y = make_float2(o[i][nb][j] * f, o[i][nb][2 + j] * f);
-            int d = 16 * i + 2 * r0;
-            if constexpr (!Q8) {
+            int d = out_column(i);
+            if constexpr (!QUANT) {
               // Rows r0 and r0 + 8 are columns r0 and r0 + 8: a neighbour's
               // value makes a pair.
               const bool odd = (r0 & 1) != 0;

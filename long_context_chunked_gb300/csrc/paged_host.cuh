@@ -11,7 +11,8 @@ cpattn_status check_pages(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t nu
   if (num_seqs > CPATTN_MAX_PAGED_SEQS)
     return fail(ctx, CPATTN_E_UNSUPPORTED, "num_seqs exceeds CPATTN_MAX_PAGED_SEQS");
   if (pages == nullptr) return fail(ctx, CPATTN_E_INVALID, "pages must not be NULL");
-  if (pages->format != CPATTN_PAGES_BF16 && pages->format != CPATTN_PAGES_E4M3)
+  if (pages->format != CPATTN_PAGES_BF16 && pages->format != CPATTN_PAGES_E4M3 &&
+      pages->format != CPATTN_PAGES_E2M1)
     return fail(ctx, CPATTN_E_INVALID, "pages: unknown format");
   int shift = 4;
   while (shift < 8 && (1 << shift) != pages->page_size) ++shift;
@@ -27,10 +28,10 @@ cpattn_status check_pages(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t nu
     return fail(ctx, CPATTN_E_INVALID, "pages: pointers must not be NULL");
   if (!aligned16(pages->k_pages) || !aligned16(pages->v_pages) || !aligned4(pages->block_table))
     return fail(ctx, CPATTN_E_INVALID, "pages: pools 16-byte, table 4-byte aligned");
-  if (pages->format == CPATTN_PAGES_E4M3 &&
+  if (pages->format != CPATTN_PAGES_BF16 &&
       (pages->k_scales == nullptr || pages->v_scales == nullptr || !aligned16(pages->k_scales) ||
        !aligned16(pages->v_scales)))
-    return fail(ctx, CPATTN_E_INVALID, "pages: e4m3 needs 16-byte aligned scales");
+    return fail(ctx, CPATTN_E_INVALID, "pages: e4m3 and e2m1 need 16-byte aligned scales");
   out->k = pages->k_pages;
   out->v = pages->v_pages;
   out->k_scales = pages->k_scales;
@@ -81,13 +82,18 @@ cpattn_status launch_dependent(cpattn_ctx* ctx, void (*kernel)(Params), dim3 gri
   return after_launch(ctx, st, what);
 }
 
+// The instance of a kernel for a page format.
+#define CPATTN_BY_FORMAT(kernel, format, ...)                                            \
+  ((format) == CPATTN_PAGES_BF16   ? kernel<__VA_ARGS__, cpattn::kBf16> \
+   : (format) == CPATTN_PAGES_E4M3 ? kernel<__VA_ARGS__, cpattn::kE4m3> \
+                                   : kernel<__VA_ARGS__, cpattn::kE2m1>)
+
 template <int ROWS>
-cpattn_status launch_paged_write(cpattn_ctx* ctx, const cpattn::PagedWriteParams& p, bool q8, int grid,
-                                 cudaStream_t st) {
-  const auto kernel = ctx->cfg.head_dim == 128 ? (q8 ? cpattn::paged_write_kernel<128, true, ROWS>
-                                                     : cpattn::paged_write_kernel<128, false, ROWS>)
-                                               : (q8 ? cpattn::paged_write_kernel<256, true, ROWS>
-                                                     : cpattn::paged_write_kernel<256, false, ROWS>);
+cpattn_status launch_paged_write(cpattn_ctx* ctx, const cpattn::PagedWriteParams& p, int format,
+                                 int grid, cudaStream_t st) {
+  const auto kernel = ctx->cfg.head_dim == 128
+                          ? CPATTN_BY_FORMAT(cpattn::paged_write_kernel, format, 128, ROWS)
+                          : CPATTN_BY_FORMAT(cpattn::paged_write_kernel, format, 256, ROWS);
   return launch_dependent(ctx, kernel, dim3(grid), 256, 0, st, p, "paged write launch");
 }
 
@@ -113,14 +119,14 @@ DecodeWorkspace decode_workspace(const cpattn_ctx* ctx) {
   return w;
 }
 
-template <int HD, bool Q8, int NB>
+template <int HD, int NB, int FMT>
 cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
                             cpattn::PagedDecodeParams* p, cudaStream_t st) {
-  using Ly = cpattn::DecodeLayout<HD, Q8, NB>;
+  using Ly = cpattn::DecodeLayout<HD, FMT, NB>;
   static_assert(Ly::NW <= 8 && Ly::HEADS <= 16, "decode_workspace");
-  bool& ready = ctx->decode_ready[HD == 256][Q8];
+  bool& ready = ctx->decode_ready[HD == 256][NB - 1][FMT == cpattn::kBf16 ? 0 : (FMT == cpattn::kE4m3 ? 1 : 2)];
   if (!ready) {
-    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, Q8, NB>,
+    cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, FMT, NB>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Ly::SMEM_BYTES);
     // The join asks for the decode kernel's division of the SM's memory, so
@@ -132,13 +138,16 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
     if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaFuncSetAttribute(paged decode)");
     ready = true;
   }
-  const uint64_t rb = static_cast<uint64_t>(HD) * Ly::ESZ;
-  const uint32_t box_rows = static_cast<uint32_t>(std::min(pages->page_size, Ly::WT));
+  // Rows of the pool, or lines of two of them (DecodeLayout::LINE_TOKENS).
+  const uint64_t rb = static_cast<uint64_t>(Ly::RB) * Ly::LINE_TOKENS;
+  const uint64_t width = FMT == cpattn::kE2m1 ? rb : HD;
+  const uint32_t box_rows =
+      static_cast<uint32_t>(std::min(pages->page_size, Ly::WT) / Ly::LINE_TOKENS);
   const CUtensorMapDataType type =
-      Q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const uint64_t rows = static_cast<uint64_t>(p->pool_rows);
-  if (!encode3d(&p->tm_k, pages->k_pages, HD, 1, rows, rb, rb, Ly::BOXW, 1, box_rows, type) ||
-      !encode3d(&p->tm_v, pages->v_pages, HD, 1, rows, rb, rb, Ly::BOXW, 1, box_rows, type))
+      Ly::QUANT ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t rows = static_cast<uint64_t>(p->pool_rows) / Ly::LINE_TOKENS;
+  if (!encode3d(&p->tm_k, pages->k_pages, width, 1, rows, rb, rb, Ly::BOXW, 1, box_rows, type) ||
+      !encode3d(&p->tm_v, pages->v_pages, width, 1, rows, rb, rb, Ly::BOXW, 1, box_rows, type))
     return fail(ctx, CPATTN_E_CUDA, "cuTensorMapEncodeTiled failed");
   // The lengths are known on the device only: the grid is sized for the most
   // tiles they can ask for, and a CTA without a tile leaves at once.
@@ -155,7 +164,7 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
       return fail(ctx, CPATTN_E_INVALID, "barrier-count records smaller than the launch");
     p->bar_counts = ctx->bar_counts;
   }
-  cpattn_status s = launch_dependent(ctx, cpattn::paged_decode_kernel<HD, Q8, NB>, dim3(p->num_ctas),
+  cpattn_status s = launch_dependent(ctx, cpattn::paged_decode_kernel<HD, FMT, NB>, dim3(p->num_ctas),
                                      Ly::THREADS, Ly::SMEM_BYTES, st, *p, "paged decode launch");
   // Rows of one tile are never cut, nor are few short ones (decode_slices).
   if (s != CPATTN_OK || tiles == 1 || (p->by_row && tiles <= cpattn::kBriefRounds * Ly::NW)) return s;
@@ -204,9 +213,8 @@ cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, 
   p.heads_per_item = heads_per_item(ctx, units);
   const int grid = copy_grid(ctx, units, p.heads_per_item);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool q8 = pages->format == CPATTN_PAGES_E4M3;
-  return per == 4 ? launch_paged_write<4>(ctx, p, q8, grid, st)
-                  : launch_paged_write<1>(ctx, p, q8, grid, st);
+  return per == 4 ? launch_paged_write<4>(ctx, p, pages->format, grid, st)
+                  : launch_paged_write<1>(ctx, p, pages->format, grid, st);
 } catch (...) {
   return CPATTN_E_NOMEM;
 }
@@ -244,11 +252,8 @@ cpattn_status cpattn_paged_read_kv(cpattn_ctx* ctx, const cpattn_pages* pages, i
   const int grid = copy_grid(ctx, runs, p.heads_per_item);
   const size_t smem = (static_cast<size_t>(num_seqs) + 1) * sizeof(int);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool q8 = pages->format == CPATTN_PAGES_E4M3;
-  const auto kernel = c.head_dim == 128 ? (q8 ? cpattn::paged_read_kernel<128, true>
-                                              : cpattn::paged_read_kernel<128, false>)
-                                        : (q8 ? cpattn::paged_read_kernel<256, true>
-                                              : cpattn::paged_read_kernel<256, false>);
+  const auto kernel = c.head_dim == 128 ? CPATTN_BY_FORMAT(cpattn::paged_read_kernel, pages->format, 128)
+                                        : CPATTN_BY_FORMAT(cpattn::paged_read_kernel, pages->format, 256);
   return launch_dependent(ctx, kernel, dim3(grid), 256, smem, st, p, "paged read launch");
 } catch (...) {
   return CPATTN_E_NOMEM;
@@ -300,19 +305,13 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
   p.hblocks = one ? 1 : (p.group + 15) / 16;
   p.scale_log2 = c.softmax_scale * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool q8 = pages->format == CPATTN_PAGES_E4M3;
-  if (c.head_dim == 128) {
-    if (one)
-      return q8 ? launch_decode<128, true, 1>(ctx, pages, &p, st)
-                : launch_decode<128, false, 1>(ctx, pages, &p, st);
-    return q8 ? launch_decode<128, true, 2>(ctx, pages, &p, st)
-              : launch_decode<128, false, 2>(ctx, pages, &p, st);
-  }
-  if (one)
-    return q8 ? launch_decode<256, true, 1>(ctx, pages, &p, st)
-              : launch_decode<256, false, 1>(ctx, pages, &p, st);
-  return q8 ? launch_decode<256, true, 2>(ctx, pages, &p, st)
-            : launch_decode<256, false, 2>(ctx, pages, &p, st);
+  const auto launch =
+      c.head_dim == 128
+          ? (one ? CPATTN_BY_FORMAT(launch_decode, pages->format, 128, 1)
+                 : CPATTN_BY_FORMAT(launch_decode, pages->format, 128, 2))
+          : (one ? CPATTN_BY_FORMAT(launch_decode, pages->format, 256, 1)
+                 : CPATTN_BY_FORMAT(launch_decode, pages->format, 256, 2));
+  return launch(ctx, pages, &p, st);
 } catch (...) {
   return CPATTN_E_NOMEM;
 }
