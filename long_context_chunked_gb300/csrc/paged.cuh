@@ -140,15 +140,37 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// A row of HD values in HD / 8 neighbouring lanes, eight each, as fp32: what the
-// page stores for it.  mag: the bits of the lane's largest magnitude.  Rows
-// that hold an infinity or a NaN have a NaN scale and read back as NaN.
-struct Row8 {
-  uint2 x8;  // the lane's values
-  float s;   // the row's scale
+// A row of HD values in HD / 8 neighbouring lanes, eight each: what the page
+// stores for it.  In two steps, so that several rows' arithmetic can be in
+// flight before the first of them is stored.  mag: the bits of the lane's largest
+// magnitude.  Rows that hold an infinity or a NaN have a NaN scale and read back
+// as NaN.  All lanes of the warp call `quantise`.
+template <int FMT>
+struct PackedRow;
+template <>
+struct PackedRow<kBf16> {
+  uint4 x;
 };
+template <>
+struct PackedRow<kE4m3> {
+  uint2 x;
+  float s;
+};
+template <>
+struct PackedRow<kE2m1> {
+  uint32_t x;  // the first value in the lowest bits
+  float s;
+  uint32_t r;  // the r_g of four groups, from this lane's on
+};
+
 template <int HD>
-__device__ __forceinline__ Row8 quantise_e4m3(const float (&x)[8], uint32_t mag) {
+__device__ __forceinline__ void quantise(const float (&x)[8], uint32_t, bool, PackedRow<kBf16>& y) {
+  y.x = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                   pack_bf16x2(x[6], x[7]));
+}
+
+template <int HD>
+__device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, bool, PackedRow<kE4m3>& y) {
 #pragma unroll
   for (int o = HD / 16; o > 0; o >>= 1) mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, o));
   const float amax = mag >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
@@ -157,66 +179,70 @@ __device__ __forceinline__ Row8 quantise_e4m3(const float (&x)[8], uint32_t mag)
   uint32_t h[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) h[j] = pack_e4m3x2(x[2 * j] * inv, x[2 * j + 1] * inv);
-  return {make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16)), amax / kE4m3Max};
+  y.x = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  y.s = amax / kE4m3Max;
 }
 
-struct Row4 {
-  uint32_t x4;  // the lane's values, the first in the lowest bits
-  float s;      // the row's scale
-  uint32_t r;   // e4m3 scale of the lane's group (four lanes)
-};
+// e2m1.  The quotient (x / s) / r_g is made as x times (1 / s) (1 / r_g), which is
+// within 2^-22 of it.  For a bf16 x that decides every code but a tie's, which
+// another quotient misses by 2^-9 at least: so the quotient is rounded to a
+// multiple of 2^-14 first (`exact`: by adding 768, whose last place that is, and
+// taking it away), which leaves ties ties and the others on their side.
 template <int HD>
-__device__ __forceinline__ Row4 quantise_e2m1(const float (&x)[8], uint32_t mag) {
+__device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, bool exact, PackedRow<kE2m1>& y) {
   mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
   mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
   uint32_t row = mag;
 #pragma unroll
   for (int o = HD / 16; o >= 4; o >>= 1) row = max(row, __shfl_xor_sync(0xFFFFFFFFu, row, o));
-  if (row >= 0x7F800000u) return {0u, __uint_as_float(0x7FC00000u), 0u};
-  const uint32_t e = max(row >> 23, 10u);                     // exponent field of amax
-  const float inv_s = __uint_as_float((263u - e) << 23);      // 2^(9 - k), k = e - 127
-  const uint32_t r = pack_e4m3x2(__uint_as_float(mag) * inv_s / 6.f, 0.f) & 0xFFu;
-  Row4 out = {0u, __uint_as_float((e - 9u) << 23), r};
-  if (r != 0u) {
-    const float rf = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(r))).x;
+  const bool fine = row < 0x7F800000u;
+  const uint32_t e = fine ? max(row >> 23, 10u) : 10u;      // exponent field of amax
+  const float inv_s = __uint_as_float((263u - e) << 23);    // 2^(9 - k), k = e - 127
+  uint32_t r = pack_e4m3x2(__uint_as_float(mag) * inv_s / 6.f, 0.f) & 0xFFu;
+  if (!fine) r = 0u;
+  const float rf = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(r))).x;
+  // (0 for r_g = 0: the codes are 0 then.)
+  const float f = r != 0u ? __fdividef(1.f, rf) : 0.f;
+  y.x = 0u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      out.x4 |= pack_e2m1x2(x[2 * j] * inv_s / rf, x[2 * j + 1] * inv_s / rf) << (8 * j);
+  for (int j = 0; j < 4; ++j) {
+    float q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float v = x[2 * j + i] * inv_s;
+      q[i] = v * f;
+      if (exact) q[i] = copysignf(fmaf(fabsf(v), f, 768.f) - 768.f, v);
+    }
+    y.x |= pack_e2m1x2(q[0], q[1]) << (8 * j);
   }
-  return out;
+  if (r == 0u) y.x = 0u;
+  y.s = fine ? __uint_as_float((e - 9u) << 23) : __uint_as_float(0x7FC00000u);
+  // The record's words: four r_g each.
+  r |= __shfl_down_sync(0xFFFFFFFFu, r, 4) << 8;
+  r |= __shfl_down_sync(0xFFFFFFFFu, r, 8) << 16;
+  y.r = r;
 }
 
-// Eight values of lane `vec` of a row's HD / 8 lanes to row `dst` of the pool (and
-// their scales), if `dst` >= 0; mag: the bits of the largest magnitude among
-// them (not read for bf16).  All lanes of the warp call it.
-template <int HD, int FMT>
+// To row `dst` of the pool, lane `vec` of the row's HD / 8.
+template <int HD>
 __device__ __forceinline__ void store_row(const PagedPool& c, bool is_k, long long dst, int vec,
-                                          const float (&x)[8], uint32_t mag) {
-  constexpr int VECS = HD / 8;
-  void* pool = is_k ? c.k : c.v;
-  float* scales = is_k ? c.k_scales : c.v_scales;
-  if constexpr (FMT == kE4m3) {
-    const Row8 y = quantise_e4m3<HD>(x, mag);
-    if (dst < 0) return;
-    reinterpret_cast<uint2*>(pool)[dst * VECS + vec] = y.x8;
-    if (vec == 0) scales[dst] = y.s;
-  } else if constexpr (FMT == kE2m1) {
-    const Row4 y = quantise_e2m1<HD>(x, mag);
-    // The record's words: s from the first lane, then four r_g each.
-    uint32_t r = y.r;
-    r |= __shfl_down_sync(0xFFFFFFFFu, r, 4) << 8;
-    r |= __shfl_down_sync(0xFFFFFFFFu, r, 8) << 16;
-    if (dst < 0) return;
-    reinterpret_cast<uint32_t*>(pool)[dst * VECS + vec] = y.x4;
-    uint32_t* rec = reinterpret_cast<uint32_t*>(scales) + dst * (record_bytes(HD) / 4);
-    if (vec == 0) rec[0] = __float_as_uint(y.s);
-    if ((vec & 15) == 0) rec[1 + vec / 16] = r;
-  } else {
-    if (dst < 0) return;
-    reinterpret_cast<uint4*>(pool)[dst * VECS + vec] =
-        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                   pack_bf16x2(x[6], x[7]));
-  }
+                                          const PackedRow<kBf16>& y) {
+  reinterpret_cast<uint4*>(is_k ? c.k : c.v)[dst * (HD / 8) + vec] = y.x;
+}
+template <int HD>
+__device__ __forceinline__ void store_row(const PagedPool& c, bool is_k, long long dst, int vec,
+                                          const PackedRow<kE4m3>& y) {
+  reinterpret_cast<uint2*>(is_k ? c.k : c.v)[dst * (HD / 8) + vec] = y.x;
+  if (vec == 0) (is_k ? c.k_scales : c.v_scales)[dst] = y.s;
+}
+template <int HD>
+__device__ __forceinline__ void store_row(const PagedPool& c, bool is_k, long long dst, int vec,
+                                          const PackedRow<kE2m1>& y) {
+  reinterpret_cast<uint32_t*>(is_k ? c.k : c.v)[dst * (HD / 8) + vec] = y.x;
+  uint32_t* rec =
+      reinterpret_cast<uint32_t*>(is_k ? c.k_scales : c.v_scales) + dst * (record_bytes(HD) / 4);
+  if (vec == 0) rec[0] = __float_as_uint(y.s);
+  if ((vec & 15) == 0) rec[1 + vec / 16] = y.r;
 }
 __device__ __forceinline__ void bf16x8_to_f32x8(uint4 x, float (&f)[8]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -338,13 +364,34 @@ __global__ void __launch_bounds__(256)
           const bool is_k = LOADS == 1 ? k_lane : l == 0;
           const long long dst = pool_row(p.pool, static_cast<int>(place[r] >> 8), g,
                                          static_cast<int>(place[r] & 255));
-          if constexpr (FMT == kBf16) {
-            if (place[r] >= 0)
-              reinterpret_cast<uint4*>(is_k ? p.pool.k : p.pool.v)[dst * VECS + vec] = x[r][l];
-          } else {
+          void* pool = is_k ? p.pool.k : p.pool.v;
+          if constexpr (FMT == kE4m3) {
+            uint32_t m = amax_bits(x[r][l]);
+#pragma unroll
+            for (int o = VECS / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            // A row with an infinity or a NaN has no scale: all of it reads back as NaN.
+            float amax = __uint_as_float(m << 16);
+            amax = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : fmaxf(amax, kTinyAmax);
+            const float inv = kE4m3Max / amax;
+            const uint32_t w[4] = {x[r][l].x, x[r][l].y, x[r][l].z, x[r][l].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              h[j] = pack_e4m3x2(__uint_as_float(w[j] << 16) * inv,
+                                 __uint_as_float(w[j] & 0xFFFF0000u) * inv);
+            if (place[r] >= 0) {
+              reinterpret_cast<uint2*>(pool)[dst * VECS + vec] =
+                  make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+              if (vec == 0) (is_k ? p.pool.k_scales : p.pool.v_scales)[dst] = amax / kE4m3Max;
+            }
+          } else if constexpr (FMT == kE2m1) {
             float f[8];
             bf16x8_to_f32x8(x[r][l], f);
-            store_row<HD, FMT>(p.pool, is_k, place[r] < 0 ? -1 : dst, vec, f, amax_bits(x[r][l]) << 16);
+            PackedRow<FMT> y;
+            quantise<HD>(f, amax_bits(x[r][l]) << 16, true, y);
+            if (place[r] >= 0) store_row<HD>(p.pool, is_k, dst, vec, y);
+          } else {
+            if (place[r] >= 0) reinterpret_cast<uint4*>(pool)[dst * VECS + vec] = x[r][l];
           }
         }
       }

@@ -95,7 +95,7 @@ constexpr float kPMax = 57344.f;                 // Q8: W is raised where a P wo
 constexpr float kPMax4 = 32768.f;                // Q4: the same (r_g / 256 is 1.75 at most)
 constexpr float kAboveOne = 1.00000023841857910f;  // 1 + 2^-22 (bf16: P's lo)
 constexpr int kDecMaxHeads = 16;                 // of a row
-constexpr int kDecStages = 8;                    // tiles whose absent pages a worker remembers
+constexpr int kDecStages = 16;                   // tiles whose absent pages a worker remembers
 
 // NB: blocks of 8 q heads of a row (1: groups of up to 8 heads; 2: the rest).
 // NW workers per CTA with NSLOT slots of SLOT bytes each, 192 KB in all; WT
@@ -111,14 +111,20 @@ struct DecodeLayout {
   static constexpr int RB = row_bytes(HD, FMT);
   static constexpr int NW = 8;
   static constexpr int THREADS = 32 * NW;
-  static constexpr int SLOT = 8192;
+#ifndef X_SLOT128
+#define X_SLOT128 4096
+#endif
+#ifndef X_SLOT256
+#define X_SLOT256 4096
+#endif
+  static constexpr int SLOT = FMT == kE2m1 ? (HD == 128 ? X_SLOT128 : X_SLOT256) : 8192;
   static constexpr int NSLOT = 196608 / (NW * SLOT);
   static constexpr int WT = SLOT / RB;
   static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : (WT == 64 ? 6 : 7));
   // Beginning and ending a row costs a worker about as much as 40 KB of tiles;
   // the list counts them before the row's first tile (64 ragged sequences,
   // tiles of 16 KB: 70 us without, 62.9 with one, 59.3 with two, 58.9 with three).
-  static constexpr int ROW = 40960 / (2 * SLOT);
+  static constexpr int ROW = FMT == kE2m1 ? 20480 / (2 * SLOT) : 40960 / (2 * SLOT);
   // A slot holds lines of 128 bytes: NBOX column blocks of them, or (e2m1 of HD =
   // 128) two tokens to a line.
   static constexpr int BOXW = FMT == kBf16 ? 64 : 128;  // elements per line, of 2 bytes or 1
@@ -135,6 +141,7 @@ struct DecodeLayout {
   // third slot.
   static constexpr bool Q_SMEM = HD * NB == 512;
   static constexpr int Q_BYTES = HEADS * HD * 2;
+  static constexpr int QSLOTS = Q_SMEM ? (Q_BYTES + SLOT - 1) / SLOT : 0;  // slots that Q takes
   static constexpr int C_STRIDE = HD + 8;        // floats of a head's O where workers sum theirs
   static constexpr int OFF_SCALE = NW * NSLOT * SLOT;
   static constexpr int OFF_Q = OFF_SCALE + (QUANT ? NW * NSLOT * WT * REC : 0);
@@ -146,7 +153,7 @@ struct DecodeLayout {
   static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;  // spots, scan, abort flag
   static constexpr int SMEM_BYTES = OFF_MISC + NW * 16 + THREADS / 32 * 8 + 16;
   static_assert(HEADS * C_STRIDE * 4 <= NSLOT * SLOT, "a worker's O fits its slots");
-  static_assert(!Q_SMEM || (NSLOT == 3 && Q_BYTES <= SLOT && OFF_Q % 512 == 0),
+  static_assert(!Q_SMEM || (Q_BYTES <= QSLOTS * SLOT && OFF_Q % 512 == 0),
                 "a worker's Q fits a slot, and chunks can be XORed into a row's address");
   static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0 && OFF_Q % 16 == 0 && OFF_ENDS % 8 == 0,
                 "shared memory alignment");
@@ -567,7 +574,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
       }
     }
   }
-  const int nslot = Ly::Q_SMEM && !uniform ? NSLOT - 1 : NSLOT;  // (see Q_SMEM)
+  const int nslot = uniform ? NSLOT : NSLOT - Ly::QSLOTS;  // (see Q_SMEM)
   const uint32_t ring = sbase + wk * (nslot * Ly::SLOT);
   if (uniform) {
     at.s = at.s1 = at.units = 0;  // (one segment)
@@ -799,7 +806,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
     uint32_t q[Ly::Q_SMEM ? 1 : HD / 16][2 * NB];
     float qexp[NB];
     // Q_SMEM: rows of HD 16-bit values, 16-byte chunks swizzled by the row.
-    const uint32_t q_at = uniform ? Ly::OFF_Q : NW * (NSLOT - 1) * Ly::SLOT + wk * Ly::Q_BYTES;
+    const uint32_t q_at = uniform ? Ly::OFF_Q : NW * (NSLOT - Ly::QSLOTS) * Ly::SLOT + wk * Ly::Q_BYTES;
     if constexpr (Ly::Q_SMEM) {
       float* exps = reinterpret_cast<float*>(smem + Ly::OFF_QEXP) + (uniform ? 0 : wk * HEADS);
       for (int r = uniform ? wk : 0; r < HEADS; r += uniform ? NW : 1) {

@@ -99,19 +99,33 @@ cpattn_status check_norm_rope(cpattn_ctx* ctx, const cpattn_norm_rope_desc* d, i
   return CPATTN_OK;
 }
 
-cpattn_status launch_norm_rope(cpattn_ctx* ctx, void (*kernel)(cpattn::NormRopeParams), bool append,
+cpattn_status launch_norm_rope(cpattn_ctx* ctx, void (*kernel)(cpattn::NormRopeParams), int format,
                                cpattn::NormRopeParams* p, cudaStream_t st, const char* what) {
   if (ctx->d_status == nullptr) return fail(ctx, CPATTN_E_CUDA, "no CUDA device");
-  // A warp takes a row, or where that leaves less than 16 warps per SM a part of it.
+  // Batches of one unit where whole ones leave less than a warp for every slot of
+  // the GPU: few rows are a matter of latency.
+  const bool append = format >= 0;
   const int per = 32 / (ctx->cfg.head_dim / 8);
-  const int units = (p->nq + per - 1) / per + (append ? 2 : 1) * ((p->nkv + per - 1) / per);
-  const long long want = 16LL * std::max(ctx->num_sms, 1);
-  p->parts = static_cast<int>(std::min<long long>(units, std::max<long long>(1, want / p->rows)));
-  const long long warps = static_cast<long long>(p->rows) * p->parts;
+  const int uq = (p->nq + per - 1) / per, uk = (p->nkv + per - 1) / per;
   constexpr int WARPS = cpattn::kNormThreads / 32;
-  const int grid = static_cast<int>(std::min<long long>((warps + WARPS - 1) / WARPS,
-                                                        8LL * std::max(ctx->num_sms, 1)));
-  return launch_dependent(ctx, kernel, dim3(grid), cpattn::kNormThreads, 0, st, *p, what);
+  const long long room = static_cast<long long>(cpattn::kNormBlocks) * std::max(ctx->num_sms, 1);
+  long long batches = 0;
+  for (int batch : {cpattn::kNormBatch, 1}) {
+    p->batch = batch;
+    batches = static_cast<long long>(p->rows) *
+              ((uq + batch - 1) / batch + (append ? 2 : 1) * ((uk + batch - 1) / batch));
+    if (batches >= room * WARPS) break;
+  }
+  const int grid = static_cast<int>(std::min<long long>((batches + WARPS - 1) / WARPS, room));
+  const size_t smem = cpattn::norm_rope_smem(format);
+  bool& ready = ctx->norm_ready[format < 0 ? 0 : 1 + std::min<int>(format, 2)];
+  if (!ready) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaFuncSetAttribute(norm_rope)");
+    ready = true;
+  }
+  return launch_dependent(ctx, kernel, dim3(grid), cpattn::kNormThreads, smem, st, *p, what);
 }
 
 }  // namespace
@@ -157,7 +171,7 @@ cpattn_status cpattn_norm_rope(cpattn_ctx* ctx, const cpattn_norm_rope_desc* des
   p.k_out_stride = k_out_stride;
   const auto kernel = ctx->cfg.head_dim == 128 ? cpattn::norm_rope_kernel<128, -1>
                                                : cpattn::norm_rope_kernel<256, -1>;
-  return launch_norm_rope(ctx, kernel, false, &p, static_cast<cudaStream_t>(stream), "norm_rope launch");
+  return launch_norm_rope(ctx, kernel, -1, &p, static_cast<cudaStream_t>(stream), "norm_rope launch");
 } catch (...) {
   return CPATTN_E_NOMEM;
 }
@@ -184,7 +198,7 @@ cpattn_status cpattn_norm_rope_write_kv(cpattn_ctx* ctx, const cpattn_norm_rope_
   const auto kernel = ctx->cfg.head_dim == 128
                           ? CPATTN_BY_FORMAT(cpattn::norm_rope_kernel, pages->format, 128)
                           : CPATTN_BY_FORMAT(cpattn::norm_rope_kernel, pages->format, 256);
-  return launch_norm_rope(ctx, kernel, true, &p, static_cast<cudaStream_t>(stream),
+  return launch_norm_rope(ctx, kernel, pages->format, &p, static_cast<cudaStream_t>(stream),
                           "norm_rope_write_kv launch");
 } catch (...) {
   return CPATTN_E_NOMEM;
