@@ -496,7 +496,7 @@ cpattn_status cpattn_prefill_packed(cpattn_ctx* ctx, int32_t num_seqs, const int
  *                        s = 2^(floor(log2(max(amax, 2^-117))) - 9)
  *                        r_g = e4m3(amax_g / (6 s))
  *                        x4 = e2m1((x / s) / r_g), 0 where r_g = 0
- *                      (fp32, nearest even, x4 at most 6), and the value read
+ *                      (fp32, nearest even, x4 at most 6, -0 as 0), and the value read
  *                      back is s * r_g * x4.  A row that holds an infinity or a
  *                      NaN is stored with s = NaN.  Readers take any r_g >= 0 and
  *                      any s that is a power of two up to 2^118.

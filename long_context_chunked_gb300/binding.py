@@ -259,6 +259,20 @@ def _want(name, t, dtype, shape, device: int):
                          f"{device}, got {t.dtype} {list(t.shape)} on {t.device}")
 
 
+def _i32_ptrs(names, device: int, *tensors_and_sizes):
+    """Device pointers of contiguous int32 vectors on CUDA device `device`: tensor,
+    size, tensor, size .. (each of `names`)."""
+    import torch
+    i32, out = torch.int32, []
+    for i in range(0, len(tensors_and_sizes), 2):
+        t, n = tensors_and_sizes[i], tensors_and_sizes[i + 1]
+        if t.dtype is not i32 or t.numel() != n or t.dim() != 1 or t.get_device() != device \
+                or not t.is_contiguous():
+            _want(names.split()[i // 2], t, i32, (n,), device)
+        out.append(t.data_ptr())
+    return out
+
+
 def _want_rows(name, t, rows: int, heads: int, hd: int, device: int) -> int:
     """The row stride of a bf16 CUDA tensor [rows, heads, hd] whose rows are dense."""
     import torch
@@ -515,31 +529,24 @@ class Context:
         [1]: how many are free), extends pages.block_table and fills lens [num_seqs],
         row_starts [num_seqs + 1] and each row's positions and slots [rows].  All int32
         CUDA tensors; lens may be cache_lens.  What does not fit is not served."""
-        import torch
-        b, dev = pages.num_seqs, pages.device
-        for name, t, n in (("cache_lens", cache_lens, b), ("new_lens", new_lens, b), ("lens", lens, b),
-                           ("row_starts", row_starts, b + 1), ("free_pages", free_pages, pages.c.num_pages),
-                           ("free_count", free_count, 1), ("positions", positions, positions.numel()),
-                           ("slots", slots, positions.numel())):
-            _want(name, t, torch.int32, (n,), dev)
+        b, dev, rows = pages.num_seqs, pages.device, positions.numel()
         self._check_pages(pages)
-        self._check(self.lib.cpattn_paged_plan(
-            self._h, pages.ref, b, positions.numel(), cache_lens.data_ptr(), new_lens.data_ptr(),
-            free_pages.data_ptr(), free_count.data_ptr(), lens.data_ptr(), row_starts.data_ptr(),
-            positions.data_ptr(), slots.data_ptr(), _stream_on(stream, dev)))
+        have, new, free, count, out, starts, pos, at = _i32_ptrs(
+            "cache_lens new_lens free_pages free_count lens row_starts positions slots", dev, cache_lens, b,
+            new_lens, b, free_pages, pages.c.num_pages, free_count, 1, lens, b, row_starts, b + 1,
+            positions, rows, slots, rows)
+        self._check(self.lib.cpattn_paged_plan(self._h, pages.ref, b, rows, have, new, free, count, out,
+                                               starts, pos, at, _stream_on(stream, dev)))
 
     def paged_trim(self, pages: PagedKV, lens, keep, free_pages, free_count, stream=None):
         """Give back to the list the pages of sequence b behind those of its first
         keep[b] tokens, of the lens[b] it holds (0: all of them; < 0: none)."""
-        import torch
         b, dev = pages.num_seqs, pages.device
-        for name, t, n in (("lens", lens, b), ("keep", keep, b), ("free_pages", free_pages, pages.c.num_pages),
-                           ("free_count", free_count, 1)):
-            _want(name, t, torch.int32, (n,), dev)
         self._check_pages(pages)
-        self._check(self.lib.cpattn_paged_trim(
-            self._h, pages.ref, b, lens.data_ptr(), keep.data_ptr(), free_pages.data_ptr(),
-            free_count.data_ptr(), _stream_on(stream, dev)))
+        have, left, free, count = _i32_ptrs("lens keep free_pages free_count", dev, lens, b, keep, b,
+                                            free_pages, pages.c.num_pages, free_count, 1)
+        self._check(self.lib.cpattn_paged_trim(self._h, pages.ref, b, have, left, free, count,
+                                               _stream_on(stream, dev)))
 
     def norm_rope(self, nr: NormRope, positions, q, k, q_out, k_out, stream=None):
         """Per-head norm and rotation of q [rows, NQ, HD] and k [rows, NKV, HD] (bf16;

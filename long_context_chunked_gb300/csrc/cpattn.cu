@@ -58,7 +58,7 @@ struct cpattn_ctx {
   // GQA packing for short-chunk launches (cpattn_config.gqa_packing, or the
   // CPATTN_GQA_PACKING override).
   bool gqa_packing = true;
-  bool norm_ready[4] = {};  // the norm kernels: dense, and by page format
+  bool norm_ready[2][4] = {};  // the norm kernels, by pairs: dense, and by page format
   bool plan_ready = false;  // the plan and trim kernels have been set up
   bool decode_ready[2][2][3] = {};  // [HD == 256][head blocks - 1][format]: set up
   std::vector<int> block_lens;  // scratch of the unit-order choice

@@ -105,15 +105,18 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
   return r;
 }
 
-// Two fp32 values as e2m1 (round to nearest even, saturating), lo in the low half
-// of the byte; and four bytes' values as fp16 pairs (exact).
-__device__ __forceinline__ uint32_t pack_e2m1x2(float lo, float hi) {
+// Eight fp32 values as e2m1 (round to nearest even, saturating), the first in the
+// lowest bits; and eight values as fp16 pairs (exact).
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float (&x)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-      "cvt.u32.u8 %0, b;\n\t}"
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 __device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t x, uint32_t (&h)[4]) {
@@ -125,6 +128,37 @@ __device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t x, uint32_t (&h)[4]) {
       "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(x));
+}
+
+// Products and sums of pairs of fp32 values, each rounded as by itself.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair_of(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 bf16x2_to_f32x2(uint32_t x) {
+  return pair_of(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
 }
 
 // Largest magnitude of eight bf16 values, as bf16 bits: for sign-less bf16
@@ -164,13 +198,13 @@ struct PackedRow<kE2m1> {
 };
 
 template <int HD>
-__device__ __forceinline__ void quantise(const float (&x)[8], uint32_t, bool, PackedRow<kBf16>& y) {
+__device__ __forceinline__ void quantise(const float (&x)[8], uint32_t, PackedRow<kBf16>& y) {
   y.x = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                    pack_bf16x2(x[6], x[7]));
 }
 
 template <int HD>
-__device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, bool, PackedRow<kE4m3>& y) {
+__device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, PackedRow<kE4m3>& y) {
 #pragma unroll
   for (int o = HD / 16; o > 0; o >>= 1) mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, o));
   const float amax = mag >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
@@ -183,13 +217,12 @@ __device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, bool
   y.s = amax / kE4m3Max;
 }
 
-// e2m1.  The quotient (x / s) / r_g is made as x times (1 / s) (1 / r_g), which is
-// within 2^-22 of it.  For a bf16 x that decides every code but a tie's, which
-// another quotient misses by 2^-9 at least: so the quotient is rounded to a
-// multiple of 2^-14 first (`exact`: by adding 768, whose last place that is, and
-// taking it away), which leaves ties ties and the others on their side.
+// e2m1.  The quotients amax_g / s / 6 and x / s / r_g are made of products with the
+// divisor's reciprocal: by Markstein's theorem (IBM J. Res. Dev. 34, 1990), with f
+// the reciprocal of d rounded to nearest and q = a f rounded, the remainder a - q d
+// is exact in one fused step, and q + (a - q d) f rounds to a / d correctly.
 template <int HD>
-__device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, bool exact, PackedRow<kE2m1>& y) {
+__device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, PackedRow<kE2m1>& y) {
   mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
   mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
   uint32_t row = mag;
@@ -198,24 +231,21 @@ __device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, bool
   const bool fine = row < 0x7F800000u;
   const uint32_t e = fine ? max(row >> 23, 10u) : 10u;      // exponent field of amax
   const float inv_s = __uint_as_float((263u - e) << 23);    // 2^(9 - k), k = e - 127
-  uint32_t r = pack_e4m3x2(__uint_as_float(mag) * inv_s / 6.f, 0.f) & 0xFFu;
+  const float a = __uint_as_float(mag) * inv_s, a6 = a * (1.f / 6.f);
+  uint32_t r = pack_e4m3x2(fmaf(fmaf(-a6, 6.f, a), 1.f / 6.f, a6), 0.f) & 0xFFu;
   if (!fine) r = 0u;
   const float rf = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(r))).x;
-  // (0 for r_g = 0: the codes are 0 then.)
-  const float f = r != 0u ? __fdividef(1.f, rf) : 0.f;
-  y.x = 0u;
+  const float f = r != 0u ? __frcp_rn(rf) : 0.f;
+  const f32x2 s2 = pair_of(inv_s, inv_s), f2 = pair_of(f, f), d2 = pair_of(-rf, -rf);
+  float q[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float q[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float v = x[2 * j + i] * inv_s;
-      q[i] = v * f;
-      if (exact) q[i] = copysignf(fmaf(fabsf(v), f, 768.f) - 768.f, v);
-    }
-    y.x |= pack_e2m1x2(q[0], q[1]) << (8 * j);
+  for (int j = 0; j < 8; j += 2) {
+    const f32x2 v = mul2(pair_of(x[j], x[j + 1]), s2), p = mul2(v, f2);
+    const float2 z = split(fma2(fma2(p, d2, v), f2, p));
+    q[j] = z.x;
+    q[j + 1] = z.y;
   }
-  if (r == 0u) y.x = 0u;
+  y.x = r != 0u ? pack_e2m1x8(q) : 0u;
   y.s = fine ? __uint_as_float((e - 9u) << 23) : __uint_as_float(0x7FC00000u);
   // The record's words: four r_g each.
   r |= __shfl_down_sync(0xFFFFFFFFu, r, 4) << 8;
@@ -356,7 +386,21 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) place[r] = __shfl_sync(0xFFFFFFFFu, mine, r);
     for (int g = g0; g < g1; ++g) {
-      if (g > g0) load(g);
+      if (FMT != kE2m1 && g > g0) load(g);
+      uint4 y[ROWS][LOADS];
+      if constexpr (FMT == kE2m1) {
+        // The next head's rows are loaded while this one's are quantised.
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+          for (int l = 0; l < LOADS; ++l) y[r][l] = x[r][l];
+        if (g + 1 < g1) load(g + 1);
+      } else {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+          for (int l = 0; l < LOADS; ++l) y[r][l] = x[r][l];
+      }
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
 #pragma unroll
@@ -366,14 +410,14 @@ __global__ void __launch_bounds__(256)
                                          static_cast<int>(place[r] & 255));
           void* pool = is_k ? p.pool.k : p.pool.v;
           if constexpr (FMT == kE4m3) {
-            uint32_t m = amax_bits(x[r][l]);
+            uint32_t m = amax_bits(y[r][l]);
 #pragma unroll
             for (int o = VECS / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             // A row with an infinity or a NaN has no scale: all of it reads back as NaN.
             float amax = __uint_as_float(m << 16);
             amax = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : fmaxf(amax, kTinyAmax);
             const float inv = kE4m3Max / amax;
-            const uint32_t w[4] = {x[r][l].x, x[r][l].y, x[r][l].z, x[r][l].w};
+            const uint32_t w[4] = {y[r][l].x, y[r][l].y, y[r][l].z, y[r][l].w};
             uint32_t h[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -386,12 +430,12 @@ __global__ void __launch_bounds__(256)
             }
           } else if constexpr (FMT == kE2m1) {
             float f[8];
-            bf16x8_to_f32x8(x[r][l], f);
-            PackedRow<FMT> y;
-            quantise<HD>(f, amax_bits(x[r][l]) << 16, true, y);
-            if (place[r] >= 0) store_row<HD>(p.pool, is_k, dst, vec, y);
+            bf16x8_to_f32x8(y[r][l], f);
+            PackedRow<FMT> z;
+            quantise<HD>(f, amax_bits(y[r][l]) << 16, z);
+            if (place[r] >= 0) store_row<HD>(p.pool, is_k, dst, vec, z);
           } else {
-            if (place[r] >= 0) reinterpret_cast<uint4*>(pool)[dst * VECS + vec] = x[r][l];
+            if (place[r] >= 0) reinterpret_cast<uint4*>(pool)[dst * VECS + vec] = y[r][l];
           }
         }
       }

@@ -94,6 +94,10 @@ constexpr float kMaxW = 8.507059173023462e+37f;  // 2^126, far above the largest
 constexpr float kPMax = 57344.f;                 // Q8: W is raised where a P would pass this
 constexpr float kPMax4 = 32768.f;                // Q4: the same (r_g / 256 is 1.75 at most)
 constexpr float kAboveOne = 1.00000023841857910f;  // 1 + 2^-22 (bf16: P's lo)
+#ifndef X_KV
+#define X_KV 1
+#endif
+constexpr int kRollV = X_KV;
 constexpr int kDecMaxHeads = 16;                 // of a row
 constexpr int kDecStages = 16;                   // tiles whose absent pages a worker remembers
 
@@ -109,16 +113,16 @@ template <int HD, int FMT, int NB>
 struct DecodeLayout {
   static constexpr bool QUANT = FMT != kBf16;
   static constexpr int RB = row_bytes(HD, FMT);
-  static constexpr int NW = 8;
+#ifndef X_E2M1
+#define X_E2M1 {{{8, 4096, 5}, {8, 4096, 5}}, {{8, 8192, 3}, {8, 4096, 4}}}
+#endif
+  // Of e2m1 pages, by head dim and NB: workers, slot bytes and slots.
+  static constexpr int E2M1[2][2][3] = X_E2M1;
+  static constexpr bool Q4 = FMT == kE2m1;
+  static constexpr int NW = Q4 ? E2M1[HD == 256][NB - 1][0] : 8;
   static constexpr int THREADS = 32 * NW;
-#ifndef X_SLOT128
-#define X_SLOT128 4096
-#endif
-#ifndef X_SLOT256
-#define X_SLOT256 4096
-#endif
-  static constexpr int SLOT = FMT == kE2m1 ? (HD == 128 ? X_SLOT128 : X_SLOT256) : 8192;
-  static constexpr int NSLOT = 196608 / (NW * SLOT);
+  static constexpr int SLOT = Q4 ? E2M1[HD == 256][NB - 1][1] : 8192;
+  static constexpr int NSLOT = Q4 ? E2M1[HD == 256][NB - 1][2] : 196608 / (NW * SLOT);
   static constexpr int WT = SLOT / RB;
   static constexpr int WT_SHIFT = WT == 16 ? 4 : (WT == 32 ? 5 : (WT == 64 ? 6 : 7));
   // Beginning and ending a row costs a worker about as much as 40 KB of tiles;
@@ -141,19 +145,24 @@ struct DecodeLayout {
   // third slot.
   static constexpr bool Q_SMEM = HD * NB == 512;
   static constexpr int Q_BYTES = HEADS * HD * 2;
-  static constexpr int QSLOTS = Q_SMEM ? (Q_BYTES + SLOT - 1) / SLOT : 0;  // slots that Q takes
+  // Slots that a worker's Q takes, or (e2m1) a place of its own.
+  static constexpr int QSLOTS = Q_SMEM && !Q4 ? (Q_BYTES + SLOT - 1) / SLOT : 0;
   static constexpr int C_STRIDE = HD + 8;        // floats of a head's O where workers sum theirs
   static constexpr int OFF_SCALE = NW * NSLOT * SLOT;
   static constexpr int OFF_Q = OFF_SCALE + (QUANT ? NW * NSLOT * WT * REC : 0);
-  static constexpr int OFF_QEXP = OFF_Q + (Q_SMEM ? Q_BYTES : 0);  // [NW][HEADS] 2^e of each Q row
+  static constexpr int OFF_P = OFF_Q + (Q_SMEM ? (Q4 ? NW : 1) * Q_BYTES : 0);  // e2m1: [NW][NB][WT][8] fp16 P
+  static constexpr int OFF_QEXP = OFF_P + (Q4 ? NW * NB * WT * 16 : 0);  // [NW][HEADS] 2^e of each Q row
   static constexpr int OFF_ENDS = OFF_QEXP + (Q_SMEM ? NW * HEADS * 4 : 0);  // [THREADS] 64-bit
   static constexpr int OFF_ML = OFF_ENDS + THREADS * 8;  // [NW][HEADS] (m, l)
   static constexpr int OFF_BAR = OFF_ML + NW * HEADS * 8;
   static constexpr int OFF_BAD = OFF_BAR + NW * NSLOT * 8;  // [NW][kDecStages] absent boxes of a tile
   static constexpr int OFF_MISC = OFF_BAD + NW * kDecStages * 4;  // spots, scan, abort flag
   static constexpr int SMEM_BYTES = OFF_MISC + NW * 16 + THREADS / 32 * 8 + 16;
-  static_assert(HEADS * C_STRIDE * 4 <= NSLOT * SLOT, "a worker's O fits its slots");
-  static_assert(!Q_SMEM || (Q_BYTES <= QSLOTS * SLOT && OFF_Q % 512 == 0),
+  // Bytes between the places of the workers' O: their slots; e2m1: one behind the
+  // other over all that the tiles took.
+  static constexpr int O_BYTES = Q4 ? HEADS * C_STRIDE * 4 : NSLOT * SLOT;
+  static_assert(HEADS * C_STRIDE * 4 <= O_BYTES && NW * O_BYTES <= OFF_QEXP, "the workers' O fit");
+  static_assert(!Q_SMEM || ((Q4 || Q_BYTES <= QSLOTS * SLOT) && OFF_Q % 512 == 0),
                 "a worker's Q fits a slot, and chunks can be XORed into a row's address");
   static_assert(OFF_BAR % 8 == 0 && OFF_MISC % 16 == 0 && OFF_SCALE % 128 == 0 && OFF_Q % 16 == 0 && OFF_ENDS % 8 == 0,
                 "shared memory alignment");
@@ -241,6 +250,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm2_t(uint32_t& r0, uint32_t& r1, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r0), "=r"(r1)
                : "r"(addr)
                : "memory");
 }
@@ -740,6 +755,15 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
   // Accumulator fragments (16 x 8): rows r0 and r0 + 8 (tokens or columns of
   // V), columns 2 quad and 2 quad + 1 (q heads of the block).
   const int quad = lane & 3, r0 = lane >> 2, r8 = lane & 7, oct = lane >> 3;
+  // Q4: rows 8 to 15 of an m-tile are tokens 8 .. 15, at HD = 256 with neighbours
+  // swapped: V's matrices take every second row of both halves, and would meet in
+  // the same banks otherwise.  And where a lane's 16 bytes of a token are, chunk oct
+  // / 2 (others are XORed in).
+  auto second = [](int r) { return Q4 && HD == 256 ? r ^ 1 : r; };
+  auto q4_at = [&](uint32_t base, int token) {
+    return Ly::LINE_TOKENS == 2 ? sw128(base, token >> 1, (token & 1) * 4 + (oct >> 1))
+                                : sw128(base, token, oct >> 1);
+  };
   int slot = 0, used = 0;  // the next slot to read, and copies read so far
   uint32_t phase = 0;
   // A warp whose wait expired, or that another warp's expired wait ends, is
@@ -806,7 +830,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
     uint32_t q[Ly::Q_SMEM ? 1 : HD / 16][2 * NB];
     float qexp[NB];
     // Q_SMEM: rows of HD 16-bit values, 16-byte chunks swizzled by the row.
-    const uint32_t q_at = uniform ? Ly::OFF_Q : NW * (NSLOT - Ly::QSLOTS) * Ly::SLOT + wk * Ly::Q_BYTES;
+    const uint32_t q_at = uniform ? Ly::OFF_Q
+                                  : (Q4 ? Ly::OFF_Q : NW * (NSLOT - Ly::QSLOTS) * Ly::SLOT) + wk * Ly::Q_BYTES;
     if constexpr (Ly::Q_SMEM) {
       float* exps = reinterpret_cast<float*>(smem + Ly::OFF_QEXP) + (uniform ? 0 : wk * HEADS);
       for (int r = uniform ? wk : 0; r < HEADS; r += uniform ? NW : 1) {
@@ -946,9 +971,10 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
             for (int j = 0; j < 4; ++j) c[t][nb][j] = 0.f;
       }
       // (Chunks are XORed in.)
-      const uint32_t k_at = Ly::LINE_TOKENS == 2
-                                ? sw128(kb, (oct & 1) * 4 + (r8 >> 1), (r8 & 1) * 4 + (oct >> 1))
-                                : sw128(kb, (oct & 1) * 8 + r8, oct >> 1);
+      const uint32_t k_at = Q4 ? q4_at(kb, (oct & 1) ? 8 + second(r8) : r8)
+                               : sw128(kb, (oct & 1) * 8 + r8, oct >> 1);
+      // The token of row 8 i + r0 of m-tile t.
+      auto token_of = [&](int t, int i) { return 16 * t + 8 * i + (i == 1 ? second(r0) : r0); };
       // This slot's scales.
       const uint8_t* k_rec = smem + Ly::OFF_SCALE + (wk * NSLOT + slot) * (WT * Ly::REC);
       if constexpr (Q4) {
@@ -964,7 +990,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
             // r_g of the two chunks, tokens r0 and r0 + 8
             const uint8_t* rec = k_rec + (16 * t + r0) * Ly::REC + 4 + ch;
             const uint32_t g0 = *reinterpret_cast<const uint16_t*>(rec);
-            const uint32_t g8 = *reinterpret_cast<const uint16_t*>(rec + 8 * Ly::REC);
+            const uint32_t g8 = *reinterpret_cast<const uint16_t*>(rec + (8 + second(r0) - r0) * Ly::REC);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               uint32_t lo[4], hi[4];
@@ -1039,7 +1065,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float ks =
-              QUANT ? *reinterpret_cast<const float*>(k_rec + (16 * t + 8 * i + r0) * Ly::REC) : 1.f;
+              QUANT ? *reinterpret_cast<const float*>(k_rec + token_of(t, i) * Ly::REC) : 1.f;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1052,7 +1078,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int tok = 16 * t + 8 * i + r0;
+            const int tok = token_of(t, i);
             seen[t][i] = tok < valid && !((bad >> (tok >> box_shift)) & 1u);
             if (!seen[t][i]) {
 #pragma unroll
@@ -1083,7 +1109,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            vs[t][i] = *reinterpret_cast<const float*>(v_rec + (16 * t + 8 * i + r0) * Ly::REC);
+            vs[t][i] = *reinterpret_cast<const float*>(v_rec + token_of(t, i) * Ly::REC);
             if (partial && !seen[t][i]) vs[t][i] = 0.f;
           }
       }
@@ -1171,8 +1197,11 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
         }
       }
 
-      // ---- P, transposed into the B operand of V^T P^T (16 tokens per step)
-      uint32_t ph[MT][NB][2], pl[QUANT ? 1 : MT][NB][2];
+      // ---- P, transposed into the B operand of V^T P^T (16 tokens per step).  Q4:
+      // through shared memory, [head block][row][8 heads], so that V^T P^T can be
+      // a loop over the steps.
+      uint32_t ph[Q4 ? 1 : MT][NB][2], pl[QUANT ? 1 : MT][NB][2];
+      uint8_t* p_rows = smem + Ly::OFF_P + wk * (NB * WT * 16);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1180,7 +1209,10 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float e0 = c[t][nb][2 * i], e1 = c[t][nb][2 * i + 1];
-            if constexpr (QUANT) {
+            if constexpr (Q4) {
+              *reinterpret_cast<uint32_t*>(p_rows + (nb * WT + 16 * t + 8 * i + r0) * 16 + 4 * quad) =
+                  pack_f16x2(e0 * ps[nb][0], e1 * ps[nb][1]);
+            } else if constexpr (Q8) {
               ph[t][nb][i] = transpose8(pack_f16x2(e0 * ps[nb][0], e1 * ps[nb][1]));
             } else {
               // hi: the upper 16 bits; lo: the rest, and 2^-22 of the whole (kAboveOne).
@@ -1191,6 +1223,20 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
                                          fmaf(e1, kAboveOne, -__uint_as_float(b1 & 0xFFFF0000u))));
             }
           }
+      if constexpr (Q4) {
+        // What is no token has P = 0, but its r_g are whatever was there: none that
+        // would be infinite or NaN as fp16.
+        if (partial) {
+          for (int i = lane; i < WT; i += 32) {
+            if (i < valid && !((bad >> (i >> box_shift)) & 1u)) continue;
+#pragma unroll
+            for (int j = 0; j < HD / 128; ++j)
+              *reinterpret_cast<uint32_t*>(
+                  smem + Ly::OFF_SCALE + (wk * NSLOT + slot) * (WT * Ly::REC) + i * Ly::REC + 4 + 4 * j) = 0u;
+          }
+        }
+        __syncwarp();
+      }
 
       // ---- O^T += V^T P^T
       if (!Q4 && valid < WT) {
@@ -1206,46 +1252,58 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
         }
         __syncwarp();
       }
-#pragma unroll
-      for (int k = 0; k < MT; ++k) {
-        if constexpr (Q4) {
-          const uint32_t v_at = Ly::LINE_TOKENS == 2
-                                    ? sw128(vb, (oct & 1) * 4 + (r8 >> 1), (r8 & 1) * 4 + (oct >> 1))
-                                    : sw128(vb, (oct & 1) * 8 + r8, oct >> 1);
+      if constexpr (Q4) {
+        // Two matrices of V rows, the tokens of whose lanes' pairs are neighbours:
+        // rows 2 i and 2 i + 1 are the i-th even (odd) rows of an m-tile's halves.
+        const int x = (r8 & 6) + (oct & 1);
+        const uint32_t v_at = q4_at(vb, (r8 & 1) ? 8 + second(x) : x);
+        const uint8_t* rec0 = v_rec + 2 * quad * Ly::REC + 4;
+        const uint32_t p_at = smem_u32(p_rows) + (NB == 2 ? (oct >> 1) * (WT * 16) : 0) + ((oct & 1) * 8 + r8) * 16;
+#pragma unroll kRollV
+        for (int k = 0; k < MT; ++k) {
+          uint32_t pb[4];  // [head block][b0, b1]
+          if constexpr (NB == 2)
+            ldsm4_t(pb, p_at + k * 256);
+          else
+            ldsm2_t(pb[0], pb[1], p_at + k * 256);
 #pragma unroll
           for (int ch = 0; ch < HD / 32; ch += 2) {  // two 16-byte chunks: 64 columns, two groups
-            uint32_t vr[4];  // token half, then chunk, by lane octet
+            uint32_t vr[4];  // matrix, then chunk, by lane octet
             ldsm4_t(vr, (v_at ^ (ch << 4)) + k * (2048 / Ly::LINE_TOKENS));
-            // r_g of the two chunks, tokens 2 quad and + 1, + 8 and + 9
-            const uint8_t* rec = v_rec + (16 * k + 2 * quad) * Ly::REC + 4 + ch;
+            // r_g of the two chunks: tokens 2 quad and + 1, + 8 and + 9
+            const uint8_t* rec = rec0 + k * (16 * Ly::REC) + ch;
             const uint32_t g0 = *reinterpret_cast<const uint16_t*>(rec);
             const uint32_t g1 = *reinterpret_cast<const uint16_t*>(rec + Ly::REC);
-            const uint32_t g8 = *reinterpret_cast<const uint16_t*>(rec + 8 * Ly::REC);
-            const uint32_t g9 = *reinterpret_cast<const uint16_t*>(rec + 9 * Ly::REC);
+            const uint32_t g8 = *reinterpret_cast<const uint16_t*>(rec + (HD == 256 ? 9 : 8) * Ly::REC);
+            const uint32_t g9 = *reinterpret_cast<const uint16_t*>(rec + (HD == 256 ? 8 : 9) * Ly::REC);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              // An e4m3 byte without its sign, in fp16's place: 2^-8 times its value.
+              // An e4m3 byte in fp16's place: 2^-8 times its value.
               const uint32_t sel = j == 0 ? 0x4202 : 0x5212;
-              const uint32_t f0 = (__byte_perm(g0, g1, sel) >> 1) & 0x3F803F80u;
-              const uint32_t f8 = (__byte_perm(g8, g9, sel) >> 1) & 0x3F803F80u;
-              // A register holds two tokens x four columns; regrouped, columns 4 r0 +
-              // {0, 1} and {2, 3} are rows r0 and r0 + 8 of two m-tiles.
+              const uint32_t f0 = __byte_perm(g0, g1, sel) >> 1;
+              const uint32_t f8 = __byte_perm(g8, g9, sel) >> 1;
+              // Each register holds four columns of a token of rows 0 .. 7 and one of
+              // rows 8 .. 15; the nibbles of a column and of both matrices go to one
+              // byte: lo: columns 4 r0, + 2, hi: + 1, + 3, of either half.
+              const uint32_t m1 = vr[2 * j], m2 = vr[2 * j + 1];
               uint32_t lo[4], hi[4];
-              e2m1x8_to_f16x8(vr[2 * j], lo);
-              e2m1x8_to_f16x8(vr[2 * j + 1], hi);
-              const uint32_t a0[4] = {__byte_perm(lo[0], lo[2], 0x5410), __byte_perm(lo[0], lo[2], 0x7632),
-                                      __byte_perm(hi[0], hi[2], 0x5410), __byte_perm(hi[0], hi[2], 0x7632)};
-              const uint32_t a1[4] = {__byte_perm(lo[1], lo[3], 0x5410), __byte_perm(lo[1], lo[3], 0x7632),
-                                      __byte_perm(hi[1], hi[3], 0x5410), __byte_perm(hi[1], hi[3], 0x7632)};
+              e2m1x8_to_f16x8((m1 & 0x0F0F0F0Fu) | ((m2 << 4) & 0xF0F0F0F0u), lo);
+              e2m1x8_to_f16x8(((m1 >> 4) & 0x0F0F0F0Fu) | (m2 & 0xF0F0F0F0u), hi);
+              const uint32_t a0[4] = {lo[0], hi[0], lo[2], hi[2]};
+              const uint32_t a1[4] = {lo[1], hi[1], lo[3], hi[3]};
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
-                const uint32_t b0 = mul_f16x2(ph[k][nb][0], f0), b1 = mul_f16x2(ph[k][nb][1], f8);
+                const uint32_t b0 = mul_f16x2(pb[2 * nb], f0), b1 = mul_f16x2(pb[2 * nb + 1], f8);
                 mma16816<true>(o[2 * (ch + j)][nb], a0, b0, b1);
                 mma16816<true>(o[2 * (ch + j) + 1][nb], a1, b0, b1);
               }
             }
           }
-        } else if constexpr (Q8) {
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < (Q4 ? 0 : MT); ++k) {
+        if constexpr (Q8) {
 #pragma unroll
           for (int ch = 0; ch < MO; ch += 2) {  // two 16-byte chunks: 32 columns
             uint32_t vr[4];  // token half, then chunk, by lane octet
@@ -1351,7 +1409,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
       __syncthreads();
       const long long piece = 2LL * blockIdx.x * NW;
       // The slots have been read (the barrier above): worker w's O goes there.
-      constexpr int RING = NSLOT * Ly::SLOT;
+      constexpr int RING = Ly::O_BYTES;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll

@@ -109,9 +109,9 @@ struct DecodeWorkspace {
   uint64_t ml, cut, total;  // byte offsets
 };
 DecodeWorkspace decode_workspace(const cpattn_ctx* ctx) {
-  // 8 workers per CTA, at most 16 rows per piece.
-  const uint64_t workers = static_cast<uint64_t>(decode_max_ctas(ctx)) * 8;
-  const uint64_t rows = 2 * workers * 16;
+  // Up to 16 workers per CTA, whose pieces have 128 rows between them at most.
+  const uint64_t workers = static_cast<uint64_t>(decode_max_ctas(ctx)) * 16;
+  const uint64_t rows = 2 * static_cast<uint64_t>(decode_max_ctas(ctx)) * 128;
   DecodeWorkspace w;
   w.ml = cpattn::align256(rows * ctx->cfg.head_dim * sizeof(float));
   w.cut = w.ml + cpattn::align256(rows * sizeof(float2));
@@ -123,7 +123,7 @@ template <int HD, int NB, int FMT>
 cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
                             cpattn::PagedDecodeParams* p, cudaStream_t st) {
   using Ly = cpattn::DecodeLayout<HD, FMT, NB>;
-  static_assert(Ly::NW <= 8 && Ly::HEADS <= 16, "decode_workspace");
+  static_assert(Ly::NW <= 16 && Ly::NW * Ly::HEADS <= 128, "decode_workspace");
   bool& ready = ctx->decode_ready[HD == 256][NB - 1][FMT == cpattn::kBf16 ? 0 : (FMT == cpattn::kE4m3 ? 1 : 2)];
   if (!ready) {
     cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, FMT, NB>,
@@ -213,6 +213,13 @@ cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, 
   p.heads_per_item = heads_per_item(ctx, units);
   const int grid = copy_grid(ctx, units, p.heads_per_item);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+#ifdef X_ROWS
+  if (pages->format == CPATTN_PAGES_E2M1 && per == 4) {
+    const long long u = (static_cast<long long>(num_rows) + X_ROWS - 1) / X_ROWS;
+    p.heads_per_item = heads_per_item(ctx, u);
+    return launch_paged_write<X_ROWS>(ctx, p, pages->format, copy_grid(ctx, u, p.heads_per_item), st);
+  }
+#endif
   return per == 4 ? launch_paged_write<4>(ctx, p, pages->format, grid, st)
                   : launch_paged_write<1>(ctx, p, pages->format, grid, st);
 } catch (...) {

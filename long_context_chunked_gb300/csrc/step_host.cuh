@@ -116,9 +116,18 @@ cpattn_status launch_norm_rope(cpattn_ctx* ctx, void (*kernel)(cpattn::NormRopeP
               ((uq + batch - 1) / batch + (append ? 2 : 1) * ((uk + batch - 1) / batch));
     if (batches >= room * WARPS) break;
   }
-  const int grid = static_cast<int>(std::min<long long>((batches + WARPS - 1) / WARPS, room));
+  // Many rows: blocks of a row per warp, of which the SMs take the next as they end
+  // one (20161 rows, 32 + 2 heads of 256: 107.7 us, 113.9 appended to bf16 pages,
+  // 110.5 to e4m3; equal slices for resident blocks: 123.0, 137.4, 135.6; 17421 rows,
+  // 32 + 4 of 128: 53.4 and 60.3).  Rows of 128 that are appended are too little work
+  // for a block's beginning (e4m3: 68.7 us, equal slices 60.3), and few rows have to
+  // be spread (2000 rows, 32 + 4 of 128: 11.4 us and 10.4).
+  const bool rows_in_turn = p->batch > 1 && (ctx->cfg.head_dim == 256 || !append) &&
+                            p->rows >= 2 * room * WARPS;
+  const int grid = static_cast<int>(rows_in_turn ? (p->rows + WARPS - 1) / WARPS
+                                                 : std::min<long long>((batches + WARPS - 1) / WARPS, room));
   const size_t smem = cpattn::norm_rope_smem(format);
-  bool& ready = ctx->norm_ready[format < 0 ? 0 : 1 + std::min<int>(format, 2)];
+  bool& ready = ctx->norm_ready[p->neighbours][format < 0 ? 0 : 1 + std::min<int>(format, 2)];
   if (!ready) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
@@ -169,8 +178,10 @@ cpattn_status cpattn_norm_rope(cpattn_ctx* ctx, const cpattn_norm_rope_desc* des
   if (num_rows == 0) return CPATTN_OK;
   p.k_out = static_cast<__nv_bfloat16*>(k_out);
   p.k_out_stride = k_out_stride;
-  const auto kernel = ctx->cfg.head_dim == 128 ? cpattn::norm_rope_kernel<128, -1>
-                                               : cpattn::norm_rope_kernel<256, -1>;
+  const auto kernel =
+      ctx->cfg.head_dim == 128
+          ? (p.neighbours ? cpattn::norm_rope_kernel<128, true, -1> : cpattn::norm_rope_kernel<128, false, -1>)
+          : (p.neighbours ? cpattn::norm_rope_kernel<256, true, -1> : cpattn::norm_rope_kernel<256, false, -1>);
   return launch_norm_rope(ctx, kernel, -1, &p, static_cast<cudaStream_t>(stream), "norm_rope launch");
 } catch (...) {
   return CPATTN_E_NOMEM;
@@ -195,9 +206,12 @@ cpattn_status cpattn_norm_rope_write_kv(cpattn_ctx* ctx, const cpattn_norm_rope_
   p.v = static_cast<const __nv_bfloat16*>(v);
   p.v_stride = v_stride;
   p.slots = slots;
-  const auto kernel = ctx->cfg.head_dim == 128
-                          ? CPATTN_BY_FORMAT(cpattn::norm_rope_kernel, pages->format, 128)
-                          : CPATTN_BY_FORMAT(cpattn::norm_rope_kernel, pages->format, 256);
+  const auto kernel =
+      ctx->cfg.head_dim == 128
+          ? (p.neighbours ? CPATTN_BY_FORMAT(cpattn::norm_rope_kernel, pages->format, 128, true)
+                          : CPATTN_BY_FORMAT(cpattn::norm_rope_kernel, pages->format, 128, false))
+          : (p.neighbours ? CPATTN_BY_FORMAT(cpattn::norm_rope_kernel, pages->format, 256, true)
+                          : CPATTN_BY_FORMAT(cpattn::norm_rope_kernel, pages->format, 256, false));
   return launch_norm_rope(ctx, kernel, pages->format, &p, static_cast<cudaStream_t>(stream),
                           "norm_rope_write_kv launch");
 } catch (...) {

@@ -62,14 +62,15 @@ def quantise_rows(bits: np.ndarray):
 
 
 def to_e2m1(x: np.ndarray) -> np.ndarray:
-    """Codes of the nearest e2m1 values (ties to the even code, 6 at most), by search."""
+    """Codes of the nearest e2m1 values (ties to the even code, 6 at most; -0 is
+    taken as 0), by search."""
     x = np.asarray(x, dtype=np.float64)
     a = np.minimum(np.abs(x), 6.0)
     hi = np.clip(np.searchsorted(E2M1_MAGNITUDES, a), 1, 7)
     lo = hi - 1
     dl, dh = a - E2M1_MAGNITUDES[lo], E2M1_MAGNITUDES[hi] - a
     code = np.where(dl < dh, lo, np.where(dh < dl, hi, np.where(lo % 2 == 0, lo, hi)))
-    return np.where(np.signbit(x), code | 8, code).astype(np.uint8)
+    return np.where(x < 0, code | 8, code).astype(np.uint8)
 
 
 def quantise4_rows(x: np.ndarray):

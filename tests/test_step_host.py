@@ -172,7 +172,7 @@ def test_oracle_e2m1_rounding_by_hand():
     x = [0, .25, .2501, .75, .7499, 1.25, 1.2501, 1.75, 1.7499, 2.5, 2.5001, 3.5, 3.4999, 5, 5.0001, 7, 1e30]
     want = [0, 0, 1, 2, 1, 2, 3, 4, 3, 4, 5, 6, 5, 6, 7, 7, 7]
     assert oracle.to_e2m1(np.array(x)).tolist() == want
-    assert oracle.to_e2m1(-np.array(x)).tolist() == [w | 8 for w in want]
+    assert oracle.to_e2m1(-np.array(x)).tolist() == [0] + [w | 8 for w in want[1:]]
 
 
 @pytest.mark.parametrize("seed", range(3))
