@@ -736,8 +736,8 @@ cpattn_status cpattn_sync_status(cpattn_ctx* ctx, void* stream) {
                   "fp16's finite range");
     if ((word & 0xFF) == cpattn::kStatusPage)
       return fail(ctx, CPATTN_E_PAGE,
-                  "a paged call met a page id outside the pool, or a length beyond the block "
-                  "table's row or the striped cache; those tokens were skipped");
+                  "a paged call met a page id outside the pool, a length beyond the block table's row or "
+                  "the striped cache, or too few free pages or rows; those tokens were skipped");
     return fail(ctx, CPATTN_E_TIMEOUT,
                 "a bounded device wait expired (site " + std::to_string(word >> 8) + ")");
   }

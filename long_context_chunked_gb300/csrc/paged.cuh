@@ -386,21 +386,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) place[r] = __shfl_sync(0xFFFFFFFFu, mine, r);
     for (int g = g0; g < g1; ++g) {
-      if (FMT != kE2m1 && g > g0) load(g);
-      uint4 y[ROWS][LOADS];
-      if constexpr (FMT == kE2m1) {
-        // The next head's rows are loaded while this one's are quantised.
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-          for (int l = 0; l < LOADS; ++l) y[r][l] = x[r][l];
-        if (g + 1 < g1) load(g + 1);
-      } else {
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-          for (int l = 0; l < LOADS; ++l) y[r][l] = x[r][l];
-      }
+      if (g > g0) load(g);
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
 #pragma unroll
@@ -410,14 +396,14 @@ __global__ void __launch_bounds__(256)
                                          static_cast<int>(place[r] & 255));
           void* pool = is_k ? p.pool.k : p.pool.v;
           if constexpr (FMT == kE4m3) {
-            uint32_t m = amax_bits(y[r][l]);
+            uint32_t m = amax_bits(x[r][l]);
 #pragma unroll
             for (int o = VECS / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             // A row with an infinity or a NaN has no scale: all of it reads back as NaN.
             float amax = __uint_as_float(m << 16);
             amax = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : fmaxf(amax, kTinyAmax);
             const float inv = kE4m3Max / amax;
-            const uint32_t w[4] = {y[r][l].x, y[r][l].y, y[r][l].z, y[r][l].w};
+            const uint32_t w[4] = {x[r][l].x, x[r][l].y, x[r][l].z, x[r][l].w};
             uint32_t h[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -430,12 +416,12 @@ __global__ void __launch_bounds__(256)
             }
           } else if constexpr (FMT == kE2m1) {
             float f[8];
-            bf16x8_to_f32x8(y[r][l], f);
-            PackedRow<FMT> z;
-            quantise<HD>(f, amax_bits(y[r][l]) << 16, z);
-            if (place[r] >= 0) store_row<HD>(p.pool, is_k, dst, vec, z);
+            bf16x8_to_f32x8(x[r][l], f);
+            PackedRow<FMT> y;
+            quantise<HD>(f, amax_bits(x[r][l]) << 16, y);
+            if (place[r] >= 0) store_row<HD>(p.pool, is_k, dst, vec, y);
           } else {
-            if (place[r] >= 0) reinterpret_cast<uint4*>(pool)[dst * VECS + vec] = y[r][l];
+            if (place[r] >= 0) reinterpret_cast<uint4*>(pool)[dst * VECS + vec] = x[r][l];
           }
         }
       }

@@ -55,6 +55,15 @@
 // fewer below, and none below 2^-32 W.  (Against one reference per warp, which
 // was wrong: 1x128k 37.8 -> 38.9 us, 64 ragged 59.0 -> 58.3.  The largest product
 // found by a bound from p and s apart, and then once more token by token: 39.2.)
+// e2m1 (Q4): the same with two levels of scales.  A K group's r_g multiplies its 32
+// dims' part of the logit in fp32, s the sum.  P is stored with s, as above (with W
+// the P at most 32768), and for each group multiplied by r_g / 256 in fp16, which
+// rounds it once more; O is in units of 2 W.  The conversion takes a byte's two
+// values, neighbours in a row, but the operand of V^T P^T wants two tokens of one
+// column: so ldmatrix is given V's rows in an order that brings neighbouring tokens
+// into two registers, whose nibbles are merged before the conversion (4 logical
+// instructions for 16 values; regrouping them after it takes 8).  P goes through
+// shared memory, so that V^T P^T can be a loop over 16 tokens each.
 // bf16: P is carried as a bf16 hi + lo pair against bf16 V.  hi is cut, not
 // rounded, and lo takes 2^-22 p besides (far below its own rounding, 2^-16 p), so
 // that both are positive wherever p is: an infinite v_t stays infinite, where a lo
@@ -76,6 +85,17 @@
 // CTAs that end apart (9 or 10 to a row of the first case).  While tiles flow,
 // bf16 is bound by DRAM, and e4m3 by the latency of conversions and products
 // in 8 warps (a quarter of the issue slots is used).
+//   e2m1: 1 x 126977, 32 q heads on 2 of 256: 38.8 us for 71 MB (1.8 TB/s, 27 %), 8 on
+// 2: 30.0; 64 ragged, 32 on 4 of 128: 50.2 us for 150 MB (3.0 TB/s, 44 %), 16 on 2 of
+// 256: 45.8; 8 x 32768, 32 on 2 of 256: 63.8, 32 on 4 of 128: 48.3; 1 x 500, 8 on 2 of
+// 128: 7.8.  Half of e4m3's bytes take as many conversions and products and more
+// scales: 2.8 instructions per value and lane (8 x 32768 of 128: 1464 per tile of
+// 64 tokens, 256 of them conversions), of which 40 to 47 % of the issue slots are
+// used.  So it is bound by instructions and their latency, and a cache of 4 bits
+// saves more memory than time.  (16 warps that share a tile of 256 or 512 tokens,
+// each with 32 columns of O, P and one barrier per tile between them: 37.2 us and
+// 51.0 for the first and the last but one case, but 90 us for the 64 ragged ones,
+// whose many small copies one warp then has to send.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -94,10 +114,6 @@ constexpr float kMaxW = 8.507059173023462e+37f;  // 2^126, far above the largest
 constexpr float kPMax = 57344.f;                 // Q8: W is raised where a P would pass this
 constexpr float kPMax4 = 32768.f;                // Q4: the same (r_g / 256 is 1.75 at most)
 constexpr float kAboveOne = 1.00000023841857910f;  // 1 + 2^-22 (bf16: P's lo)
-#ifndef X_KV
-#define X_KV 1
-#endif
-constexpr int kRollV = X_KV;
 constexpr int kDecMaxHeads = 16;                 // of a row
 constexpr int kDecStages = 16;                   // tiles whose absent pages a worker remembers
 
@@ -113,11 +129,11 @@ template <int HD, int FMT, int NB>
 struct DecodeLayout {
   static constexpr bool QUANT = FMT != kBf16;
   static constexpr int RB = row_bytes(HD, FMT);
-#ifndef X_E2M1
-#define X_E2M1 {{{8, 4096, 5}, {8, 4096, 5}}, {{8, 8192, 3}, {8, 4096, 4}}}
-#endif
-  // Of e2m1 pages, by head dim and NB: workers, slot bytes and slots.
-  static constexpr int E2M1[2][2][3] = X_E2M1;
+  // Of e2m1 pages, by head dim and NB: workers, slot bytes and slots.  Slots of 4 KB
+  // where 8 KB would take more tokens than P and the logits have registers for (1 x
+  // 126977, 32 q heads on 2 of 256: 38.8 us, 45.6 with 8 KB), and more workers where O
+  // is small (8 x 32768, 32 on 4 of 128: 8 workers 52.8 us, 12 48.2, 16 49.7).
+  static constexpr int E2M1[2][2][3] = {{{12, 4096, 3}, {8, 4096, 4}}, {{8, 8192, 3}, {8, 4096, 4}}};
   static constexpr bool Q4 = FMT == kE2m1;
   static constexpr int NW = Q4 ? E2M1[HD == 256][NB - 1][0] : 8;
   static constexpr int THREADS = 32 * NW;
@@ -128,7 +144,10 @@ struct DecodeLayout {
   // Beginning and ending a row costs a worker about as much as 40 KB of tiles;
   // the list counts them before the row's first tile (64 ragged sequences,
   // tiles of 16 KB: 70 us without, 62.9 with one, 59.3 with two, 58.9 with three).
-  static constexpr int ROW = FMT == kE2m1 ? 20480 / (2 * SLOT) : 40960 / (2 * SLOT);
+  // E2M1: 20 KB for HD = 128 (64 ragged sequences, 64 and 32 heads on 4: 70.4 and
+  // 50.1 us, with 32 KB 73.5 and 50.5), 32 KB for HD = 256 (64 on 4 and 32 on 4: 76.0
+  // and 45.8 us, with 20 KB 94.4 and 47.4, with 8 KB 95.4 and 55.6).
+  static constexpr int ROW = (Q4 ? (HD == 256 ? 32768 : 20480) : 40960) / (2 * SLOT);
   // A slot holds lines of 128 bytes: NBOX column blocks of them, or (e2m1 of HD =
   // 128) two tokens to a line.
   static constexpr int BOXW = FMT == kBf16 ? 64 : 128;  // elements per line, of 2 bytes or 1
@@ -1259,7 +1278,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
         const uint32_t v_at = q4_at(vb, (r8 & 1) ? 8 + second(x) : x);
         const uint8_t* rec0 = v_rec + 2 * quad * Ly::REC + 4;
         const uint32_t p_at = smem_u32(p_rows) + (NB == 2 ? (oct >> 1) * (WT * 16) : 0) + ((oct & 1) * 8 + r8) * 16;
-#pragma unroll kRollV
+#pragma unroll 1
         for (int k = 0; k < MT; ++k) {
           uint32_t pb[4];  // [head block][b0, b1]
           if constexpr (NB == 2)

@@ -88,12 +88,21 @@ cpattn_status launch_dependent(cpattn_ctx* ctx, void (*kernel)(Params), dim3 gri
    : (format) == CPATTN_PAGES_E4M3 ? kernel<__VA_ARGS__, cpattn::kE4m3> \
                                    : kernel<__VA_ARGS__, cpattn::kE2m1>)
 
+// Rows that a warp of the write takes, of the 1 or 4 that the number of rows asks
+// for: e2m1 of head_dim 256 has two instead of four, which leave registers for more
+// warps (28672 tokens of 2 heads 22.9 us, by four 28.3).
+constexpr int write_rows(int head_dim, int format, int rows) {
+  return format == CPATTN_PAGES_E2M1 && head_dim == 256 ? std::min(rows, 2) : rows;
+}
 template <int ROWS>
 cpattn_status launch_paged_write(cpattn_ctx* ctx, const cpattn::PagedWriteParams& p, int format,
                                  int grid, cudaStream_t st) {
-  const auto kernel = ctx->cfg.head_dim == 128
-                          ? CPATTN_BY_FORMAT(cpattn::paged_write_kernel, format, 128, ROWS)
-                          : CPATTN_BY_FORMAT(cpattn::paged_write_kernel, format, 256, ROWS);
+  constexpr int PACKED = write_rows(256, CPATTN_PAGES_E2M1, ROWS);
+  const auto kernel =
+      ctx->cfg.head_dim == 128           ? CPATTN_BY_FORMAT(cpattn::paged_write_kernel, format, 128, ROWS)
+      : format == CPATTN_PAGES_E2M1      ? cpattn::paged_write_kernel<256, PACKED, cpattn::kE2m1>
+      : format == CPATTN_PAGES_E4M3      ? cpattn::paged_write_kernel<256, ROWS, cpattn::kE4m3>
+                                         : cpattn::paged_write_kernel<256, ROWS, cpattn::kBf16>;
   return launch_dependent(ctx, kernel, dim3(grid), 256, 0, st, p, "paged write launch");
 }
 
@@ -109,8 +118,8 @@ struct DecodeWorkspace {
   uint64_t ml, cut, total;  // byte offsets
 };
 DecodeWorkspace decode_workspace(const cpattn_ctx* ctx) {
-  // Up to 16 workers per CTA, whose pieces have 128 rows between them at most.
-  const uint64_t workers = static_cast<uint64_t>(decode_max_ctas(ctx)) * 16;
+  // Up to 12 workers per CTA, whose pieces have 128 rows between them at most.
+  const uint64_t workers = static_cast<uint64_t>(decode_max_ctas(ctx)) * 12;
   const uint64_t rows = 2 * static_cast<uint64_t>(decode_max_ctas(ctx)) * 128;
   DecodeWorkspace w;
   w.ml = cpattn::align256(rows * ctx->cfg.head_dim * sizeof(float));
@@ -123,7 +132,7 @@ template <int HD, int NB, int FMT>
 cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
                             cpattn::PagedDecodeParams* p, cudaStream_t st) {
   using Ly = cpattn::DecodeLayout<HD, FMT, NB>;
-  static_assert(Ly::NW <= 16 && Ly::NW * Ly::HEADS <= 128, "decode_workspace");
+  static_assert(Ly::NW <= 12 && Ly::NW * Ly::HEADS <= 128, "decode_workspace");
   bool& ready = ctx->decode_ready[HD == 256][NB - 1][FMT == cpattn::kBf16 ? 0 : (FMT == cpattn::kE4m3 ? 1 : 2)];
   if (!ready) {
     cudaError_t e = cudaFuncSetAttribute(cpattn::paged_decode_kernel<HD, FMT, NB>,
@@ -207,21 +216,15 @@ cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, 
   p.rows = num_rows;
   // Four rows a warp where that leaves 16 warps per SM, else one (the same
   // write: 22.5 us by single rows, 19.7 by four).
-  const int per = static_cast<long long>(num_rows) * ctx->cfg.num_kv_heads >=
-                          4LL * 16 * std::max(ctx->num_sms, 1) ? 4 : 1;
+  const bool many = static_cast<long long>(num_rows) * ctx->cfg.num_kv_heads >=
+                    4LL * 16 * std::max(ctx->num_sms, 1);
+  const int per = write_rows(ctx->cfg.head_dim, pages->format, many ? 4 : 1);
   const long long units = (static_cast<long long>(num_rows) + per - 1) / per;
   p.heads_per_item = heads_per_item(ctx, units);
   const int grid = copy_grid(ctx, units, p.heads_per_item);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-#ifdef X_ROWS
-  if (pages->format == CPATTN_PAGES_E2M1 && per == 4) {
-    const long long u = (static_cast<long long>(num_rows) + X_ROWS - 1) / X_ROWS;
-    p.heads_per_item = heads_per_item(ctx, u);
-    return launch_paged_write<X_ROWS>(ctx, p, pages->format, copy_grid(ctx, u, p.heads_per_item), st);
-  }
-#endif
-  return per == 4 ? launch_paged_write<4>(ctx, p, pages->format, grid, st)
-                  : launch_paged_write<1>(ctx, p, pages->format, grid, st);
+  return per > 1 ? launch_paged_write<4>(ctx, p, pages->format, grid, st)
+                 : launch_paged_write<1>(ctx, p, pages->format, grid, st);
 } catch (...) {
   return CPATTN_E_NOMEM;
 }

@@ -7,7 +7,7 @@ import torch
 
 import long_context_chunked_gb300 as cp
 import oracle
-from paged_helpers import Buffer, Paged, lse_bound
+from paged_helpers import Buffer, Paged, bf16_normal, lse_bound
 
 
 class Paged4(Paged):
@@ -20,6 +20,18 @@ class Paged4(Paged):
         self.pools = [np.full((n, nkv, page, hd // 2), 0xFF, np.uint8) for _ in range(2)]
         self.scales = [np.full((n, nkv, page, 4 + hd // 32), 0xFF, np.uint8) for _ in range(2)]
         self.dt = torch.uint8
+
+    def fill(self, rng, lens):
+        """As Paged.fill, all rows quantised at once."""
+        n = np.maximum(lens, 0)
+        seq = np.repeat(np.arange(len(n)), n)
+        t = np.concatenate([np.arange(i) for i in n])
+        page, slot = self.table[seq, t // self.page], t % self.page
+        for pool, scale in zip(self.pools, self.scales):
+            for at in range(0, len(t), 8192):
+                part = slice(at, at + 8192)
+                x = oracle.bits_to_f64(bf16_normal(rng, len(t[part]), self.nkv, self.hd))
+                pool[page[part], :, slot[part]], scale[page[part], :, slot[part]] = oracle.quantise4_rows(x)
 
     def upload(self):
         self.d_pools = [Buffer(x, torch.uint8) for x in self.pools]
