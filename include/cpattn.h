@@ -700,7 +700,9 @@ cpattn_status cpattn_rope_steps(const double* inv_freq, int32_t n, uint64_t* ste
  *                   parts of the rows of one projection
  *   k, k_out        the same of NKV heads
  * q_out may be q with the same stride, and k_out k; no other overlap.  A NaN or an
- * infinity stays within its row and head.  One launch.  Errors: E_INVALID, E_CUDA.
+ * infinity stays within its row and head, other values of which it may make NaN;
+ * where the squares' mean passes fp32's range the head is 0 or NaN.  One launch.
+ * Errors: E_INVALID, E_CUDA.
  */
 cpattn_status cpattn_norm_rope(cpattn_ctx* ctx, const cpattn_norm_rope_desc* desc, int32_t num_rows,
                                const int32_t* positions, const void* q, int64_t q_stride,

@@ -143,7 +143,7 @@ class NormRope:
                     w.dim() != 1 or w.shape != weights[0].shape or not w.is_cuda or \
                     not w.is_contiguous() or w.device != weights[0].device:
                 raise ValueError("weights must be alike, contiguous bfloat16 or float32 [HD] on one CUDA device")
-        if device is None:
+        if device is None or torch.device(device) == torch.device("cuda"):
             device = weights[0].device if weights else torch.device("cuda", torch.cuda.current_device())
         self.steps = torch.from_numpy(steps.view(np.int64)).to(device) if freq.size else None
         self.q_weight, self.k_weight, self.rotary_dim = q_weight, k_weight, 2 * freq.size
@@ -280,7 +280,7 @@ def _want_rows(name, t, rows: int, heads: int, hd: int, device: int) -> int:
             or device < 0 or (t.numel() > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != hd))):
         raise ValueError(f"{name}: expected a bfloat16 tensor [{rows}, {heads}, {hd}] with dense rows on "
                          f"CUDA device {device}, got {t.dtype} {list(t.shape)} on {t.device}")
-    return t.stride(0) if rows > 1 else max(t.stride(0), heads * hd)
+    return t.stride(0) if rows > 1 else heads * hd
 
 
 def _workspace_bytes(workspace, device: int) -> int:

@@ -198,6 +198,11 @@ HEADS = [  # nq, nkv, hd, rows, rot, interleaved, weights, farthest position
 IDS = [str(h) for h in HEADS]
 
 
+def _randn(*shape):
+    x = np.random.default_rng(sum(shape)).standard_normal(shape).astype(np.float32)
+    return torch.from_numpy(x).to(torch.bfloat16).cuda()
+
+
 class Heads:
     def __init__(self, nq, nkv, hd, rows, rot, interleaved, weights, far, seed=0, fused=True, pad=0):
         rng = np.random.default_rng(seed + hd + rows)
@@ -423,6 +428,76 @@ def test_append_reports_slots_outside_the_pool_and_nan_rows(fmt):
         assert set(changed) <= {5, last - 1}
 
 
+@pytest.mark.parametrize("nq,nkv,hd,rows,fmt", [(9, 1, 128, 7700, None), (2, 1, 256, 7400, None), (4, 2, 256, 7999, "e2m1"),
+                                                (32, 2, 256, 7300, "bf16"), (6, 3, 128, 8000, "e4m3")], ids=str)
+def test_many_rows_are_those_of_fewer_at_once(nq, nkv, hd, rows, fmt):
+    """The same bits as calls of at most 2000 rows, which are dealt to the GPU in
+    another way, with rows left out in both."""
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    qkv = torch.randn(rows, nq + 2 * nkv, hd, generator=gen, device="cuda").to(torch.bfloat16)
+    x = qkv.split([nq, nkv, nkv], 1)
+    pos = torch.randint(0, 2 ** 31 - 1, (rows,), generator=gen, device="cuda").int()
+    pos[3::97] = -1
+    w = torch.rand(hd, generator=gen, device="cuda") + 0.5
+    nr = cp.NormRope(1e4 ** (-np.arange(hd // 2) / (hd // 2)), w, w)
+    ctx = cp.Context(nq, nkv, hd, 1, 1, 1)
+    slots = torch.randperm(rows, generator=gen, device="cuda").int()
+    got = []
+    for size in (rows, 2000):
+        q = torch.zeros(rows, nq, hd, dtype=torch.bfloat16, device="cuda")
+        k = torch.zeros(rows, nkv, hd, dtype=torch.bfloat16, device="cuda")
+        c = None if fmt is None else _paged(fmt, nkv, hd, 64, [rows], seed=1).upload()
+        for a in range(0, rows, size):
+            part = slice(a, a + size)
+            if c is None:
+                ctx.norm_rope(nr, pos[part], x[0][part], x[1][part], q[part], k[part])
+            else:
+                ctx.norm_rope_write_kv(nr, c.kv, pos[part], slots[part], *(y[part] for y in x), q[part])
+        _ok(ctx)
+        got.append([q, k] if c is None else [q] + [b.t for b in c.d_pools + (c.d_scales or [])])
+    for a, b in zip(*got):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    ref, size = oracle.norm_rope_ref(x[0][-40:].double().cpu().numpy(), pos[-40:].tolist(),
+                                     1e4 ** (-np.arange(hd // 2) / (hd // 2)), w.double().cpu().numpy())
+    skip = np.flatnonzero(pos[-40:].cpu().numpy() < 0)
+    _check_bf16(oracle.bf16_bits(got[0][0][-40:].cpu()), ref, size, skip)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_append_offsets_beyond_32_bits(fmt):
+    """Rows 2^29 elements apart, and pools of more than 2^32 bytes whose last pages are used:
+    the bits of a call on dense rows and a small pool."""
+    nq, nkv, hd, rows, apart = 4, 2, 256, 6, 2 ** 29
+    wide = nq + 2 * nkv
+    far = torch.empty((rows - 1) * apart + wide * hd, dtype=torch.bfloat16, device="cuda")
+    far = far.as_strided((rows, wide, hd), (apart, hd, 1))
+    qkv = _randn(rows, wide, hd)
+    far.copy_(qkv)
+    pages, tail = (140000 if fmt == "e4m3" else 70000), 4
+    dt = torch.float8_e4m3fn if fmt == "e4m3" else torch.bfloat16
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+
+    def cache(n):
+        pools = [torch.empty(n, nkv, 64, hd, dtype=dt, device="cuda") for _ in range(2)]
+        scales = [torch.empty(n, nkv, 64, device="cuda") for _ in range(2)] if fmt == "e4m3" else []
+        for x in pools + scales:
+            x[-tail:].view(torch.uint8).zero_()
+        return pools + scales, cp.PagedKV(*pools, table, *scales)
+
+    nr = cp.NormRope(1e4 ** (-np.arange(128) / 128))
+    ctx = cp.Context(nq, nkv, hd, 1, 1, 1)
+    pos, at, got = i32([0, 5, 9, 70000, 2 ** 31 - 1, 3]), torch.tensor([255, 0, 77, 128, 9, 200]), []
+    for x, n in ((qkv, tail), (far, pages)):
+        held, kv = cache(n)
+        q = torch.zeros(rows, nq, hd, dtype=torch.bfloat16, device="cuda")
+        q = x[:, :nq] if n == pages else q                # (in place, far apart)
+        ctx.norm_rope_write_kv(nr, kv, pos, i32((at + (n - tail) * 64).tolist()), *x.split([nq, nkv, nkv], 1), q)
+        _ok(ctx)
+        got.append([q.contiguous()] + [y[-tail:].contiguous().clone() for y in held])
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) and a.view(torch.uint8).any()
+
+
 # ------------------------------------------------------- the step as a whole
 
 @FORMATS
@@ -614,6 +689,8 @@ def test_binding_refuses_wrong_tensors():
         other.norm_rope(**good)
     with pytest.raises(ValueError):
         h.ctx.norm_rope_write_kv(h.nr, c.kv, h.d_pos.t, i32([1, 2]), *h.d, out)
+    one = _randn(1, 4 * 128 + 4).as_strided((1, 4, 128), (4 * 128 + 4, 128, 1))
+    h.ctx.norm_rope(h.nr, i32([1]), one, one[:, :2], out[:1], ko[:1])       # one row: its stride says nothing
     none = torch.zeros(0, 4, 128, dtype=torch.bfloat16, device="cuda")
     h.ctx.norm_rope(h.nr, i32([]), none, none[:, :2], none, none[:, :2])    # no rows: nothing to do
     p = Plan([3], 16, 2, 2)
