@@ -221,6 +221,38 @@ __device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, Pack
 // divisor's reciprocal: by Markstein's theorem (IBM J. Res. Dev. 34, 1990), with f
 // the reciprocal of d rounded to nearest and q = a f rounded, the remainder a - q d
 // is exact in one fused step, and q + (a - q d) f rounds to a / d correctly.
+struct Scales4 {
+  float s;            // of the row
+  uint32_t r;         // of the lane's group
+  f32x2 inv_s, f, d;  // 1 / s, 1 / r_g (0 where r_g is), -r_g
+};
+// mag: the bits of the group's largest magnitude, row: of the row's.
+__device__ __forceinline__ Scales4 scales4(uint32_t mag, uint32_t row) {
+  const bool fine = row < 0x7F800000u;
+  const uint32_t e = fine ? max(row >> 23, 10u) : 10u;      // exponent field of amax
+  const float inv_s = __uint_as_float((263u - e) << 23);    // 2^(9 - k), k = e - 127
+  const float a = __uint_as_float(mag) * inv_s, a6 = a * (1.f / 6.f);
+  Scales4 y;
+  y.r = pack_e4m3x2(fmaf(fmaf(-a6, 6.f, a), 1.f / 6.f, a6), 0.f) & 0xFFu;
+  if (!fine) y.r = 0u;
+  // 1 / r_g to nearest: one of Newton's steps from the approximation, whose error it
+  // squares; r_g has 4 bits, so no quotient is that close to two floats' middle.
+  const float rf = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(y.r))).x;
+  float f;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(rf));
+  f = fmaf(fmaf(-rf, f, 1.f), f, f);
+  if (y.r == 0u) f = 0.f;
+  y.s = fine ? __uint_as_float((e - 9u) << 23) : __uint_as_float(0x7FC00000u);
+  y.inv_s = pair_of(inv_s, inv_s);
+  y.f = pair_of(f, f);
+  y.d = pair_of(-rf, -rf);
+  return y;
+}
+__device__ __forceinline__ float2 quotients4(f32x2 x, const Scales4& c) {
+  const f32x2 v = mul2(x, c.inv_s), p = mul2(v, c.f);
+  return split(fma2(fma2(p, c.d, v), c.f, p));
+}
+
 template <int HD>
 __device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, PackedRow<kE2m1>& y) {
   mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
@@ -228,26 +260,18 @@ __device__ __forceinline__ void quantise(const float (&x)[8], uint32_t mag, Pack
   uint32_t row = mag;
 #pragma unroll
   for (int o = HD / 16; o >= 4; o >>= 1) row = max(row, __shfl_xor_sync(0xFFFFFFFFu, row, o));
-  const bool fine = row < 0x7F800000u;
-  const uint32_t e = fine ? max(row >> 23, 10u) : 10u;      // exponent field of amax
-  const float inv_s = __uint_as_float((263u - e) << 23);    // 2^(9 - k), k = e - 127
-  const float a = __uint_as_float(mag) * inv_s, a6 = a * (1.f / 6.f);
-  uint32_t r = pack_e4m3x2(fmaf(fmaf(-a6, 6.f, a), 1.f / 6.f, a6), 0.f) & 0xFFu;
-  if (!fine) r = 0u;
-  const float rf = f16x2_to_f32x2(e4m3x2_to_f16x2(static_cast<uint16_t>(r))).x;
-  const float f = r != 0u ? __frcp_rn(rf) : 0.f;
-  const f32x2 s2 = pair_of(inv_s, inv_s), f2 = pair_of(f, f), d2 = pair_of(-rf, -rf);
+  const Scales4 c = scales4(mag, row);
   float q[8];
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    const f32x2 v = mul2(pair_of(x[j], x[j + 1]), s2), p = mul2(v, f2);
-    const float2 z = split(fma2(fma2(p, d2, v), f2, p));
+    const float2 z = quotients4(pair_of(x[j], x[j + 1]), c);
     q[j] = z.x;
     q[j + 1] = z.y;
   }
-  y.x = r != 0u ? pack_e2m1x8(q) : 0u;
-  y.s = fine ? __uint_as_float((e - 9u) << 23) : __uint_as_float(0x7FC00000u);
+  y.x = c.r != 0u ? pack_e2m1x8(q) : 0u;
+  y.s = c.s;
   // The record's words: four r_g each.
+  uint32_t r = c.r;
   r |= __shfl_down_sync(0xFFFFFFFFu, r, 4) << 8;
   r |= __shfl_down_sync(0xFFFFFFFFu, r, 8) << 16;
   y.r = r;
@@ -414,18 +438,113 @@ __global__ void __launch_bounds__(256)
                   make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
               if (vec == 0) (is_k ? p.pool.k_scales : p.pool.v_scales)[dst] = amax / kE4m3Max;
             }
-          } else if constexpr (FMT == kE2m1) {
-            float f[8];
-            bf16x8_to_f32x8(x[r][l], f);
-            PackedRow<FMT> y;
-            quantise<HD>(f, amax_bits(x[r][l]) << 16, y);
-            if (place[r] >= 0) store_row<HD>(p.pool, is_k, dst, vec, y);
           } else {
             if (place[r] >= 0) reinterpret_cast<uint4*>(pool)[dst * VECS + vec] = x[r][l];
           }
         }
       }
     }
+  }
+}
+
+// The write to e2m1 pages.  The arithmetic of 8 values is 33 instructions, but that
+// of their row's and group's scales, their place and their record some 80 for a
+// lane that has no more than 8 of them.  So a lane takes 16, half a group: a row
+// lies in HD / 16 lanes, and a warp has a row's K and V side by side, at HD = 128
+// two rows' (write4_at_once).  As many blocks as the SMs hold (write4_blocks) go
+// through the rows, and load the next ones before they quantise these: many rows by
+// two, few at HD = 256 by one.
+//   28672 tokens of 2 heads of 256: 17.6 us for 75 MB, 4.2 TB/s; 17421 tokens of 4
+// heads of 128: 12.8 us for 46 MB, 3.6 TB/s (8 values a lane: 22.8 and 15.7; blocks
+// in waves, as above: 19.6 and 13.1; four rows of 256 with two blocks per SM: 17.5).
+// Bound by instructions and by the look-ups, three dependent loads for two rows.
+__host__ __device__ constexpr int write4_at_once(int hd) { return 256 / hd; }
+__host__ __device__ constexpr int write4_blocks(int hd, int rows) { return hd * rows > 256 ? 3 : 4; }
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(256, write4_blocks(HD, ROWS))
+    paged_write4_kernel(const __grid_constant__ PagedWriteParams p) {
+  constexpr int LANES = HD / 16, AT_ONCE = write4_at_once(HD), STEPS = ROWS / AT_ONCE;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, l = lane % LANES;
+  const bool is_k = (lane / LANES & 1) == 0;
+  const int own = lane / (2 * LANES);  // row of a step's
+  const int nkv = p.pool.nkv;
+  const int groups = (nkv + p.heads_per_item - 1) / p.heads_per_item;
+  const long long items = static_cast<long long>((p.rows + ROWS - 1) / ROWS) * groups;
+  const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+  const uint4* from = is_k ? p.k_new : p.v_new;
+  uint2* codes = static_cast<uint2*>(is_k ? p.pool.k : p.pool.v);
+  uint32_t* records = reinterpret_cast<uint32_t*>(is_k ? p.pool.k_scales : p.pool.v_scales);
+  uint4 x[STEPS][2], y[STEPS][2];
+  auto load = [&](int row0, int g) {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int row = min(row0 + i * AT_ONCE + own, p.rows - 1);
+      const uint4* src = from + (static_cast<long long>(row) * nkv + g) * (HD / 8) + 2 * l;
+      y[i][0] = load_now(src);
+      y[i][1] = load_now(src + 1);
+    }
+  };
+  long long it = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (it >= items) return;
+  int row0 = static_cast<int>(it / groups) * ROWS, g0 = static_cast<int>(it % groups) * p.heads_per_item;
+  load(row0, g0);
+  while (true) {
+    const int g1 = min(nkv, g0 + p.heads_per_item);
+    const int seq = p.row_starts != nullptr ? write_seq(p, row0, lane) : 0;
+    const int row = row0 + lane;
+    const long long mine =
+        lane < ROWS ? write_place(p, row, p.row_starts != nullptr ? seq : row) : -1;
+    long long place[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) place[i] = __shfl_sync(0xFFFFFFFFu, mine, i * AT_ONCE + own);
+    it += warps;
+    for (int g = g0; g < g1; ++g) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        x[i][0] = y[i][0];
+        x[i][1] = y[i][1];
+      }
+      if (g + 1 < g1) {
+        load(row0, g + 1);
+      } else if (it < items) {
+        row0 = static_cast<int>(it / groups) * ROWS;
+        g0 = static_cast<int>(it % groups) * p.heads_per_item;
+        load(row0, g0);
+      }
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
+                               x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+        uint32_t mag = max(amax_bits(x[i][0]), amax_bits(x[i][1])) << 16;
+        mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
+        uint32_t all = mag;
+#pragma unroll
+        for (int o = LANES / 2; o >= 2; o >>= 1) all = max(all, __shfl_xor_sync(0xFFFFFFFFu, all, o));
+        const Scales4 c = scales4(mag, all);
+        float q[2][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 v = quotients4(bf16x2_to_f32x2(w[j]), c);
+          q[j >> 2][2 * (j & 3)] = v.x;
+          q[j >> 2][2 * (j & 3) + 1] = v.y;
+        }
+        const bool some = c.r != 0u;
+        const uint2 z = make_uint2(some ? pack_e2m1x8(q[0]) : 0u, some ? pack_e2m1x8(q[1]) : 0u);
+        uint32_t r = c.r;
+        r |= __shfl_down_sync(0xFFFFFFFFu, r, 2) << 8;
+        r |= __shfl_down_sync(0xFFFFFFFFu, r, 4) << 16;
+        if (place[i] < 0) continue;
+        const long long dst =
+            pool_row(p.pool, static_cast<int>(place[i] >> 8), g, static_cast<int>(place[i] & 255));
+        codes[dst * LANES + l] = z;
+        uint32_t* rec = records + dst * (record_bytes(HD) / 4);
+        if (l == 0) rec[0] = __float_as_uint(c.s);
+        if ((l & 7) == 0) rec[1 + l / 8] = r;
+      }
+    }
+    if (it >= items) break;
   }
 }
 

@@ -88,21 +88,24 @@ cpattn_status launch_dependent(cpattn_ctx* ctx, void (*kernel)(Params), dim3 gri
    : (format) == CPATTN_PAGES_E4M3 ? kernel<__VA_ARGS__, cpattn::kE4m3> \
                                    : kernel<__VA_ARGS__, cpattn::kE2m1>)
 
-// Rows that a warp of the write takes, of the 1 or 4 that the number of rows asks
-// for: e2m1 of head_dim 256 has two instead of four, which leave registers for more
-// warps (28672 tokens of 2 heads 22.9 us, by four 28.3).
-constexpr int write_rows(int head_dim, int format, int rows) {
-  return format == CPATTN_PAGES_E2M1 && head_dim == 256 ? std::min(rows, 2) : rows;
+// Rows that a warp of the write takes: of many four, or two in e2m1 pages, of few one,
+// or as many as it has side by side.
+int write_rows(const cpattn_ctx* ctx, int format, bool many) {
+  if (format != CPATTN_PAGES_E2M1) return many ? 4 : 1;
+  return many ? 2 : cpattn::write4_at_once(ctx->cfg.head_dim);
 }
-template <int ROWS>
+template <bool MANY>
 cpattn_status launch_paged_write(cpattn_ctx* ctx, const cpattn::PagedWriteParams& p, int format,
                                  int grid, cudaStream_t st) {
-  constexpr int PACKED = write_rows(256, CPATTN_PAGES_E2M1, ROWS);
+  constexpr int ROWS = MANY ? 4 : 1, ROWS4 = MANY ? 2 : 1;  // (two rows of 128 are side by side)
   const auto kernel =
-      ctx->cfg.head_dim == 128           ? CPATTN_BY_FORMAT(cpattn::paged_write_kernel, format, 128, ROWS)
-      : format == CPATTN_PAGES_E2M1      ? cpattn::paged_write_kernel<256, PACKED, cpattn::kE2m1>
-      : format == CPATTN_PAGES_E4M3      ? cpattn::paged_write_kernel<256, ROWS, cpattn::kE4m3>
-                                         : cpattn::paged_write_kernel<256, ROWS, cpattn::kBf16>;
+      ctx->cfg.head_dim == 128
+          ? (format == CPATTN_PAGES_BF16   ? cpattn::paged_write_kernel<128, ROWS, cpattn::kBf16>
+             : format == CPATTN_PAGES_E4M3 ? cpattn::paged_write_kernel<128, ROWS, cpattn::kE4m3>
+                                           : cpattn::paged_write4_kernel<128, 2>)
+          : (format == CPATTN_PAGES_BF16   ? cpattn::paged_write_kernel<256, ROWS, cpattn::kBf16>
+             : format == CPATTN_PAGES_E4M3 ? cpattn::paged_write_kernel<256, ROWS, cpattn::kE4m3>
+                                           : cpattn::paged_write4_kernel<256, ROWS4>);
   return launch_dependent(ctx, kernel, dim3(grid), 256, 0, st, p, "paged write launch");
 }
 
@@ -214,17 +217,19 @@ cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, 
   p.status = ctx->d_status;
   p.num_seqs = num_seqs;
   p.rows = num_rows;
-  // Four rows a warp where that leaves 16 warps per SM, else one (the same
+  // Several rows a warp where four leave 16 warps per SM, else one (the same
   // write: 22.5 us by single rows, 19.7 by four).
   const bool many = static_cast<long long>(num_rows) * ctx->cfg.num_kv_heads >=
                     4LL * 16 * std::max(ctx->num_sms, 1);
-  const int per = write_rows(ctx->cfg.head_dim, pages->format, many ? 4 : 1);
+  const int per = write_rows(ctx, pages->format, many);
   const long long units = (static_cast<long long>(num_rows) + per - 1) / per;
   p.heads_per_item = heads_per_item(ctx, units);
-  const int grid = copy_grid(ctx, units, p.heads_per_item);
+  int grid = copy_grid(ctx, units, p.heads_per_item);
+  if (pages->format == CPATTN_PAGES_E2M1)
+    grid = std::min(grid, std::max(ctx->num_sms, 1) * cpattn::write4_blocks(ctx->cfg.head_dim, per));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return per > 1 ? launch_paged_write<4>(ctx, p, pages->format, grid, st)
-                 : launch_paged_write<1>(ctx, p, pages->format, grid, st);
+  return many ? launch_paged_write<true>(ctx, p, pages->format, grid, st)
+              : launch_paged_write<false>(ctx, p, pages->format, grid, st);
 } catch (...) {
   return CPATTN_E_NOMEM;
 }
