@@ -103,7 +103,7 @@ class PagedKV:
             raise ValueError("pages, scales and block_table must be on one CUDA device")
         self.k_pages, self.v_pages, self.block_table = k_pages, v_pages, block_table
         self.k_scales, self.v_scales = k_scales, v_scales
-        self.device = k_pages.get_device()
+        self.device, self.i32 = k_pages.get_device(), torch.int32
         self.num_seqs, cols = block_table.shape
         self.num_kv_heads, self.head_dim = k_pages.shape[1], hd
         self.c = Pages(fmt, k_pages.shape[2], k_pages.shape[0], cols,
@@ -152,6 +152,7 @@ class NormRope:
             raise ValueError("weights and device must be the same CUDA device")
         self.device = held[0].get_device() if held else torch.device(device).index
         self.head_dim = weights[0].numel() if weights else None
+        self.types = torch.bfloat16, torch.int32  # of heads and of positions
         f32 = bool(weights) and weights[0].dtype is torch.float32
         self.c = NormRopeDesc(_ptr(q_weight), _ptr(k_weight), _ptr(self.steps), int(f32),
                               self.rotary_dim, int(bool(interleaved)), float(eps), float(scale))
@@ -259,28 +260,28 @@ def _want(name, t, dtype, shape, device: int):
                          f"{device}, got {t.dtype} {list(t.shape)} on {t.device}")
 
 
-def _i32_ptrs(names, device: int, *tensors_and_sizes):
+def _i32_ptrs(i32, names, device: int, *tensors_and_sizes):
     """Device pointers of contiguous int32 vectors on CUDA device `device`: tensor,
-    size, tensor, size .. (each of `names`)."""
-    import torch
-    i32, out = torch.int32, []
-    for i in range(0, len(tensors_and_sizes), 2):
-        t, n = tensors_and_sizes[i], tensors_and_sizes[i + 1]
+    size, tensor, size .. (each of `names`).  i32: torch.int32."""
+    out = []
+    sizes = iter(tensors_and_sizes)
+    for t in sizes:
+        n = next(sizes)
         if t.dtype is not i32 or t.numel() != n or t.dim() != 1 or t.get_device() != device \
                 or not t.is_contiguous():
-            _want(names.split()[i // 2], t, i32, (n,), device)
+            _want(names.split()[len(out)], t, i32, (n,), device)
         out.append(t.data_ptr())
     return out
 
 
-def _want_rows(name, t, rows: int, heads: int, hd: int, device: int) -> int:
+def _want_rows(name, t, rows: int, heads: int, hd: int, device: int, bf16) -> int:
     """The row stride of a bf16 CUDA tensor [rows, heads, hd] whose rows are dense."""
-    import torch
-    if t.dtype is not torch.bfloat16 or t.shape != (rows, heads, hd) or t.get_device() != device \
-            or device < 0 or (t.numel() > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != hd))):
-        raise ValueError(f"{name}: expected a bfloat16 tensor [{rows}, {heads}, {hd}] with dense rows on "
-                         f"CUDA device {device}, got {t.dtype} {list(t.shape)} on {t.device}")
-    return t.stride(0) if rows > 1 else heads * hd
+    if t.dtype is bf16 and t.shape == (rows, heads, hd) and t.get_device() == device >= 0:
+        at, head, value = t.stride()
+        if value == 1 and (head == hd or heads == 1) or rows == 0:
+            return at if rows > 1 else heads * hd
+    raise ValueError(f"{name}: expected a bfloat16 tensor [{rows}, {heads}, {hd}] with dense rows on "
+                     f"CUDA device {device}, got {t.dtype} {list(t.shape)} on {t.device}")
 
 
 def _workspace_bytes(workspace, device: int) -> int:
@@ -532,7 +533,7 @@ class Context:
         b, dev, rows = pages.num_seqs, pages.device, positions.numel()
         self._check_pages(pages)
         have, new, free, count, out, starts, pos, at = _i32_ptrs(
-            "cache_lens new_lens free_pages free_count lens row_starts positions slots", dev, cache_lens, b,
+            pages.i32, "cache_lens new_lens free_pages free_count lens row_starts positions slots", dev, cache_lens, b,
             new_lens, b, free_pages, pages.c.num_pages, free_count, 1, lens, b, row_starts, b + 1,
             positions, rows, slots, rows)
         self._check(self.lib.cpattn_paged_plan(self._h, pages.ref, b, rows, have, new, free, count, out,
@@ -543,8 +544,8 @@ class Context:
         keep[b] tokens, of the lens[b] it holds (0: all of them; < 0: none)."""
         b, dev = pages.num_seqs, pages.device
         self._check_pages(pages)
-        have, left, free, count = _i32_ptrs("lens keep free_pages free_count", dev, lens, b, keep, b,
-                                            free_pages, pages.c.num_pages, free_count, 1)
+        have, left, free, count = _i32_ptrs(pages.i32, "lens keep free_pages free_count", dev, lens, b,
+                                            keep, b, free_pages, pages.c.num_pages, free_count, 1)
         self._check(self.lib.cpattn_paged_trim(self._h, pages.ref, b, have, left, free, count,
                                                _stream_on(stream, dev)))
 
@@ -553,41 +554,40 @@ class Context:
         rows may lie apart, as in a projection's output) into q_out and k_out, which
         may be q and k.  positions: int32 [rows]; < 0: the row is left alone."""
         rows, nq, nkv, hd, dev = self._check_norm_rope(nr, positions)
-        args = []
-        for name, t, heads in (("q", q, nq), ("k", k, nkv), ("q_out", q_out, nq), ("k_out", k_out, nkv)):
-            args += [t.data_ptr(), _want_rows(name, t, rows, heads, hd, dev)]
+        bf16, _ = nr.types
+        at = _want_rows("q", q, rows, nq, hd, dev, bf16), _want_rows("k", k, rows, nkv, hd, dev, bf16), \
+            _want_rows("q_out", q_out, rows, nq, hd, dev, bf16), _want_rows("k_out", k_out, rows, nkv, hd, dev, bf16)
         if rows:
-            self._check(self.lib.cpattn_norm_rope(self._h, nr.ref, rows, positions.data_ptr(), *args,
-                                                  _stream_on(stream, dev)))
+            self._check(self.lib.cpattn_norm_rope(
+                self._h, nr.ref, rows, positions.data_ptr(), q.data_ptr(), at[0], k.data_ptr(), at[1],
+                q_out.data_ptr(), at[2], k_out.data_ptr(), at[3], _stream_on(stream, dev)))
 
     def norm_rope_write_kv(self, nr: NormRope, pages: PagedKV, positions, slots, q, k, v, q_out,
                            stream=None):
         """The same, with K and V [rows, NKV, HD] going straight into their pages: row r
         to slots[r] = page * page_size + slot (int32, from paged_plan; < 0: not stored)."""
-        import torch
         rows, nq, nkv, hd, dev = self._check_norm_rope(nr, positions)
+        bf16, i32 = nr.types
         self._check_pages(pages)
-        _want("slots", slots, torch.int32, (rows,), dev)
+        _want("slots", slots, i32, (rows,), dev)
         if pages.device != dev:
             raise ValueError("pages and positions must be on one CUDA device")
-        args = []
-        for name, t, heads in (("q", q, nq), ("k", k, nkv), ("v", v, nkv), ("q_out", q_out, nq)):
-            args += [t.data_ptr(), _want_rows(name, t, rows, heads, hd, dev)]
+        at = _want_rows("q", q, rows, nq, hd, dev, bf16), _want_rows("k", k, rows, nkv, hd, dev, bf16), \
+            _want_rows("v", v, rows, nkv, hd, dev, bf16), _want_rows("q_out", q_out, rows, nq, hd, dev, bf16)
         if rows:
             self._check(self.lib.cpattn_norm_rope_write_kv(
-                self._h, nr.ref, pages.ref, rows, positions.data_ptr(), slots.data_ptr(), *args,
-                _stream_on(stream, dev)))
+                self._h, nr.ref, pages.ref, rows, positions.data_ptr(), slots.data_ptr(), q.data_ptr(), at[0],
+                k.data_ptr(), at[1], v.data_ptr(), at[2], q_out.data_ptr(), at[3], _stream_on(stream, dev)))
 
     def _check_norm_rope(self, nr: NormRope, positions):
-        import torch
         nq, nkv, hd = self.dims
-        dev = positions.get_device()
-        _want("positions", positions, torch.int32, (positions.numel(),), dev)
+        rows, dev = positions.numel(), positions.get_device()
+        _want("positions", positions, nr.types[1], (rows,), dev)
         if nr.device != dev:
             raise ValueError("the norm's weights and positions must be on one CUDA device")
         if nr.head_dim not in (None, hd):
             raise ValueError(f"norm weights of {nr.head_dim} values, the context's heads have {hd}")
-        return positions.numel(), nq, nkv, hd, dev
+        return rows, nq, nkv, hd, dev
 
     def _check_pages(self, pages: PagedKV):
         if pages.num_kv_heads != self.dims[1] or pages.head_dim != self.dims[2]:

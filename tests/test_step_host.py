@@ -163,7 +163,7 @@ def test_binding_checks_tensors():
         with pytest.raises(ValueError):
             cp.NormRope(**kw)
     with pytest.raises(ValueError):
-        binding._want_rows("q", torch.zeros(2, 3, 128, dtype=torch.bfloat16), 2, 3, 128, -1)
+        binding._want_rows("q", torch.zeros(2, 3, 128, dtype=torch.bfloat16), 2, 3, 128, -1, torch.bfloat16)
 
 
 # ------------------------------------------------------------------ oracle pins
