@@ -85,17 +85,19 @@
 // CTAs that end apart (9 or 10 to a row of the first case).  While tiles flow,
 // bf16 is bound by DRAM, and e4m3 by the latency of conversions and products
 // in 8 warps (a quarter of the issue slots is used).
-//   e2m1: 1 x 126977, 32 q heads on 2 of 256: 38.8 us for 71 MB (1.8 TB/s, 27 %), 8 on
-// 2: 30.0; 64 ragged, 32 on 4 of 128: 50.2 us for 150 MB (3.0 TB/s, 44 %), 16 on 2 of
-// 256: 45.8; 8 x 32768, 32 on 2 of 256: 63.8, 32 on 4 of 128: 48.3; 1 x 500, 8 on 2 of
-// 128: 7.8.  Half of e4m3's bytes take as many conversions and products and more
+//   e2m1: 1 x 126977, 32 q heads on 2 of 256: 38.7 us for 71 MB (1.8 TB/s, 27 %), 8 on
+// 2: 29.5; 64 ragged, 32 on 4 of 128: 49.5 us for 150 MB (3.0 TB/s, 45 %), 16 on 2 of
+// 256: 46.4; 8 x 32768, 32 on 2 of 256: 63.7, 32 on 4 of 128: 47.6; 1 x 500, 8 on 2 of
+// 128: 7.7.  Half of e4m3's bytes take as many conversions and products and more
 // scales: 2.8 instructions per value and lane (8 x 32768 of 128: 1464 per tile of
 // 64 tokens, 256 of them conversions), of which 40 to 47 % of the issue slots are
 // used.  So it is bound by instructions and their latency, and a cache of 4 bits
 // saves more memory than time.  (16 warps that share a tile of 256 or 512 tokens,
 // each with 32 columns of O, P and one barrier per tile between them: 37.2 us and
 // 51.0 for the first and the last but one case, but 90 us for the 64 ragged ones,
-// whose many small copies one warp then has to send.)
+// whose many small copies one warp then has to send.  V's r_g as fp16 once per tile,
+// through shared memory, 70 instructions fewer for each: 50.0 for the 64 ragged, 64.2
+// for 8 x 32768 of 256, no faster.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -1025,10 +1027,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
                 float part[4];
                 mma16816<true, true>(part, a0, qf[2 * j][2 * nb], qf[2 * j][2 * nb + 1]);
                 mma16816<true>(part, a1, qf[2 * j + 1][2 * nb], qf[2 * j + 1][2 * nb + 1]);
-                c[t][nb][0] = fmaf(part[0], f0, c[t][nb][0]);
-                c[t][nb][1] = fmaf(part[1], f0, c[t][nb][1]);
-                c[t][nb][2] = fmaf(part[2], f8, c[t][nb][2]);
-                c[t][nb][3] = fmaf(part[3], f8, c[t][nb][3]);
+                fma_pair(part[0], part[1], pair_of(f0, f0), pair_of(c[t][nb][0], c[t][nb][1]), c[t][nb][0], c[t][nb][1]);
+                fma_pair(part[2], part[3], pair_of(f8, f8), pair_of(c[t][nb][2], c[t][nb][3]), c[t][nb][2], c[t][nb][3]);
               }
             }
           }
@@ -1087,9 +1087,17 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
               QUANT ? *reinterpret_cast<const float*>(k_rec + token_of(t, i) * Ly::REC) : 1.f;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (QUANT) c[t][nb][2 * i + j] = (Q4 ? c[t][nb][2 * i + j] * 0x1p120f : c[t][nb][2 * i + j]) * ks;
+          {
+            float& c0 = c[t][nb][2 * i];
+            float& c1 = c[t][nb][2 * i + 1];
+            if constexpr (Q4) {
+              mul_pair(c0, c1, pair_of(0x1p120f, 0x1p120f));
+              mul_pair(c0, c1, pair_of(ks, ks));
+            } else if constexpr (QUANT) {
+              c0 *= ks;
+              c1 *= ks;
+            }
+          }
         }
       bool seen[MT][2];
       if (partial) {
@@ -1177,13 +1185,23 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
           for (int i = 0; i < 2; ++i) {
             float& e0 = c[t][nb][2 * i];
             float& e1 = c[t][nb][2 * i + 1];
-            e0 = ex2_approx(fmaf(e0, sl[nb][0], -m0));
-            e1 = ex2_approx(fmaf(e1, sl[nb][1], -m1));
-            l[nb][0] += e0;
-            l[nb][1] += e1;
+            if constexpr (Q4) {
+              fma_pair(e0, e1, pair_of(sl[nb][0], sl[nb][1]), pair_of(-m0, -m1), e0, e1);
+              e0 = ex2_approx(e0);
+              e1 = ex2_approx(e1);
+              add_pair(l[nb][0], l[nb][1], pair_of(e0, e1));
+              mul_pair(e0, e1, pair_of(vs[t][i], vs[t][i]));
+            } else {
+              e0 = ex2_approx(fmaf(e0, sl[nb][0], -m0));
+              e1 = ex2_approx(fmaf(e1, sl[nb][1], -m1));
+              l[nb][0] += e0;
+              l[nb][1] += e1;
+            }
             if constexpr (QUANT) {
-              e0 *= vs[t][i];
-              e1 *= vs[t][i];
+              if constexpr (!Q4) {
+                e0 *= vs[t][i];
+                e1 *= vs[t][i];
+              }
               wx[nb][0] = fmaxf(wx[nb][0], fabsf(e0));
               wx[nb][1] = fmaxf(wx[nb][1], fabsf(e1));
             }
@@ -1229,8 +1247,9 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
           for (int i = 0; i < 2; ++i) {
             const float e0 = c[t][nb][2 * i], e1 = c[t][nb][2 * i + 1];
             if constexpr (Q4) {
+              const float2 x = split(mul2(pair_of(e0, e1), pair_of(ps[nb][0], ps[nb][1])));
               *reinterpret_cast<uint32_t*>(p_rows + (nb * WT + 16 * t + 8 * i + r0) * 16 + 4 * quad) =
-                  pack_f16x2(e0 * ps[nb][0], e1 * ps[nb][1]);
+                  pack_f16x2(x.x, x.y);
             } else if constexpr (Q8) {
               ph[t][nb][i] = transpose8(pack_f16x2(e0 * ps[nb][0], e1 * ps[nb][1]));
             } else {
