@@ -89,10 +89,10 @@
 // 2: 29.5; 64 ragged, 32 on 4 of 128: 49.5 us for 150 MB (3.0 TB/s, 45 %), 16 on 2 of
 // 256: 46.4; 8 x 32768, 32 on 2 of 256: 63.7, 32 on 4 of 128: 47.6; 1 x 500, 8 on 2 of
 // 128: 7.7.  Half of e4m3's bytes take as many conversions and products and more
-// scales: 2.8 instructions per value and lane (8 x 32768 of 128: 1464 per tile of
-// 64 tokens, 256 of them conversions), of which 40 to 47 % of the issue slots are
-// used.  So it is bound by instructions and their latency, and a cache of 4 bits
-// saves more memory than time.  (16 warps that share a tile of 256 or 512 tokens,
+// scales: 2.7 instructions per value and lane (8 x 32768 of 128: 1393 per tile of
+// 64 tokens, 256 of them conversions), in 46 to 50 % of the issue slots.  So it is
+// bound by the latency of a warp's instructions, and a cache of 4 bits saves more
+// memory than time.  (16 warps that share a tile of 256 or 512 tokens,
 // each with 32 columns of O, P and one barrier per tile between them: 37.2 us and
 // 51.0 for the first and the last but one case, but 90 us for the 64 ragged ones,
 // whose many small copies one warp then has to send.  V's r_g as fp16 once per tile,
