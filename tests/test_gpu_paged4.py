@@ -89,6 +89,21 @@ def test_write_step_without_row_starts_and_skipped_sequences():
     assert c.intact()
 
 
+@pytest.mark.parametrize("hd", [128, 256])
+def test_write_step_of_the_largest_batches(hd):
+    """One token each for so many sequences that a warp takes two of them."""
+    rng = np.random.default_rng(10)
+    have = [int(n) for n in rng.choice([-1, 0, 5, 15, 16, 31], cp.MAX_PAGED_SEQS - 3)]
+    c = Paged4(3, hd, 16, [max(n, 0) + 1 for n in have]).upload()
+    new = [bf16_normal(rng, len(have), 3, hd) for _ in range(2)]
+    ctx = cp.Context(3, 3, hd, 1, 1, 1)
+    ctx.paged_write_kv(c.kv, i32(have), *(Buffer(x, torch.bfloat16).t for x in new))
+    _ok(ctx)
+    oracle.paged_write_ref(c.pools, c.scales, c.table, 16, have, np.arange(len(have) + 1), new)
+    c.check_pools()
+    assert c.intact()
+
+
 def test_write_beyond_the_table_and_bad_pages_are_reported():
     rng = np.random.default_rng(9)
     c = Paged4(2, 128, 16, [32, 32])
