@@ -132,10 +132,13 @@ __device__ __forceinline__ void as_values(const Pairs& y, float (&x)[8]) {
 // cos and sin of two angles, given in turns times 2^32 (modulo 2^32), times `scale`.
 __device__ __forceinline__ void cos_sin(uint32_t t0, uint32_t t1, float scale, f32x2* cs, f32x2* sn) {
   const uint32_t q0 = t0 + 0x20000000u, q1 = t1 + 0x20000000u;  // quarters: the upper two bits
-  constexpr float kUnit = 1.4629180792671596e-9f;               // 2 pi / 2^32
-  const f32x2 x = pair_of(static_cast<float>(static_cast<int>(t0 - (q0 & 0xC0000000u))) * kUnit,
-                          static_cast<float>(static_cast<int>(t1 - (q1 & 0xC0000000u))) * kUnit);
+  // 2 pi / 2^32, and what is left of it in fp32.
+  constexpr double kTurn = 6.283185307179586 / 4294967296.;
+  constexpr float kUnit = static_cast<float>(kTurn), kRest = static_cast<float>(kTurn - kUnit);
   auto both = [](float v) { return pair_of(v, v); };
+  const f32x2 n = pair_of(static_cast<float>(static_cast<int>(t0 - (q0 & 0xC0000000u))),
+                          static_cast<float>(static_cast<int>(t1 - (q1 & 0xC0000000u))));
+  const f32x2 x = fma2(n, both(kUnit), mul2(n, both(kRest)));
   const f32x2 z = mul2(x, x);
   f32x2 s = fma2(z, both(1.f / 362880.f), both(-1.f / 5040.f));
   s = fma2(z, s, both(1.f / 120.f));
