@@ -553,6 +553,22 @@ cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, 
                                     const void* v_new, void* stream);
 
 /*
+ * The same after cpattn_paged_plan: tokens from lens[b] on are left out.
+ *   lens         device int32 [B], the plan's; not the same array as cache_lens
+ * A plan's row_starts count the rows of sequences that it did not serve too, and
+ * their columns of the table are whatever was there: zeros of a fresh table, or
+ * pages that another sequence holds by now.  Their lens[b] is cache_lens[b], so
+ * this call writes none of them, where cpattn_paged_write_kv would write every one
+ * whose column names a page of the pool.
+ * One launch.  Errors: as cpattn_paged_write_kv.
+ */
+cpattn_status cpattn_paged_write_planned_kv(cpattn_ctx* ctx, const cpattn_pages* pages,
+                                            int32_t num_seqs, int32_t num_rows,
+                                            const int32_t* cache_lens, const int32_t* lens,
+                                            const int32_t* row_starts, const void* k_new,
+                                            const void* v_new, void* stream);
+
+/*
  * Read tokens first[b] .. lens[b]-1 of every sequence back from its pages
  * into the striped caches that cpattn_prefill takes:
  *   k_cache[b, g, t mod P, t div P, :] = value of token t, kv head g   (same for V)
@@ -610,7 +626,7 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
  * A serving step around the attention
  * -----------------------------------
  * plan (once per step), then in every layer norm_rope_write_kv and paged_decode
- * (or norm_rope, prefill_packed and paged_write_kv for whole prompts), and trim
+ * (or norm_rope, prefill_packed and paged_write_planned_kv for whole prompts), and trim
  * when requests end or drafted tokens are rejected.  All of it is captured and
  * replayed like the paged calls: lengths and lists are device arrays.
  */
@@ -630,7 +646,8 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
  *   lens         device int32 [B], out: cache_lens[b] + new_lens[b], or cache_lens[b]
  *                where the sequence is not served.  May be cache_lens.
  *   row_starts   device int32 [B+1], out: rows row_starts[b] .. row_starts[b+1] - 1 are
- *                the new tokens of sequence b
+ *                the new tokens of sequence b, served or not (see
+ *                cpattn_paged_write_planned_kv)
  *   positions    device int32 [num_rows], out: each row's position in its sequence
  *   slots        device int32 [num_rows], out: page * page_size + slot of each row
  * A row of nobody's (behind the last sequence's, or of one that is not served) gets

@@ -33,7 +33,7 @@ EXPORTS = ("cpattn_create", "cpattn_write_kv", "cpattn_prefill", "cpattn_sync_st
            "cpattn_set_barrier_counts", "cpattn_set_v_staging", "cpattn_v_staging_bytes",
            "cpattn_prefill_packed", "cpattn_prefill_packed_workspace", "cpattn_paged_write_kv",
            "cpattn_paged_read_kv", "cpattn_paged_decode", "cpattn_paged_decode_workspace",
-           "cpattn_paged_plan", "cpattn_paged_trim", "cpattn_rope_steps", "cpattn_norm_rope",
+           "cpattn_paged_write_planned_kv", "cpattn_paged_plan", "cpattn_paged_trim", "cpattn_rope_steps", "cpattn_norm_rope",
            "cpattn_norm_rope_write_kv")
 
 # cpattn_config.pairing values, by name.
@@ -224,6 +224,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                 ("cpattn_paged_decode", [P, PAGES, I32, P, P, P, P, P, U64, P])):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = I32
+    if hasattr(lib, "cpattn_paged_write_planned_kv"):
+        lib.cpattn_paged_write_planned_kv.argtypes = [P, PAGES, I32, I32] + [P] * 6
+        lib.cpattn_paged_write_planned_kv.restype = I32
     if hasattr(lib, "cpattn_paged_plan"):
         I64, NR = ctypes.c_int64, ctypes.POINTER(NormRopeDesc)
         for name, args in (
@@ -466,11 +469,14 @@ class Context:
             workspace.data_ptr(), _workspace_bytes(workspace, dev), _stream_on(stream, dev)))
 
     def paged_write_kv(self, pages: PagedKV, cache_lens, k_new, v_new, row_starts=None,
-                       stream=None):
-        """Write (for e4m3 pages: quantise) new tokens into their pages: rows
+                       stream=None, lens=None):
+        """Write (for e4m3 and e2m1 pages: quantise) new tokens into their pages: rows
         row_starts[b] .. row_starts[b + 1] - 1 of k_new and v_new [rows, NKV, HD]
         are the tokens of sequence b from cache_lens[b] on; row_starts None: one
-        token per sequence.  cache_lens and row_starts: int32 CUDA tensors."""
+        token per sequence.  lens: tokens from lens[b] on are left out -- after
+        paged_plan give it the plan's lens (another tensor than cache_lens then), or
+        sequences that the plan did not serve are written through whatever their rows
+        of the table hold.  cache_lens, row_starts and lens: int32 CUDA tensors."""
         import torch
         self._check_pages(pages)
         b, dev, rows = pages.num_seqs, pages.device, k_new.shape[0]
@@ -480,9 +486,13 @@ class Context:
         _want("cache_lens", cache_lens, torch.int32, (b,), dev)
         if row_starts is not None:
             _want("row_starts", row_starts, torch.int32, (b + 1,), dev)
-        self._check(self.lib.cpattn_paged_write_kv(
-            self._h, pages.ref, b, rows, cache_lens.data_ptr(), _ptr(row_starts), k_new.data_ptr(),
-            v_new.data_ptr(), _stream_on(stream, dev)))
+        given = _ptr(row_starts), k_new.data_ptr(), v_new.data_ptr(), _stream_on(stream, dev)
+        if lens is None:
+            self._check(self.lib.cpattn_paged_write_kv(self._h, pages.ref, b, rows, cache_lens.data_ptr(), *given))
+        else:
+            _want("lens", lens, torch.int32, (b,), dev)
+            self._check(self.lib.cpattn_paged_write_planned_kv(self._h, pages.ref, b, rows, cache_lens.data_ptr(),
+                                                               lens.data_ptr(), *given))
 
     def paged_read_kv(self, pages: PagedKV, lens, k_cache, v_cache, first=None, stream=None):
         """Read tokens first[b] (None: 0) .. lens[b] - 1 back into the striped

@@ -330,6 +330,7 @@ struct PagedWriteParams {
   const uint4* v_new;
   const int* cache_lens;  // [num_seqs]; < 0: the sequence is skipped
   const int* row_starts;  // [num_seqs + 1], or null: row b belongs to sequence b
+  const int* lens;        // [num_seqs] tokens from here on are left out, or null
   int* status;
   int num_seqs, rows;
   int heads_per_item;     // kv heads one warp takes of its rows
@@ -351,8 +352,8 @@ __device__ __forceinline__ int write_seq(const PagedWriteParams& p, int row, int
 }
 
 // Place of row `row` of the call in the pool: (page << 8) | slot, or -1: nobody's
-// (before the first sequence or behind the last one), a skipped sequence's, or
-// no page for it.  b: a sequence that starts at or before the row's own.
+// (before the first sequence or behind the last one), a skipped sequence's, one
+// from its length on, or no page for it.  b: a sequence that starts at or before the row's own.
 __device__ __forceinline__ long long write_place(const PagedWriteParams& p, int row, int b) {
   if (row >= p.rows) return -1;
   int i = 0;
@@ -367,8 +368,9 @@ __device__ __forceinline__ long long write_place(const PagedWriteParams& p, int 
     i = row - begin;
   }
   const int have = load_now(p.cache_lens + b);
-  if (have < 0) return -1;
+  const int len = p.lens != nullptr ? load_now(p.lens + b) : 0x7FFFFFFF;
   const long long t = static_cast<long long>(have) + i;
+  if (have < 0 || (t >= len && p.lens != nullptr)) return -1;
   const int page =
       page_id(p.pool, b, static_cast<int>(min(t >> p.pool.page_shift, 0x7FFFFFFFLL)), p.status);
   return page < 0 ? -1 : (static_cast<long long>(page) << 8) | (t & ((1 << p.pool.page_shift) - 1));

@@ -189,15 +189,11 @@ cpattn_status launch_decode(cpattn_ctx* ctx, const cpattn_pages* pages,
                           p->by_row ? cpattn::kJoinThreads : 256, 0, st, *p, "paged join launch");
 }
 
-}  // namespace
-
-extern "C" {
-
-cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
-                                    int32_t num_rows, const int32_t* cache_lens,
-                                    const int32_t* row_starts, const void* k_new,
-                                    const void* v_new, void* stream) try {
-  if (ctx == nullptr) return CPATTN_E_INVALID;
+// The write with (lens not NULL) or without a limit to each sequence's tokens.
+cpattn_status paged_write(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                          int32_t num_rows, const int32_t* cache_lens, const int32_t* lens,
+                          const int32_t* row_starts, const void* k_new, const void* v_new,
+                          void* stream) {
   cpattn::PagedWriteParams p;
   cpattn_status s = check_pages(ctx, pages, num_seqs, &p.pool);
   if (s != CPATTN_OK) return s;
@@ -207,13 +203,15 @@ cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, 
   if (num_rows == 0) return CPATTN_OK;
   if (cache_lens == nullptr || k_new == nullptr || v_new == nullptr)
     return fail(ctx, CPATTN_E_INVALID, "device pointers must not be NULL");
-  if (!aligned16(k_new) || !aligned16(v_new) || !aligned4(cache_lens) || !aligned4(row_starts))
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned4(cache_lens) || !aligned4(lens) ||
+      !aligned4(row_starts))
     return fail(ctx, CPATTN_E_INVALID, "k_new, v_new 16-byte, integer arrays 4-byte aligned");
   if (ctx->d_status == nullptr) return fail(ctx, CPATTN_E_CUDA, "no CUDA device");
   p.k_new = static_cast<const uint4*>(k_new);
   p.v_new = static_cast<const uint4*>(v_new);
   p.cache_lens = cache_lens;
   p.row_starts = row_starts;
+  p.lens = lens;
   p.status = ctx->d_status;
   p.num_seqs = num_seqs;
   p.rows = num_rows;
@@ -230,6 +228,30 @@ cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return many ? launch_paged_write<true>(ctx, p, pages->format, grid, st)
               : launch_paged_write<false>(ctx, p, pages->format, grid, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+cpattn_status cpattn_paged_write_kv(cpattn_ctx* ctx, const cpattn_pages* pages, int32_t num_seqs,
+                                    int32_t num_rows, const int32_t* cache_lens,
+                                    const int32_t* row_starts, const void* k_new,
+                                    const void* v_new, void* stream) try {
+  if (ctx == nullptr) return CPATTN_E_INVALID;
+  return paged_write(ctx, pages, num_seqs, num_rows, cache_lens, nullptr, row_starts, k_new, v_new, stream);
+} catch (...) {
+  return CPATTN_E_NOMEM;
+}
+
+cpattn_status cpattn_paged_write_planned_kv(cpattn_ctx* ctx, const cpattn_pages* pages,
+                                            int32_t num_seqs, int32_t num_rows,
+                                            const int32_t* cache_lens, const int32_t* lens,
+                                            const int32_t* row_starts, const void* k_new,
+                                            const void* v_new, void* stream) try {
+  if (ctx == nullptr) return CPATTN_E_INVALID;
+  if (lens == nullptr) return fail(ctx, CPATTN_E_INVALID, "lens must not be NULL");
+  return paged_write(ctx, pages, num_seqs, num_rows, cache_lens, lens, row_starts, k_new, v_new, stream);
 } catch (...) {
   return CPATTN_E_NOMEM;
 }

@@ -1,0 +1,69 @@
+"""Edges of the serving step and of 4-bit pages on the GPU: prompts written after a plan
+that did not serve everyone."""
+import numpy as np
+import pytest
+import torch
+
+import long_context_chunked_gb300 as cp
+import oracle
+from paged_helpers import Buffer, bf16_normal, i32
+from test_gpu_paged import _ok
+from test_gpu_step import FORMATS, _paged
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------- prompts written after a plan
+
+WAITING = [  # held, new, free pages, table columns in use (page 16)
+    ([33, 0, 0], [1, 100, 20], 3, 8),         # the second wants seven pages, and the third comes after it
+    ([17, 30, 0], [3, 99, 15], 20, 8),        # the second has no room in its row of the table
+    ([20, 5, -1], [12, 200, 9], 0, 16),       # nothing is free; the third place is empty
+]
+
+
+@FORMATS
+@pytest.mark.parametrize("case", range(len(WAITING)))
+def test_prompts_that_a_plan_did_not_serve_are_not_written(fmt, case):
+    """Block tables that begin as zeros: the columns that a sequence would have got name
+    page 0, which another one holds."""
+    held, new, spare, cols = WAITING[case]
+    rng = np.random.default_rng(case)
+    nkv, hd, page = 2, 128, 16
+    need = [-(-max(h, 0) // page) for h in held]
+    c = _paged(fmt, nkv, hd, page, [page * (sum(need) + spare)], spare_pages=0)
+    pages = c.pools[0].shape[0]
+    c.table, c.cols = np.zeros((len(held), cols), np.int32), cols
+    at = 0
+    for b, n in enumerate(need):                          # (page 0 is the first sequence's first)
+        c.table[b, :n] = np.arange(at, at + n)
+        at += n
+    c.fill(rng, np.maximum(held, 0))
+    c.upload()
+    free = list(range(at, pages))
+    stack = Buffer(np.array(free + [-9] * (pages - len(free)), np.int32), torch.int32)
+    rows = sum(n for h, n in zip(held, new) if h >= 0)
+    x = [bf16_normal(rng, rows, nkv, hd) for _ in range(2)]
+    d = [i32(v) for v in (held, new, [0] * 3, [0] * 4, [0] * rows, [0] * rows)]
+    ctx = cp.Context(2 * nkv, nkv, hd, 1, 1, 1)
+    ctx.paged_plan(c.kv, d[0], d[1], stack.t, i32([len(free)]), d[2], d[3], d[4], d[5])
+    ctx.paged_write_kv(c.kv, d[0], *(Buffer(v, torch.bfloat16).t for v in x), row_starts=d[3], lens=d[2])
+    assert ctx.sync_status() == cp.E_PAGE                 # (the plan's)
+    lens, starts, _, _, fine = oracle.plan_ref(held, new, free, c.table, page, rows)
+    assert not fine and d[2].tolist() == lens and d[3].tolist() == starts
+    for b, (h, n) in enumerate(zip(held, lens)):
+        if n > h >= 0:
+            part = [v[starts[b]:starts[b + 1]] for v in x]
+            oracle.paged_write_ref(c.pools, c.scales, c.table[b:], page, [h], [0, n - h], part)
+    c.check_pools()
+    assert c.intact()
+    # a step of a token each, without row_starts
+    step = [bf16_normal(rng, 3, nkv, hd) for _ in range(2)]
+    have = [max(n - 1, -1) for n in lens]                 # (the last token of each again)
+    upto = [n if b != 0 else n - 1 for b, n in enumerate(lens)]
+    ctx.paged_write_kv(c.kv, i32(have), *(Buffer(v, torch.bfloat16).t for v in step), lens=i32(upto))
+    _ok(ctx)
+    have[0] = -1
+    oracle.paged_write_ref(c.pools, c.scales, c.table, page, have, np.arange(4), step)
+    c.check_pools()
+    assert c.intact()
