@@ -598,9 +598,8 @@ cpattn_status cpattn_paged_read_kv(cpattn_ctx* ctx, const cpattn_pages* pages, i
  * row of e4m3 or e2m1 pages that held either is NaN.  For e4m3 pages a token's
  * probability times its V scale is rounded to fp16, with 11 bits where it is
  * at least 2^-20 of the largest such product of the q head, fewer below, and 0
- * below 2^-31.  For e2m1 pages the same is done with s, and the product times
- * r_g / 256 is rounded to fp16 once more.  A sequence without tokens (lens[b] <= 0) gets O = 0 and an LSE
- * of -infinity.
+ * below 2^-31.  For e2m1 pages the same is done with s; r_g adds no rounding.  A
+ * sequence without tokens (lens[b] <= 0) gets O = 0 and an LSE of -infinity.
  *   lens        device int32 [B], B in 1..CPATTN_MAX_PAGED_SEQS
  *   q, out      device bf16 [B, NQ, HD]
  *   lse         device fp32 [B, NQ] natural-log sum-exp, or NULL

@@ -56,9 +56,12 @@
 // was wrong: 1x128k 37.8 -> 38.9 us, 64 ragged 59.0 -> 58.3.  The largest product
 // found by a bound from p and s apart, and then once more token by token: 39.2.)
 // e2m1 (Q4): the same with two levels of scales.  A K group's r_g multiplies its 32
-// dims' part of the logit in fp32, s the sum.  P is stored with s, as above (with W
-// the P at most 32768), and for each group multiplied by r_g / 256 in fp16, which
-// rounds it once more; O is in units of 2 W.  The conversion takes a byte's two
+// dims' part of the logit in fp32, s the sum.  P is stored with s, as above, and V's
+// values are multiplied by r_g / 256 in fp16, which is exact (6 significant bits,
+// 2^-18 at least); O is in units of 2 W.  (P times r_g / 256 takes a quarter or half of
+// the products, but rounds P again and leaves fp16's range where r_g is small: a group
+// of 2^-6 lost its tokens below 2^-18 W, 64 ragged of 128 took 49.7 us for 51.3.)  The
+// conversion takes a byte's two
 // values, neighbours in a row, but the operand of V^T P^T wants two tokens of one
 // column: so ldmatrix is given V's rows in an order that brings neighbouring tokens
 // into two registers, whose nibbles are merged before the conversion (4 logical
@@ -85,12 +88,12 @@
 // CTAs that end apart (9 or 10 to a row of the first case).  While tiles flow,
 // bf16 is bound by DRAM, and e4m3 by the latency of conversions and products
 // in 8 warps (a quarter of the issue slots is used).
-//   e2m1: 1 x 126977, 32 q heads on 2 of 256: 38.7 us for 71 MB (1.8 TB/s, 27 %), 8 on
-// 2: 29.5; 64 ragged, 32 on 4 of 128: 49.5 us for 150 MB (3.0 TB/s, 45 %), 16 on 2 of
-// 256: 46.4; 8 x 32768, 32 on 2 of 256: 63.7, 32 on 4 of 128: 47.6; 1 x 500, 8 on 2 of
-// 128: 7.7.  Half of e4m3's bytes take as many conversions and products and more
-// scales: 2.7 instructions per value and lane (8 x 32768 of 128: 1393 per tile of
-// 64 tokens, 256 of them conversions), in 46 to 50 % of the issue slots.  So it is
+//   e2m1: 1 x 126977, 32 q heads on 2 of 256: 39.5 us for 71 MB (1.8 TB/s, 27 %), 8 on
+// 2: 30.1; 64 ragged, 32 on 4 of 128: 51.4 us for 150 MB (2.9 TB/s, 43 %), 16 on 2 of
+// 256: 47.3; 8 x 32768, 32 on 2 of 256: 64.9, 32 on 4 of 128: 49.0; 1 x 500, 8 on 2 of
+// 128: 7.9.  Half of e4m3's bytes take as many conversions and products and more
+// scales: 2.9 instructions per value and lane (8 x 32768 of 128: some 1490 per tile of
+// 64 tokens, 256 of them conversions), in about half of the issue slots.  So it is
 // bound by the latency of a warp's instructions, and a cache of 4 bits saves more
 // memory than time.  (16 warps that share a tile of 256 or 512 tokens,
 // each with 32 columns of O, P and one barrier per tile between them: 37.2 us and
@@ -113,8 +116,7 @@ constexpr float kRaise = 8.f;                    // m is raised when a logit exc
 constexpr float kPScale = 128.f;                 // Q8: P is stored times 2^7 / W
 constexpr float kMinW = 7.888609052210118e-31f;  // 2^-100: kPScale / W stays finite
 constexpr float kMaxW = 8.507059173023462e+37f;  // 2^126, far above the largest scale of 2^119
-constexpr float kPMax = 57344.f;                 // Q8: W is raised where a P would pass this
-constexpr float kPMax4 = 32768.f;                // Q4: the same (r_g / 256 is 1.75 at most)
+constexpr float kPMax = 57344.f;                 // QUANT: W is raised where a P would pass this
 constexpr float kAboveOne = 1.00000023841857910f;  // 1 + 2^-22 (bf16: P's lo)
 constexpr int kDecMaxHeads = 16;                 // of a row
 constexpr int kDecStages = 16;                   // tiles whose absent pages a worker remembers
@@ -131,6 +133,8 @@ template <int HD, int FMT, int NB>
 struct DecodeLayout {
   static constexpr bool QUANT = FMT != kBf16;
   static constexpr int RB = row_bytes(HD, FMT);
+  // (The times of choices for e2m1, here and at ROW, are of P times r_g instead of V:
+  // 1 to 4 % less.)
   // Of e2m1 pages, by head dim and NB: workers, slot bytes and slots.  Slots of 4 KB
   // where 8 KB would take more tokens than P and the logits have registers for (1 x
   // 126977, 32 q heads on 2 of 256: 38.8 us, 45.6 with 8 KB), and more workers where O
@@ -1211,7 +1215,7 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) raise |= wx[nb][j] * ps[nb][j] > (Q4 ? kPMax4 : kPMax);
+          for (int j = 0; j < 2; ++j) raise |= wx[nb][j] * ps[nb][j] > kPMax;
         if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
@@ -1262,8 +1266,8 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
             }
           }
       if constexpr (Q4) {
-        // What is no token has P = 0, but its r_g are whatever was there: none that
-        // would be infinite or NaN as fp16.
+        // What is no token has P = 0, but its r_g are whatever was there, and as fp16
+        // infinite or NaN with their sign's bit.
         if (partial) {
           for (int i = lane; i < WT; i += 32) {
             if (i < valid && !((bad >> (i >> box_shift)) & 1u)) continue;
@@ -1327,13 +1331,19 @@ __global__ void __launch_bounds__(DecodeLayout<HD, FMT, NB>::THREADS, 1)
               uint32_t lo[4], hi[4];
               e2m1x8_to_f16x8((m1 & 0x0F0F0F0Fu) | ((m2 << 4) & 0xF0F0F0F0u), lo);
               e2m1x8_to_f16x8(((m1 >> 4) & 0x0F0F0F0Fu) | (m2 & 0xF0F0F0F0u), hi);
+              // Times their r_g / 256: no rounding (x4 has 2 significant bits, r_g 4, and
+              // the least product is 2^-18).
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                lo[i] = mul_f16x2(lo[i], i < 2 ? f0 : f8);
+                hi[i] = mul_f16x2(hi[i], i < 2 ? f0 : f8);
+              }
               const uint32_t a0[4] = {lo[0], hi[0], lo[2], hi[2]};
               const uint32_t a1[4] = {lo[1], hi[1], lo[3], hi[3]};
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
-                const uint32_t b0 = mul_f16x2(pb[2 * nb], f0), b1 = mul_f16x2(pb[2 * nb + 1], f8);
-                mma16816<true>(o[2 * (ch + j)][nb], a0, b0, b1);
-                mma16816<true>(o[2 * (ch + j) + 1][nb], a1, b0, b1);
+                mma16816<true>(o[2 * (ch + j)][nb], a0, pb[2 * nb], pb[2 * nb + 1]);
+                mma16816<true>(o[2 * (ch + j) + 1][nb], a1, pb[2 * nb], pb[2 * nb + 1]);
               }
             }
           }
