@@ -716,8 +716,12 @@ cpattn_status cpattn_rope_steps(const double* inv_freq, int32_t n, uint64_t* ste
  *                   parts of the rows of one projection
  *   k, k_out        the same of NKV heads
  * q_out may be q with the same stride, and k_out k; no other overlap.  A NaN or an
- * infinity stays within its row and head, other values of which it may make NaN;
- * where the squares' mean passes fp32's range the head is 0 or NaN.  One launch.
+ * infinity stays within its row and head: without a norm within its pair, or, where
+ * nothing turns, to itself (such values are copies, bit for bit, but for a NaN's);
+ * with one, a NaN makes the whole head NaN, and where the squares' mean passes fp32's
+ * range finite values become 0 and infinite ones NaN (a pair of both: NaN).  Where that
+ * mean plus eps is below 2^-126 (eps 0 or next to it, values around 2^-63 and less) the
+ * result is inaccurate, infinite or NaN.  One launch.
  * Errors: E_INVALID, E_CUDA.
  */
 cpattn_status cpattn_norm_rope(cpattn_ctx* ctx, const cpattn_norm_rope_desc* desc, int32_t num_rows,

@@ -20,12 +20,13 @@
 //   y_a = r (x_a (w_a cos) - x_b (w_b sin)),  y_b = r (x_b (w_b cos) + x_a (w_a sin)),
 // r = 1 / sqrt(mean + eps), a head takes four products of pairs of values in
 // packed fp32 instructions, and r.
-//   17421 rows of 32 + 4 heads of 128: 51.4 us for 321 MB (6.3 TB/s, 92 % of a copy's);
-// 20161 rows of 32 + 2 of 256: 106.5 us (702 MB, 6.6 TB/s), with K and V going to bf16
-// pages 115.8 (743 MB, 6.4), to e4m3 pages 113.0; the first case to e4m3 pages 62.6 us
-// for 340 MB (5.4 TB/s, 64 % of the issue slots: what each unit of K and V needs for its
-// scale, two reductions and a division, is not hidden whole).  7 rows: 3.2 and 3.6 us as
-// nodes of a graph.
+//   17421 rows of 32 + 4 heads of 128: 51.1 us for 321 MB (6.3 TB/s, 92 % of a copy's);
+// 20161 rows of 32 + 2 of 256: 107 us (702 MB, 6.6 TB/s), with K and V going to bf16
+// pages 113.8 (743 MB, 6.5), to e4m3 pages 115.3, to e2m1 pages 115.1 (712 MB); the first
+// case to e4m3 pages 60.8 us for 340 MB (5.6 TB/s, 64 % of the issue slots: what each unit
+// of K and V needs for its scale, two reductions and a division, is not hidden whole),
+// to e2m1 pages 56.6 (331 MB, 5.9 TB/s).  7 rows: 3.1 and 3.5 us as nodes of a graph, to
+// e2m1 pages 3.8.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -84,9 +85,12 @@ struct Factors {
   f32x2 ac[2], bs[2], bc[2], as[2];
 };
 
-// (r0, r1: the lane's two runs of four bf16 values.)
+// (r0, r1: the lane's two runs of four bf16 values; turn: they turn.  What does not is
+// a product with its own factor alone: 0 times the other value would be NaN where that
+// is infinite.)
 template <int HD, bool NEIGHBOURS>
-__device__ __forceinline__ Pairs norm_and_turn(uint2 r0, uint2 r1, bool norm, float eps, const Factors& f) {
+__device__ __forceinline__ Pairs norm_and_turn(uint2 r0, uint2 r1, bool norm, float eps, bool turn,
+                                               const Factors& f) {
   if (NEIGHBOURS) regroup(r0, r1);
   const Pairs x = {{bf16x2_to_f32x2(r0.x), bf16x2_to_f32x2(r0.y)}, {bf16x2_to_f32x2(r1.x), bf16x2_to_f32x2(r1.y)}};
   f32x2 s2 = mul2(x.a[0], x.a[0]);
@@ -102,8 +106,20 @@ __device__ __forceinline__ Pairs norm_and_turn(uint2 r0, uint2 r1, bool norm, fl
   Pairs y;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    y.a[i] = mul2(fma2(x.b[i], f.bs[i], mul2(x.a[i], f.ac[i])), r2);
-    y.b[i] = mul2(fma2(x.a[i], f.as[i], mul2(x.b[i], f.bc[i])), r2);
+    y.a[i] = mul2(x.a[i], f.ac[i]);
+    y.b[i] = mul2(x.b[i], f.bc[i]);
+  }
+  if (turn) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      y.a[i] = fma2(x.b[i], f.bs[i], y.a[i]);
+      y.b[i] = fma2(x.a[i], f.as[i], y.b[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    y.a[i] = mul2(y.a[i], r2);
+    y.b[i] = mul2(y.b[i], r2);
   }
   return y;
 }
@@ -396,7 +412,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks)
     const int run0 = sub * (2 * HD) + 2 * d0, run1 = sub * (2 * HD) + 2 * d1;
     auto turned = [&](const uint8_t* unit) {
       return norm_and_turn<HD, NEIGHBOURS>(*reinterpret_cast<const uint2*>(unit + run0),
-                                           *reinterpret_cast<const uint2*>(unit + run1), norm, p.eps, f);
+                                           *reinterpret_cast<const uint2*>(unit + run1), norm, p.eps, turn, f);
     };
     if (FMT > 0 && kind == 1) {
       if constexpr (FMT > 0) {

@@ -67,3 +67,50 @@ def test_prompts_that_a_plan_did_not_serve_are_not_written(fmt, case):
     oracle.paged_write_ref(c.pools, c.scales, c.table, page, have, np.arange(4), step)
     c.check_pools()
     assert c.intact()
+
+
+# ------------------------------------------- what does not turn
+
+@pytest.mark.parametrize("appended", [False, True], ids=["dense", "bf16 pages"])
+@pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "neighbours"])
+@pytest.mark.parametrize("hd,rot", [(128, 24), (128, 0), (256, 64), (256, 0)])
+def test_dims_that_do_not_turn_keep_to_themselves(hd, rot, interleaved, appended):
+    """Without norm weights they are copies, bit for bit, whatever stands beside them: NaN,
+    infinities and zeros of either sign.  With weights an infinity makes the root infinite,
+    so every finite value 0."""
+    rng = np.random.default_rng(hd + rot)
+    rows, nq, nkv = 9, 4, 2
+    x = bf16_normal(rng, rows, nq + nkv, hd)
+    still = x[..., rot:]
+    still[rng.random(still.shape) < 0.2] = 0x7F80
+    still[rng.random(still.shape) < 0.2] = 0xFF80
+    still[::2][rng.random(still[::2].shape) < 0.1] = 0x7FC1      # (of every second row)
+    still[rng.random(still.shape) < 0.1] = 0x8000
+    t = Buffer(x, torch.bfloat16)
+    q, k = t.t[:, :nq], t.t[:, nq:]
+    freq = 1e4 ** (-np.arange(rot // 2) / max(rot // 2, 1))
+    w = torch.ones(hd, device="cuda")
+    pos, slots = i32(range(1, rows + 1)), i32(range(rows))
+    ctx = cp.Context(nq, nkv, hd, 1, 1, 1)
+    for normed in (False, True):
+        nr = cp.NormRope(freq, *([w, w] if normed else []), interleaved=interleaved, device="cuda")
+        q_out = torch.zeros(rows, nq, hd, dtype=torch.bfloat16, device="cuda")
+        k_out = torch.zeros(rows, nkv, hd, dtype=torch.bfloat16, device="cuda")
+        if appended:
+            c = _paged("bf16", nkv, hd, 16, [rows]).upload()
+            ctx.norm_rope_write_kv(nr, c.kv, pos, slots, q, k, k, q_out)
+            k_out = c.d_pools[0].t[0, :, :rows].transpose(0, 1)
+        else:
+            ctx.norm_rope(nr, pos, q, k, q_out, k_out)
+        _ok(ctx)
+        got = np.concatenate([oracle.bf16_bits(y.contiguous().cpu()) for y in (q_out, k_out)], 1)
+        if not normed:
+            nan = (still & 0x7FFF) > 0x7F80
+            assert np.array_equal(got[..., rot:][~nan], still[~nan])
+            assert np.all((got[..., rot:][nan] & 0x7FFF) > 0x7F80)
+            assert np.isfinite(oracle.bits_to_f64(got[..., :rot])).all()
+        else:
+            holds = lambda v: (((x & 0x7FFF) > 0x7F80) if v else ((x & 0x7FFF) == 0x7F80)).any(-1)  # noqa: E731
+            infinite = holds(False) & ~holds(True)
+            finite = infinite[..., None] & ((x & 0x7F80) != 0x7F80)
+            assert finite.any() and np.all((got[finite] & 0x7FFF) == 0)
