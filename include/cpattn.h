@@ -673,7 +673,9 @@ cpattn_status cpattn_paged_plan(cpattn_ctx* ctx, const cpattn_pages* pages, int3
  * page that several sequences hold must not go back while one still needs it.
  * More pages than the pool has left to give back (some would go back twice): none
  * does, and cpattn_sync_status returns E_PAGE, as for a length beyond the table's
- * row, which is cut there.
+ * row, which is cut there, and for a page outside the pool: that goes to the list as it
+ * is, so that the list is still what it was before a plan that took it from there, and
+ * the next plan that takes it reports it again.
  *   lens, keep   device int32 [B]
  * One launch.  Errors: as cpattn_paged_write_kv.
  */

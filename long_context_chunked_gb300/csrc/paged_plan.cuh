@@ -254,7 +254,10 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int k = first; k < total; k += step) {
     const int b = slice_of(page_end, p.num_seqs, k);
     const int col = kept[b] + k - (b > 0 ? page_end[b - 1] : 0);
-    p.free_pages[count + total - 1 - k] = load_now(p.table + b * c.table_stride + col);
+    const int page = load_now(p.table + b * c.table_stride + col);
+    p.free_pages[count + total - 1 - k] = page;
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_pages) && p.status != nullptr)
+      atomicCAS(p.status, kStatusOk, kStatusPage);
   }
   cluster_await();
   if (blockIdx.x == 0 && tid == 0) *p.free_count = count + total;

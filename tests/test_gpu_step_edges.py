@@ -8,7 +8,7 @@ import long_context_chunked_gb300 as cp
 import oracle
 from paged_helpers import Buffer, bf16_normal, i32
 from test_gpu_paged import _ok
-from test_gpu_step import FORMATS, _paged
+from test_gpu_step import FORMATS, Plan, _paged
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +114,26 @@ def test_dims_that_do_not_turn_keep_to_themselves(hd, rot, interleaved, appended
             infinite = holds(False) & ~holds(True)
             finite = infinite[..., None] & ((x & 0x7F80) != 0x7F80)
             assert finite.any() and np.all((got[finite] & 0x7FFF) == 0)
+
+
+# ------------------------------------------- pages outside the pool
+
+def test_trim_reports_pages_outside_the_pool():
+    """They go to the list as they are, as the other pages do, and a plan that takes them
+    from there reports them again and gives their rows no slot."""
+    p = Plan([40, 20], 16, 3, 1, stride_pad=0)
+    pages = len(p.free) + 5
+    for bad in (-1, pages, 2 ** 31 - 1, -2 ** 31):
+        p = Plan([40, 20], 16, 3, 1, stride_pad=0)
+        p.d_table.t[0, 1] = bad
+        p.table[0, 1] = bad
+        assert p.trim([40, 20], [40, 16]) == cp.OK                # (not among those that go back)
+        assert p.trim([40, 16], [0, -1]) == cp.E_PAGE
+        d = [i32(v) for v in ([0, 0], [32, 0], [0, 0], [0, 0, 0], [0] * 32, [0] * 32)]
+        first, second = p.free[-1], p.free[-2]
+        assert second == bad
+        p.ctx.paged_plan(p.kv, d[0], d[1], p.d_free.t, p.d_count.t, d[2], d[3], d[4], d[5])
+        assert p.ctx.sync_status() == cp.E_PAGE
+        assert d[5].tolist() == [first * 16 + i for i in range(16)] + [-1] * 16
+        assert p.d_free.intact() and p.d_table.intact() and p.d_count.intact()
+    _ok(p.ctx)
