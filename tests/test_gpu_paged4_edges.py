@@ -1,11 +1,14 @@
 """Edges of attention over 4-bit pages on the GPU: column groups that are small in
-every token, next to a token that outweighs the others."""
+every token, next to a token that outweighs the others; and the number of copies, in
+tiles of the one size that each kernel has."""
 import numpy as np
 import pytest
 import torch
 
 import long_context_chunked_gb300 as cp
 import oracle
+from long_context_chunked_gb300 import build as cpbuild
+from long_context_chunked_gb300.binding import COUNT_BARS, COUNT_RECORD
 from paged4_helpers import Paged4, largest_product
 from paged_helpers import Buffer, i32
 from test_gpu_paged import _ok
@@ -62,3 +65,26 @@ def test_small_groups_keep_their_tokens(nq, hd, small):
     got = out.double().cpu().numpy()
     err = np.abs(got - ref)
     assert np.all(err <= bound), f"worst {np.max(err / bound):.3f} of the bound"
+
+
+@pytest.mark.parametrize("nq,nkv,hd,page,lens", [
+    (8, 2, 128, 64, [40001, 5]), (16, 1, 128, 16, [20001, 300]), (8, 2, 256, 64, [20001, 5]), (16, 1, 256, 128, [20001]),
+    (16, 1, 256, 64, [300] * 350), (8, 1, 256, 16, [33 + i for i in range(300)]), (4, 4, 128, 32, [1200 + 26 * i for i in range(40)])],
+    ids=str)
+def test_every_tile_is_copied_once(nq, nkv, hd, page, lens):
+    """K and V of each tile: of 32 tokens for more than 8 heads of 256 to a kv head, else of 64."""
+    c = Paged4(nkv, hd, page, lens, seed=33)
+    c.fill(np.random.default_rng(33), lens)
+    c.upload()
+    ctx = cp.Context(nq, nkv, hd, 1, 1, 1, library=cpbuild.build(variant="counted"))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rec = torch.zeros(sms * COUNT_RECORD, dtype=torch.int32, device="cuda")
+    ctx.set_barrier_counts(rec)
+    q = torch.zeros(len(lens), nq, hd, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(ctx.paged_decode_workspace(len(lens)), dtype=torch.uint8, device="cuda")
+    ctx.paged_decode(c.kv, i32(lens), q, torch.zeros_like(q), ws)
+    _ok(ctx)
+    tile = 32 if hd == 256 and nq // nkv > 8 else 64
+    counts = rec.cpu().numpy().reshape(sms, -1, COUNT_BARS)
+    assert int(counts[:, 0].sum()) == 2 * nkv * sum(-(-n // tile) for n in lens)
+    assert np.array_equal(counts[:, 0], counts[:, 1])
