@@ -358,7 +358,7 @@ cpattn_status cpattn_set_fault_injection(cpattn_ctx* ctx, int32_t flags, int32_t
  *   row 3  [120, 160) completed waits of the MMA warp
  *   row 4  [160, 200) softmax waits for the previous tile's P.V before a
  *                     rescale of O (data-dependent; apart from row 1)
- * A cpattn_paged_decode launch adds, for warp w (< 8) of CTA b, the copies it
+ * A cpattn_paged_decode launch adds, for warp w (< 12) of CTA b, the copies it
  * sent into row 0 at w, and those it saw land into row 1 at w: as many, even
  * after a wait expired.
  * The caller zeroes the records before a launch and reads them after it.
