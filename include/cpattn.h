@@ -601,7 +601,7 @@ cpattn_status cpattn_paged_read_kv(cpattn_ctx* ctx, const cpattn_pages* pages, i
  * below 2^-31.  For e2m1 pages the same is done with s; r_g adds no rounding.  A
  * sequence without tokens (lens[b] <= 0) gets O = 0 and an LSE of -infinity.
  *   lens        device int32 [B], B in 1..CPATTN_MAX_PAGED_SEQS
- *   q, out      device bf16 [B, NQ, HD]
+ *   q, out      device bf16 [B, NQ, HD], by sequence (not by a plan's rows)
  *   lse         device fp32 [B, NQ] natural-log sum-exp, or NULL
  *   workspace   device memory, 256-byte aligned, at least
  *               cpattn_paged_decode_workspace() bytes, used by the call's
@@ -628,6 +628,11 @@ cpattn_status cpattn_paged_decode(cpattn_ctx* ctx, const cpattn_pages* pages, in
  * (or norm_rope, prefill_packed and paged_write_planned_kv for whole prompts), and trim
  * when requests end or drafted tokens are rejected.  All of it is captured and
  * replayed like the paged calls: lengths and lists are device arrays.
+ * A plan packs the step's rows one sequence behind the other; paged_decode takes row
+ * b of q for sequence b.  Only where every sequence has exactly one new token are
+ * they the same: else gather row row_starts[b+1] - 1, the last new one of sequence b.
+ * (Sequences without a new token then get a row of another's, and their output is of
+ * no use; one that was not served gets its own row as the buffer held it before.)
  */
 
 /*

@@ -518,7 +518,9 @@ class Context:
 
     def paged_decode(self, pages: PagedKV, lens, q, out, workspace, lse=None, stream=None):
         """Attention of one new token per sequence, q [num_seqs, NQ, HD], over
-        the first lens[b] (int32 CUDA tensor) tokens of its pages."""
+        the first lens[b] (int32 CUDA tensor) tokens of its pages.  Row b of q is
+        sequence b's: of the rows that paged_plan packed, q[row_starts[1:] - 1],
+        unless every sequence has exactly one new token."""
         import torch
         self._check_pages(pages)
         b, nq, hd, dev = pages.num_seqs, self.dims[0], pages.head_dim, pages.device

@@ -1,11 +1,13 @@
 """Edges of the serving step and of 4-bit pages on the GPU: prompts written after a plan
-that did not serve everyone."""
+that did not serve everyone, attention of packed rows by place, dims that do not turn, and
+pages outside the pool."""
 import numpy as np
 import pytest
 import torch
 
 import long_context_chunked_gb300 as cp
 import oracle
+from paged4_helpers import check_decode4
 from paged_helpers import Buffer, bf16_normal, i32
 from test_gpu_paged import _ok
 from test_gpu_step import FORMATS, Plan, _paged
@@ -67,6 +69,60 @@ def test_prompts_that_a_plan_did_not_serve_are_not_written(fmt, case):
     oracle.paged_write_ref(c.pools, c.scales, c.table, page, have, np.arange(4), step)
     c.check_pools()
     assert c.intact()
+
+
+@pytest.mark.parametrize("captured", [False, True], ids=["eager", "captured"])
+def test_packed_rows_are_attended_by_place(captured):
+    """A step with an empty place, one without a new token, one with several and one that
+    is not served: each served place's last new row."""
+    rng = np.random.default_rng(5)
+    nq, nkv, hd, page, held, new = 8, 2, 128, 16, [20, -1, 37, 0, 64, 11], [1, 9, 0, 3, 200, 30]
+    need = [-(-max(h, 0) // page) for h in held]
+    c = _paged("e2m1", nkv, hd, page, [page * (sum(need) + 5)], spare_pages=0)
+    pages = c.pools[0].shape[0]
+    c.table, c.cols = np.full((len(held), 8), 2 ** 30, np.int32), 8
+    at = 0
+    for b, n in enumerate(need):
+        c.table[b, :n] = np.arange(at, at + n)
+        at += n
+    c.fill(rng, np.maximum(held, 0))
+    c.upload()
+    rows = sum(n for h, n in zip(held, new) if h >= 0)
+    x = Buffer(bf16_normal(rng, rows, nq + 2 * nkv, hd), torch.bfloat16)
+    ctx, nr = cp.Context(nq, nkv, hd, 1, 1, 1), cp.NormRope(1e4 ** (-np.arange(64) / 64))
+    free = i32(list(range(at, pages)) + [0] * at)
+    have, more, count, lens, starts, pos, slots = (
+        i32(v) for v in (held, new, [pages - at], [0] * 6, [0] * 7, [0] * rows, [0] * rows))
+    q = torch.zeros(rows, nq, hd, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.zeros(6, nq, hd, dtype=torch.bfloat16, device="cuda"), torch.zeros(6, nq, device="cuda")
+    ws = torch.empty(ctx.paged_decode_workspace(6), dtype=torch.uint8, device="cuda")
+
+    def step():
+        ctx.paged_plan(c.kv, have, more, free, count, lens, starts, pos, slots)
+        ctx.norm_rope_write_kv(nr, c.kv, pos, slots, *x.t.split([nq, nkv, nkv], 1), q)
+        ctx.paged_decode(c.kv, lens, q[starts[1:] - 1], out, ws, lse=lse)
+
+    state = [t.clone() for t in (free, count, c.d_table.t)]
+    step()
+    if captured:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for t, was in zip((free, count, c.d_table.t), state):
+            t.copy_(was)
+        for t in (q, out, lse):
+            t.zero_()
+        graph.replay()
+    assert ctx.sync_status() == cp.E_PAGE                 # (the fifth's columns end before its tokens)
+    assert lens.tolist() == [21, -1, 37, 3, 64, 41]
+    c.pools, c.scales, c.table = [d.host() for d in c.d_pools], [d.host() for d in c.d_scales], c.d_table.host()
+    served = [0, 3, 5]
+    c.table = c.table[served]
+    last = [int(starts[b + 1]) - 1 for b in served]
+    assert last == [0, 3, 233]
+    check_decode4(c, q[last].double().cpu().numpy(), [21, 3, 41], hd ** -0.5, out[served].double().cpu().numpy(),
+                  lse[served].double().cpu().numpy())
 
 
 # ------------------------------------------- what does not turn
