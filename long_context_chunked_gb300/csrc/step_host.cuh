@@ -117,12 +117,18 @@ cpattn_status launch_norm_rope(cpattn_ctx* ctx, void (*kernel)(cpattn::NormRopeP
     if (batches >= room * WARPS) break;
   }
   // Many rows: blocks of a row per warp, of which the SMs take the next as they end
-  // one (when this was chosen: 20161 rows, 32 + 2 heads of 256: 107.7 us, 113.9 appended to bf16 pages,
-  // 110.5 to e4m3; equal slices for resident blocks: 123.0, 137.4, 135.6; 17421 rows,
-  // 32 + 4 of 128: 53.4 and 60.3).  Rows of 128 that are appended are too little work
-  // for a block's beginning (e4m3: 68.7 us, equal slices 60.3), and few rows have to
-  // be spread (2000 rows, 32 + 4 of 128: 11.4 us and 10.4).
-  const bool rows_in_turn = p->batch > 1 && (ctx->cfg.head_dim == 256 || !append) &&
+  // one, or equal slices for resident blocks, which end apart.  A block's beginning
+  // (weights, frequencies, a barrier) wants rows of 8 KB of Q and K, and 16 KB where K and
+  // V are quantised, which balances the slices too.  Slices and in turn, us, by bytes of a row:
+  //   dense   2560: 62.9, 89.2   5120: 76.8, 76.0   9216: 59.6, 50.6   17408: 124, 107
+  //   bf16    2560: 80.4, 107    5120: 91.8, 91.2   9216: 67.8, 59.8   17408: 136, 113
+  //   e4m3    5120: 87.9, 105    9216: 60.5, 62.2  17408: 136, 113     18432: 75.7, 65.4
+  //   e2m1    5120: 97.7, 115    9216: 56.0, 63.9  17408: 135, 114     18432: 72.4, 63.4
+  // (4 + 1 and 8 + 2 heads of 256, 32 + 4 of 128, 32 + 2 of 256, 64 + 8 of 128; 60000,
+  // 40000, 17421, 20161, 10000 rows; 1024 B, 200000 rows of 1 + 1 of 256: 168, 269.)  Few
+  // rows have to be spread (2000 rows, 32 + 4 of 128: in turn 11.4 us, slices 10.4).
+  const int row_bytes = 2 * ctx->cfg.head_dim * (p->nq + p->nkv);
+  const bool rows_in_turn = p->batch > 1 && row_bytes >= (format > 0 ? 16384 : 8192) &&
                             p->rows >= 2 * room * WARPS;
   const int grid = static_cast<int>(rows_in_turn ? (p->rows + WARPS - 1) / WARPS
                                                  : std::min<long long>((batches + WARPS - 1) / WARPS, room));

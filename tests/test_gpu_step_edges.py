@@ -1,6 +1,6 @@
 """Edges of the serving step and of 4-bit pages on the GPU: prompts written after a plan
-that did not serve everyone, attention of packed rows by place, dims that do not turn, and
-pages outside the pool."""
+that did not serve everyone, attention of packed rows by place, dims that do not turn, rows
+dealt in two ways, and pages outside the pool."""
 import numpy as np
 import pytest
 import torch
@@ -170,6 +170,38 @@ def test_dims_that_do_not_turn_keep_to_themselves(hd, rot, interleaved, appended
             infinite = holds(False) & ~holds(True)
             finite = infinite[..., None] & ((x & 0x7F80) != 0x7F80)
             assert finite.any() and np.all((got[finite] & 0x7FFF) == 0)
+
+
+# ------------------------------------------- rows dealt to the GPU in two ways
+
+@pytest.mark.parametrize("fmt", [None, "bf16", "e4m3", "e2m1"])
+@pytest.mark.parametrize("nq,nkv,hd", [(1, 1, 256), (30, 2, 128), (32, 4, 128), (62, 2, 128), (28, 4, 256)], ids=str)
+def test_rows_of_any_size_are_those_of_fewer_at_once(nq, nkv, hd, fmt):
+    """Many rows, below and above the sizes from which blocks take rows in turn: the bits
+    of calls of at most 2500."""
+    rows = 7501
+    gen = torch.Generator(device="cuda").manual_seed(nq)
+    x = torch.randn(rows, nq + 2 * nkv, hd, generator=gen, device="cuda").to(torch.bfloat16).split([nq, nkv, nkv], 1)
+    pos = torch.randint(-5, 10 ** 6, (rows,), generator=gen, device="cuda").int()
+    slots = torch.randperm(rows, generator=gen, device="cuda").int()
+    w = torch.rand(hd, generator=gen, device="cuda") + 0.5
+    nr = cp.NormRope(1e4 ** (-np.arange(hd // 4) / (hd // 4)), w, w)
+    ctx = cp.Context(nq, nkv, hd, 1, 1, 1)
+    got = []
+    for size in (rows, 2500):
+        q = torch.zeros(rows, nq, hd, dtype=torch.bfloat16, device="cuda")
+        k = torch.zeros(rows, nkv, hd, dtype=torch.bfloat16, device="cuda")
+        c = None if fmt is None else _paged(fmt, nkv, hd, 64, [rows], seed=1).upload()
+        for a in range(0, rows, size):
+            part = slice(a, a + size)
+            if c is None:
+                ctx.norm_rope(nr, pos[part], x[0][part], x[1][part], q[part], k[part])
+            else:
+                ctx.norm_rope_write_kv(nr, c.kv, pos[part], slots[part], *(y[part] for y in x), q[part])
+        _ok(ctx)
+        got.append([q, k] if c is None else [q] + [b.t for b in c.d_pools + (c.d_scales or [])])
+    for a, b in zip(*got):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)) and a.view(torch.uint8).any()
 
 
 # ------------------------------------------- pages outside the pool
