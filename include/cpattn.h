@@ -498,8 +498,10 @@ cpattn_status cpattn_prefill_packed(cpattn_ctx* ctx, int32_t num_seqs, const int
  *                        x4 = e2m1((x / s) / r_g), 0 where r_g = 0
  *                      (fp32, nearest even, x4 at most 6, -0 as 0), and the value read
  *                      back is s * r_g * x4.  A row that holds an infinity or a
- *                      NaN is stored with s = NaN.  Readers take any r_g >= 0 and
- *                      any s that is a power of two up to 2^118.
+ *                      NaN is stored with s = NaN.  (In rows whose largest value
+ *                      is above 3.35e38, values above 2.9e38 come to 1056 * 2^118,
+ *                      which reads back as an infinity.)  Readers take any r_g >= 0
+ *                      and any s that is a power of two up to 2^118.
  * Lengths, row_starts and block_table are DEVICE arrays, read when the kernels
  * run: a captured graph of these calls can be replayed after they changed.
  * So they are checked on the device: a page id outside [0, num_pages), or a

@@ -1,6 +1,6 @@
 """Edges of attention over 4-bit pages on the GPU: column groups that are small in
-every token, next to a token that outweighs the others; and the number of copies, in
-tiles of the one size that each kernel has."""
+every token, next to a token that outweighs the others; values next to the largest;
+and the number of copies, in tiles of the one size that each kernel has."""
 import numpy as np
 import pytest
 import torch
@@ -65,6 +65,28 @@ def test_small_groups_keep_their_tokens(nq, hd, small):
     got = out.double().cpu().numpy()
     err = np.abs(got - ref)
     assert np.all(err <= bound), f"worst {np.max(err / bound):.3f} of the bound"
+
+
+@pytest.mark.parametrize("hd", [128, 256])
+def test_values_next_to_the_largest(hd):
+    """A row whose largest value is above 1008 * 2^118 has r_g = 176, and its values above 5
+    * 176 * 2^118 read back as 6 * 176 * 2^118: an infinity.  From 1008 * 2^118 down: 160."""
+    x = np.zeros((2, 1, hd))
+    x[0, 0, :3] = np.array([1012, 884, -876]) * 2.0 ** 118
+    x[1, 0, :3] = np.array([1008, -884, 700]) * 2.0 ** 118
+    bits = oracle.bf16_bits(torch.from_numpy(x).to(torch.bfloat16))
+    assert np.array_equal(oracle.bits_to_f64(bits), x)
+    c = Paged4(1, hd, 16, [2]).upload()
+    ctx = cp.Context(1, 1, hd, 1, 2, 1)
+    d = [Buffer(bits, torch.bfloat16).t for _ in range(2)]
+    ctx.paged_write_kv(c.kv, i32([0]), *d, row_starts=i32([0, 2]))
+    cache = [torch.zeros(1, 1, 1, 2, hd, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ctx.paged_read_kv(c.kv, i32([2]), *cache)
+    _ok(ctx)
+    for y in cache:
+        y = y[0, 0, 0].double().cpu().numpy()
+        assert y[0, :3].tolist() == [np.inf, np.inf, -704 * 2.0 ** 118] and not y[:, 3:].any()
+        assert y[1, :3].tolist() == [960 * 2.0 ** 118, -960 * 2.0 ** 118, 640 * 2.0 ** 118]
 
 
 @pytest.mark.parametrize("nq,nkv,hd,page,lens", [
