@@ -383,7 +383,7 @@ __device__ __forceinline__ long long write_place(const PagedWriteParams& p, int 
 //   64961 prompt tokens of 2 heads of 256 to bf16 pages: 41.8 us for 266 MB,
 // 6.4 TB/s.  To e4m3 pages a head's rows are quantised before the next head's are
 // loaded: 17421 tokens of 4 heads of 128 take 14.0 us for 54 MB, 3.9 TB/s, and
-// 40000 tokens of 2 heads of 256 37.7 us for 124 MB, 3.3 TB/s (108 registers, so
+// 40000 tokens of 2 heads of 256 37.3 us for 124 MB, 3.3 TB/s (96 registers, so
 // two blocks per SM).  A decode step of 7 tokens: 2.3 us as a node of a graph.
 template <int HD, int ROWS, int FMT>
 __global__ void __launch_bounds__(256)

@@ -95,9 +95,9 @@
 // scales: 2.9 instructions per value and lane (8 x 32768 of 128: some 1490 per tile of
 // 64 tokens, 256 of them conversions), in about half of the issue slots.  So it is
 // bound by the latency of a warp's instructions, and a cache of 4 bits saves more
-// memory than time.  (16 warps that share a tile of 256 or 512 tokens,
-// each with 32 columns of O, P and one barrier per tile between them: 37.2 us and
-// 51.0 for the first and the last but one case, but 90 us for the 64 ragged ones,
+// memory than time.  (With P times r_g, 1 to 4 % less time: 16 warps that share a tile
+// of 256 or 512 tokens, each with 32 columns of O, P and one barrier per tile between
+// them: 37.2 us for 38.7 of the first case, but 90 us for the 64 ragged ones,
 // whose many small copies one warp then has to send.  V's r_g as fp16 once per tile,
 // through shared memory, 70 instructions fewer for each: 50.0 for the 64 ragged, 64.2
 // for 8 x 32768 of 256, no faster.)
